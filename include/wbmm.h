@@ -315,6 +315,120 @@ wbmm_status wbmm_backward_bf16(int B, int C, int H, int W, int w, int layout, co
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * 8-bit activation checkpoints: what a training step keeps of a map between forward and backward.
+ * A tensor of n elements is n code bytes and ceil(n / WBMM_CKPT_GROUP) scale bytes, one per group
+ * of WBMM_CKPT_GROUP elements in memory order (the last group may be short):
+ *   value = q(code) * 2^(byte - 127);   byte 255: every value of the group is NaN,
+ * q(code) the int8 value (WBMM_CKPT_INT8) or the OCP 8-bit float 4-3 value (WBMM_CKPT_E4M3).
+ * int8 spreads its steps evenly below the group's largest magnitude, e4m3 keeps a relative error
+ * of at most 2^-4 over the 15 binades below it. Decoded values are exact in bf16 and fp32 (results
+ * below fp32's range aside: byte 0 to 2 with the smallest codes).
+ */
+#define WBMM_CKPT_GROUP 32
+typedef enum wbmm_ckpt_format { WBMM_CKPT_INT8 = 0, WBMM_CKPT_E4M3 = 1 } wbmm_ckpt_format;
+
+/*
+ * wbmm_ckpt_pack — tensor to checkpoint. Per group, with amax the largest magnitude and top = 127
+ * (int8) or 448 (e4m3): e is the least integer >= -126 with amax <= top 2^e, the byte e + 127, and
+ * a code the nearest to x 2^-e, ties to even. A group that holds an infinity or a NaN gets byte
+ * 255 (codes 0).
+ * x:      device, n elements of `dtype`, any layout (dense).
+ * codes:  device, n bytes, written. scales: device, ceil(n / WBMM_CKPT_GROUP) bytes, written.
+ * wbmm_ckpt_unpack — the inverse: x = the values, in `dtype`.
+ * Any pointer alignment down to the element works; x aligned to 16 and codes to 8 bytes takes the
+ * wide accesses. Bit-exact. Errors: WBMM_E_INVALID (n < 1, dtype, fmt, NULL or overlapping
+ * buffers), WBMM_E_UNSUPPORTED (n > 2^35, x not aligned to its elements), WBMM_E_HIP.
+ */
+wbmm_status wbmm_ckpt_pack(const void* x, int64_t n, int dtype, int fmt, uint8_t* codes,
+                           uint8_t* scales, void* stream);
+wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_t n, int dtype,
+                             int fmt, void* x, void* stream);
+
+/*
+ * wbmm_backward_ckpt_workspace_bytes / wbmm_backward_ckpt — wbmm_backward with the two maps that
+ * a training step keeps, x and the pre-mix z, as checkpoints in `fmt` (packed in the maps' own
+ * memory order, B C H W elements). dT sums over the checkpoint's x, dmix_w over its z; dx needs
+ * neither. Every other argument, output, rule and error as in wbmm_backward (table input).
+ * dtype:   of T, dy and dx: WBMM_F32, or WBMM_BF16 (widened exactly; products and sums in fp32
+ *          and fp64 as for fp32 maps, the mix adjoint of dy in fp32, dx rounded once, RNE). mix_w,
+ *          dT and dmix_w are fp32 in both.
+ * x_codes, x_scales, z_codes, z_scales: as wbmm_ckpt_pack writes them; z_* exactly with mix_w.
+ * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned.
+ * Errors as in wbmm_backward; also WBMM_E_INVALID for an unknown fmt.
+ */
+size_t wbmm_backward_ckpt_workspace_bytes(int B, int C, int H, int W, int w, int layout, int dtype,
+                                          int has_mix);
+wbmm_status wbmm_backward_ckpt(int B, int C, int H, int W, int w, int layout, int dtype, int fmt,
+                               const uint8_t* x_codes, const uint8_t* x_scales, const void* T,
+                               const float* mix_w, const uint8_t* z_codes,
+                               const uint8_t* z_scales, const void* dy, void* dx, float* dT,
+                               float* dmix_w, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * wbmm_scan_forward_workspace_bytes / wbmm_scan_forward — gated linear recurrence along one axis: a mixer
+ * of any reach, next to the windowed one and on the same maps. Tensors are dense (outer, len,
+ * inner); the recurrence runs along len, independently for every (outer, inner):
+ *   a_t = sigmoid(g_t),   h_t = a_t h_{t-1} + (1 - a_t) u_t,   h_{-1} = h0.
+ * A map in raster order is (B C, H W, 1) in NCHW and (B, H W, C) in NHWC; its columns in NCHW are
+ * (B C, H, W), its rows (B C H, W, 1). A serving step is len = 1 with h0 and h_last.
+ * dtype:    of g, u and h: WBMM_F32 or WBMM_BF16. The recurrence itself is fp32.
+ * reverse:  nonzero: sequences run from their last position to their first.
+ * h0:       device fp32 [outer][inner], or NULL for zeros.
+ * lens:     device int32 [n_lens], n_lens dividing outer, or NULL (n_lens ignored): sequence o has
+ *           lens[o / (outer / n_lens)] positions, held to [0, len]. Positions past it are not
+ *           used, whatever they hold, and h is 0 there; a reversed sequence starts at its own last
+ *           position.
+ * h:        device map, written.
+ * h_last:   device fp32 [outer][inner], or NULL: the state after the last step (h0 for an empty
+ *           sequence). May be h0 itself (updated in place).
+ * states:   device fp32 [outer][ceil(len / WBMM_SCAN_CHUNK)][inner], or NULL: the state before
+ *           steps 0, WBMM_SCAN_CHUNK, 2 WBMM_SCAN_CHUNK, ... in the order the sequence runs (its
+ *           last state past its end). The backward starts from them.
+ * workspace: wbmm_scan_forward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0; needed only
+ *           where few columns make the axis run in segments). Calls that share one must be ordered
+ *           on one stream.
+ * No atomics: bitwise reproducible. Errors: WBMM_E_INVALID (sizes, dtype, n_lens, NULL or
+ * overlapping buffers), WBMM_E_UNSUPPORTED (outer * inner >= 2^26, len > 2^30, more than 2^38
+ * elements, misaligned pointer), WBMM_E_WORKSPACE, WBMM_E_HIP.
+ */
+#define WBMM_SCAN_CHUNK 32
+size_t wbmm_scan_forward_workspace_bytes(int64_t outer, int64_t len, int64_t inner);
+wbmm_status wbmm_scan_forward(int64_t outer, int64_t len, int64_t inner, int dtype, int reverse,
+                              const void* g, const void* u, const float* h0, const int32_t* lens,
+                              int64_t n_lens, void* h, float* h_last, float* states,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * wbmm_scan_backward_workspace_bytes / wbmm_scan_backward — gradients of wbmm_scan_forward, from the last step to the first:
+ *   G_t = dh_t + a_{t+1} G_{t+1}   (dh_last in place of a_n G_n at the last step),
+ *   du_t = (1 - a_t) G_t,   dg_t = a_t (1 - a_t) (h_{t-1} - u_t) G_t,   dh0 = a_0 G_0
+ * (dh0 = dh_last for an empty sequence). The h_{t-1} are run again from `states`, in fp32.
+ * g, reverse, lens, sizes: as in the forward.
+ * u:        the forward's u, or its checkpoint's codes when u_scales is given (u_fmt: the
+ *           checkpoint's format; ignored without u_scales).
+ * states:   as the forward wrote them, or NULL: the call then runs the recurrence for them first,
+ *           on the u that it is given, from h0 (device fp32 [outer][inner], or NULL for zeros; NULL
+ *           with states), into its workspace, reading g and u a second time. With a checkpointed u
+ *           and the forward's states, each run of WBMM_SCAN_CHUNK steps starts from the state of
+ *           the forward's own u.
+ * dh:       device map in dtype. dh_last: device fp32 [outer][inner], the gradient of h_last, or
+ *           NULL for zeros.
+ * dg, du:   device maps in dtype, written; 0 past the end of a sequence. dh0: device fp32
+ *           [outer][inner], written, or NULL.
+ * workspace: wbmm_scan_backward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0).
+ * Errors as in the forward; also WBMM_E_INVALID for an unknown u_fmt, or h0 beside states.
+ */
+size_t wbmm_scan_backward_workspace_bytes(int64_t outer, int64_t len, int64_t inner,
+                                          int has_states);
+wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inner, int dtype, int reverse,
+                               int u_fmt, const void* g, const void* u, const uint8_t* u_scales,
+                               const float* states, const float* h0, const void* dh,
+                               const float* dh_last, const int32_t* lens, int64_t n_lens, void* dg,
+                               void* du, float* dh0, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
  * wbmm_probe_mfma — measurement aid, not part of the method: a matrix-core peak probe. Launches
  * `blocks` workgroups of 4 waves; every wave runs `iters` rounds of 8 independent MFMA
  * accumulation chains on register operands (dtype WBMM_F32: v_mfma_f32_16x16x4f32, WBMM_BF16:
@@ -329,7 +443,7 @@ wbmm_status wbmm_probe_mfma(int dtype, int blocks, int iters, float* out, void* 
 
 /*
  * wbmm_set_launch_events — measurement aid, not part of the method. The next wbmm_forward,
- * wbmm_backward (or their _hier, _shifted and _bf16 forms), wbmm_dwconv_forward or wbmm_probe_mfma
+ * wbmm_backward (or their _hier, _shifted, _bf16 and _ckpt forms), wbmm_dwconv_forward or wbmm_probe_mfma
  * call made on the calling thread
  * attaches `before` and `after` (hipEvent_t
  * handles passed as void*) to the dispatch of its main contraction kernel (hipExtLaunchKernel's

@@ -22,12 +22,18 @@ __all__ = [
     "wbmm_forward_shifted", "wbmm_forward_shifted_workspace_bytes", "wbmm_backward_shifted",
     "wbmm_backward_shifted_workspace_bytes", "wbmm_probe_mfma", "wbmm_backward_bf16",
     "wbmm_backward_bf16_workspace_bytes", "wbmm_backward_noalloc", "WBMM_NOALLOC_SCRATCH_BYTES",
+    "wbmm_ckpt_pack", "wbmm_ckpt_unpack", "wbmm_backward_ckpt",
+    "wbmm_backward_ckpt_workspace_bytes", "wbmm_scan_forward", "wbmm_scan_backward",
+    "wbmm_scan_forward_workspace_bytes", "wbmm_scan_backward_workspace_bytes", "WBMM_CKPT_GROUP", "WBMM_SCAN_CHUNK",
     "WBMM_OK", "WBMM_E_INVALID", "WBMM_E_UNSUPPORTED", "WBMM_E_WORKSPACE", "WBMM_E_HIP",
 ]
 
 WBMM_OK, WBMM_E_INVALID, WBMM_E_UNSUPPORTED, WBMM_E_WORKSPACE, WBMM_E_HIP = range(5)
 WBMM_F32, WBMM_BF16 = 0, 1
 WBMM_NCHW, WBMM_NHWC = 0, 1
+WBMM_CKPT_INT8, WBMM_CKPT_E4M3 = 0, 1
+WBMM_CKPT_GROUP = 32   # elements per scale of an 8-bit checkpoint
+WBMM_SCAN_CHUNK = 32   # steps between two states that the recurrence's forward keeps
 WBMM_NOALLOC_SCRATCH_BYTES = 32 << 20  # the library's fixed scratch for wbmm_backward_noalloc
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +53,7 @@ def lib_path() -> str:
 
 def _declare(lib):
     c_int, c_size, vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    c_i64 = ctypes.c_int64
     sigs = {
         "wbmm_abi_version": (c_int, []),
         "wbmm_last_error": (ctypes.c_char_p, []),
@@ -72,6 +79,16 @@ def _declare(lib):
         "wbmm_backward_shifted_workspace_bytes": (c_size, [c_int] * 9),
         "wbmm_backward_shifted": (c_int, [c_int] * 8 + [vp] * 10 + [c_size, vp]),
         "wbmm_backward_noalloc": (c_int, [c_int] * 6 + [vp] * 10),
+        "wbmm_ckpt_pack": (c_int, [vp, c_i64, c_int, c_int, vp, vp, vp]),
+        "wbmm_ckpt_unpack": (c_int, [vp, vp, c_i64, c_int, c_int, vp, vp]),
+        "wbmm_backward_ckpt_workspace_bytes": (c_size, [c_int] * 8),
+        "wbmm_backward_ckpt": (c_int, [c_int] * 8 + [vp] * 11 + [c_size, vp]),
+        "wbmm_scan_forward_workspace_bytes": (c_size, [c_i64] * 3),
+        "wbmm_scan_backward_workspace_bytes": (c_size, [c_i64] * 3 + [c_int]),
+        "wbmm_scan_forward": (c_int, [c_i64] * 3 + [c_int] * 2 + [vp] * 4 + [c_i64] + [vp] * 4 +
+                              [c_size, vp]),
+        "wbmm_scan_backward": (c_int, [c_i64] * 3 + [c_int] * 3 + [vp] * 8 + [c_i64] + [vp] * 4 +
+                               [c_size, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -443,3 +460,268 @@ def wbmm_backward_bf16(x, dy, w: int, T, mix_w=None, z_saved=None, *, layout: st
                                      _ptr(z_saved), _ptr(dy), _ptr(dx_t), _ptr(dT_t), _ptr(dW_t),
                                      _ptr(workspace), ws_bytes, _stream(stream)))
     return dx_t, dT_t, dW_t
+
+
+# ----------------------------------------------------------------------------- 8-bit checkpoints
+def _fmt_code(fmt: str) -> int:
+    if fmt == "int8":
+        return WBMM_CKPT_INT8
+    if fmt == "e4m3":
+        return WBMM_CKPT_E4M3
+    raise WbmmError(WBMM_E_INVALID, f"unknown checkpoint format {fmt!r} (int8 or e4m3)")
+
+
+def _tensor(name, t, shape, dtype, device, optional=False):
+    """Checks one tensor argument: shape, dtype, dense, and on `device` (None: the current one)."""
+    torch = _torch()
+    if t is None:
+        if optional:
+            return
+        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
+    if tuple(t.shape) != tuple(shape):
+        raise WbmmError(WBMM_E_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise WbmmError(WBMM_E_INVALID, f"{name} must be {dtype}, got {t.dtype}")
+    _ptr(t)  # on the GPU, contiguous
+    if t.device != device:
+        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, not on {device}")
+    if device.index != torch.cuda.current_device():
+        raise WbmmError(WBMM_E_INVALID, f"{name} is on {device}, which is not the current device")
+
+
+def _gpu(name, t):
+    """The device of a call, taken from its first tensor."""
+    if t is None:
+        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
+    _ptr(t)
+    return t.device
+
+
+class _on_stream:
+    """Allocations of a call belong to the stream that the call runs on."""
+
+    def __init__(self, stream, device):
+        torch = _torch()
+        if stream is None:
+            self.ctx = None
+        elif isinstance(stream, torch.cuda.Stream):
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            self.ctx = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
+                                         else torch.cuda.default_stream(device))
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _out(name, v, shape, dtype, device):
+    """An output argument: True allocates it, False or None skips it, a tensor is written."""
+    if v is False or v is None:
+        return None
+    if v is True:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _tensor(name, v, shape, dtype, device)
+    return v
+
+
+def _workspace(need, workspace, device):
+    """A caller's workspace when it is given (the library checks its size), else a new one."""
+    if workspace is not None:
+        if _gpu("workspace", workspace) != device:
+            raise WbmmError(WBMM_E_INVALID, f"workspace is on {workspace.device}, not on {device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    return _torch().empty(need, dtype=_torch().uint8, device=device), need
+
+
+def _ckpt_scales(n: int) -> int:
+    return -(-n // WBMM_CKPT_GROUP)
+
+
+def wbmm_ckpt_pack(x, *, fmt: str = "int8", codes=None, scales=None, stream=None):
+    """Packs x (fp32 or bf16, any shape) into an 8-bit checkpoint: (codes, scales), codes uint8 in
+    x's shape, scales uint8 with one entry per WBMM_CKPT_GROUP elements in memory order."""
+    torch = _torch()
+    code, dev = _fmt_code(fmt), _gpu("x", x)
+    dt = _dtype_code(x.dtype)
+    _tensor("x", x, x.shape, x.dtype, dev)
+    with _on_stream(stream, dev):
+        codes = _out("codes", True if codes is None else codes, tuple(x.shape), torch.uint8, dev)
+        scales = _out("scales", True if scales is None else scales, (_ckpt_scales(x.numel()),),
+                      torch.uint8, dev)
+        _check(_lib().wbmm_ckpt_pack(_ptr(x), x.numel(), dt, code, _ptr(codes), _ptr(scales),
+                                     _stream(stream)))
+    return codes, scales
+
+
+def wbmm_ckpt_unpack(codes, scales, *, fmt: str = "int8", dtype=None, out=None, stream=None):
+    """The values of a checkpoint in `dtype` (fp32 by default, or out's)."""
+    torch = _torch()
+    code, dev = _fmt_code(fmt), _gpu("codes", codes)
+    dtype = dtype or (torch.float32 if out is None else out.dtype)
+    dt = _dtype_code(dtype)
+    _tensor("codes", codes, codes.shape, torch.uint8, dev)
+    _tensor("scales", scales, (_ckpt_scales(codes.numel()),), torch.uint8, dev)
+    with _on_stream(stream, dev):
+        out = _out("out", True if out is None else out, tuple(codes.shape), dtype, dev)
+        _check(_lib().wbmm_ckpt_unpack(_ptr(codes), _ptr(scales), codes.numel(), dt, code,
+                                       _ptr(out), _stream(stream)))
+    return out
+
+
+def wbmm_backward_ckpt_workspace_bytes(B, C, H, W, w, layout="NCHW", dtype=None,
+                                       has_mix=False) -> int:
+    code = WBMM_F32 if dtype is None else _dtype_code(dtype)
+    return int(_lib().wbmm_backward_ckpt_workspace_bytes(B, C, H, W, int(w), _layout_code(layout),
+                                                         code, int(bool(has_mix))))
+
+
+def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: str = "int8",
+                       layout: str = "NCHW", dx=True, dT=True, dmix_w=True, workspace=None,
+                       stream=None):
+    """Layer backward with x and z kept as 8-bit checkpoints: x_ckpt and z_ckpt are the (codes,
+    scales) that wbmm_ckpt_pack returned for the maps (z_ckpt exactly with mix_w). dy and T are
+    both fp32 or both bf16. Returns (dx in dy's dtype, dT fp32, dmix_w fp32); an output passed as
+    False is skipped."""
+    torch = _torch()
+    dev = _gpu("dy", dy)
+    B, C, H, W = _bchw(dy, layout)
+    w = int(w)
+    fcode, dt = _fmt_code(fmt), _dtype_code(dy.dtype)
+    L = 2 * w - 1
+    if (mix_w is None) != (z_ckpt is None):
+        raise WbmmError(WBMM_E_INVALID, "z_ckpt is required exactly when mix_w is given")
+    xc, xs = x_ckpt
+    zc, zs = (None, None) if z_ckpt is None else z_ckpt
+    scales = (_ckpt_scales(dy.numel()),)
+    _tensor("dy", dy, dy.shape, dy.dtype, dev)
+    _tensor("x codes", xc, dy.shape, torch.uint8, dev)
+    _tensor("x scales", xs, scales, torch.uint8, dev)
+    _tensor("T", T, (C, L, L), dy.dtype, dev)
+    _tensor("mix_w", mix_w, (C, 3, 3), torch.float32, dev, optional=True)
+    _tensor("z codes", zc, dy.shape, torch.uint8, dev, optional=z_ckpt is None)
+    _tensor("z scales", zs, scales, torch.uint8, dev, optional=z_ckpt is None)
+    with _on_stream(stream, dev):
+        dx_t = _out("dx", dx, tuple(dy.shape), dy.dtype, dev)
+        dT_t = _out("dT", dT, (C, L, L), torch.float32, dev)
+        dW_t = None if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), torch.float32, dev)
+        need = wbmm_backward_ckpt_workspace_bytes(B, C, H, W, w, layout, dy.dtype,
+                                                  mix_w is not None)
+        ws, ws_bytes = _workspace(need, workspace, dev)
+        _check(_lib().wbmm_backward_ckpt(B, C, H, W, w, _layout_code(layout), dt, fcode, _ptr(xc),
+                                         _ptr(xs), _ptr(T), _ptr(mix_w), _ptr(zc), _ptr(zs),
+                                         _ptr(dy), _ptr(dx_t), _ptr(dT_t), _ptr(dW_t), _ptr(ws),
+                                         ws_bytes, _stream(stream)))
+    return dx_t, dT_t, dW_t
+
+
+# ----------------------------------------------------------------------------- recurrence
+def wbmm_scan_forward_workspace_bytes(outer: int, length: int, inner: int) -> int:
+    return int(_lib().wbmm_scan_forward_workspace_bytes(int(outer), int(length), int(inner)))
+
+
+def wbmm_scan_backward_workspace_bytes(outer: int, length: int, inner: int,
+                                       has_states: bool = True) -> int:
+    return int(_lib().wbmm_scan_backward_workspace_bytes(int(outer), int(length), int(inner),
+                                                         int(bool(has_states))))
+
+
+def _scan_sizes(g, dim: int):
+    if g.dim() < 1 or not -g.dim() <= dim < g.dim():
+        raise WbmmError(WBMM_E_INVALID, f"dim={dim} is no dimension of a tensor of {g.dim()}")
+    dim %= g.dim()
+    lead, tail = tuple(g.shape[:dim]), tuple(g.shape[dim + 1:])
+    outer = inner = 1
+    for v in lead:
+        outer *= int(v)
+    for v in tail:
+        inner *= int(v)
+    length = int(g.shape[dim])
+    return outer, length, inner, lead + tail, lead + (-(-length // WBMM_SCAN_CHUNK),) + tail
+
+
+def _scan_lens(lens, device):
+    if lens is None:
+        return 0
+    _tensor("lens", lens, (lens.numel(),), _torch().int32, device)
+    if lens.numel() == 0:
+        raise WbmmError(WBMM_E_INVALID, "lens is empty")
+    return lens.numel()
+
+
+def wbmm_scan_forward(g, u, dim: int, *, h0=None, lens=None, reverse: bool = False, h=None,
+                      h_last=False, states=False, workspace=None, stream=None):
+    """Gated linear recurrence along dimension `dim` of g and u (same shape, fp32 or bf16, dense):
+    h_t = a_t h_{t-1} + (1 - a_t) u_t with a_t = sigmoid(g_t).
+
+    h0: fp32 state in g's shape without `dim`, or None for zeros. lens: int32 lengths (1-D, on the
+    GPU), one for each of the leading dimensions' sequences or for each equal run of them; h is 0
+    past a sequence's end. reverse: from each sequence's last position to its first. h_last and
+    states: True allocates them, a tensor is written (h_last may be h0), False skips them; states
+    (fp32, `dim` divided by WBMM_SCAN_CHUNK and rounded up) is what wbmm_scan_backward starts
+    from. Returns (h, h_last, states)."""
+    torch = _torch()
+    dev = _gpu("g", g)
+    outer, length, inner, flat, kept = _scan_sizes(g, dim)
+    dt = _dtype_code(g.dtype)
+    _tensor("g", g, g.shape, g.dtype, dev)
+    _tensor("u", u, g.shape, g.dtype, dev)
+    _tensor("h0", h0, flat, torch.float32, dev, optional=True)
+    n_lens = _scan_lens(lens, dev)
+    with _on_stream(stream, dev):
+        h = _out("h", True if h is None else h, tuple(g.shape), g.dtype, dev)
+        h_last = _out("h_last", h_last, flat, torch.float32, dev)
+        states = _out("states", states, kept, torch.float32, dev)
+        ws, ws_bytes = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace, dev)
+        _check(_lib().wbmm_scan_forward(outer, length, inner, dt, int(bool(reverse)), _ptr(g),
+                                        _ptr(u), _ptr(h0), _ptr(lens), n_lens, _ptr(h),
+                                        _ptr(h_last), _ptr(states), _ptr(ws), ws_bytes,
+                                        _stream(stream)))
+    return h, h_last, states
+
+
+def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str = "int8",
+                       h0=None, dh_last=None, lens=None, reverse: bool = False, dg=None, du=None,
+                       dh0=True, workspace=None, stream=None):
+    """Gradients of wbmm_scan_forward (same g, dim, lens and reverse; states as it wrote them).
+    Without states (None) they are formed again from h0 (fp32, or None for zeros) and the u given.
+    u: the forward's u, or u_ckpt: its checkpoint (codes, scales) in `fmt`. dh: gradient of h;
+    dh_last: fp32 gradient of h_last, or None. Returns (dg, du, dh0), dg and du in g's dtype and 0
+    past a sequence's end, dh0 fp32 (False skips it)."""
+    torch = _torch()
+    dev = _gpu("g", g)
+    outer, length, inner, flat, kept = _scan_sizes(g, dim)
+    dt = _dtype_code(g.dtype)
+    if (u is None) == (u_ckpt is None):
+        raise WbmmError(WBMM_E_INVALID, "exactly one of u and u_ckpt must be given")
+    _tensor("g", g, g.shape, g.dtype, dev)
+    if u_ckpt is None:
+        uu, us, fcode = u, None, 0
+        _tensor("u", u, g.shape, g.dtype, dev)
+    else:
+        (uu, us), fcode = u_ckpt, _fmt_code(fmt)
+        _tensor("u codes", uu, g.shape, torch.uint8, dev)
+        _tensor("u scales", us, (_ckpt_scales(g.numel()),), torch.uint8, dev)
+    _tensor("states", states, kept, torch.float32, dev, optional=True)
+    _tensor("h0", h0, flat, torch.float32, dev, optional=True)
+    _tensor("dh", dh, g.shape, g.dtype, dev)
+    _tensor("dh_last", dh_last, flat, torch.float32, dev, optional=True)
+    n_lens = _scan_lens(lens, dev)
+    with _on_stream(stream, dev):
+        dg = _out("dg", True if dg is None else dg, tuple(g.shape), g.dtype, dev)
+        du = _out("du", True if du is None else du, tuple(g.shape), g.dtype, dev)
+        dh0 = _out("dh0", dh0, flat, torch.float32, dev)
+        need = wbmm_scan_backward_workspace_bytes(outer, length, inner, states is not None)
+        ws, ws_bytes = _workspace(need, workspace, dev)
+        _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode,
+                                         _ptr(g), _ptr(uu), _ptr(us), _ptr(states), _ptr(h0), _ptr(dh),
+                                         _ptr(dh_last), _ptr(lens), n_lens, _ptr(dg), _ptr(du),
+                                         _ptr(dh0), _ptr(ws), ws_bytes, _stream(stream)))
+    return dg, du, dh0

@@ -10,6 +10,7 @@
 
 #include "../../include/wbmm.h"
 #include "wbmm_launch.hpp"
+#include "wbmm_scan.hpp"
 
 #define WBMM_API extern "C" __attribute__((visibility("default")))
 
@@ -605,4 +606,263 @@ WBMM_API wbmm_status wbmm_backward_bf16(int B, int C, int H, int W, int w, int l
   r.zsaved = (const uint16_t*)z_saved; r.dy = (const uint16_t*)dy; r.dx = (uint16_t*)dx;
   r.dT = dT; r.dmixw = mix_w ? dmix_w : nullptr; r.ws = workspace;
   return hip_status(wbmm::launch_backward_bf16(r, (hipStream_t)stream), "wbmm_backward_bf16");
+}
+
+// ---------------------------------------------------------------------------- 8-bit checkpoints
+namespace {
+
+constexpr int64_t kMaxCkpt = 1ll << 35;
+
+bool valid_fmt(int f) { return f == WBMM_CKPT_INT8 || f == WBMM_CKPT_E4M3; }
+
+// A buffer of a call: outputs must not overlap inputs or one another.
+struct Span {
+  const void* p;
+  size_t n;
+  const char* name;
+};
+wbmm_status check_spans(const Span* in, int nin, const Span* out, int nout) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n))
+        return fail(WBMM_E_INVALID, "%s overlaps %s", out[i].name, in[j].name);
+    for (int j = i + 1; j < nout; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(WBMM_E_INVALID, "%s overlaps %s", out[i].name, out[j].name);
+  }
+  return WBMM_OK;
+}
+
+wbmm_status check_ckpt(int64_t n, int dtype, int fmt) {
+  if (n < 1) return fail(WBMM_E_INVALID, "n=%lld must be >= 1", (long long)n);
+  if (n > kMaxCkpt) return fail(WBMM_E_UNSUPPORTED, "n=%lld exceeds 2^35", (long long)n);
+  if (!valid_dtype(dtype)) return fail(WBMM_E_INVALID, "unknown dtype %d", dtype);
+  if (!valid_fmt(fmt)) return fail(WBMM_E_INVALID, "unknown checkpoint format %d", fmt);
+  return WBMM_OK;
+}
+
+size_t ckpt_scales(int64_t n) {
+  return (size_t)(n + WBMM_CKPT_GROUP - 1) / WBMM_CKPT_GROUP;
+}
+
+}  // namespace
+
+WBMM_API wbmm_status wbmm_ckpt_pack(const void* x, int64_t n, int dtype, int fmt, uint8_t* codes,
+                                    uint8_t* scales, void* stream) {
+  wbmm_status st = check_ckpt(n, dtype, fmt);
+  if (st != WBMM_OK) return st;
+  if (!x || !codes || !scales) return fail(WBMM_E_INVALID, "x, codes and scales must be non-NULL");
+  if (!aligned(x, dtype_size(dtype)))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const Span in[] = {{x, (size_t)n * dtype_size(dtype), "x"}};
+  const Span out[] = {{codes, (size_t)n, "codes"}, {scales, ckpt_scales(n), "scales"}};
+  st = check_spans(in, 1, out, 2);
+  if (st != WBMM_OK) return st;
+  return hip_status(wbmm::launch_ckpt_pack(x, (size_t)n, dtype == WBMM_BF16, fmt, codes, scales,
+                                           (hipStream_t)stream),
+                    "wbmm_ckpt_pack");
+}
+
+WBMM_API wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_t n,
+                                      int dtype, int fmt, void* x, void* stream) {
+  wbmm_status st = check_ckpt(n, dtype, fmt);
+  if (st != WBMM_OK) return st;
+  if (!x || !codes || !scales) return fail(WBMM_E_INVALID, "x, codes and scales must be non-NULL");
+  if (!aligned(x, dtype_size(dtype)))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const Span in[] = {{codes, (size_t)n, "codes"}, {scales, ckpt_scales(n), "scales"}};
+  const Span out[] = {{x, (size_t)n * dtype_size(dtype), "x"}};
+  st = check_spans(in, 2, out, 1);
+  if (st != WBMM_OK) return st;
+  return hip_status(wbmm::launch_ckpt_unpack(codes, scales, (size_t)n, dtype == WBMM_BF16, fmt, x,
+                                             (hipStream_t)stream),
+                    "wbmm_ckpt_unpack");
+}
+
+namespace {
+
+wbmm_status check_bwd_ckpt(const wbmm::BwdCkptRequest& r, int dtype) {
+  wbmm_status st = check_map(r.B, r.C, r.H, r.W, r.w, r.layout);
+  if (st != WBMM_OK) return st;
+  return check_ckpt((int64_t)r.B * r.C * r.H * r.W, dtype, r.fmt);
+}
+
+}  // namespace
+
+WBMM_API size_t wbmm_backward_ckpt_workspace_bytes(int B, int C, int H, int W, int w, int layout,
+                                                   int dtype, int has_mix) {
+  static const float dummy = 0.f;
+  wbmm::BwdCkptRequest r{};
+  r.B = B; r.C = C; r.H = H; r.W = W; r.w = w; r.layout = layout;
+  r.bf16 = dtype == WBMM_BF16;
+  r.mixw = has_mix ? &dummy : nullptr;
+  if (check_bwd_ckpt(r, dtype) != WBMM_OK || !wbmm::backward_ckpt_plan_ok(r)) return 0;
+  return wbmm::backward_ckpt_workspace(r);
+}
+
+WBMM_API wbmm_status wbmm_backward_ckpt(int B, int C, int H, int W, int w, int layout, int dtype,
+                                        int fmt, const uint8_t* x_codes, const uint8_t* x_scales,
+                                        const void* T, const float* mix_w, const uint8_t* z_codes,
+                                        const uint8_t* z_scales, const void* dy, void* dx,
+                                        float* dT, float* dmix_w, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  wbmm::BwdCkptRequest r{};
+  r.B = B; r.C = C; r.H = H; r.W = W; r.w = w; r.layout = layout;
+  r.bf16 = dtype == WBMM_BF16;
+  r.fmt = fmt;
+  r.xc = x_codes; r.xs = x_scales; r.T = T; r.mixw = mix_w; r.zc = z_codes; r.zs = z_scales;
+  r.dy = dy; r.dx = dx; r.dT = dT; r.dmixw = mix_w ? dmix_w : nullptr;
+  r.ws = workspace;
+  wbmm_status st = check_bwd_ckpt(r, dtype);
+  if (st != WBMM_OK) return st;
+  if (!x_codes || !x_scales || !T || !dy)
+    return fail(WBMM_E_INVALID, "x_codes, x_scales, T and dy must be non-NULL");
+  if ((mix_w == nullptr) != (z_codes == nullptr) || (mix_w == nullptr) != (z_scales == nullptr))
+    return fail(WBMM_E_INVALID, "z_codes and z_scales are required exactly when mix_w is given");
+  const size_t es = dtype_size(dtype);
+  if (!aligned(T, es) || !aligned(dy, es) || !aligned(dx, es) || !aligned(mix_w, 4) ||
+      !aligned(dT, 4) || !aligned(dmix_w, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const size_t n = (size_t)B * C * H * W, L = (size_t)C * (2 * w - 1) * (2 * w - 1);
+  const size_t wb = (size_t)C * 36;
+  const Span in[] = {{x_codes, n, "x_codes"}, {x_scales, ckpt_scales((int64_t)n), "x_scales"},
+                     {T, L * es, "T"}, {mix_w, wb, "mix_w"}, {z_codes, n, "z_codes"},
+                     {z_scales, ckpt_scales((int64_t)n), "z_scales"}, {dy, n * es, "dy"}};
+  const Span out[] = {{dx, n * es, "dx"}, {dT, L * 4, "dT"}, {r.dmixw, wb, "dmix_w"}};
+  st = check_spans(in, 7, out, 3);
+  if (st != WBMM_OK) return st;
+  if (!wbmm::backward_ckpt_plan_ok(r))
+    return fail(WBMM_E_UNSUPPORTED, "no launch shape fits this problem (w=%d)", w);
+  const size_t need = wbmm::backward_ckpt_workspace(r);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(WBMM_E_WORKSPACE, "workspace of %zu bytes required, %zu given", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 256))
+    return fail(WBMM_E_UNSUPPORTED, "workspace not 256-byte aligned");
+  if (!r.dx && !r.dT && !r.dmixw) return ok();
+  return hip_status(wbmm::launch_backward_ckpt(r, (hipStream_t)stream), "wbmm_backward_ckpt");
+}
+
+// ---------------------------------------------------------------------------- recurrence
+namespace {
+
+constexpr int64_t kMaxScanLen = 1ll << 30, kMaxScanCols = (1ll << 26) - 1;
+
+wbmm_status check_scan_sizes(int64_t outer, int64_t len, int64_t inner) {
+  if (outer < 1 || len < 1 || inner < 1)
+    return fail(WBMM_E_INVALID, "sizes must be >= 1 (outer=%lld len=%lld inner=%lld)",
+                (long long)outer, (long long)len, (long long)inner);
+  if (len > kMaxScanLen) return fail(WBMM_E_UNSUPPORTED, "len=%lld exceeds 2^30", (long long)len);
+  if (outer > kMaxScanCols || inner > kMaxScanCols || outer * inner > kMaxScanCols)
+    return fail(WBMM_E_UNSUPPORTED, "outer * inner must be below 2^26");
+  if (outer * inner > kMaxElems / len) return fail(WBMM_E_UNSUPPORTED, "tensor too large");
+  return WBMM_OK;
+}
+
+wbmm_status check_scan_ws(const wbmm::ScanRequest& r, size_t need, size_t bytes) {
+  if (need > 0 && (!r.ws || bytes < need))
+    return fail(WBMM_E_WORKSPACE, "workspace of %zu bytes required, %zu given", need,
+                r.ws ? bytes : (size_t)0);
+  if (need > 0 && !aligned(r.ws, 16))
+    return fail(WBMM_E_UNSUPPORTED, "workspace not 16-byte aligned");
+  return WBMM_OK;
+}
+
+wbmm_status check_scan_lens(const int32_t* lens, int64_t n_lens, int64_t outer) {
+  if (!lens) return WBMM_OK;
+  if (n_lens < 1 || outer % n_lens != 0)
+    return fail(WBMM_E_INVALID, "n_lens=%lld must divide outer=%lld", (long long)n_lens,
+                (long long)outer);
+  if (!aligned(lens, 4)) return fail(WBMM_E_UNSUPPORTED, "lens not 4-byte aligned");
+  return WBMM_OK;
+}
+
+}  // namespace
+
+WBMM_API size_t wbmm_scan_forward_workspace_bytes(int64_t outer, int64_t len, int64_t inner) {
+  if (check_scan_sizes(outer, len, inner) != WBMM_OK) return 0;
+  return wbmm::scan_workspace(outer, len, inner);
+}
+
+WBMM_API size_t wbmm_scan_backward_workspace_bytes(int64_t outer, int64_t len, int64_t inner,
+                                                   int has_states) {
+  if (check_scan_sizes(outer, len, inner) != WBMM_OK) return 0;
+  return wbmm::scan_backward_workspace(outer, len, inner, has_states != 0);
+}
+
+WBMM_API wbmm_status wbmm_scan_forward(int64_t outer, int64_t len, int64_t inner, int dtype,
+                                       int reverse, const void* g, const void* u, const float* h0,
+                                       const int32_t* lens, int64_t n_lens, void* h, float* h_last,
+                                       float* states, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  wbmm_status st = check_scan_sizes(outer, len, inner);
+  if (st != WBMM_OK) return st;
+  if (!valid_dtype(dtype)) return fail(WBMM_E_INVALID, "unknown dtype %d", dtype);
+  if (!g || !u || !h) return fail(WBMM_E_INVALID, "g, u and h must be non-NULL");
+  st = check_scan_lens(lens, n_lens, outer);
+  if (st != WBMM_OK) return st;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(g, es) || !aligned(u, es) || !aligned(h, es) || !aligned(h0, 4) ||
+      !aligned(h_last, 4) || !aligned(states, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const size_t cols = (size_t)outer * inner, n = cols * len * es, cb = cols * 4;
+  const size_t sb = cb * ((len + WBMM_SCAN_CHUNK - 1) / WBMM_SCAN_CHUNK);
+  const Span in[] = {{g, n, "g"}, {u, n, "u"}, {lens, lens ? (size_t)n_lens * 4 : 0, "lens"},
+                     {h0 == h_last ? nullptr : h0, cb, "h0"}};   // in place: exactly the same
+  const Span out[] = {{h, n, "h"}, {h_last, cb, "h_last"}, {states, sb, "states"}};
+  st = check_spans(in, 4, out, 3);
+  if (st != WBMM_OK) return st;
+  wbmm::ScanRequest r{};
+  r.outer = outer; r.len = len; r.inner = inner; r.n_lens = n_lens;
+  r.bf16 = dtype == WBMM_BF16;
+  r.reverse = reverse != 0;
+  r.g = g; r.u = u; r.carry_in = h0; r.lens = lens;
+  r.out0 = h; r.carry_out = h_last; r.states = states; r.ws = workspace;
+  st = check_scan_ws(r, wbmm::scan_workspace(outer, len, inner), workspace_bytes);
+  if (st != WBMM_OK) return st;
+  return hip_status(wbmm::launch_scan_forward(r, (hipStream_t)stream), "wbmm_scan_forward");
+}
+
+WBMM_API wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inner, int dtype,
+                                        int reverse, int u_fmt, const void* g, const void* u,
+                                        const uint8_t* u_scales, const float* states,
+                                        const float* h0, const void* dh, const float* dh_last,
+                                        const int32_t* lens, int64_t n_lens, void* dg, void* du, float* dh0,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  wbmm_status st = check_scan_sizes(outer, len, inner);
+  if (st != WBMM_OK) return st;
+  if (!valid_dtype(dtype)) return fail(WBMM_E_INVALID, "unknown dtype %d", dtype);
+  if (u_scales && !valid_fmt(u_fmt))
+    return fail(WBMM_E_INVALID, "unknown checkpoint format %d", u_fmt);
+  if (!g || !u || !dh || !dg || !du)
+    return fail(WBMM_E_INVALID, "g, u, dh, dg and du must be non-NULL");
+  if (states && h0) return fail(WBMM_E_INVALID, "h0 goes with states == NULL only");
+  st = check_scan_lens(lens, n_lens, outer);
+  if (st != WBMM_OK) return st;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(g, es) || !aligned(dh, es) || !aligned(dg, es) || !aligned(du, es) ||
+      (!u_scales && !aligned(u, es)) || !aligned(states, 4) || !aligned(h0, 4) ||
+      !aligned(dh_last, 4) || !aligned(dh0, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const size_t cols = (size_t)outer * inner, e = cols * len, cb = cols * 4;
+  const size_t sb = cb * ((len + WBMM_SCAN_CHUNK - 1) / WBMM_SCAN_CHUNK);
+  const Span in[] = {{g, e * es, "g"}, {u, u_scales ? e : e * es, "u"},
+                     {u_scales, ckpt_scales((int64_t)e), "u_scales"}, {states, sb, "states"},
+                     {dh, e * es, "dh"}, {dh_last, cb, "dh_last"},
+                     {lens, lens ? (size_t)n_lens * 4 : 0, "lens"}, {h0, cb, "h0"}};
+  const Span out[] = {{dg, e * es, "dg"}, {du, e * es, "du"}, {dh0, cb, "dh0"}};
+  st = check_spans(in, 8, out, 3);
+  if (st != WBMM_OK) return st;
+  wbmm::ScanRequest r{};
+  r.outer = outer; r.len = len; r.inner = inner; r.n_lens = n_lens;
+  r.bf16 = dtype == WBMM_BF16;
+  r.reverse = reverse != 0;
+  r.fmt = u_fmt;
+  r.g = g; r.u = u; r.us = u_scales; r.states = const_cast<float*>(states);
+  r.dh = dh; r.carry_in = dh_last; r.h0 = h0; r.lens = lens;
+  r.out0 = dg; r.out1 = du; r.carry_out = dh0; r.ws = workspace;
+  st = check_scan_ws(r, wbmm::scan_backward_workspace(outer, len, inner, states != nullptr),
+                     workspace_bytes);
+  if (st != WBMM_OK) return st;
+  return hip_status(wbmm::launch_scan_backward(r, (hipStream_t)stream), "wbmm_scan_backward");
 }

@@ -222,4 +222,28 @@ template <typename TM>
 hipError_t launch_mix_bwd_weight_t(const TM* dy, const TM* z, float* dw9, int B, int C, int H,
                                    int W, int layout, hipStream_t st);
 
+// 8-bit checkpoints (fmt: WBMM_CKPT_*), and the backward on x and z kept that way (bf16: dy, T and
+// dx in bf16).
+hipError_t launch_ckpt_pack(const void* x, size_t n, int bf16, int fmt, uint8_t* codes,
+                            uint8_t* scales, hipStream_t st);
+hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, int bf16,
+                              int fmt, void* x, hipStream_t st);
+struct BwdCkptRequest {
+  int B, C, H, W, w, layout, bf16, fmt;
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const void* T;
+  const float* mixw;
+  const uint8_t* zc;
+  const uint8_t* zs;
+  const void* dy;
+  void* dx;
+  float* dT;
+  float* dmixw;
+  void* ws;
+};
+bool backward_ckpt_plan_ok(const BwdCkptRequest& r);
+size_t backward_ckpt_workspace(const BwdCkptRequest& r);
+hipError_t launch_backward_ckpt(const BwdCkptRequest& r, hipStream_t st);
+
 }  // namespace wbmm

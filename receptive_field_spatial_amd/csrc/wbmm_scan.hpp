@@ -1,0 +1,373 @@
+// Gated linear recurrence, device pieces shared by the forward and backward kernels.
+//
+// Along one axis of a (outer, len, inner) tensor, for every (outer, inner) column:
+//   a_t = sigmoid(g_t),   h_t = a_t h_{t-1} + (1 - a_t) u_t.
+// A run of steps acts on the state entering it as the affine map h -> P h + H, with P the product
+// of its a_t and H its result from a zero state; runs compose by
+//   (P2, H2) after (P1, H1) = (P2 P1, P2 H1 + H2),
+// so a column is cut into pieces whose maps are formed independently and joined in order. a_t lies
+// in [0, 1]: P never overflows, and where it underflows the state entering no longer counts. The
+// backward is the same recurrence from the other end: with R_t the gradient entering step t from
+// step t + 1, G_t = dh_t + R_t and R_{t-1} = a_t G_t.
+//
+// States, gates, products and sums are fp32 whatever the tensors' type.
+//
+// Scan order: step s of a sequence of n steps is position s, or n - 1 - s when reversed; positions
+// n .. len - 1 (padding) are never used: inside the kernels they are the identity map (a = 1,
+// b = 0), and outputs there are zero.
+#pragma once
+
+#include "wbmm_ckpt.hpp"
+#include "wbmm_launch.hpp"
+
+namespace wbmm {
+
+constexpr int kScanChunk = 32;    // steps between two kept states
+constexpr int kScanK = 16;        // steps per wave and tile of the column kernels
+constexpr int kScanE = 8;         // steps per lane and tile of the row kernels
+constexpr int kScanWaves = 8;     // waves of a workgroup at most
+
+struct ScanArgs {
+  const void* g;
+  const void* u;              // tensor, or the codes of a checkpoint when us is set
+  const uint8_t* us;
+  const void* dh;
+  const float* carry_in;      // h0 (forward), dh_last (backward), or null
+  const int* lens;            // or null
+  void* out0;                 // h, or dg (backward)
+  void* out1;                 // du (backward)
+  float* carry_out;           // h_last, or dh0, or null
+  float* states;              // [outer][chunks][inner]
+  float2* agg;                // [segs][cols] maps of the segments
+  float* carry_copy;          // [cols] carry_in, kept for the second launch
+  int len, chunks, reverse, fmt;
+  uint32_t inner, cols, rows_per_len;   // cols = outer * inner; lens[outer index / rows_per_len]
+  int segs, seg_len;          // seg_len: a multiple of the workgroup's tile
+  int lanes;                  // row kernels: lanes per row (64: the workgroup's waves share a row)
+};
+
+// a = sigmoid(g) and c = 1 - a = sigmoid(-g), each with its own relative accuracy (c from 1 - a
+// would lose what a long memory lives on): with t = exp(-g), a = 1 / (1 + t) and c = t a. t takes
+// the rounding of g log2(e) back in, which otherwise costs |g| half steps; the reciprocal gets one
+// Newton step: over hundreds of steps near a = 1 its last bit shows in the fp32 states. g is held
+// to [-87, 87], where a or c is the least normal number and t finite; a NaN passes.
+__device__ __forceinline__ void scan_gate(float g, float& a, float& c) {
+  constexpr float kL = 1.44269502f, kLlo = 1.92596299e-8f, kLn2 = 0.693147181f;
+  float x = g < -87.f ? -87.f : g;
+  x = x > 87.f ? 87.f : x;
+  const float y = x * kL;
+  const float r = fmaf(x, kLlo, fmaf(x, kL, -y));
+  float t = __builtin_amdgcn_exp2f(-y);
+  t = fmaf(t, -kLn2 * r, t);
+  const float d = 1.f + t;
+  a = __builtin_amdgcn_rcpf(d);
+  a = fmaf(a, fmaf(-d, a, 1.f), a);
+  c = t * a;
+}
+
+template <typename T>
+__device__ __forceinline__ float scan_widen(T v);
+template <>
+__device__ __forceinline__ float scan_widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float scan_widen<uint16_t>(uint16_t v) { return bf2f(v); }
+template <typename T>
+__device__ __forceinline__ T scan_narrow(float v);
+template <>
+__device__ __forceinline__ float scan_narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t scan_narrow<uint16_t>(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
+}
+
+// x of the lane that CTRL names; `id` where there is none.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float scan_dpp(float id, float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(id), __float_as_int(x), CTRL,
+                                                    ROW_MASK, 0xf, false));
+}
+__device__ __forceinline__ float scan_readlane(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+// Inclusive prefix composition over each group of `lanes` lanes (a power of two; each lane's own
+// map is the later one): row shifts within 16 lanes, then the two row broadcasts.
+template <int CTRL, int ROW_MASK, int D>
+__device__ __forceinline__ void scan_prefix_step(float& P, float& H, int li, int lanes) {
+  if (lanes <= D) return;
+  float ps = scan_dpp<CTRL, ROW_MASK>(1.f, P), hs = scan_dpp<CTRL, ROW_MASK>(0.f, H);
+  if (D < 16 && lanes < 16) {
+    ps = li < D ? 1.f : ps;
+    hs = li < D ? 0.f : hs;
+  }
+  H = fmaf(P, hs, H);
+  P *= ps;
+}
+__device__ __forceinline__ void scan_prefix(float& P, float& H, int li, int lanes) {
+  scan_prefix_step<0x111, 0xf, 1>(P, H, li, lanes);
+  scan_prefix_step<0x112, 0xf, 2>(P, H, li, lanes);
+  scan_prefix_step<0x114, 0xf, 4>(P, H, li, lanes);
+  scan_prefix_step<0x118, 0xf, 8>(P, H, li, lanes);
+  scan_prefix_step<0x142, 0xa, 16>(P, H, li, lanes);
+  scan_prefix_step<0x143, 0xc, 32>(P, H, li, lanes);
+}
+// The map of the lanes before this one in its group (identity for the first).
+__device__ __forceinline__ void scan_before(float P, float H, int li, float& Pe, float& He) {
+  Pe = scan_dpp<0x138, 0xf>(1.f, P);
+  He = scan_dpp<0x138, 0xf>(0.f, H);
+  Pe = li == 0 ? 1.f : Pe;
+  He = li == 0 ? 0.f : He;
+}
+
+// Inclusive suffix composition (the later lanes' map is applied first, as the backward runs):
+// row shifts within 16 lanes, then the totals of the later rows by lane reads.
+template <int CTRL, int D>
+__device__ __forceinline__ void scan_suffix_step(float& P, float& R, int li, int lanes) {
+  if (lanes <= D) return;
+  float ps = scan_dpp<CTRL, 0xf>(1.f, P), rs = scan_dpp<CTRL, 0xf>(0.f, R);
+  if (lanes < 16) {
+    ps = li + D >= lanes ? 1.f : ps;
+    rs = li + D >= lanes ? 0.f : rs;
+  }
+  R = fmaf(P, rs, R);
+  P *= ps;
+}
+__device__ __forceinline__ void scan_suffix(float& P, float& R, int li, int lanes, int lane) {
+  scan_suffix_step<0x101, 1>(P, R, li, lanes);
+  scan_suffix_step<0x102, 2>(P, R, li, lanes);
+  scan_suffix_step<0x104, 4>(P, R, li, lanes);
+  scan_suffix_step<0x108, 8>(P, R, li, lanes);
+  if (lanes <= 16) return;
+  const int row = lane >> 4;
+  const float p1 = scan_readlane(P, 16), r1 = scan_readlane(R, 16);
+  const float p3 = scan_readlane(P, 48), r3 = scan_readlane(R, 48);
+  float ps = row == 2 ? p3 : 1.f, rs = row == 2 ? r3 : 0.f;
+  if (lanes == 32) {
+    ps = row == 0 ? p1 : ps;
+    rs = row == 0 ? r1 : rs;
+  } else {
+    const float p2 = scan_readlane(P, 32), r2 = scan_readlane(R, 32);
+    const float p23 = p2 * p3, r23 = fmaf(p2, r3, r2);
+    ps = row == 1 ? p23 : ps;
+    rs = row == 1 ? r23 : rs;
+    ps = row == 0 ? p1 * p23 : ps;
+    rs = row == 0 ? fmaf(p1, r23, r1) : rs;
+  }
+  R = fmaf(P, rs, R);
+  P *= ps;
+}
+// The map of the lanes after this one in its group (identity for the last).
+__device__ __forceinline__ void scan_after(float P, float R, int li, int lanes, float& Pe,
+                                           float& Re) {
+  Pe = scan_dpp<0x130, 0xf>(1.f, P);
+  Re = scan_dpp<0x130, 0xf>(0.f, R);
+  Pe = li + 1 == lanes ? 1.f : Pe;
+  Re = li + 1 == lanes ? 0.f : Re;
+}
+
+// Steps of a sequence: its entry of lens held to [0, len], or len.
+__device__ __forceinline__ int scan_steps(const ScanArgs& a, uint32_t seq) {
+  if (!a.lens) return a.len;
+  const int n = a.lens[seq / a.rows_per_len];
+  return n < 0 ? 0 : (n > a.len ? a.len : n);
+}
+
+// ------------------------------------------------------------------ column kernels (inner > 1)
+// One lane owns V neighbouring columns; a wave takes kScanK steps of 64 V columns per tile.
+template <typename T, int V>
+struct ScanVec;
+template <> struct ScanVec<float, 1> { typedef float type; };
+template <> struct ScanVec<uint16_t, 1> { typedef uint16_t type; };
+template <> struct ScanVec<uint16_t, 2> { typedef uint32_t type; };
+
+template <int V>
+__device__ __forceinline__ void scan_unpack(float r, float (&v)[V]) { v[0] = r; }
+template <int V>
+__device__ __forceinline__ void scan_unpack(uint16_t r, float (&v)[V]) { v[0] = bf2f(r); }
+template <int V>
+__device__ __forceinline__ void scan_unpack(uint32_t r, float (&v)[V]) {
+  v[0] = __uint_as_float(r << 16);
+  v[V - 1] = __uint_as_float(r & 0xffff0000u);
+}
+template <typename R, int V>
+__device__ __forceinline__ R scan_pack(const float (&v)[V]) {
+  if constexpr (sizeof(R) == 4 && V == 2)
+    return (uint32_t)scan_narrow<uint16_t>(v[0]) | ((uint32_t)scan_narrow<uint16_t>(v[1]) << 16);
+  else
+    return scan_narrow<R>(v[0]);
+}
+
+template <int V>
+struct ScanCol {
+  uint32_t col, o, i;   // first column, its sequence and place in the row
+  bool active;
+  int n;                // steps of its sequence
+  size_t base;          // element offset of position 0
+  size_t start;         // element offset of step 0
+  long long stride;     // elements from step s to step s + 1
+  __device__ __forceinline__ ScanCol(const ScanArgs& a, uint32_t group, int lane) {
+    const uint64_t c = ((uint64_t)group * 64 + lane) * V;
+    active = c < a.cols;
+    col = active ? (uint32_t)c : a.cols - V;
+    o = col / a.inner;
+    i = col - o * a.inner;
+    n = scan_steps(a, o);
+    base = (size_t)o * a.len * a.inner + i;
+    stride = a.reverse ? -(long long)a.inner : (long long)a.inner;
+    start = a.reverse && n > 0 ? base + (size_t)(n - 1) * a.inner : base;
+  }
+  // V elements of a map or checkpoint at offset o, as fp32
+  template <typename T, bool CK>
+  struct Raw {
+    typedef typename ScanVec<T, V>::type R;
+    R r;
+    uint16_t code, scale;
+    __device__ __forceinline__ void load(const ScanArgs& a, size_t o) {
+      if constexpr (CK) {
+        const uint8_t* p = (const uint8_t*)a.u + o;
+        code = V == 2 ? *(const uint16_t*)p : *p;
+        scale = a.us[o / kCkptGroup];   // V elements from an even one share a group
+      } else {
+        r = *(const R*)((const T*)a.u + o);
+      }
+    }
+    __device__ __forceinline__ void widen(const ScanArgs& a, float (&v)[V]) const {
+      if constexpr (CK) {
+        const float f = ckpt_factor(scale);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = ckpt_decode1((code >> (8 * j)) & 0xffu, a.fmt) * f;
+      } else {
+        scan_unpack<V>(r, v);
+      }
+    }
+  };
+  // element offset of step s, held to the sequence's own steps (position 0 of an empty one)
+  __device__ __forceinline__ size_t at(int s) const {
+    s = s < n ? s : n - 1;
+    s = s > 0 ? s : 0;
+    return start + (long long)s * stride;
+  }
+  // zeros at the positions from step s's tile on that lie past the end of the sequence
+  template <typename R, typename T>
+  __device__ __forceinline__ void zero(T* p, int s, int len, uint32_t inner) const {
+    for (int k = 0; k < kScanK; ++k)
+      if (s + k >= n && s + k < len) *(R*)(p + base + (size_t)(s + k) * inner) = R(0);
+  }
+};
+
+// ------------------------------------------------------------------ row kernels (inner = 1)
+// kScanE consecutive steps of a row, in scan order; rows start at any element, so the wide
+// accesses carry the element's alignment only.
+template <typename T, bool REV>
+struct ScanRow {
+  static constexpr int E = kScanE;
+  struct __attribute__((packed, aligned(sizeof(T)))) Wide { T v[E]; };
+  size_t base;
+  int len, n;
+  __device__ __forceinline__ ScanRow(uint32_t row, int len_, int n_)
+      : base((size_t)row * len_), len(len_), n(n_) {}
+  __device__ __forceinline__ size_t at(int s) const { return base + (REV ? n - 1 - s : s); }
+  // steps past the end of the sequence come back as zeros
+  __device__ __forceinline__ void load(const T* __restrict__ p, int s, T (&v)[E]) const {
+    if (s + E <= n) {
+      Wide w;
+      __builtin_memcpy(&w, p + at(REV ? s + E - 1 : s), sizeof(w));
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = w.v[REV ? E - 1 - k : k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        v[k] = T(0);
+        if (s + k < n) v[k] = p[at(s + k)];
+      }
+    }
+  }
+  // zeros at the positions past the end of the sequence
+  __device__ __forceinline__ void store(T* __restrict__ p, int s, const float (&o)[E]) const {
+    if (s + E <= n) {
+      Wide w;
+#pragma unroll
+      for (int k = 0; k < E; ++k) w.v[REV ? E - 1 - k : k] = scan_narrow<T>(o[k]);
+      __builtin_memcpy(p + at(REV ? s + E - 1 : s), &w, sizeof(w));
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        if (s + k < n) p[at(s + k)] = scan_narrow<T>(o[k]);
+        else if (s + k < len) p[base + s + k] = T(0);
+      }
+    }
+  }
+};
+
+// kScanE steps of a row's u, from the map or from a checkpoint (whose groups run through the whole
+// tensor: a lane's steps lie in one or two).
+template <typename T, bool REV, bool CK>
+struct ScanU {
+  static constexpr int E = kScanE;
+  T r[CK ? 1 : E];
+  uint8_t code[CK ? E : 1];
+  uint32_t s0, s1;
+  __device__ __forceinline__ ScanU() : s0(0), s1(0) {}
+  __device__ __forceinline__ void load(const ScanArgs& a, const ScanRow<T, REV>& rw,
+                                       const ScanRow<uint8_t, REV>& rwc, int s) {
+    if constexpr (CK) {
+      rwc.load((const uint8_t*)a.u, s, code);
+      if (s < rw.n) {   // the scales of the lane's first and last step
+        const int last = s + E <= rw.n ? s + E - 1 : rw.n - 1;
+        s0 = a.us[rw.at(s) / kCkptGroup];
+        s1 = a.us[rw.at(last) / kCkptGroup];
+      }
+    } else {
+      rw.load((const T*)a.u, s, r);
+    }
+  }
+  __device__ __forceinline__ void widen(const ScanArgs& a, const ScanRow<T, REV>& rw, int s,
+                                        float (&v)[E]) const {
+    if constexpr (CK) {
+      const float f0 = ckpt_factor(s0), f1 = ckpt_factor(s1);
+      // place of the first step in its group; the second scale from where the group ends
+      const int at0 = (int)(rw.at(s) % kCkptGroup);
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const bool first = REV ? at0 - k >= 0 : at0 + k < kCkptGroup;
+        v[k] = ckpt_decode1(code[k], a.fmt) * (first ? f0 : f1);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = scan_widen<T>(r[k]);
+    }
+  }
+};
+
+// ------------------------------------------------------------------ host side
+struct ScanRequest {
+  int64_t outer, len, inner, n_lens;
+  int bf16, reverse, fmt;
+  const void* g;
+  const void* u;
+  const uint8_t* us;
+  const void* dh;
+  const float* carry_in;   // h0, or dh_last in the backward
+  const float* h0;         // backward that gets no states
+  const int* lens;
+  void* out0;              // h, or dg; null in a forward that only forms states
+  void* out1;
+  float* carry_out;
+  float* states;
+  void* ws;
+};
+struct ScanPlan {
+  bool rows;
+  int V, lanes, waves, segs, seg_len;
+};
+ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, int V, bool backward);
+int scan_vec(const ScanRequest& r);
+ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p);
+// Device workspace of a call (16-byte aligned), 0 when none: the segments' maps, and the states of
+// a backward that gets none.
+size_t scan_workspace(int64_t outer, int64_t len, int64_t inner);
+size_t scan_backward_workspace(int64_t outer, int64_t len, int64_t inner, bool has_states);
+hipError_t launch_scan_forward(const ScanRequest& r, hipStream_t st);
+hipError_t launch_scan_backward(const ScanRequest& r, hipStream_t st);
+
+}  // namespace wbmm

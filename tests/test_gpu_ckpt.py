@@ -1,0 +1,250 @@
+"""8-bit activation checkpoints and the backward that reads them, on the GPU, against the fp64
+oracles. Packing and unpacking are exact, so their comparisons are too."""
+import numpy as np
+import pytest
+
+from oracle import ops_oracle as Q
+from oracle import wbmm_oracle as O
+from receptive_field_spatial_amd import synth
+from tests.parity_util import assert_f32
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def R():
+    import receptive_field_spatial_amd as mod
+    mod.load_library()
+    return mod
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def values(n, seed):
+    """fp32 values over many magnitudes, with the borders of the formats among them."""
+    rng = np.random.default_rng(seed)
+    x = (rng.standard_normal(n) * np.exp(rng.standard_normal(n) * 4)).astype(np.float32)
+    special = np.array([0, -0.0, 127, 127.5, 127.25, 448, 448.5, 464, 1e-45, 1.2e-38, 3e38, -3e38,
+                        2.0 ** -126, 1.5 * 2.0 ** -9, 2.0 ** -10, 254, 63.5, 64], np.float32)
+    at = rng.permutation(n)[: min(n, 5 * special.size)]
+    x[at] = np.resize(special, at.size)
+    if n > 40:
+        x[n // 2: n // 2 + 20] = 0
+    if n > 200:
+        x[64:96] = 1e-42 * np.arange(32)     # a group of subnormal numbers
+    return x
+
+
+def check_pack(x, fmt, bf16, shape=None):
+    if bf16:
+        x = synth.round_to_bf16(x)
+    t = dev(x).to(torch.bfloat16) if bf16 else dev(x)
+    if shape:
+        t = t.reshape(shape)
+    codes, scales = R().wbmm_ckpt_pack(t, fmt=fmt)
+    wc, ws = Q.pack(x.astype(np.float64), fmt)
+    assert codes.shape == t.shape and np.array_equal(scales.cpu().numpy(), ws)
+    assert np.array_equal(codes.cpu().numpy().reshape(-1), wc.reshape(-1))
+    want = Q.unpack(wc, ws, fmt).reshape(-1)
+    got = R().wbmm_ckpt_unpack(codes, scales, fmt=fmt)
+    assert got.dtype == torch.float32 and got.shape == t.shape
+    with np.errstate(over="ignore"):
+        assert np.array_equal(got.cpu().numpy().reshape(-1), want.astype(np.float32), equal_nan=True)
+    b = R().wbmm_ckpt_unpack(codes, scales, fmt=fmt, dtype=torch.bfloat16)
+    assert torch.equal(b.nan_to_num(7.0), got.to(torch.bfloat16).nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("n", [1, 7, 31, 32, 33, 100, 511, 4096, 4097, 9001])
+def test_pack_unpack_bit_exact(fmt, bf16, n):
+    check_pack(values(n, n), fmt, bf16)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_pack_nonfinite_groups(fmt):
+    x = values(200, 3)
+    x[5], x[70], x[199] = np.inf, np.nan, -np.inf
+    check_pack(x, fmt, False)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_unpack_every_code_and_scale(fmt):
+    codes = np.repeat(np.arange(256, dtype=np.uint8), 32).reshape(32 * 8, 32).T.copy().reshape(-1)
+    codes = np.tile(np.arange(256, dtype=np.uint8), 256)       # every code under every scale
+    scales = np.repeat(np.arange(256, dtype=np.uint8), 8)
+    got = R().wbmm_ckpt_unpack(dev(codes), dev(scales), fmt=fmt).cpu().numpy()
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = Q.unpack(codes, scales, fmt).astype(np.float32)
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("bf16,off", [(False, 1), (False, 3), (True, 1), (True, 4)])
+def test_pack_at_odd_addresses(fmt, bf16, off):
+    x = values(1000, 8)
+    if bf16:
+        x = synth.round_to_bf16(x)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    base = torch.zeros(1100, dtype=dt, device="cuda")
+    base[off:off + 1000] = dev(x).to(dt)
+    codes = torch.full((1100,), 171, dtype=torch.uint8, device="cuda")
+    scales = torch.full((64,), 171, dtype=torch.uint8, device="cuda")
+    R().wbmm_ckpt_pack(base[off:off + 1000], fmt=fmt, codes=codes[off:off + 1000],
+                       scales=scales[off:off + 32])
+    wc, ws = Q.pack(x.astype(np.float64), fmt)
+    c, s = codes.cpu().numpy(), scales.cpu().numpy()
+    assert np.array_equal(c[off:off + 1000], wc) and np.array_equal(s[off:off + 32], ws)
+    assert np.all(c[:off] == 171) and np.all(c[off + 1000:] == 171)
+    assert np.all(s[:off] == 171) and np.all(s[off + 32:] == 171)
+    out = torch.full((1100,), 9.0, dtype=dt, device="cuda")
+    R().wbmm_ckpt_unpack(codes[off:off + 1000], scales[off:off + 32], fmt=fmt,
+                         out=out[off:off + 1000])
+    assert torch.all(out[:off] == 9) and torch.all(out[off + 1000:] == 9)
+    want = torch.from_numpy(Q.unpack(wc, ws, fmt).astype(np.float32)).to(dt).cuda()
+    assert torch.equal(out[off:off + 1000], want)
+
+
+def bwd_inputs(B, C, H, W, w, mix, fmt, bf16, layout, seed):
+    shape = (B, C, H, W) if layout == "NCHW" else (B, H, W, C)
+    x = synth.normal_f32(shape, 1.0, seed)
+    z = synth.normal_f32(shape, 0.02 * w, seed + 1)
+    dy = synth.normal_f32(shape, 1.0, seed + 2)
+    T = synth.normal_f32((C, 2 * w - 1, 2 * w - 1), 0.02, seed + 3)
+    Wm = synth.normal_f32((C, 3, 3), 0.1, seed + 4) if mix else None
+    if bf16:
+        x, z, dy, T = (synth.round_to_bf16(v) for v in (x, z, dy, T))
+    return x, z, dy, T, Wm
+
+
+def nchw(a, layout):
+    return a if layout == "NCHW" else np.ascontiguousarray(a.transpose(0, 3, 1, 2))
+
+
+def check_bwd(B, C, H, W, w, mix, fmt, bf16, layout="NCHW", seed=0, **kw):
+    print(f"\n[case] bwd_ckpt {B}x{C}x{H}x{W} w={w} mix={mix} {fmt} bf16={bf16} {layout}", flush=True)
+    x, z, dy, T, Wm = bwd_inputs(B, C, H, W, w, mix, fmt, bf16, layout, seed)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    pk = lambda a: R().wbmm_ckpt_pack(dev(a).to(dt), fmt=fmt)
+    xc, zc = pk(x), pk(z) if mix else None
+    un = lambda c: nchw(R().wbmm_ckpt_unpack(*c, fmt=fmt).cpu().numpy().astype(np.float64), layout)
+    dx, dT, dW = R().wbmm_backward_ckpt(xc, dev(dy).to(dt), w, dev(T).to(dt),
+                                        mix_w=dev(Wm) if mix else None, z_ckpt=zc, fmt=fmt,
+                                        layout=layout, **kw)
+    wdx, wdT, wdW = O.layer_backward(un(xc), nchw(dy, layout).astype(np.float64), w,
+                                     T=T.astype(np.float64), Wmix=Wm, z=un(zc) if mix else None)
+    if dx is not None:
+        got = nchw(dx.float().cpu().numpy(), layout)
+        if bf16:   # fp32 arithmetic, then one rounding of half a bf16 step
+            err = np.abs(got - wdx)
+            assert np.all(err <= 2.0 ** -8 * np.abs(wdx) + 1e-5), err.max()
+        else:
+            assert_f32(got, wdx, "dx")
+    if dT is not None:
+        assert_f32(dT.cpu().numpy(), wdT, "dT")
+    if dW is not None:
+        assert_f32(dW.cpu().numpy(), wdW, "dWmix")
+    return dx, dT, dW
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("B,C,H,W,w", [
+    (5, 3, 28, 28, 14), (3, 2, 56, 56, 14), (18, 3, 14, 14, 14),   # whole-image kernels, part units
+    (1, 1, 28, 28, 14), (2, 3, 30, 45, 7), (3, 5, 9, 9, 3), (2, 3, 5, 40, 8), (2, 2, 20, 20, 16),
+    (2, 2, 30, 20, 20), (1, 2, 4, 5, 14),
+])
+def test_backward_ckpt(fmt, bf16, mix, B, C, H, W, w):
+    check_bwd(B, C, H, W, w, mix, fmt, bf16, seed=B + w)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("mix", [False, True])
+def test_backward_ckpt_nhwc(bf16, mix):
+    check_bwd(2, 12, 17, 19, 7, mix, "int8", bf16, layout="NHWC")
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("B,H,w", [(5, 28, 14), (2, 13, 5)])
+def test_backward_ckpt_partial_outputs(bf16, B, H, w):
+    """Each output alone is what the whole call gives."""
+    whole = check_bwd(B, 3, H, H, w, True, "int8", bf16, seed=4)
+    for k in range(3):
+        flags = dict(dx=k == 0, dT=k == 1, dmix_w=k == 2)
+        part = check_bwd(B, 3, H, H, w, True, "int8", bf16, seed=4, **flags)
+        for j in range(3):
+            assert (part[j] is None) == (j != k)
+        assert torch.equal(part[k], whole[k])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_backward_ckpt_is_the_backward_of_the_decoded_maps(fmt):
+    """fp32: the same gradients as wbmm_backward on the unpacked maps, to rounding."""
+    x, z, dy, T, Wm = bwd_inputs(9, 4, 28, 28, 14, True, fmt, False, "NCHW", 11)
+    xc, zc = (R().wbmm_ckpt_pack(dev(a), fmt=fmt) for a in (x, z))
+    un = lambda c: R().wbmm_ckpt_unpack(*c, fmt=fmt)
+    got = R().wbmm_backward_ckpt(xc, dev(dy), 14, dev(T), mix_w=dev(Wm), z_ckpt=zc, fmt=fmt)
+    want = R().wbmm_backward(un(xc), dev(dy), 14, T=dev(T), mix_w=dev(Wm), z_saved=un(zc))
+    for a, b, name in zip(got, want, ("dx", "dT", "dW")):
+        assert_f32(a.cpu().numpy(), b.double().cpu().numpy(), name)
+
+
+def test_backward_ckpt_nan_group_reaches_its_channel_only():
+    x, z, dy, T, Wm = bwd_inputs(2, 3, 28, 28, 14, False, "int8", False, "NCHW", 1)
+    x[0, 1, 3, 3] = np.inf
+    xc = R().wbmm_ckpt_pack(dev(x))
+    dx, dT, _ = R().wbmm_backward_ckpt(xc, dev(dy), 14, dev(T))
+    assert torch.isfinite(dx).all() and torch.isfinite(dT[[0, 2]]).all()
+    assert torch.isnan(dT[1]).any()
+
+
+def test_backward_ckpt_determinism_stream_and_graph():
+    x, z, dy, T, Wm = bwd_inputs(17, 6, 28, 28, 14, True, "int8", False, "NCHW", 2)
+    xc, zc = (R().wbmm_ckpt_pack(dev(a)) for a in (x, z))
+    args = (xc, dev(dy), 14, dev(T))
+    kw = dict(mix_w=dev(Wm), z_ckpt=zc)
+    want = R().wbmm_backward_ckpt(*args, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on_side = R().wbmm_backward_ckpt(*args, stream=side, **kw)
+    side.synchronize()
+    for a, b in zip(on_side, want):
+        assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = R().wbmm_backward_ckpt(*args, **kw)
+    for k in range(3):
+        for t in out:
+            t.fill_(float(k))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+def test_binding_refusals():
+    M = R()
+    x = torch.zeros(2, 3, 28, 28, device="cuda")
+    codes, scales = M.wbmm_ckpt_pack(x)
+    T = torch.zeros(3, 27, 27, device="cuda")
+    bad = [
+        lambda: M.wbmm_ckpt_pack(x.cpu()), lambda: M.wbmm_ckpt_pack(x, fmt="fp4"),
+        lambda: M.wbmm_ckpt_pack(x.half()), lambda: M.wbmm_ckpt_pack(x[..., ::2]),
+        lambda: M.wbmm_ckpt_pack(x[:0]), lambda: M.wbmm_ckpt_pack(x, codes=codes[:1]),
+        lambda: M.wbmm_ckpt_unpack(codes, scales[:-1]),
+        lambda: M.wbmm_ckpt_unpack(codes.float(), scales),
+        lambda: M.wbmm_backward_ckpt((codes, scales), x.bfloat16(), 14, T),
+        lambda: M.wbmm_backward_ckpt((codes, scales), x, 7, T),
+        lambda: M.wbmm_backward_ckpt((codes, scales), x, 14, T, z_ckpt=(codes, scales)),
+        lambda: M.wbmm_backward_ckpt((codes[:1], scales), x, 14, T),
+        lambda: M.wbmm_backward_ckpt((codes, scales), x, 14, T, dx=x),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(M.WbmmError):
+            f()
+            pytest.fail(f"call {k} was accepted")

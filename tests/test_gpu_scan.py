@@ -1,0 +1,325 @@
+"""The gated linear recurrence on the GPU against the fp64 oracle, element by element, within the
+bound that the oracle carries along for fp32 arithmetic, plus half a step of the output's type."""
+import numpy as np
+import pytest
+
+from oracle import ops_oracle as Q
+from receptive_field_spatial_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def R():
+    import receptive_field_spatial_amd as mod
+    mod.load_library()
+    return mod
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def draw(shape, bf16, seed, spread=3.0):
+    O, L, I = shape
+    rng = np.random.default_rng(seed)
+    g = rng.standard_normal(shape) + rng.uniform(-1, 2 * spread, (O, 1, I))
+    u, dh = rng.standard_normal(shape), rng.standard_normal(shape)
+    h0, dl = rng.standard_normal((O, I)), rng.standard_normal((O, I))
+    arrs = [a.astype(np.float32) for a in (g, u, dh, h0, dl)]
+    if bf16:
+        arrs[:3] = [synth.round_to_bf16(a) for a in arrs[:3]]
+    return arrs
+
+
+def close(got, want, bound, bf16, what):
+    got = got.double().cpu().numpy().reshape(want.shape)
+    half = 2.0 ** -8 if bf16 else 2.0 ** -24
+    tol = bound * (1 + half) + half * np.abs(want) + 1e-36
+    err = np.abs(got - want)
+    worst = np.max(np.where(tol > 0, err / tol, np.where(err > 0, np.inf, 0)))
+    print(f"    {what}: worst error/bound {worst:.3f}, max abs {err.max():.2e}", flush=True)
+    assert np.all(err <= tol), (what, worst)
+
+
+def run_case(O, L, I, bf16=False, reverse=False, lens=None, ckpt=None, h0=True, seed=0, arrs=None,
+             recompute=False):
+    print(f"\n[case] scan {O}x{L}x{I} bf16={bf16} rev={reverse} lens={lens} ckpt={ckpt}", flush=True)
+    shape = (O, L, I)
+    g, u, dh, s0, dl = arrs or draw(shape, bf16, seed)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gd, ud, dd = (dev(a).to(dt) for a in (g, u, dh))
+    n = None
+    ln = None
+    if lens is not None:
+        ln = dev(np.asarray(lens, np.int32))
+        n = np.clip(np.repeat(lens, O // len(lens)), 0, L)
+        # positions past the end may hold anything
+        for o in range(O):
+            for t in (gd, ud, dd):
+                t[o, n[o]:] = float("nan")
+        g, u, dh = g.copy(), u.copy(), dh.copy()
+        for o in range(O):
+            g[o, n[o]:] = u[o, n[o]:] = dh[o, n[o]:] = 0
+    st0 = dev(s0) if h0 else None
+    h, last, states = R().wbmm_scan_forward(gd, ud, 1, h0=st0, lens=ln, reverse=reverse,
+                                            h_last=True, states=True)
+    f64 = [a.astype(np.float64) for a in (g, u, dh, s0, dl)]
+    wh, wl, wst, bh, bl, bst = Q.scan_forward(f64[0], f64[1], f64[3] if h0 else None, n, reverse,
+                                              bf16)
+    close(h, wh, bh, bf16, "h")
+    close(last, wl, bl, False, "h_last")
+    close(states, wst, bst, False, "states")
+    kw = dict(u=ud)
+    uval = f64[1]
+    if ckpt:
+        clean = ud.nan_to_num(0.0)
+        kw = dict(u_ckpt=R().wbmm_ckpt_pack(clean, fmt=ckpt), fmt=ckpt)
+        uval = R().wbmm_ckpt_unpack(*kw["u_ckpt"], fmt=ckpt).double().cpu().numpy()
+        if lens is not None:
+            for o in range(O):
+                uval[o, n[o]:] = 0
+        # the oracle is the recurrence on the decoded u: its states, or none (then the call runs
+        # it for them)
+        states = R().wbmm_scan_forward(gd, dev(uval.astype(np.float32)).to(dt), 1, h0=st0, lens=ln,
+                                       reverse=reverse, states=True)[2]
+    if recompute:
+        states = None
+        kw["h0"] = st0
+    dg, du, d0 = R().wbmm_scan_backward(gd, states, dd, 1, dh_last=dev(dl), lens=ln,
+                                        reverse=reverse, **kw)
+    wdg, wdu, wd0, bg, bu, b0 = Q.scan_backward(f64[0], uval, f64[3] if h0 else None, f64[2],
+                                                f64[4], n, reverse, bf16)
+    close(dg, wdg, bg, bf16, "dg")
+    close(du, wdu, bu, bf16, "du")
+    close(d0, wd0, b0, False, "dh0")
+
+
+SHAPES = [
+    (1, 1, 1), (3, 1, 5), (7, 1, 1), (1, 2, 1), (2, 5, 1), (5, 8, 1), (9, 9, 1), (4, 16, 1),
+    (3, 17, 1), (3, 33, 1), (2, 64, 1), (3, 65, 1), (3, 127, 1), (2, 129, 1), (2, 256, 1),
+    (2, 257, 1), (3, 511, 1), (2, 513, 1), (5, 784, 1), (2, 1000, 1), (1, 4097, 1),
+    (2, 2, 2), (3, 7, 3), (2, 15, 64), (2, 16, 65), (1, 17, 130), (2, 31, 6), (2, 32, 192),
+    (3, 33, 97), (1, 128, 63), (1, 129, 64), (2, 255, 10), (1, 300, 2), (1, 1531, 97),
+]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("O,L,I", SHAPES)
+def test_scan(O, L, I, bf16, reverse):
+    run_case(O, L, I, bf16, reverse, seed=O + L + I)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("O,L,I,lens", [
+    (4, 40, 1, [0, 1, 40, 17]), (4, 700, 1, [0, 1, 700, 513]), (4, 90, 7, [0, 1, 90, 33]),
+    (4, 300, 66, [300, 0, 16, 129]), (6, 50, 1, [3, 50]), (6, 50, 3, [0, 50, 7]),
+    (2, 1, 1, [0, 1]), (2, 1, 4, [1, 0]), (2, 20, 5, [-3, 99]), (3, 5000, 1, [4999, 0, 512]),
+    (3, 2600, 10, [2600, 0, 1100]),
+])
+def test_scan_lengths(O, L, I, lens, bf16, reverse):
+    run_case(O, L, I, bf16, reverse, lens=lens, seed=L)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("O,L,I,reverse,lens", [
+    (5, 784, 1, False, None), (3, 37, 1, True, None), (3, 37, 1, True, [37, 0, 9]),
+    (2, 1001, 1, True, None), (2, 100, 7, False, None), (2, 100, 64, True, [100, 41]),
+    (1, 5003, 1, False, None), (1, 2001, 9, True, None),
+])
+def test_scan_backward_from_checkpoint(O, L, I, reverse, lens, fmt, bf16):
+    run_case(O, L, I, bf16, reverse, lens=lens, ckpt=fmt, seed=L)
+    run_case(O, L, I, bf16, reverse, lens=lens, ckpt=fmt, seed=L, recompute=True)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("O,L,I,reverse,lens", [
+    (2, 1, 1, False, None), (2, 1, 3, False, [0, 1]), (3, 20, 1, True, None), (2, 600, 1, True, [600, 5]),
+    (2, 90, 7, False, None), (2, 33, 64, True, [33, 0]), (1, 9000, 1, True, None), (1, 3001, 4, False, None),
+])
+def test_scan_backward_without_states(O, L, I, reverse, lens, bf16):
+    run_case(O, L, I, bf16, reverse, lens=lens, seed=L, recompute=True)
+    run_case(O, L, I, bf16, reverse, lens=lens, seed=L, recompute=True, h0=False)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("O,L,I", [(1, 20000, 1), (2, 9001, 1), (1, 12000, 3), (1, 4097, 192)])
+def test_scan_long_few_columns(O, L, I, bf16):
+    """The axis runs in segments here."""
+    assert R().wbmm_scan_forward_workspace_bytes(O, L, I) > 0
+    run_case(O, L, I, bf16, False, seed=1)
+    run_case(O, L, I, bf16, True, lens=[L - 700] * O, seed=2)
+
+
+def test_scan_without_initial_state_and_extreme_gates():
+    shape = (3, 70, 2)
+    arrs = draw(shape, False, 3)
+    arrs[0][0, ::3] = 100.0     # a = 1: u ignored
+    arrs[0][1, ::5] = -100.0    # a = 0: the state is replaced
+    arrs[0][2, 7] = 3e38
+    arrs[0][2, 9] = -3e38
+    run_case(*shape, h0=False, arrs=arrs)
+    flat = [np.ascontiguousarray(a.reshape(1, -1, 1) if a.ndim == 3 else a[:1, :1]) for a in arrs]
+    run_case(1, 420, 1, arrs=flat)
+
+
+def test_scan_gate_infinite():
+    g = torch.tensor([0.0, float("inf"), 1.0, float("-inf"), 2.0], device="cuda").reshape(1, 5, 1)
+    u = torch.tensor([1.0, 5.0, 1.0, 7.0, 1.0], device="cuda").reshape(1, 5, 1)
+    for t in (g, g.expand(1, 5, 2).contiguous()):
+        h = R().wbmm_scan_forward(t, u.expand_as(t).contiguous(), 1)[0]
+        assert torch.isfinite(h).all()
+        assert torch.equal(h[0, 1], h[0, 0])
+        # a = 0 to within the least normal number; c = t (1 / (1 + t)) with 1 + t = t: the
+        # reciprocal is within one step (2^-23), its product with t and that with u take half a
+        # step (2^-24) each
+        assert torch.all((h[0, 3] - 7).abs() <= 7 * (2.0 ** -23 + 2 * 2.0 ** -24))
+
+
+def test_scan_nan_stays_in_its_column():
+    for shape in ((3, 100, 1), (1, 100, 3)):
+        g = torch.zeros(shape, device="cuda")
+        u = torch.ones(shape, device="cuda")
+        idx = (1, 50, 0) if shape[0] == 3 else (0, 50, 1)
+        for t in (g, u):
+            t[idx] = float("nan")
+            h, last, st = R().wbmm_scan_forward(g, u, 1, h_last=True, states=True)
+            bad = torch.isnan(h).reshape(3, 100) if shape[0] == 3 else torch.isnan(h)[0].T
+            assert bad[1, 50:].all() and not bad[1, :50].any() and not bad[[0, 2]].any()
+            t[idx] = 0.0
+
+
+@pytest.mark.parametrize("O,L,I", [(8, 1, 192), (5, 37, 1), (1, 9000, 1), (1, 3000, 4), (4, 70, 3)])
+def test_scan_state_updated_in_place(O, L, I):
+    g, u, _, h0, _ = draw((O, L, I), False, 6)
+    gd, ud = dev(g), dev(u)
+    h, last, _ = R().wbmm_scan_forward(gd, ud, 1, h0=dev(h0), h_last=True)
+    st = dev(h0)
+    h2, st2, _ = R().wbmm_scan_forward(gd, ud, 1, h0=st, h_last=st)
+    assert st2.data_ptr() == st.data_ptr() and torch.equal(st, last) and torch.equal(h, h2)
+
+
+def test_scan_steps_one_by_one_equal_one_run():
+    O, L, I = 4, 50, 24
+    g, u, _, h0, _ = draw((O, L, I), False, 9)
+    h, last, _ = R().wbmm_scan_forward(dev(g), dev(u), 1, h0=dev(h0), h_last=True)
+    st = dev(h0)
+    for t in range(L):
+        ht, st, _ = R().wbmm_scan_forward(dev(g[:, t:t + 1]), dev(u[:, t:t + 1]), 1, h0=st, h_last=st)
+        assert torch.allclose(ht[:, 0], h[:, t], rtol=0, atol=60 * 2.0 ** -22)
+    assert torch.allclose(st, last, rtol=0, atol=60 * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2, 3, -1])
+def test_scan_any_dimension(dim):
+    shape = (3, 5, 14, 9)
+    rng = np.random.default_rng(0)
+    g, u = (rng.standard_normal(shape).astype(np.float32) for _ in range(2))
+    h, last, st = R().wbmm_scan_forward(dev(g), dev(u), dim, h_last=True, states=True)
+    mv = lambda a: np.moveaxis(a, dim, -1).reshape(-1, shape[dim], 1).astype(np.float64)
+    wh, wl, _, bh, bl, _ = Q.scan_forward(mv(g), mv(u))
+    close(torch.movedim(h, dim, -1).contiguous(), wh, bh, False, "h")
+    close(last, wl, bl, False, "h_last")
+    assert st.shape[dim] == 1
+
+
+@pytest.mark.parametrize("O,L,I,bf16", [(3, 130, 1, False), (2, 70, 5, True), (3, 77, 4, True),
+                                        (1, 9000, 1, True), (1, 3000, 3, False), (4, 1, 9, True)])
+def test_scan_writes_only_its_outputs(O, L, I, bf16):
+    dt = torch.bfloat16 if bf16 else torch.float32
+    g, u, dh, h0, dl = draw((O, L, I), bf16, 5)
+    N, G = O * L * I, 67    # odd guard: outputs at the element's own alignment
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 2 * G,), 33.0, dtype=dtype, device="cuda")
+        return buf, buf[G:G + n].view(shape)
+
+    def intact(buf):
+        b = buf.float().cpu().numpy()
+        return np.all(b[:G] == 33) and np.all(b[-G:] == 33)
+
+    ck = -(-L // 32)
+    bh, h = guarded((O, L, I), dt)
+    bl, last = guarded((O, I), torch.float32)
+    bs, st = guarded((O, ck, I), torch.float32)
+    need = max(R().wbmm_scan_forward_workspace_bytes(O, L, I),
+               R().wbmm_scan_backward_workspace_bytes(O, L, I, False))
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    gd, ud, dd = (dev(a).to(dt) for a in (g, u, dh))
+    w = ws[:need] if need else None
+    lens = dev(np.array([max(L - 40, 1)], np.int32))
+    for ln in (None, lens):
+        h.fill_(float("nan")), st.fill_(float("nan"))
+        R().wbmm_scan_forward(gd, ud, 1, h0=dev(h0), h=h, h_last=last, states=st, lens=ln, workspace=w)
+        assert torch.isfinite(h.float()).all() and torch.isfinite(st).all()
+        bg, dg = guarded((O, L, I), dt)
+        bu, du = guarded((O, L, I), dt)
+        b0, d0 = guarded((O, I), torch.float32)
+        dg.fill_(float("nan")), du.fill_(float("nan"))
+        R().wbmm_scan_backward(gd, st, dd, 1, u=ud, dg=dg, du=du, dh0=d0, lens=ln, workspace=w)
+        assert torch.isfinite(dg.float()).all() and torch.isfinite(du.float()).all()
+        kept = [t.clone() for t in (dg, du, d0)]
+        R().wbmm_scan_backward(gd, None, dd, 1, u=ud, h0=dev(h0), dg=dg, du=du, dh0=d0, lens=ln,
+                               workspace=w)
+        assert all(torch.equal(p, q) for p, q in zip(kept, (dg, du, d0)))
+        for b in (bh, bl, bs, bg, bu, b0):
+            assert intact(b)
+        assert torch.all(ws[need:] == 77)
+
+
+def test_scan_stream_and_graph():
+    for shape in ((6, 300, 1), (2, 100, 20), (1, 9000, 2)):
+        g, u, dh, h0, dl = (dev(a) for a in draw(shape, False, 1))
+
+        def both(stream=None):
+            h, last, st = R().wbmm_scan_forward(g, u, 1, h0=h0, h_last=True, states=True, stream=stream)
+            return [h, last, st, *R().wbmm_scan_backward(g, st, dh, 1, u=u, dh_last=dl, stream=stream)]
+
+        want = both()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = both(side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = both()
+        for k in range(3):
+            for t in out:
+                t.fill_(float(k))
+            both()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_scan_binding_refusals():
+    M = R()
+    g = torch.zeros(2, 40, 3, device="cuda")
+    st = torch.zeros(2, 2, 3, device="cuda")
+    h0 = torch.zeros(2, 3, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: M.wbmm_scan_forward(g, g.bfloat16(), 1), lambda: M.wbmm_scan_forward(g, g[:1], 1),
+        lambda: M.wbmm_scan_forward(g, g, 3), lambda: M.wbmm_scan_forward(g.cpu(), g, 1),
+        lambda: M.wbmm_scan_forward(g.half(), g.half(), 1), lambda: M.wbmm_scan_forward(g[:0], g[:0], 1),
+        lambda: M.wbmm_scan_forward(g, g, 1, h0=h0[:1]), lambda: M.wbmm_scan_forward(g, g, 1, h=g),
+        lambda: M.wbmm_scan_forward(g, g, 1, lens=i32(1, 2, 3)),
+        lambda: M.wbmm_scan_forward(g, g, 1, lens=i32()),
+        lambda: M.wbmm_scan_forward(g, g, 1, lens=torch.tensor([1, 2], device="cuda")),
+        lambda: M.wbmm_scan_forward(g.transpose(0, 1), g.transpose(0, 1), 1),
+        lambda: M.wbmm_scan_backward(g, st, g, 1), lambda: M.wbmm_scan_backward(g, st[:, :1], g, 1, u=g),
+        lambda: M.wbmm_scan_backward(g, st, g, 1, u=g, u_ckpt=(g, g)),
+        lambda: M.wbmm_scan_backward(g, st, g, 1, u=g, dg=g),
+        lambda: M.wbmm_scan_backward(g, st, g, 1, u_ckpt=M.wbmm_ckpt_pack(g), fmt="x"),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(M.WbmmError):
+            f()
+            pytest.fail(f"call {k} was accepted")
