@@ -384,10 +384,13 @@ def _run_own(s):
                                                 states=case["states"])
         return [h, h_last, states] if case["states"] else [h, h_last]
     if case["ckpt"]:
-        kw = dict(u_ckpt=s["u_ckpt"], fmt=case["ckpt"])
+        # the recurrence on the kept u, from its first state: the other states are those of the
+        # u that was not kept
+        states = None
+        kw = dict(u_ckpt=s["u_ckpt"], fmt=case["ckpt"], h0=s["states"][:, 0].contiguous())
     else:
-        kw = dict(u=s["u"])
-    dg, du, dh0 = R.wbmm_scan_backward(s["g"], s["states"], s["dh"], 1, dh_last=s["dh_last"],
+        states, kw = s["states"], dict(u=s["u"])
+    dg, du, dh0 = R.wbmm_scan_backward(s["g"], states, s["dh"], 1, dh_last=s["dh_last"],
                                        lens=s["lens"], reverse=case["reverse"], **kw)
     return [dg, du, dh0]
 
