@@ -7,7 +7,10 @@ There is no CPU fallback: if the library is missing or cannot load, calls raise 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import math
 import os
 import threading
 from typing import Optional
@@ -471,74 +474,76 @@ def _fmt_code(fmt: str) -> int:
     raise WbmmError(WBMM_E_INVALID, f"unknown checkpoint format {fmt!r} (int8 or e4m3)")
 
 
-def _tensor(name, t, shape, dtype, device, optional=False):
-    """Checks one tensor argument: shape, dtype, dense, and on `device` (None: the current one)."""
-    torch = _torch()
+# Per-call host time counts in a one-step call, so the checks below take one pass over each tensor
+# and hand back its address.
+def _device(name, t) -> int:
+    """The device of a call, from one of its tensors: the current one."""
     if t is None:
-        if optional:
-            return
         raise WbmmError(WBMM_E_INVALID, f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    idx = t.get_device()
+    if idx < 0:
+        raise WbmmError(WBMM_E_INVALID, f"{name} must be on the GPU")
+    if idx != _torch()._C._cuda_getDevice():
+        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, which is not the current device")
+    return idx
+
+
+def _need(name, t, shape, dtype, idx):
+    """Address of a tensor argument of this shape and dtype, dense, on device idx."""
+    if t is None:
+        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
+    if t.shape != shape:
         raise WbmmError(WBMM_E_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise WbmmError(WBMM_E_INVALID, f"{name} must be {dtype}, got {t.dtype}")
-    _ptr(t)  # on the GPU, contiguous
-    if t.device != device:
-        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, not on {device}")
-    if device.index != torch.cuda.current_device():
-        raise WbmmError(WBMM_E_INVALID, f"{name} is on {device}, which is not the current device")
+    if t.get_device() != idx:
+        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, not on GPU {idx}")
+    if not t.is_contiguous():
+        raise WbmmError(WBMM_E_INVALID, f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _gpu(name, t):
-    """The device of a call, taken from its first tensor."""
-    if t is None:
-        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
-    _ptr(t)
-    return t.device
+def _opt(name, t, shape, dtype, idx):
+    return None if t is None else _need(name, t, shape, dtype, idx)
 
 
-class _on_stream:
-    """Allocations of a call belong to the stream that the call runs on."""
-
-    def __init__(self, stream, device):
-        torch = _torch()
-        if stream is None:
-            self.ctx = None
-        elif isinstance(stream, torch.cuda.Stream):
-            self.ctx = torch.cuda.stream(stream)
-        else:
-            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            self.ctx = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw
-                                         else torch.cuda.default_stream(device))
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-
-def _out(name, v, shape, dtype, device):
-    """An output argument: True allocates it, False or None skips it, a tensor is written."""
-    if v is False or v is None:
-        return None
+def _out(name, v, shape, dtype, idx):
+    """An output argument: True allocates it, False or None skips it, a tensor is written. Returns
+    the tensor and its address."""
     if v is True:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    _tensor(name, v, shape, dtype, device)
-    return v
+        v = _torch().empty(shape, dtype=dtype, device=idx)
+        return v, v.data_ptr()
+    if v is False or v is None:
+        return None, None
+    return v, _need(name, v, shape, dtype, idx)
 
 
-def _workspace(need, workspace, device):
-    """A caller's workspace when it is given (the library checks its size), else a new one."""
+def _raw_stream(stream, idx) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream)
+
+
+def _on_stream(stream, idx):
+    """Allocations of a call belong to the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch().cuda
+    if not isinstance(stream, cuda.Stream):
+        raw = _stream(stream)
+        stream = cuda.ExternalStream(raw, device=idx) if raw else cuda.default_stream(idx)
+    return cuda.stream(stream)
+
+
+def _workspace(need, workspace, idx):
+    """A caller's workspace when it is given (the library checks its size), else a new one; its
+    address and size."""
     if workspace is not None:
-        if _gpu("workspace", workspace) != device:
-            raise WbmmError(WBMM_E_INVALID, f"workspace is on {workspace.device}, not on {device}")
-        return workspace, workspace.numel() * workspace.element_size()
+        if workspace.get_device() != idx or not workspace.is_contiguous():
+            raise WbmmError(WBMM_E_INVALID, f"workspace must be contiguous and on GPU {idx}")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
-        return None, 0
-    return _torch().empty(need, dtype=_torch().uint8, device=device), need
+        return None, None, 0
+    workspace = _torch().empty(need, dtype=_torch().uint8, device=idx)
+    return workspace, workspace.data_ptr(), need
 
 
 def _ckpt_scales(n: int) -> int:
@@ -548,39 +553,40 @@ def _ckpt_scales(n: int) -> int:
 def wbmm_ckpt_pack(x, *, fmt: str = "int8", codes=None, scales=None, stream=None):
     """Packs x (fp32 or bf16, any shape) into an 8-bit checkpoint: (codes, scales), codes uint8 in
     x's shape, scales uint8 with one entry per WBMM_CKPT_GROUP elements in memory order."""
-    torch = _torch()
-    code, dev = _fmt_code(fmt), _gpu("x", x)
-    dt = _dtype_code(x.dtype)
-    _tensor("x", x, x.shape, x.dtype, dev)
-    with _on_stream(stream, dev):
-        codes = _out("codes", True if codes is None else codes, tuple(x.shape), torch.uint8, dev)
-        scales = _out("scales", True if scales is None else scales, (_ckpt_scales(x.numel()),),
-                      torch.uint8, dev)
-        _check(_lib().wbmm_ckpt_pack(_ptr(x), x.numel(), dt, code, _ptr(codes), _ptr(scales),
-                                     _stream(stream)))
+    u8 = _torch().uint8
+    code, dt, idx = _fmt_code(fmt), _dtype_code(x.dtype), _device("x", x)
+    xp, n = _need("x", x, x.shape, x.dtype, idx), x.numel()
+    with _on_stream(stream, idx):
+        codes, cp = _out("codes", True if codes is None else codes, x.shape, u8, idx)
+        scales, sp = _out("scales", True if scales is None else scales, (_ckpt_scales(n),), u8, idx)
+        _check(_lib().wbmm_ckpt_pack(xp, n, dt, code, cp, sp, _raw_stream(stream, idx)))
     return codes, scales
 
 
 def wbmm_ckpt_unpack(codes, scales, *, fmt: str = "int8", dtype=None, out=None, stream=None):
     """The values of a checkpoint in `dtype` (fp32 by default, or out's)."""
     torch = _torch()
-    code, dev = _fmt_code(fmt), _gpu("codes", codes)
+    code, idx = _fmt_code(fmt), _device("codes", codes)
     dtype = dtype or (torch.float32 if out is None else out.dtype)
-    dt = _dtype_code(dtype)
-    _tensor("codes", codes, codes.shape, torch.uint8, dev)
-    _tensor("scales", scales, (_ckpt_scales(codes.numel()),), torch.uint8, dev)
-    with _on_stream(stream, dev):
-        out = _out("out", True if out is None else out, tuple(codes.shape), dtype, dev)
-        _check(_lib().wbmm_ckpt_unpack(_ptr(codes), _ptr(scales), codes.numel(), dt, code,
-                                       _ptr(out), _stream(stream)))
+    dt, n = _dtype_code(dtype), codes.numel()
+    cp = _need("codes", codes, codes.shape, torch.uint8, idx)
+    sp = _need("scales", scales, (_ckpt_scales(n),), torch.uint8, idx)
+    with _on_stream(stream, idx):
+        out, xp = _out("out", True if out is None else out, codes.shape, dtype, idx)
+        _check(_lib().wbmm_ckpt_unpack(cp, sp, n, dt, code, xp, _raw_stream(stream, idx)))
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_ckpt_bytes(*sizes) -> int:
+    return int(_lib().wbmm_backward_ckpt_workspace_bytes(*sizes))
 
 
 def wbmm_backward_ckpt_workspace_bytes(B, C, H, W, w, layout="NCHW", dtype=None,
                                        has_mix=False) -> int:
     code = WBMM_F32 if dtype is None else _dtype_code(dtype)
-    return int(_lib().wbmm_backward_ckpt_workspace_bytes(B, C, H, W, int(w), _layout_code(layout),
-                                                         code, int(bool(has_mix))))
+    return _backward_ckpt_bytes(int(B), int(C), int(H), int(W), int(w), _layout_code(layout), code,
+                                int(bool(has_mix)))
 
 
 def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: str = "int8",
@@ -591,69 +597,64 @@ def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: s
     both fp32 or both bf16. Returns (dx in dy's dtype, dT fp32, dmix_w fp32); an output passed as
     False is skipped."""
     torch = _torch()
-    dev = _gpu("dy", dy)
+    idx = _device("dy", dy)
     B, C, H, W = _bchw(dy, layout)
-    w = int(w)
-    fcode, dt = _fmt_code(fmt), _dtype_code(dy.dtype)
+    w, n, shape = int(w), dy.numel(), dy.shape
+    lay, fcode, dt = _layout_code(layout), _fmt_code(fmt), _dtype_code(dy.dtype)
     L = 2 * w - 1
     if (mix_w is None) != (z_ckpt is None):
         raise WbmmError(WBMM_E_INVALID, "z_ckpt is required exactly when mix_w is given")
-    xc, xs = x_ckpt
-    zc, zs = (None, None) if z_ckpt is None else z_ckpt
-    scales = (_ckpt_scales(dy.numel()),)
-    _tensor("dy", dy, dy.shape, dy.dtype, dev)
-    _tensor("x codes", xc, dy.shape, torch.uint8, dev)
-    _tensor("x scales", xs, scales, torch.uint8, dev)
-    _tensor("T", T, (C, L, L), dy.dtype, dev)
-    _tensor("mix_w", mix_w, (C, 3, 3), torch.float32, dev, optional=True)
-    _tensor("z codes", zc, dy.shape, torch.uint8, dev, optional=z_ckpt is None)
-    _tensor("z scales", zs, scales, torch.uint8, dev, optional=z_ckpt is None)
-    with _on_stream(stream, dev):
-        dx_t = _out("dx", dx, tuple(dy.shape), dy.dtype, dev)
-        dT_t = _out("dT", dT, (C, L, L), torch.float32, dev)
-        dW_t = None if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), torch.float32, dev)
-        need = wbmm_backward_ckpt_workspace_bytes(B, C, H, W, w, layout, dy.dtype,
-                                                  mix_w is not None)
-        ws, ws_bytes = _workspace(need, workspace, dev)
-        _check(_lib().wbmm_backward_ckpt(B, C, H, W, w, _layout_code(layout), dt, fcode, _ptr(xc),
-                                         _ptr(xs), _ptr(T), _ptr(mix_w), _ptr(zc), _ptr(zs),
-                                         _ptr(dy), _ptr(dx_t), _ptr(dT_t), _ptr(dW_t), _ptr(ws),
-                                         ws_bytes, _stream(stream)))
-    return dx_t, dT_t, dW_t
+    u8, f32, scales = torch.uint8, torch.float32, (_ckpt_scales(n),)
+    dyp = _need("dy", dy, shape, dy.dtype, idx)
+    xc, xs = _need("x codes", x_ckpt[0], shape, u8, idx), _need("x scales", x_ckpt[1], scales, u8, idx)
+    Tp = _need("T", T, (C, L, L), dy.dtype, idx)
+    mp = zc = zs = None
+    if mix_w is not None:
+        mp = _need("mix_w", mix_w, (C, 3, 3), f32, idx)
+        zc = _need("z codes", z_ckpt[0], shape, u8, idx)
+        zs = _need("z scales", z_ckpt[1], scales, u8, idx)
+    with _on_stream(stream, idx):
+        dx, dxp = _out("dx", dx, shape, dy.dtype, idx)
+        dT, dTp = _out("dT", dT, (C, L, L), f32, idx)
+        dmix_w, dWp = (None, None) if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), f32, idx)
+        ws, wp, wb = _workspace(_backward_ckpt_bytes(B, C, H, W, w, lay, dt, int(mix_w is not None)),
+                                workspace, idx)
+        _check(_lib().wbmm_backward_ckpt(B, C, H, W, w, lay, dt, fcode, xc, xs, Tp, mp, zc, zs, dyp,
+                                         dxp, dTp, dWp, wp, wb, _raw_stream(stream, idx)))
+    return dx, dT, dmix_w
 
 
 # ----------------------------------------------------------------------------- recurrence
+@functools.lru_cache(maxsize=256)
 def wbmm_scan_forward_workspace_bytes(outer: int, length: int, inner: int) -> int:
     return int(_lib().wbmm_scan_forward_workspace_bytes(int(outer), int(length), int(inner)))
 
 
+@functools.lru_cache(maxsize=256)
 def wbmm_scan_backward_workspace_bytes(outer: int, length: int, inner: int,
                                        has_states: bool = True) -> int:
     return int(_lib().wbmm_scan_backward_workspace_bytes(int(outer), int(length), int(inner),
                                                          int(bool(has_states))))
 
 
-def _scan_sizes(g, dim: int):
-    if g.dim() < 1 or not -g.dim() <= dim < g.dim():
-        raise WbmmError(WBMM_E_INVALID, f"dim={dim} is no dimension of a tensor of {g.dim()}")
-    dim %= g.dim()
-    lead, tail = tuple(g.shape[:dim]), tuple(g.shape[dim + 1:])
-    outer = inner = 1
-    for v in lead:
-        outer *= int(v)
-    for v in tail:
-        inner *= int(v)
-    length = int(g.shape[dim])
-    return outer, length, inner, lead + tail, lead + (-(-length // WBMM_SCAN_CHUNK),) + tail
+@functools.lru_cache(maxsize=256)
+def _scan_sizes(shape, dim: int):
+    """(outer, len, inner) of a tensor's shape, and the shapes of h0 / h_last and of states."""
+    if not -len(shape) <= dim < len(shape):
+        raise WbmmError(WBMM_E_INVALID, f"dim={dim} is no dimension of a tensor of {len(shape)}")
+    dim %= len(shape)
+    lead, tail, length = tuple(shape[:dim]), tuple(shape[dim + 1:]), shape[dim]
+    return (math.prod(lead), length, math.prod(tail), lead + tail,
+            lead + (-(-length // WBMM_SCAN_CHUNK),) + tail)
 
 
-def _scan_lens(lens, device):
+def _scan_lens(lens, idx):
     if lens is None:
-        return 0
-    _tensor("lens", lens, (lens.numel(),), _torch().int32, device)
-    if lens.numel() == 0:
+        return None, 0
+    n = lens.numel()
+    if n == 0:
         raise WbmmError(WBMM_E_INVALID, "lens is empty")
-    return lens.numel()
+    return _need("lens", lens, (n,), _torch().int32, idx), n
 
 
 def wbmm_scan_forward(g, u, dim: int, *, h0=None, lens=None, reverse: bool = False, h=None,
@@ -667,23 +668,20 @@ def wbmm_scan_forward(g, u, dim: int, *, h0=None, lens=None, reverse: bool = Fal
     states: True allocates them, a tensor is written (h_last may be h0), False skips them; states
     (fp32, `dim` divided by WBMM_SCAN_CHUNK and rounded up) is what wbmm_scan_backward starts
     from. Returns (h, h_last, states)."""
-    torch = _torch()
-    dev = _gpu("g", g)
-    outer, length, inner, flat, kept = _scan_sizes(g, dim)
-    dt = _dtype_code(g.dtype)
-    _tensor("g", g, g.shape, g.dtype, dev)
-    _tensor("u", u, g.shape, g.dtype, dev)
-    _tensor("h0", h0, flat, torch.float32, dev, optional=True)
-    n_lens = _scan_lens(lens, dev)
-    with _on_stream(stream, dev):
-        h = _out("h", True if h is None else h, tuple(g.shape), g.dtype, dev)
-        h_last = _out("h_last", h_last, flat, torch.float32, dev)
-        states = _out("states", states, kept, torch.float32, dev)
-        ws, ws_bytes = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace, dev)
-        _check(_lib().wbmm_scan_forward(outer, length, inner, dt, int(bool(reverse)), _ptr(g),
-                                        _ptr(u), _ptr(h0), _ptr(lens), n_lens, _ptr(h),
-                                        _ptr(h_last), _ptr(states), _ptr(ws), ws_bytes,
-                                        _stream(stream)))
+    f32, dtype, shape = _torch().float32, g.dtype, g.shape
+    dt, idx = _dtype_code(dtype), _device("g", g)
+    outer, length, inner, flat, kept = _scan_sizes(shape, dim)
+    gp, up = _need("g", g, shape, dtype, idx), _need("u", u, shape, dtype, idx)
+    h0p = _opt("h0", h0, flat, f32, idx)
+    lp, n_lens = _scan_lens(lens, idx)
+    with _on_stream(stream, idx):
+        h, hp = _out("h", True if h is None else h, shape, dtype, idx)
+        h_last, hlp = _out("h_last", h_last, flat, f32, idx)
+        states, sp = _out("states", states, kept, f32, idx)
+        ws, wp, wb = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace,
+                                idx)
+        _check(_lib().wbmm_scan_forward(outer, length, inner, dt, int(bool(reverse)), gp, up, h0p,
+                                        lp, n_lens, hp, hlp, sp, wp, wb, _raw_stream(stream, idx)))
     return h, h_last, states
 
 
@@ -696,32 +694,28 @@ def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str
     dh_last: fp32 gradient of h_last, or None. Returns (dg, du, dh0), dg and du in g's dtype and 0
     past a sequence's end, dh0 fp32 (False skips it)."""
     torch = _torch()
-    dev = _gpu("g", g)
-    outer, length, inner, flat, kept = _scan_sizes(g, dim)
-    dt = _dtype_code(g.dtype)
+    f32, dtype, shape = torch.float32, g.dtype, g.shape
+    dt, idx = _dtype_code(dtype), _device("g", g)
+    outer, length, inner, flat, kept = _scan_sizes(shape, dim)
     if (u is None) == (u_ckpt is None):
         raise WbmmError(WBMM_E_INVALID, "exactly one of u and u_ckpt must be given")
-    _tensor("g", g, g.shape, g.dtype, dev)
+    gp, dhp = _need("g", g, shape, dtype, idx), _need("dh", dh, shape, dtype, idx)
     if u_ckpt is None:
-        uu, us, fcode = u, None, 0
-        _tensor("u", u, g.shape, g.dtype, dev)
+        up, us, fcode = _need("u", u, shape, dtype, idx), None, 0
     else:
-        (uu, us), fcode = u_ckpt, _fmt_code(fmt)
-        _tensor("u codes", uu, g.shape, torch.uint8, dev)
-        _tensor("u scales", us, (_ckpt_scales(g.numel()),), torch.uint8, dev)
-    _tensor("states", states, kept, torch.float32, dev, optional=True)
-    _tensor("h0", h0, flat, torch.float32, dev, optional=True)
-    _tensor("dh", dh, g.shape, g.dtype, dev)
-    _tensor("dh_last", dh_last, flat, torch.float32, dev, optional=True)
-    n_lens = _scan_lens(lens, dev)
-    with _on_stream(stream, dev):
-        dg = _out("dg", True if dg is None else dg, tuple(g.shape), g.dtype, dev)
-        du = _out("du", True if du is None else du, tuple(g.shape), g.dtype, dev)
-        dh0 = _out("dh0", dh0, flat, torch.float32, dev)
+        fcode = _fmt_code(fmt)
+        up = _need("u codes", u_ckpt[0], shape, torch.uint8, idx)
+        us = _need("u scales", u_ckpt[1], (_ckpt_scales(g.numel()),), torch.uint8, idx)
+    sp, h0p = _opt("states", states, kept, f32, idx), _opt("h0", h0, flat, f32, idx)
+    dlp = _opt("dh_last", dh_last, flat, f32, idx)
+    lp, n_lens = _scan_lens(lens, idx)
+    with _on_stream(stream, idx):
+        dg, dgp = _out("dg", True if dg is None else dg, shape, dtype, idx)
+        du, dup = _out("du", True if du is None else du, shape, dtype, idx)
+        dh0, d0p = _out("dh0", dh0, flat, f32, idx)
         need = wbmm_scan_backward_workspace_bytes(outer, length, inner, states is not None)
-        ws, ws_bytes = _workspace(need, workspace, dev)
-        _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode,
-                                         _ptr(g), _ptr(uu), _ptr(us), _ptr(states), _ptr(h0), _ptr(dh),
-                                         _ptr(dh_last), _ptr(lens), n_lens, _ptr(dg), _ptr(du),
-                                         _ptr(dh0), _ptr(ws), ws_bytes, _stream(stream)))
+        ws, wp, wb = _workspace(need, workspace, idx)
+        _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode, gp,
+                                         up, us, sp, h0p, dhp, dlp, lp, n_lens, dgp, dup, d0p, wp,
+                                         wb, _raw_stream(stream, idx)))
     return dg, du, dh0

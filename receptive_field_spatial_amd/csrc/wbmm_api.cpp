@@ -697,7 +697,11 @@ WBMM_API size_t wbmm_backward_ckpt_workspace_bytes(int B, int C, int H, int W, i
   r.bf16 = dtype == WBMM_BF16;
   r.mixw = has_mix ? &dummy : nullptr;
   if (check_bwd_ckpt(r, dtype) != WBMM_OK || !wbmm::backward_ckpt_plan_ok(r)) return 0;
-  return wbmm::backward_ckpt_workspace(r);
+  // the buffers' addresses are not arguments: the larger need of an aligned and a misaligned call
+  const size_t fused = wbmm::backward_ckpt_workspace(r);
+  r.xc = (const uint8_t*)1;
+  const size_t general = wbmm::backward_ckpt_workspace(r);
+  return fused > general ? fused : general;
 }
 
 WBMM_API wbmm_status wbmm_backward_ckpt(int B, int C, int H, int W, int w, int layout, int dtype,

@@ -226,9 +226,16 @@ hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, size_
 }
 
 // ---------------------------------------------------------------------------- backward
-// Any shape: the checkpoints are decoded into fp32 maps in the workspace and the fp32 backward
-// runs on them; bf16 dy and T are widened exactly and dx is rounded to bf16 once at the end.
+// w = 14 on whole images: the fused kernel of wbmm_ckptbwd.hip. Any other shape: the checkpoints
+// are decoded into fp32 maps in the workspace and the fp32 backward runs on them; bf16 dy and T are
+// widened exactly and dx is rounded to bf16 once at the end.
 namespace {
+
+bool fast_call(const BwdCkptRequest& r) {
+  const size_t es = r.bf16 ? 2 : 4;
+  return fast_ckpt_shape(r.C, r.H, r.W, r.w, r.layout) && (uintptr_t)r.dy % (4 * es) == 0 &&
+         (uintptr_t)r.dx % (2 * es) == 0 && (uintptr_t)r.xc % 4 == 0 && (uintptr_t)r.zc % 4 == 0;
+}
 
 size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -269,9 +276,12 @@ CkptWs ckpt_ws(const BwdCkptRequest& r) {
 
 bool backward_ckpt_plan_ok(const BwdCkptRequest& r) { return backward_plan_ok(fp32_request(r)); }
 
-size_t backward_ckpt_workspace(const BwdCkptRequest& r) { return ckpt_ws(r).total; }
+size_t backward_ckpt_workspace(const BwdCkptRequest& r) {
+  return fast_call(r) ? fast_ckpt_workspace(r) : ckpt_ws(r).total;
+}
 
 hipError_t launch_backward_ckpt(const BwdCkptRequest& r, hipStream_t st) {
+  if (fast_call(r)) return launch_backward_ckpt_fast(r, st);
   const CkptWs w = ckpt_ws(r);
   const size_t n = (size_t)r.B * r.C * r.H * r.W;
   unsigned char* ws = (unsigned char*)r.ws;

@@ -242,6 +242,11 @@ struct BwdCkptRequest {
   float* dmixw;
   void* ws;
 };
+// The fused kernel (w = 14, NCHW, whole square images of 14, 28 or 56): shapes, and a call's
+// alignment (dx and dy to 4 elements, codes to 4 bytes).
+bool fast_ckpt_shape(int C, int H, int W, int w, int layout);
+size_t fast_ckpt_workspace(const BwdCkptRequest& r);
+hipError_t launch_backward_ckpt_fast(const BwdCkptRequest& r, hipStream_t st);
 bool backward_ckpt_plan_ok(const BwdCkptRequest& r);
 size_t backward_ckpt_workspace(const BwdCkptRequest& r);
 hipError_t launch_backward_ckpt(const BwdCkptRequest& r, hipStream_t st);

@@ -164,6 +164,44 @@ def test_backward_ckpt(fmt, bf16, mix, B, C, H, W, w):
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("B,C,H", [(64, 2, 28), (33, 3, 56), (97, 2, 14), (8, 1, 28), (9, 1, 28),
+                                   (2, 1, 56), (3, 1, 56), (32, 1, 14), (33, 1, 14)])
+def test_backward_ckpt_whole_images(B, C, H, mix, bf16):
+    """Many units of the fused kernel, and units with one image or all but one missing."""
+    check_bwd(B, C, H, H, 14, mix, "int8", bf16, seed=H + B)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_backward_ckpt_misaligned_buffers(bf16):
+    """Buffers that the fused kernel's wide accesses cannot take go through the general kernels."""
+    B, C, H, w = 9, 3, 28, 14
+    x, z, dy, T, Wm = bwd_inputs(B, C, H, H, w, True, "int8", bf16, "NCHW", 3)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    (xc, xs), (zc, zs) = (R().wbmm_ckpt_pack(dev(a).to(dt)) for a in (x, z))
+    kw = dict(mix_w=dev(Wm), w=w, T=dev(T).to(dt))
+    want = R().wbmm_backward_ckpt((xc, xs), dev(dy).to(dt), z_ckpt=(zc, zs), **kw)
+
+    def moved(t, by=1):
+        buf = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        out = buf[by:by + t.numel()].view(t.shape)
+        out.copy_(t)
+        return out
+
+    dyd = dev(dy).to(dt)
+    for args in (dict(x_ckpt=(moved(xc), xs), dy=dyd, z_ckpt=(zc, zs)),
+                 dict(x_ckpt=(xc, moved(xs)), dy=dyd, z_ckpt=(moved(zc, 3), zs)),
+                 dict(x_ckpt=(xc, xs), dy=moved(dyd), z_ckpt=(zc, zs)),
+                 dict(x_ckpt=(xc, xs), dy=dyd, z_ckpt=(zc, zs), dx=moved(dyd))):
+        got = R().wbmm_backward_ckpt(**args, **kw)
+        assert_f32(got[1].cpu().numpy(), want[1].double().cpu().numpy(), "dT")
+        assert_f32(got[2].cpu().numpy(), want[2].double().cpu().numpy(), "dW")
+        a, b = got[0].double(), want[0].double()
+        half = 2.0 ** -8 if bf16 else 2.0 ** -22    # each side rounds once
+        assert torch.all((a - b).abs() <= 2 * half * b.abs() + 1e-5)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("mix", [False, True])
 def test_backward_ckpt_nhwc(bf16, mix):
     check_bwd(2, 12, 17, 19, 7, mix, "int8", bf16, layout="NHWC")
 
