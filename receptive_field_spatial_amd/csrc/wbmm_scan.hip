@@ -18,184 +18,161 @@ namespace {
 
 // ------------------------------------------------------------------ columns
 // CK: u is a checkpoint. Without out0 only the states (and the last one) are formed.
-template <typename T, int V, bool CK>
+template <typename T, bool CK, typename OFF>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
-  typedef typename ScanVec<T, V>::type R;
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sm[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
-  const ScanCol<V> cl(a, blockIdx.x, lane);
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanCol<T, OFF> cl(a, lane);
   const int seg = blockIdx.y, sbeg = seg * a.seg_len;
   const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
-  const T* gp = (const T*)a.g;
-  T* hp = (T*)a.out0;
+  const int tile = NW * cl.subs * K, lofs = (wv * cl.subs + cl.sub) * K;
+  const T pad = scan_narrow<T>(kScanPad);
 
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
+  float carry = 0.f;
   if (seg == 0) {
     const float* ci = a.segs > 1 ? a.carry_copy : a.carry_in;
-    if (ci) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = ci[cl.col + v];
-    }
+    if (ci) carry = ci[cl.col];
   } else {
-    for (int j = 0; j < seg; ++j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 m = a.agg[(size_t)j * a.cols + cl.col + v];
-        carry[v] = fmaf(m.x, carry[v], m.y);
-      }
+    for (int j = 0; j < seg; ++j) {
+      const float2 m = a.agg[(size_t)j * a.cols + cl.col];
+      carry = fmaf(m.x, carry, m.y);
+    }
   }
 
-  R rg[K];
-  typename ScanCol<V>::template Raw<T, CK> ru[K];
+  T rg[K];
+  ScanRaw<T, CK> ru[K];
   auto load = [&](int s) {
     if (__all(s + K <= cl.n)) {
-      size_t off = cl.start + (long long)s * cl.stride;
+      OFF o = cl.at(s);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        rg[k] = *(const R*)(gp + off);
-        ru[k].load(a, off);
-        off += cl.stride;
+      for (int k = 0; k < K; ++k, o += cl.stride) {
+        rg[k] = cl.load(a.g, o);
+        ru[k].load(a, o);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const size_t off = cl.at(s + k);
-        rg[k] = *(const R*)(gp + off);
-        ru[k].load(a, off);
+        const OFF o = cl.held(s + k);
+        const T g = cl.load(a.g, o);
+        ru[k].load(a, o);
+        rg[k] = s + k < cl.n ? g : pad;
+        if (s + k >= cl.n) ru[k].clear();
       }
     }
   };
-  load(sbeg + wv * K);
+  load(sbeg + lofs);
   int buf = 0;
-  for (int t0 = sbeg; t0 < send; t0 += NW * K, buf ^= 1) {
-    const int s = t0 + wv * K;
-    float av[K][V], bv[K][V], P[V], H[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
+  for (int t0 = sbeg; t0 < send; t0 += tile, buf ^= 1) {
+    const int s = t0 + lofs;
+    float av[K], bv[K], P = 1.f, H = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float g[V], u[V];
-      scan_unpack<V>(rg[k], g);
-      ru[k].widen(a, u);
-      const bool live = s + k < cl.n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float aa, cc;
-        scan_gate(g[v], aa, cc);
-        av[k][v] = live ? aa : 1.f;
-        bv[k][v] = live ? cc * u[v] : 0.f;
-        H[v] = fmaf(av[k][v], H[v], bv[k][v]);
-        P[v] *= av[k][v];
-      }
+      float c;
+      scan_gate(scan_widen<T>(rg[k]), av[k], c);
+      bv[k] = c * ru[k].widen(a);
+      H = fmaf(av[k], H, bv[k]);
+      P *= av[k];
     }
-    if (t0 + NW * K < send) load(s + NW * K);
-    float start[V];
+    if (t0 + tile < send) load(s + tile);
+    float start = carry;
+    if (cl.subs > 1) scan_sub_prefix(P, H, lane, cl.cw);
     if (NW > 1) {
-      float2* sb = sm + (size_t)buf * NW * 64 * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) sb[(wv * 64 + lane) * V + v] = make_float2(P[v], H[v]);
+      float2* sb = sm + buf * NW * cl.cw;
+      if (cl.sub == cl.subs - 1) sb[wv * cl.cw + cl.cl] = make_float2(P, H);
       __syncthreads();
-      for (int w = 0; w < NW; ++w)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 m = sb[(w * 64 + lane) * V + v];
-          if (w == wv) start[v] = carry[v];
-          carry[v] = fmaf(m.x, carry[v], m.y);
-        }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        start[v] = carry[v];
-        carry[v] = fmaf(P[v], carry[v], H[v]);
+      for (int w = 0; w < NW; ++w) {
+        const float2 m = sb[w * cl.cw + cl.cl];
+        if (w == wv) start = carry;
+        carry = fmaf(m.x, carry, m.y);
       }
+    } else {
+      const float p = cl.subs > 1 ? __shfl(P, 64 - cl.cw + cl.cl) : P;
+      const float h = cl.subs > 1 ? __shfl(H, 64 - cl.cw + cl.cl) : H;
+      carry = fmaf(p, carry, h);
+    }
+    if (cl.subs > 1) {
+      const float p = __shfl(P, lane - cl.cw), h = __shfl(H, lane - cl.cw);
+      start = cl.sub > 0 ? fmaf(p, start, h) : start;
     }
     if (cl.active && s < a.len) {
-      if (a.states && s % kScanChunk == 0) {
+      if (a.states && s % kScanChunk == 0) a.states[cl.kept(a, s)] = start;
+      float h = start;
+      if (a.out0) {
+        OFF o = cl.at(s);
+        if (__all(s + K <= cl.n)) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          a.states[((size_t)cl.o * a.chunks + s / kScanChunk) * a.inner + cl.i + v] = start[v];
+          for (int k = 0; k < K; ++k, o += cl.stride) {
+            h = fmaf(av[k], h, bv[k]);
+            cl.store(a.out0, o, h);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < K; ++k, o += cl.stride) {
+            h = fmaf(av[k], h, bv[k]);
+            if (s + k < cl.n) cl.store(a.out0, o, h);
+          }
+          cl.zero(a.out0, s, a.len, a.inner);
+        }
       }
-      float h[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = start[v];
-      size_t off = cl.start + (long long)s * cl.stride;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(av[k][v], h[v], bv[k][v]);
-        if (hp && s + k < cl.n) *(R*)(hp + off) = scan_pack<R, V>(h);
-        off += cl.stride;
-      }
-      if (hp && s + K > cl.n) cl.template zero<R>(hp, s, a.len, a.inner);
     }
   }
-  if (seg == a.segs - 1 && wv == 0 && cl.active && a.carry_out) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.carry_out[cl.col + v] = carry[v];
-  }
+  if (seg == a.segs - 1 && wv == 0 && cl.sub == 0 && cl.active && a.carry_out)
+    a.carry_out[cl.col] = carry;
 }
 
 // Maps of segments 0 .. segs - 2; segment 0's has the initial state folded in (P = 0).
-template <typename T, int V, bool CK>
+template <typename T, bool CK, typename OFF>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols_agg(ScanArgs a) {
-  typedef typename ScanVec<T, V>::type R;
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sm[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
-  const ScanCol<V> cl(a, blockIdx.x, lane);
-  const int seg = blockIdx.y, part = a.seg_len / NW;   // a multiple of K
-  const int sbeg = seg * a.seg_len + wv * part;
-  const T* gp = (const T*)a.g;
-  float P[V], H[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
-  for (int s = sbeg; s < sbeg + part; s += K) {
-    R rg[K];
-    typename ScanCol<V>::template Raw<T, CK> ru[K];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanCol<T, OFF> cl(a, lane);
+  const int seg = blockIdx.y, part = a.seg_len / (NW * cl.subs);   // a multiple of K
+  const int sbeg = seg * a.seg_len + (wv * cl.subs + cl.sub) * part;
+  const T pad = scan_narrow<T>(kScanPad);
+  float P = 1.f, H = 0.f;
+  for (int it = 0; it < part; it += K) {
+    const int s = sbeg + it;
+    T rg[K];
+    ScanRaw<T, CK> ru[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const size_t off = cl.at(s + k);
-      rg[k] = *(const R*)(gp + off);
-      ru[k].load(a, off);
+      const OFF o = cl.held(s + k);
+      rg[k] = cl.load(a.g, o);
+      ru[k].load(a, o);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float g[V], u[V];
-      scan_unpack<V>(rg[k], g);
-      ru[k].widen(a, u);
-      const bool live = s + k < cl.n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float aa, cc;
-        scan_gate(g[v], aa, cc);
-        H[v] = live ? fmaf(aa, H[v], cc * u[v]) : H[v];
-        P[v] = live ? P[v] * aa : P[v];
+      if (s + k >= cl.n) {
+        rg[k] = pad;
+        ru[k].clear();
       }
+      float aa, c;
+      scan_gate(scan_widen<T>(rg[k]), aa, c);
+      H = fmaf(aa, H, c * ru[k].widen(a));
+      P *= aa;
     }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sm[(wv * 64 + lane) * V + v] = make_float2(P[v], H[v]);
+  if (cl.subs > 1) scan_sub_prefix(P, H, lane, cl.cw);
+  if (cl.sub == cl.subs - 1) sm[wv * cl.cw + cl.cl] = make_float2(P, H);
   __syncthreads();
-  if (wv == 0 && cl.active) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float p = 1.f, h = 0.f;
-      for (int w = 0; w < NW; ++w) {
-        const float2 m = sm[(w * 64 + lane) * V + v];
-        h = fmaf(m.x, h, m.y);
-        p *= m.x;
-      }
-      if (seg == 0) {
-        const float c0 = a.carry_in ? a.carry_in[cl.col + v] : 0.f;
-        h = fmaf(p, c0, h);
-        p = 0.f;
-        a.carry_copy[cl.col + v] = c0;
-      }
-      a.agg[(size_t)seg * a.cols + cl.col + v] = make_float2(p, h);
+  if (wv == 0 && cl.sub == 0 && cl.active) {
+    float p = 1.f, h = 0.f;
+    for (int w = 0; w < NW; ++w) {
+      const float2 m = sm[w * cl.cw + cl.cl];
+      h = fmaf(m.x, h, m.y);
+      p *= m.x;
     }
+    if (seg == 0) {
+      const float c0 = a.carry_in ? a.carry_in[cl.col] : 0.f;
+      h = fmaf(p, c0, h);
+      p = 0.f;
+      a.carry_copy[cl.col] = c0;
+    }
+    a.agg[(size_t)seg * a.cols + cl.col] = make_float2(p, h);
   }
 }
 
@@ -207,7 +184,9 @@ template <typename T, bool REV, int LANES, bool CK, bool AGG>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
   constexpr int E = kScanE;
   __shared__ float2 sm[2][kScanWaves];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const T pad = scan_narrow<T>(kScanPad);
   const int lanes = LANES ? LANES : a.lanes, li = lane & (lanes - 1);
   uint64_t r64 = blockIdx.x;
   if (!LANES) r64 = ((uint64_t)blockIdx.x * NW + wv) * (64 / lanes) + lane / lanes;
@@ -235,7 +214,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
   }
   T rg[E];
   ScanU<T, REV, CK> ru;
-  rw.load(gp, sbeg + lofs, rg);
+  rw.load(gp, sbeg + lofs, rg, pad);
   ru.load(a, rw, rwc, sbeg + lofs);
   int buf = 0;
   for (int t0 = sbeg; t0 < send; t0 += tile, buf ^= 1) {
@@ -244,16 +223,14 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
     ru.widen(a, rw, s, bv);
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      float aa, cc;
-      scan_gate(scan_widen<T>(rg[k]), aa, cc);
-      const bool live = s + k < n;
-      av[k] = live ? aa : 1.f;
-      bv[k] = live ? cc * bv[k] : 0.f;
+      float c;
+      scan_gate(scan_widen<T>(rg[k]), av[k], c);
+      bv[k] *= c;
       H = fmaf(av[k], H, bv[k]);
       P *= av[k];
     }
     if (t0 + tile < send) {
-      rw.load(gp, s + tile, rg);
+      rw.load(gp, s + tile, rg, pad);
       ru.load(a, rw, rwc, s + tile);
     }
     scan_prefix(P, H, li, lanes);
@@ -339,17 +316,17 @@ hipError_t launch_rows(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int V, bool CK>
+template <typename T, bool CK, typename OFF>
 hipError_t launch_cols(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
-  const uint32_t groups = (uint32_t)(((uint64_t)a.cols + 64 * V - 1) / (64 * V));
-  const dim3 block(64 * p.waves);
-  const unsigned lds = p.waves * 64 * V * sizeof(float2);
+  const uint32_t groups = (a.cols + a.cw - 1) / a.cw;
+  const unsigned lds = a.cw * sizeof(float2);
   if (p.segs > 1) {
-    k_scan_cols_agg<T, V, CK><<<dim3(groups, p.segs - 1), block, lds, st>>>(a);
+    k_scan_cols_agg<T, CK, OFF><<<dim3(groups, p.segs - 1), 64 * kScanAggWaves,
+                                  kScanAggWaves * lds, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  k_scan_cols<T, V, CK><<<dim3(groups, p.segs), block, 2 * lds, st>>>(a);
+  k_scan_cols<T, CK, OFF><<<dim3(groups, p.segs), 64 * p.waves, 2 * p.waves * lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -357,10 +334,7 @@ template <typename T, bool CK>
 hipError_t launch_forward(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   if (p.rows)
     return a.reverse ? launch_rows<T, true, CK>(a, p, st) : launch_rows<T, false, CK>(a, p, st);
-  if constexpr (sizeof(T) == 2) {
-    if (p.V == 2) return launch_cols<T, 2, CK>(a, p, st);
-  }
-  return launch_cols<T, 1, CK>(a, p, st);
+  return p.wide ? launch_cols<T, CK, uint64_t>(a, p, st) : launch_cols<T, CK, uint32_t>(a, p, st);
 }
 
 }  // namespace
@@ -371,50 +345,77 @@ int scan_pow2(long long v) {  // least power of two >= v, at least 1
   return p;
 }
 
-// Launch shape. Waves per workgroup: as many as the axis has pieces for, up to kScanWaves, and
-// only as many as it takes to put kWantWaves on the chip. Where that is not reached, segments.
-ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, int V, bool backward) {
-  constexpr long long kWantWaves = 4096, kSegWaves = 1024;
-  ScanPlan p{};
-  p.V = V;
-  p.rows = inner == 1;
-  p.segs = 1;
-  const int piece = p.rows ? 64 * kScanE : kScanK;
-  long long units;   // workgroups without segments
-  if (p.rows) {
-    p.lanes = len >= 32 * kScanE + 1 ? 64 : scan_pow2((len + kScanE - 1) / kScanE);
-    if (p.lanes < 64) {
-      p.waves = 4;
-      p.seg_len = 64 * kScanE;
-      return p;
-    }
-    units = outer;
-  } else {
-    p.lanes = 64;
-    units = (outer * inner + 64 * V - 1) / (64 * V);
+// Waves of a workgroup, at most `most`, for an axis of `pieces` wave pieces: enough to put 4096
+// waves on the chip with `units` workgroups, then (down to half of that) the count whose tiles fit
+// the axis best.
+static int scan_waves(long long units, long long pieces, int least, int most) {
+  const long long want = (4096 + units - 1) / units;
+  int hi = (int)std::max<long long>(least, std::min<long long>({want, pieces, (long long)most}));
+  int best = hi;
+  double score = 0;
+  for (int n = hi; n >= std::max(least, (hi + 1) / 2); --n) {
+    const double fit = (double)pieces / (double)((pieces + n - 1) / n * n);
+    if (fit > score + 0.02) score = fit, best = n;
   }
-  const int least = !p.rows && backward ? 2 : 1;   // the backward's waves work in pairs there
-  const int most = std::max(least, std::min(kScanWaves, scan_pow2((len + piece - 1) / piece)));
-  p.waves = (int)std::min<long long>(most, std::max<long long>(least, scan_pow2((kWantWaves + units - 1) / units)));
-  const long long tile = (long long)p.waves * piece;
-  if (units * p.waves < kSegWaves) {
-    const long long tiles = (len + tile - 1) / tile;
-    long long segs = std::min<long long>({(2 * kSegWaves + units * p.waves - 1) / (units * p.waves),
-                                          (tiles + 1) / 2, 64});
-    if (segs > 1) {
-      const long long per = (tiles + segs - 1) / segs;
-      p.segs = (int)((tiles + per - 1) / per);
-      p.seg_len = (int)(per * tile);
-      return p;
-    }
-  }
-  p.seg_len = (int)((len + tile - 1) / tile * tile);
-  return p;
+  return best;
 }
 
-int scan_vec(const ScanRequest& r) {   // columns per lane of the forward
-  const uintptr_t p = (uintptr_t)r.g | (uintptr_t)r.u | (uintptr_t)r.out0;
-  return r.bf16 && r.inner % 2 == 0 && p % 4 == 0 ? 2 : 1;
+ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kind, bool ck) {
+  constexpr long long kCus = 256;
+  const int64_t cols = outer * inner;
+  const int es = bf16 ? 2 : 4;
+  ScanPlan p{};
+  p.rows = inner == 1;
+  p.segs = 1;
+  p.lanes = 64;
+  p.cw = p.run = 1;
+  p.wide = cols * len * es >= (1ll << 32);
+  long long piece, units;   // steps of a wave's tile; workgroups without segments
+  int least = 1, most = kScanWaves;
+  if (p.rows) {
+    if (len <= 32 * kScanE) {   // a row in part of a wave
+      p.lanes = scan_pow2((len + kScanE - 1) / kScanE);
+      p.waves = 4;
+      p.seg_len = 64 * kScanE;
+      p.self = true;
+      return p;
+    }
+    piece = 64 * kScanE;
+    units = outer;
+  } else {
+    // Columns per wave: 64, or down to 32 bytes of a row where that still leaves CUs without a
+    // workgroup, and no more than there are.
+    int low = scan_pow2(std::min<int64_t>(cols, 32 / es));
+    p.cw = scan_pow2(std::min<int64_t>(cols, 64));
+    while (p.cw > low && (cols + p.cw - 1) / p.cw < kCus && 64 / p.cw * kScanK < len) p.cw /= 2;
+    p.run = std::max(1, 128 / (p.cw * es));
+    piece = (64 / p.cw) * kScanK;
+    units = (cols + p.cw - 1) / p.cw;
+    if (kind) most = scan_bwd_waves(ck || p.wide);
+    if (kind && p.cw == 64) least = 2;   // waves pair up for the kept states
+  }
+  const long long pieces = (len + piece - 1) / piece;
+  p.waves = scan_waves(units, pieces, least, most);
+  // one tile: a short axis costs a barrier less, and a backward without states no second run
+  if (pieces <= 2 || (kind == 2 && pieces <= most)) p.waves = (int)std::max<long long>(least, pieces);
+  if (least == 2) p.waves += p.waves & 1;
+  p.self = pieces <= p.waves;
+  if (units < kCus * 3 / 4) {
+    // segments of whole kScanAggWaves pieces, which the tiles of 8 or 16 waves divide
+    const long long step = kScanAggWaves * piece, steps = (len + step - 1) / step;
+    const long long segs = std::min<long long>({(kCus + units - 1) / units, steps, 64});
+    if (segs > 1) {
+      const long long per = (steps + segs - 1) / segs;
+      p.segs = (int)((steps + per - 1) / per);
+      p.seg_len = (int)(per * step);
+      p.waves = p.rows || !kind ? 16 : 8;
+      p.self = false;
+      return p;
+    }
+  }
+  const long long tile = p.waves * piece;
+  p.seg_len = (int)((len + tile - 1) / tile * tile);
+  return p;
 }
 
 namespace {
@@ -422,19 +423,25 @@ size_t maps_bytes(const ScanPlan& p, size_t cols) { return p.segs > 1 ? cols * (
 }  // namespace
 
 size_t scan_workspace(int64_t outer, int64_t len, int64_t inner) {
-  // the type and the alignment are not arguments: the larger need
+  // the type is not an argument: the larger need
   const size_t cols = (size_t)(outer * inner);
-  return std::max(maps_bytes(scan_plan(outer, len, inner, 1, false), cols),
-                  maps_bytes(scan_plan(outer, len, inner, 2, false), cols));
+  return std::max(maps_bytes(scan_plan(outer, len, inner, false, 0, false), cols),
+                  maps_bytes(scan_plan(outer, len, inner, true, 0, false), cols));
 }
 
 size_t scan_backward_workspace(int64_t outer, int64_t len, int64_t inner, bool has_states) {
   const size_t cols = (size_t)(outer * inner);
-  const size_t maps = maps_bytes(scan_plan(outer, len, inner, 1, true), cols);
-  if (has_states) return maps;
-  // states (whole 16 bytes), then the maps of either launch
-  const size_t kept = cols * ((len + kScanChunk - 1) / kScanChunk) * 4;
-  return (kept + 15) / 16 * 16 + std::max(maps, scan_workspace(outer, len, inner));
+  size_t need = 0;
+  for (int b = 0; b < 4; ++b) {   // the types of g and u are not arguments: the largest need
+    const ScanPlan p = scan_plan(outer, len, inner, b & 1, has_states ? 1 : 2, b & 2);
+    size_t n = maps_bytes(p, cols);
+    if (!has_states && !p.self) {   // states (whole 16 bytes), then the maps of either launch
+      const size_t kept = cols * ((len + kScanChunk - 1) / kScanChunk) * 4;
+      n = (kept + 15) / 16 * 16 + std::max(n, scan_workspace(outer, len, inner));
+    }
+    need = std::max(need, n);
+  }
+  return need;
 }
 
 ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p) {
@@ -445,6 +452,7 @@ ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p) {
   a.fmt = r.fmt;
   a.dh = r.dh;
   a.carry_in = r.carry_in;
+  a.h0 = r.h0;
   a.lens = r.lens;
   a.out0 = r.out0;
   a.out1 = r.out1;
@@ -459,14 +467,15 @@ ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p) {
   a.segs = p.segs;
   a.seg_len = p.seg_len;
   a.lanes = p.lanes;
+  a.cw = p.cw;
+  a.run = p.run;
   a.agg = (float2*)r.ws;
   a.carry_copy = r.ws ? (float*)r.ws + (size_t)2 * p.segs * a.cols : nullptr;
   return a;
 }
 
 hipError_t launch_scan_forward(const ScanRequest& r, hipStream_t st) {
-  const int V = scan_vec(r);
-  const ScanPlan p = scan_plan(r.outer, r.len, r.inner, V, false);
+  const ScanPlan p = scan_plan(r.outer, r.len, r.inner, r.bf16, 0, r.us != nullptr);
   const ScanArgs a = scan_args(r, p);
   if (r.len == 1 && r.out0) {
     const dim3 grid((unsigned)(((uint64_t)a.cols + kThreads - 1) / kThreads));

@@ -13,8 +13,8 @@
 // States, gates, products and sums are fp32 whatever the tensors' type.
 //
 // Scan order: step s of a sequence of n steps is position s, or n - 1 - s when reversed; positions
-// n .. len - 1 (padding) are never used: inside the kernels they are the identity map (a = 1,
-// b = 0), and outputs there are zero.
+// n .. len - 1 (padding) are never used: in their place the kernels take g = kScanPad and zeros,
+// the identity map (a = 1, b = 0), and outputs there are zero.
 #pragma once
 
 #include "wbmm_ckpt.hpp"
@@ -23,9 +23,14 @@
 namespace wbmm {
 
 constexpr int kScanChunk = 32;    // steps between two kept states
-constexpr int kScanK = 16;        // steps per wave and tile of the column kernels
+constexpr int kScanK = 16;        // steps per lane and tile of the column kernels
 constexpr int kScanE = 8;         // steps per lane and tile of the row kernels
-constexpr int kScanWaves = 8;     // waves of a workgroup at most
+constexpr int kScanWaves = 16;    // waves of a workgroup at most
+// The same for the columns' backward: 3 waves per SIMD, 2 where a checkpoint or 64-bit offsets take
+// more registers.
+constexpr int scan_bwd_waves(bool more) { return more ? 8 : 12; }
+constexpr int kScanAggWaves = 16; // waves of a workgroup that forms a segment's map
+constexpr float kScanPad = 100.f; // a gate that leaves the state alone (a = 1 exactly)
 
 struct ScanArgs {
   const void* g;
@@ -33,6 +38,7 @@ struct ScanArgs {
   const uint8_t* us;
   const void* dh;
   const float* carry_in;      // h0 (forward), dh_last (backward), or null
+  const float* h0;            // backward without states: the initial state, or null
   const int* lens;            // or null
   void* out0;                 // h, or dg (backward)
   void* out1;                 // du (backward)
@@ -44,6 +50,8 @@ struct ScanArgs {
   uint32_t inner, cols, rows_per_len;   // cols = outer * inner; lens[outer index / rows_per_len]
   int segs, seg_len;          // seg_len: a multiple of the workgroup's tile
   int lanes;                  // row kernels: lanes per row (64: the workgroup's waves share a row)
+  int cw;                     // column kernels: columns of a wave
+  int run;                    // column kernels: neighbour groups that share memory lines
 };
 
 // a = sigmoid(g) and c = 1 - a = sigmoid(-g), each with its own relative accuracy (c from 1 - a
@@ -173,87 +181,104 @@ __device__ __forceinline__ int scan_steps(const ScanArgs& a, uint32_t seq) {
 }
 
 // ------------------------------------------------------------------ column kernels (inner > 1)
-// One lane owns V neighbouring columns; a wave takes kScanK steps of 64 V columns per tile.
-template <typename T, int V>
-struct ScanVec;
-template <> struct ScanVec<float, 1> { typedef float type; };
-template <> struct ScanVec<uint16_t, 1> { typedef uint16_t type; };
-template <> struct ScanVec<uint16_t, 2> { typedef uint32_t type; };
-
-template <int V>
-__device__ __forceinline__ void scan_unpack(float r, float (&v)[V]) { v[0] = r; }
-template <int V>
-__device__ __forceinline__ void scan_unpack(uint16_t r, float (&v)[V]) { v[0] = bf2f(r); }
-template <int V>
-__device__ __forceinline__ void scan_unpack(uint32_t r, float (&v)[V]) {
-  v[0] = __uint_as_float(r << 16);
-  v[V - 1] = __uint_as_float(r & 0xffff0000u);
-}
-template <typename R, int V>
-__device__ __forceinline__ R scan_pack(const float (&v)[V]) {
-  if constexpr (sizeof(R) == 4 && V == 2)
-    return (uint32_t)scan_narrow<uint16_t>(v[0]) | ((uint32_t)scan_narrow<uint16_t>(v[1]) << 16);
-  else
-    return scan_narrow<R>(v[0]);
-}
-
-template <int V>
+// A wave takes cw neighbouring columns (a power of two) and 64 / cw consecutive pieces of kScanK
+// steps: fewer columns per wave make more workgroups of few columns, without cutting the axis.
+// Addresses are a uniform base plus a byte offset of type OFF: 32 bits where a tensor has less than
+// 4 GiB (one add per step, shared by the tensors), else 64.
+template <typename T, typename OFF>
 struct ScanCol {
-  uint32_t col, o, i;   // first column, its sequence and place in the row
+  int cw, subs, sub, cl;      // columns and pieces per wave, the lane's piece and column
+  uint32_t col, o, i;         // the lane's column, its sequence and place in the row
   bool active;
-  int n;                // steps of its sequence
-  size_t base;          // element offset of position 0
-  size_t start;         // element offset of step 0
-  long long stride;     // elements from step s to step s + 1
-  __device__ __forceinline__ ScanCol(const ScanArgs& a, uint32_t group, int lane) {
-    const uint64_t c = ((uint64_t)group * 64 + lane) * V;
+  int n;                      // steps of its sequence
+  OFF base, start, stride;    // byte offsets of position 0 and step 0, bytes from step to step
+  __device__ __forceinline__ ScanCol(const ScanArgs& a, int lane) {
+    cw = a.cw;
+    subs = 64 / cw;
+    sub = lane / cw;
+    cl = lane & (cw - 1);
+    // workgroups go round the XCDs: a run of groups that share memory lines stays on one
+    uint32_t group = blockIdx.x;
+    const uint32_t whole = gridDim.x / (8 * a.run) * (8 * a.run);
+    if (group < whole) {
+      const uint32_t x = group % 8, k = group / 8;
+      group = (k / a.run * 8 + x) * a.run + k % a.run;
+    }
+    const uint64_t c = (uint64_t)group * cw + cl;
     active = c < a.cols;
-    col = active ? (uint32_t)c : a.cols - V;
+    col = active ? (uint32_t)c : a.cols - 1;
     o = col / a.inner;
     i = col - o * a.inner;
     n = scan_steps(a, o);
-    base = (size_t)o * a.len * a.inner + i;
-    stride = a.reverse ? -(long long)a.inner : (long long)a.inner;
-    start = a.reverse && n > 0 ? base + (size_t)(n - 1) * a.inner : base;
+    const OFF row = (OFF)a.inner * sizeof(T);
+    base = (OFF)o * a.len * row + (OFF)i * sizeof(T);
+    start = a.reverse && n > 0 ? base + (OFF)(n - 1) * row : base;
+    stride = a.reverse ? (OFF)0 - row : row;
   }
-  // V elements of a map or checkpoint at offset o, as fp32
-  template <typename T, bool CK>
-  struct Raw {
-    typedef typename ScanVec<T, V>::type R;
-    R r;
-    uint16_t code, scale;
-    __device__ __forceinline__ void load(const ScanArgs& a, size_t o) {
-      if constexpr (CK) {
-        const uint8_t* p = (const uint8_t*)a.u + o;
-        code = V == 2 ? *(const uint16_t*)p : *p;
-        scale = a.us[o / kCkptGroup];   // V elements from an even one share a group
-      } else {
-        r = *(const R*)((const T*)a.u + o);
-      }
-    }
-    __device__ __forceinline__ void widen(const ScanArgs& a, float (&v)[V]) const {
-      if constexpr (CK) {
-        const float f = ckpt_factor(scale);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = ckpt_decode1((code >> (8 * j)) & 0xffu, a.fmt) * f;
-      } else {
-        scan_unpack<V>(r, v);
-      }
-    }
-  };
-  // element offset of step s, held to the sequence's own steps (position 0 of an empty one)
-  __device__ __forceinline__ size_t at(int s) const {
+  __device__ __forceinline__ OFF at(int s) const { return start + (OFF)s * stride; }
+  // the same held to the sequence's own steps (position 0 of an empty one)
+  __device__ __forceinline__ OFF held(int s) const {
     s = s < n ? s : n - 1;
-    s = s > 0 ? s : 0;
-    return start + (long long)s * stride;
+    return at(s > 0 ? s : 0);
   }
-  // zeros at the positions from step s's tile on that lie past the end of the sequence
-  template <typename R, typename T>
-  __device__ __forceinline__ void zero(T* p, int s, int len, uint32_t inner) const {
+  __device__ __forceinline__ T load(const void* p, OFF o) const {
+    return *(const T*)((const char*)p + o);
+  }
+  __device__ __forceinline__ void store(void* p, OFF o, float v) const {
+    *(T*)((char*)p + o) = scan_narrow<T>(v);
+  }
+  // zeros at the positions of steps s .. s + kScanK - 1 that lie past the end of the sequence
+  __device__ __forceinline__ void zero(void* p, int s, int len, uint32_t inner) const {
     for (int k = 0; k < kScanK; ++k)
-      if (s + k >= n && s + k < len) *(R*)(p + base + (size_t)(s + k) * inner) = R(0);
+      if (s + k >= n && s + k < len) store(p, base + (OFF)(s + k) * inner * sizeof(T), 0.f);
+  }
+  // index of the kept state before step s
+  __device__ __forceinline__ size_t kept(const ScanArgs& a, int s) const {
+    return ((size_t)o * a.chunks + s / kScanChunk) * a.inner + i;
   }
 };
+
+// One element of u: of a map, or of a checkpoint.
+template <typename T, bool CK>
+struct ScanRaw {
+  T r;
+  uint8_t code, scale;
+  template <typename OFF>
+  __device__ __forceinline__ void load(const ScanArgs& a, OFF o) {
+    if constexpr (CK) {
+      const OFF e = o / sizeof(T);
+      code = *((const uint8_t*)a.u + e);
+      scale = *(a.us + e / kCkptGroup);
+    } else {
+      r = *(const T*)((const char*)a.u + o);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    r = T(0);
+    code = 0;
+    scale = 127;
+  }
+  __device__ __forceinline__ float widen(const ScanArgs& a) const {
+    if constexpr (CK) return ckpt_decode1(code, a.fmt) * ckpt_factor(scale);
+    else return scan_widen<T>(r);
+  }
+};
+
+// Composition over a wave's pieces (lanes cw apart): inclusive prefix, or suffix.
+__device__ __forceinline__ void scan_sub_prefix(float& P, float& H, int lane, int cw) {
+  for (int d = cw; d < 64; d *= 2) {
+    const float ps = __shfl(P, lane - d), hs = __shfl(H, lane - d);
+    H = lane >= d ? fmaf(P, hs, H) : H;
+    P = lane >= d ? P * ps : P;
+  }
+}
+__device__ __forceinline__ void scan_sub_suffix(float& P, float& R, int lane, int cw) {
+  for (int d = cw; d < 64; d *= 2) {
+    const float ps = __shfl(P, lane + d), rs = __shfl(R, lane + d);
+    R = lane + d < 64 ? fmaf(P, rs, R) : R;
+    P = lane + d < 64 ? P * ps : P;
+  }
+}
 
 // ------------------------------------------------------------------ row kernels (inner = 1)
 // kScanE consecutive steps of a row, in scan order; rows start at any element, so the wide
@@ -267,8 +292,8 @@ struct ScanRow {
   __device__ __forceinline__ ScanRow(uint32_t row, int len_, int n_)
       : base((size_t)row * len_), len(len_), n(n_) {}
   __device__ __forceinline__ size_t at(int s) const { return base + (REV ? n - 1 - s : s); }
-  // steps past the end of the sequence come back as zeros
-  __device__ __forceinline__ void load(const T* __restrict__ p, int s, T (&v)[E]) const {
+  // steps past the end of the sequence come back as `pad`
+  __device__ __forceinline__ void load(const T* __restrict__ p, int s, T (&v)[E], T pad) const {
     if (s + E <= n) {
       Wide w;
       __builtin_memcpy(&w, p + at(REV ? s + E - 1 : s), sizeof(w));
@@ -277,7 +302,7 @@ struct ScanRow {
     } else {
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        v[k] = T(0);
+        v[k] = pad;
         if (s + k < n) v[k] = p[at(s + k)];
       }
     }
@@ -307,18 +332,18 @@ struct ScanU {
   T r[CK ? 1 : E];
   uint8_t code[CK ? E : 1];
   uint32_t s0, s1;
-  __device__ __forceinline__ ScanU() : s0(0), s1(0) {}
   __device__ __forceinline__ void load(const ScanArgs& a, const ScanRow<T, REV>& rw,
                                        const ScanRow<uint8_t, REV>& rwc, int s) {
     if constexpr (CK) {
-      rwc.load((const uint8_t*)a.u, s, code);
+      rwc.load((const uint8_t*)a.u, s, code, 0);
+      s0 = s1 = 127;
       if (s < rw.n) {   // the scales of the lane's first and last step
         const int last = s + E <= rw.n ? s + E - 1 : rw.n - 1;
         s0 = a.us[rw.at(s) / kCkptGroup];
         s1 = a.us[rw.at(last) / kCkptGroup];
       }
     } else {
-      rw.load((const T*)a.u, s, r);
+      rw.load((const T*)a.u, s, r, T(0));
     }
   }
   __device__ __forceinline__ void widen(const ScanArgs& a, const ScanRow<T, REV>& rw, int s,
@@ -357,11 +382,12 @@ struct ScanRequest {
   void* ws;
 };
 struct ScanPlan {
-  bool rows;
-  int V, lanes, waves, segs, seg_len;
+  bool rows, wide;      // rows: inner = 1; wide: 64-bit offsets (column kernels)
+  bool self;            // backward: one tile holds the axis, no states needed
+  int cw, run, lanes, waves, segs, seg_len;
 };
-ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, int V, bool backward);
-int scan_vec(const ScanRequest& r);
+// kind: 0 = forward, 1 = backward from kept states, 2 = backward without; ck: u is a checkpoint.
+ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kind, bool ck);
 ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p);
 // Device workspace of a call (16-byte aligned), 0 when none: the segments' maps, and the states of
 // a backward that gets none.

@@ -8,226 +8,231 @@
 // as the affine maps of wbmm_scan.hpp. One pass: g, u, dh read, dg, du written.
 #include "wbmm_scan.hpp"
 
+#include <type_traits>
+
 namespace wbmm {
 
 namespace {
 
-struct SegMap {
+// A run of steps: h -> p h + h of the state, r -> p r + r of its gradient.
+struct RunMap {
   float p, r, h;
 };
 
 // ------------------------------------------------------------------ columns
-// A wave's tile is half the distance between two states: the wave of an odd half gets its state
-// from the wave before it, beside the maps that are exchanged anyway, so waves come in pairs.
-// CK: u is a checkpoint.
-template <typename T, int V, bool CK>
-__global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols_bwd(ScanArgs a) {
-  typedef typename ScanVec<T, V>::type R;
+// As k_scan_cols. A lane's piece is half the distance between two kept states: the odd half's state
+// is where the even half before it ends, one piece back in the wave, or in the wave before (then
+// waves come in pairs). CK: u is a checkpoint. SELF: one tile holds the axis and no state is kept:
+// the pieces' maps of the state are exchanged beside those of its gradient, from h0 (a.h0).
+template <typename T, bool CK, bool SELF, typename OFF>
+__global__ void __launch_bounds__(64 * scan_bwd_waves(CK || sizeof(OFF) == 8))
+k_scan_cols_bwd(ScanArgs a) {
   constexpr int K = kScanK;
-  static_assert(kScanChunk == 2 * K, "two tiles between states");
-  extern __shared__ __attribute__((aligned(16))) SegMap smb[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
-  const ScanCol<V> cl(a, blockIdx.x, lane);
+  static_assert(kScanChunk == 2 * K, "two pieces between states");
+  extern __shared__ __attribute__((aligned(16))) RunMap smb[];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanCol<T, OFF> cl(a, lane);
   const int seg = blockIdx.y, sbeg = seg * a.seg_len;
   const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
-  const T* gp = (const T*)a.g;
-  const T* dp = (const T*)a.dh;
-  T* dgp = (T*)a.out0;
-  T* dup = (T*)a.out1;
+  const int tile = NW * cl.subs * K, lofs = (wv * cl.subs + cl.sub) * K;
+  const T pad = scan_narrow<T>(kScanPad);
+  const bool odd = cl.subs > 1 ? cl.sub & 1 : wv & 1;
 
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
+  float carry = 0.f;
   if (seg == a.segs - 1) {
-    if (a.carry_in) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = a.carry_in[cl.col + v];
-    }
+    if (a.carry_in) carry = a.carry_in[cl.col];
   } else {
-    for (int j = a.segs - 1; j > seg; --j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 m = a.agg[(size_t)j * a.cols + cl.col + v];
-        carry[v] = fmaf(m.x, carry[v], m.y);
-      }
+    for (int j = a.segs - 1; j > seg; --j) {
+      const float2 m = a.agg[(size_t)j * a.cols + cl.col];
+      carry = fmaf(m.x, carry, m.y);
+    }
   }
 
-  R rg[K], rd[K];
-  typename ScanCol<V>::template Raw<T, CK> ru[K];
+  T rg[K], rd[K];
+  ScanRaw<T, CK> ru[K];
+  float rst = 0.f;
   auto load = [&](int s) {
-    const bool full = __all(s + K <= cl.n);
-    size_t off = cl.start + (long long)s * cl.stride;
+    if (!SELF && !odd && s < a.len) rst = a.states[cl.kept(a, s)];
+    if (__all(s + K <= cl.n)) {
+      OFF o = cl.at(s);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const size_t o = full ? off : cl.at(s + k);
-      rg[k] = *(const R*)(gp + o);
-      rd[k] = *(const R*)(dp + o);
-      ru[k].load(a, o);
-      off += cl.stride;
+      for (int k = 0; k < K; ++k, o += cl.stride) {
+        rg[k] = cl.load(a.g, o);
+        rd[k] = cl.load(a.dh, o);
+        ru[k].load(a, o);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const OFF o = cl.held(s + k);
+        const T g = cl.load(a.g, o), d = cl.load(a.dh, o);
+        ru[k].load(a, o);
+        const bool live = s + k < cl.n;
+        rg[k] = live ? g : pad;
+        rd[k] = live ? d : T(0);
+        if (!live) ru[k].clear();
+      }
     }
   };
-  const int tile = NW * K;
   int t0 = sbeg + (send - sbeg - 1) / tile * tile;
-  load(t0 + wv * K);
+  load(t0 + lofs);
   for (int buf = 0; t0 >= sbeg; t0 -= tile, buf ^= 1) {
-    const int s = t0 + wv * K;
-    float av[K][V], cv[K][V], ev[K][V], dv[K][V], P[V], Rl[V], h[V];
-    const bool even = (wv & 1) == 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      P[v] = 1.f;
-      Rl[v] = 0.f;
-      h[v] = 0.f;
-      if (even && s < a.len)
-        h[v] = a.states[((size_t)cl.o * a.chunks + s / kScanChunk) * a.inner + cl.i + v];
-    }
+    const int s = t0 + lofs;
+    // ev: u, later the gradient of g up to the factor G
+    float av[K], cv[K], ev[K], dv[K], P = 1.f, Rl = 0.f, H = 0.f, h = rst;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float g[V], d[V];
-      scan_unpack<V>(rg[k], g);
-      scan_unpack<V>(rd[k], d);
-      ru[k].widen(a, ev[k]);   // u for now
-      const bool live = s + k < cl.n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float aa, cc;
-        scan_gate(g[v], aa, cc);
-        av[k][v] = live ? aa : 1.f;
-        cv[k][v] = live ? cc : 0.f;
-        dv[k][v] = live ? d[v] : 0.f;
-        ev[k][v] = live ? ev[k][v] : 0.f;
-        P[v] *= av[k][v];
-      }
+      scan_gate(scan_widen<T>(rg[k]), av[k], cv[k]);
+      ev[k] = ru[k].widen(a);
+      dv[k] = scan_widen<T>(rd[k]);
+      P *= av[k];
+      H = fmaf(av[k], H, cv[k] * ev[k]);
     }
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) Rl[v] = av[k][v] * (dv[k][v] + Rl[v]);
-    // the gradient of g up to the factor G; the state runs along
-    auto run = [&]() {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float u = ev[k][v];
-          ev[k][v] = av[k][v] * cv[k][v] * (h[v] - u);
-          h[v] = fmaf(av[k][v], h[v], cv[k][v] * u);
-        }
-    };
-    if (even) run();
+    for (int k = K - 1; k >= 0; --k) Rl = av[k] * (dv[k] + Rl);
     if (t0 - tile >= sbeg) load(s - tile);
-    SegMap* sb = smb + (size_t)buf * NW * 64 * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) sb[(wv * 64 + lane) * V + v] = SegMap{P[v], Rl[v], h[v]};
-    __syncthreads();
-    float Rt[V];
-    for (int w = NW - 1; w >= 0; --w)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const SegMap m = sb[(w * 64 + lane) * V + v];
-        if (w == wv) Rt[v] = carry[v];
-        if (w == wv - 1 && !even) h[v] = m.h;
-        carry[v] = fmaf(m.p, carry[v], m.r);
+    float ph = P, hend = SELF ? H : fmaf(P, h, H);   // the state's map, or where the piece ends
+    if (cl.subs > 1) {
+      if constexpr (SELF) {
+        scan_sub_prefix(ph, hend, lane, cl.cw);
+      } else {
+        const float b = __shfl(hend, lane - cl.cw);
+        h = odd ? b : h;
       }
-    if (!even) run();
+      scan_sub_suffix(P, Rl, lane, cl.cw);
+    }
+    // exchange: gradient maps of whole waves (their first piece has it), state maps or ends of
+    // their last piece
+    float Rt = carry, hw = SELF && a.h0 ? a.h0[cl.col] : 0.f, hs = hw;
+    if (NW > 1) {
+      RunMap* sb = smb + buf * NW * cl.cw;
+      if (cl.subs == 1) {
+        sb[wv * 64 + lane] = RunMap{P, Rl, hend};
+      } else {
+        if (cl.sub == 0) sb[wv * cl.cw + cl.cl].p = P, sb[wv * cl.cw + cl.cl].r = Rl;
+        if (SELF && cl.sub == cl.subs - 1) sb[wv * cl.cw + cl.cl].h = hend;
+      }
+      __syncthreads();
+      for (int w = NW - 1; w >= 0; --w) {
+        const RunMap m = sb[w * cl.cw + cl.cl];
+        if (w == wv) Rt = carry;
+        if (!SELF && cl.subs == 1 && odd && w == wv - 1) h = m.h;
+        carry = fmaf(m.p, carry, m.r);
+      }
+      if constexpr (SELF) {
+        for (int w = 0; w < wv; ++w) {
+          const RunMap m = sb[w * cl.cw + cl.cl];
+          hs = fmaf(m.p, hs, m.h);
+        }
+      }
+    } else {
+      const float p = cl.subs > 1 ? __shfl(P, cl.cl) : P, r = cl.subs > 1 ? __shfl(Rl, cl.cl) : Rl;
+      carry = fmaf(p, carry, r);
+    }
+    if (cl.subs > 1) {
+      const float p = __shfl(P, lane + cl.cw), r = __shfl(Rl, lane + cl.cw);
+      Rt = cl.sub + 1 < cl.subs ? fmaf(p, Rt, r) : Rt;
+      if constexpr (SELF) {
+        const float pe = __shfl(ph, lane - cl.cw), he = __shfl(hend, lane - cl.cw);
+        hs = cl.sub > 0 ? fmaf(pe, hs, he) : hs;
+      }
+    }
+    if constexpr (SELF) h = hs;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float u = ev[k];
+      ev[k] = av[k] * cv[k] * (h - u);
+      h = fmaf(av[k], h, cv[k] * u);
+    }
     if (cl.active && s < a.len) {
-      size_t off = cl.start + (long long)(s + K - 1) * cl.stride;
+      OFF o = cl.at(s + K - 1);
+      if (__all(s + K <= cl.n)) {
 #pragma unroll
-      for (int k = K - 1; k >= 0; --k) {
-        float dg[V], du[V];
+        for (int k = K - 1; k >= 0; --k, o -= cl.stride) {
+          const float Gt = dv[k] + Rt;
+          Rt = av[k] * Gt;
+          cl.store(a.out0, o, ev[k] * Gt);
+          cl.store(a.out1, o, cv[k] * Gt);
+        }
+      } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float G = dv[k][v] + Rt[v];
-          dg[v] = ev[k][v] * G;
-          du[v] = cv[k][v] * G;
-          Rt[v] = av[k][v] * G;
+        for (int k = K - 1; k >= 0; --k, o -= cl.stride) {
+          const float Gt = dv[k] + Rt;
+          Rt = av[k] * Gt;
+          if (s + k < cl.n) {
+            cl.store(a.out0, o, ev[k] * Gt);
+            cl.store(a.out1, o, cv[k] * Gt);
+          }
         }
-        if (s + k < cl.n) {
-          *(R*)(dgp + off) = scan_pack<R, V>(dg);
-          *(R*)(dup + off) = scan_pack<R, V>(du);
-        }
-        off -= cl.stride;
-      }
-      if (s + K > cl.n) {
-        cl.template zero<R>(dgp, s, a.len, a.inner);
-        cl.template zero<R>(dup, s, a.len, a.inner);
+        cl.zero(a.out0, s, a.len, a.inner);
+        cl.zero(a.out1, s, a.len, a.inner);
       }
     }
   }
-  if (seg == 0 && wv == 0 && cl.active && a.carry_out) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.carry_out[cl.col + v] = carry[v];
-  }
+  if (seg == 0 && wv == 0 && cl.sub == 0 && cl.active && a.carry_out) a.carry_out[cl.col] = carry;
 }
 
 // Maps of segments 1 .. segs - 1 (blockIdx.y + 1); the last one's has dh_last folded in (P = 0).
-template <typename T, int V>
-__global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols_bwd_agg(ScanArgs a) {
-  typedef typename ScanVec<T, V>::type R;
+template <typename T, typename OFF>
+__global__ void __launch_bounds__(64 * kScanAggWaves) k_scan_cols_bwd_agg(ScanArgs a) {
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sma[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
-  const ScanCol<V> cl(a, blockIdx.x, lane);
-  const int seg = blockIdx.y + 1, part = a.seg_len / NW;   // a multiple of K
-  const int sbeg = seg * a.seg_len + wv * part;
-  const T* gp = (const T*)a.g;
-  const T* dp = (const T*)a.dh;
-  float P[V], Rl[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) P[v] = 1.f, Rl[v] = 0.f;
-  for (int s = sbeg + part - K; s >= sbeg; s -= K) {
-    R rg[K], rd[K];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanCol<T, OFF> cl(a, lane);
+  const int seg = blockIdx.y + 1, part = a.seg_len / (NW * cl.subs);   // a multiple of K
+  const int sbeg = seg * a.seg_len + (wv * cl.subs + cl.sub) * part;
+  const T pad = scan_narrow<T>(kScanPad);
+  float P = 1.f, Rl = 0.f;
+  for (int it = part - K; it >= 0; it -= K) {
+    const int s = sbeg + it;
+    T rg[K], rd[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const size_t off = cl.at(s + k);
-      rg[k] = *(const R*)(gp + off);
-      rd[k] = *(const R*)(dp + off);
+      const OFF o = cl.held(s + k);
+      rg[k] = cl.load(a.g, o);
+      rd[k] = cl.load(a.dh, o);
     }
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-      float g[V], d[V];
-      scan_unpack<V>(rg[k], g);
-      scan_unpack<V>(rd[k], d);
       const bool live = s + k < cl.n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float aa, cc;
-        scan_gate(g[v], aa, cc);
-        Rl[v] = live ? aa * (d[v] + Rl[v]) : Rl[v];
-        P[v] = live ? P[v] * aa : P[v];
-      }
+      float aa, c;
+      scan_gate(scan_widen<T>(live ? rg[k] : pad), aa, c);
+      Rl = aa * (scan_widen<T>(live ? rd[k] : T(0)) + Rl);
+      P *= aa;
     }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sma[(wv * 64 + lane) * V + v] = make_float2(P[v], Rl[v]);
+  if (cl.subs > 1) scan_sub_suffix(P, Rl, lane, cl.cw);
+  if (cl.sub == 0) sma[wv * cl.cw + cl.cl] = make_float2(P, Rl);
   __syncthreads();
-  if (wv == 0 && cl.active) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float p = 1.f, r = 0.f;
-      for (int w = NW - 1; w >= 0; --w) {
-        const float2 m = sma[(w * 64 + lane) * V + v];
-        r = fmaf(m.x, r, m.y);
-        p *= m.x;
-      }
-      if (seg == a.segs - 1) {
-        r = fmaf(p, a.carry_in ? a.carry_in[cl.col + v] : 0.f, r);
-        p = 0.f;
-      }
-      a.agg[(size_t)seg * a.cols + cl.col + v] = make_float2(p, r);
+  if (wv == 0 && cl.sub == 0 && cl.active) {
+    float p = 1.f, r = 0.f;
+    for (int w = NW - 1; w >= 0; --w) {
+      const float2 m = sma[w * cl.cw + cl.cl];
+      r = fmaf(m.x, r, m.y);
+      p *= m.x;
     }
+    if (seg == a.segs - 1) {
+      r = fmaf(p, a.carry_in ? a.carry_in[cl.col] : 0.f, r);
+      p = 0.f;
+    }
+    a.agg[(size_t)seg * a.cols + cl.col] = make_float2(p, r);
   }
 }
 
 // ------------------------------------------------------------------ rows
 // As k_scan_rows. A lane's state follows from the kept one of its 32 steps through the maps of
-// the (up to three) lanes before it. CK: u is a checkpoint. AGG: maps of segments 1 .. segs - 1.
-template <typename T, bool REV, int LANES, bool CK, bool AGG>
+// the (up to three) lanes before it, or (SELF: one tile holds the row) from h0 through the maps of
+// all lanes before it. CK: u is a checkpoint. AGG: maps of segments 1 .. segs - 1.
+template <typename T, bool REV, int LANES, bool CK, bool SELF, bool AGG>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   constexpr int E = kScanE;
   static_assert(kScanChunk == 4 * E, "four lanes between states");
-  __shared__ float2 sm[2][kScanWaves];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, NW = blockDim.x >> 6;
+  __shared__ RunMap sm[2][kScanWaves];
+  const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const T pad = scan_narrow<T>(kScanPad);
   const int lanes = LANES ? LANES : a.lanes, li = lane & (lanes - 1);
   uint64_t r64 = blockIdx.x;
   if (!LANES) r64 = ((uint64_t)blockIdx.x * NW + wv) * (64 / lanes) + lane / lanes;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   const T* gp = (const T*)a.g;
   const T* dp = (const T*)a.dh;
 
-  float carry = 0.f, carryP = 1.f;
+  float carry = 0.f, carryP = 1.f, h0 = SELF && a.h0 ? a.h0[row] : 0.f;
   if (seg == a.segs - 1) {
     carry = a.carry_in ? a.carry_in[row] : 0.f;
   } else if (!AGG) {
@@ -256,11 +261,11 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   ScanU<T, REV, CK> ru;
   float kept = 0.f;
   auto load = [&](int s) {
-    rw.load(gp, s, rg);
-    rw.load(dp, s, rd);
+    rw.load(gp, s, rg, pad);
+    rw.load(dp, s, rd, T(0));
     if constexpr (!AGG) {
       ru.load(a, rw, rwc, s);
-      if (s < a.len) kept = a.states[(size_t)row * a.chunks + s / kScanChunk];
+      if (!SELF && s < a.len) kept = a.states[(size_t)row * a.chunks + s / kScanChunk];
     }
   };
   int t0 = sbeg + (send - sbeg - 1) / tile * tile;
@@ -271,24 +276,19 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
     if constexpr (!AGG) ru.widen(a, rw, s, ev);   // u for now
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      float aa, cc;
-      scan_gate(scan_widen<T>(rg[k]), aa, cc);
-      const bool live = s + k < n;
-      av[k] = live ? aa : 1.f;
-      cv[k] = live ? cc : 0.f;
-      dv[k] = live ? scan_widen<T>(rd[k]) : 0.f;
+      scan_gate(scan_widen<T>(rg[k]), av[k], cv[k]);
+      dv[k] = scan_widen<T>(rd[k]);
       P *= av[k];
-      if constexpr (!AGG) {
-        ev[k] = live ? ev[k] : 0.f;
-        H = fmaf(av[k], H, cv[k] * ev[k]);
-      }
+      if constexpr (!AGG) H = fmaf(av[k], H, cv[k] * ev[k]);
     }
 #pragma unroll
     for (int k = E - 1; k >= 0; --k) Rl = av[k] * (dv[k] + Rl);
     float h = 0.f;
-    if constexpr (!AGG) {   // the lane's state, from the one kept for its group of four lanes
+    float ph = P, hh = H, pe, he;
+    if constexpr (SELF) {
+      scan_prefix(ph, hh, li, lanes);
+    } else if constexpr (!AGG) {   // from the state kept for its group of four lanes
       const int q = lanes < 4 ? lanes : 4, qi = lane & (q - 1);
-      float ph = P, hh = H, pe, he;
       if (q > 1) {
         pe = scan_dpp<0x111, 0xf>(1.f, ph);
         he = scan_dpp<0x111, 0xf>(0.f, hh);
@@ -310,15 +310,18 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
     if (LANES) {
       const float tp = scan_readlane(P, 0), tr = scan_readlane(Rl, 0);
       if (NW > 1) {
-        if (lane == 0) sm[buf][wv] = make_float2(tp, tr);
+        const float th = SELF ? scan_readlane(hh, 63) : 0.f;
+        if (lane == 0) sm[buf][wv] = RunMap{tp, tr, th};
         __syncthreads();
         Rt = 0.f;
         for (int w = NW - 1; w >= 0; --w) {
-          const float2 m = sm[buf][w];
+          const RunMap m = sm[buf][w];
           if (w == wv) Rt = carry;
-          carry = fmaf(m.x, carry, m.y);
-          carryP *= m.x;
+          carry = fmaf(m.p, carry, m.r);
+          carryP *= m.p;
         }
+        if constexpr (SELF)
+          for (int w = 0; w < wv; ++w) h0 = fmaf(sm[buf][w].p, h0, sm[buf][w].h);
       } else {
         Rt = carry;
         carry = fmaf(tp, carry, tr);
@@ -328,7 +331,11 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
       Rt = carry;
     }
     if constexpr (!AGG) {
-      float pe, re;
+      if constexpr (SELF) {
+        scan_before(ph, hh, li, pe, he);
+        h = fmaf(pe, h0, he);
+      }
+      float re;
       scan_after(P, Rl, li, lanes, pe, re);
       if (!LANES) carry = fmaf(P, Rt, Rl);   // the group's first lane has the row's dh0
       Rt = fmaf(pe, Rt, re);
@@ -360,57 +367,53 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   }
 }
 
-template <typename T, bool REV>
+template <typename T, bool REV, bool CK, bool SELF>
 hipError_t launch_rows(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   const dim3 block(64 * p.waves);
   if (a.lanes < 64) {
     const uint32_t per = (uint32_t)p.waves * (64 / a.lanes);
-    const dim3 grid((a.cols + per - 1) / per);
-    if (a.us)
-      k_scan_rows_bwd<T, REV, 0, true, false><<<grid, block, 0, st>>>(a);
-    else
-      k_scan_rows_bwd<T, REV, 0, false, false><<<grid, block, 0, st>>>(a);
+    k_scan_rows_bwd<T, REV, 0, CK, SELF, false><<<dim3((a.cols + per - 1) / per), block, 0, st>>>(a);
     return hipGetLastError();
   }
   if (p.segs > 1) {
-    k_scan_rows_bwd<T, REV, 64, false, true><<<dim3(a.cols, p.segs - 1), block, 0, st>>>(a);
+    k_scan_rows_bwd<T, REV, 64, false, false, true><<<dim3(a.cols, p.segs - 1), block, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid(a.cols, p.segs);
-  if (a.us)
-    k_scan_rows_bwd<T, REV, 64, true, false><<<grid, block, 0, st>>>(a);
-  else
-    k_scan_rows_bwd<T, REV, 64, false, false><<<grid, block, 0, st>>>(a);
+  k_scan_rows_bwd<T, REV, 64, CK, SELF, false><<<dim3(a.cols, p.segs), block, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int V>
+template <typename T, bool CK, bool SELF, typename OFF>
 hipError_t launch_cols(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
-  const uint32_t groups = (uint32_t)(((uint64_t)a.cols + 64 * V - 1) / (64 * V));
-  const dim3 block(64 * p.waves);
-  const unsigned per = p.waves * 64 * V;
+  const uint32_t groups = (a.cols + a.cw - 1) / a.cw;
   if (p.segs > 1) {
-    k_scan_cols_bwd_agg<T, V><<<dim3(groups, p.segs - 1), block, per * sizeof(float2), st>>>(a);
+    k_scan_cols_bwd_agg<T, OFF><<<dim3(groups, p.segs - 1), 64 * kScanAggWaves,
+                                  kScanAggWaves * a.cw * sizeof(float2), st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid(groups, p.segs);
-  const unsigned lds = 2 * per * sizeof(SegMap);
-  static_assert(2 * kScanWaves * 64 * V * sizeof(SegMap) <= 64 * 1024, "LDS of a launch");
-  if (a.us)
-    k_scan_cols_bwd<T, V, true><<<grid, block, lds, st>>>(a);
-  else
-    k_scan_cols_bwd<T, V, false><<<grid, block, lds, st>>>(a);
+  static_assert(2 * scan_bwd_waves(false) * 64 * sizeof(RunMap) <= 64 * 1024, "LDS of a launch");
+  k_scan_cols_bwd<T, CK, SELF, OFF><<<dim3(groups, p.segs), 64 * p.waves,
+                                      2 * p.waves * a.cw * sizeof(RunMap), st>>>(a);
   return hipGetLastError();
+}
+
+template <typename T, bool CK, bool SELF>
+hipError_t launch_backward_t(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+  if (p.rows)
+    return a.reverse ? launch_rows<T, true, CK, SELF>(a, p, st) : launch_rows<T, false, CK, SELF>(a, p, st);
+  return p.wide ? launch_cols<T, CK, SELF, uint64_t>(a, p, st)
+                : launch_cols<T, CK, SELF, uint32_t>(a, p, st);
 }
 
 }  // namespace
 
 hipError_t launch_scan_backward(const ScanRequest& r, hipStream_t st) {
-  const ScanPlan p = scan_plan(r.outer, r.len, r.inner, 1, true);
+  const ScanPlan p = scan_plan(r.outer, r.len, r.inner, r.bf16, r.states ? 1 : 2, r.us != nullptr);
   ScanArgs a = scan_args(r, p);
-  if (!r.states) {   // run the forward for its states, into the workspace
+  const bool self = !r.states && p.self;
+  if (!r.states && !self) {   // run the forward for its states, into the workspace
     ScanRequest f = r;
     f.carry_in = r.h0;
     f.carry_out = nullptr;
@@ -425,11 +428,14 @@ hipError_t launch_scan_backward(const ScanRequest& r, hipStream_t st) {
     b.ws = f.ws;
     a = scan_args(b, p);
   }
-  if (p.rows) {
-    if (r.bf16) return r.reverse ? launch_rows<uint16_t, true>(a, p, st) : launch_rows<uint16_t, false>(a, p, st);
-    return r.reverse ? launch_rows<float, true>(a, p, st) : launch_rows<float, false>(a, p, st);
-  }
-  return r.bf16 ? launch_cols<uint16_t, 1>(a, p, st) : launch_cols<float, 1>(a, p, st);
+  auto go = [&](auto ck, auto sf) {
+    return r.bf16 ? launch_backward_t<uint16_t, decltype(ck)::value, decltype(sf)::value>(a, p, st)
+                  : launch_backward_t<float, decltype(ck)::value, decltype(sf)::value>(a, p, st);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (r.us) return self ? go(Yes{}, Yes{}) : go(Yes{}, No{});
+  return self ? go(No{}, Yes{}) : go(No{}, No{});
 }
 
 }  // namespace wbmm

@@ -137,6 +137,42 @@ def test_scan_backward_from_checkpoint(O, L, I, reverse, lens, fmt, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("O,L,I,reverse", [
+    (300, 50, 7, False), (1000, 40, 40, True), (17, 200, 130, True), (129, 65, 128, False),
+    (1, 1000, 1000, False), (2, 700, 2, True), (5000, 300, 1, False), (1, 900, 17, True),
+])
+def test_scan_many_columns(O, L, I, reverse, bf16):
+    """Column groups of every width, with and without columns to spare."""
+    run_case(O, L, I, bf16, reverse, seed=3)
+    run_case(O, L, I, bf16, reverse, seed=4, lens=[L // 2 + 1], recompute=True)
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 23) + 5, 257), (3, (1 << 30) - 3, 1)])
+def test_scan_offsets_past_32_bits(shape):
+    """More than 4 GiB of bf16: the ends of the long run against runs of the ends alone."""
+    O, L, I = shape
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    g, u, dh = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for t in (g, u, dh):
+        t.normal_(generator=gen)
+    h, last, st = R().wbmm_scan_forward(g, u, 1, h_last=True, states=True)
+    k = (L // 32 - 3) * 32      # a chunk's start near the end
+    cut = lambda t, a, b: t[-1:, a:b].contiguous()
+    h2, last2, _ = R().wbmm_scan_forward(cut(g, k, L), cut(u, k, L), 1,
+                                         h0=st[-1:, k // 32].contiguous(), h_last=True)
+    same = lambda a, b: torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=1e-5)
+    assert same(h[-1:, k:], h2) and same(last[-1:], last2)
+    dg, du, d0 = R().wbmm_scan_backward(g, st, dh, 1, u=u)
+    n = 3000                    # the last sequence's end, and its beginning (the rest forgotten)
+    for a, b, keep in ((L - n, L, slice(0, n)), (0, n, slice(0, n - 1000))):
+        a = a // 32 * 32
+        x, y, z = R().wbmm_scan_backward(cut(g, a, b), None, cut(dh, a, b), 1, u=cut(u, a, b),
+                                         h0=st[-1:, a // 32].contiguous())
+        assert same(dg[-1:, a:b][:, keep], x[:, keep]) and same(du[-1:, a:b][:, keep], y[:, keep])
+    assert torch.allclose(d0[-1:], z, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("O,L,I,reverse,lens", [
     (2, 1, 1, False, None), (2, 1, 3, False, [0, 1]), (3, 20, 1, True, None), (2, 600, 1, True, [600, 5]),
     (2, 90, 7, False, None), (2, 33, 64, True, [33, 0]), (1, 9000, 1, True, None), (1, 3001, 4, False, None),
@@ -251,22 +287,30 @@ def test_scan_writes_only_its_outputs(O, L, I, bf16):
                R().wbmm_scan_backward_workspace_bytes(O, L, I, False))
     ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
     gd, ud, dd = (dev(a).to(dt) for a in (g, u, dh))
-    w = ws[:need] if need else None
+    wsp = ws[:need] if need else None
     lens = dev(np.array([max(L - 40, 1)], np.int32))
     for ln in (None, lens):
         h.fill_(float("nan")), st.fill_(float("nan"))
-        R().wbmm_scan_forward(gd, ud, 1, h0=dev(h0), h=h, h_last=last, states=st, lens=ln, workspace=w)
+        R().wbmm_scan_forward(gd, ud, 1, h0=dev(h0), h=h, h_last=last, states=st, lens=ln, workspace=wsp)
         assert torch.isfinite(h.float()).all() and torch.isfinite(st).all()
         bg, dg = guarded((O, L, I), dt)
         bu, du = guarded((O, L, I), dt)
         b0, d0 = guarded((O, I), torch.float32)
         dg.fill_(float("nan")), du.fill_(float("nan"))
-        R().wbmm_scan_backward(gd, st, dd, 1, u=ud, dg=dg, du=du, dh0=d0, lens=ln, workspace=w)
+        R().wbmm_scan_backward(gd, st, dd, 1, u=ud, dg=dg, du=du, dh0=d0, lens=ln, workspace=wsp)
         assert torch.isfinite(dg.float()).all() and torch.isfinite(du.float()).all()
         kept = [t.clone() for t in (dg, du, d0)]
         R().wbmm_scan_backward(gd, None, dd, 1, u=ud, h0=dev(h0), dg=dg, du=du, dh0=d0, lens=ln,
-                               workspace=w)
-        assert all(torch.equal(p, q) for p, q in zip(kept, (dg, du, d0)))
+                               workspace=wsp)
+        # the states are joined in another order here: either side is within the oracle's bound
+        # and half a step of the exact value, so they differ by twice that at most
+        n = None if ln is None else np.full(O, max(L - 40, 1))
+        f = [v.astype(np.float64) for v in (g, u, h0, dh)]
+        want = Q.scan_backward(*f, n=n, bf16=bf16)
+        half = [2.0 ** -8 if bf16 else 2.0 ** -24] * 2 + [2.0 ** -24]
+        for p, q, w, b, e in zip(kept, (dg, du, d0), want[:3], want[3:], half):
+            diff = (p.double() - q.double()).abs().cpu().numpy()
+            assert np.all(diff <= 2 * (b * (1 + e) + e * np.abs(w) + 1e-36))
         for b in (bh, bl, bs, bg, bu, b0):
             assert intact(b)
         assert torch.all(ws[need:] == 77)

@@ -112,7 +112,7 @@ def back(lib, **kw):
 
 @pytest.mark.parametrize("kw,want", SCAN + [
     (dict(h0=8 * A), INV), (dict(st=None, h0=E_), INV), (dict(dh=None), INV),
-    (dict(st=None, wsb=64), WS), (dict(dg=None), INV), (dict(du=None), INV),
+    (dict(LONG, st=None, wsb=64), WS), (dict(dg=None), INV), (dict(du=None), INV),
     (dict(us=9 * A, fmt=2), INV), (dict(dg=A), INV), (dict(du=E_ + 4), INV), (dict(dg=D_ + 4), INV),
     (dict(du=C_), INV), (dict(us=E_ + 4, fmt=1), INV), (dict(dhl=9 * A, dh0=9 * A), INV),
     (dict(LONG, ws=None), WS), (dict(st=C_ + 2), UNS),
@@ -133,5 +133,6 @@ def test_scan_workspace_rules(lib):
 def test_scan_backward_workspace_rules(lib):
     q = lib.wbmm_scan_backward_workspace_bytes
     assert q(64 * 192, 784, 1, 1) == 0
-    assert q(64 * 192, 784, 1, 0) >= 64 * 192 * 25 * 4      # the states of 784 steps
+    assert q(64 * 192, 784, 1, 0) == 0                      # one tile holds the axis
+    assert q(64, 30000, 192, 0) >= 64 * 192 * 938 * 4       # the states of 30000 steps
     assert q(0, 5, 5, 1) == 0 and q(1, 1 << 31, 1, 0) == 0
