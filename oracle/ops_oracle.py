@@ -67,15 +67,16 @@ def unpack(codes, scales, fmt):
 
 
 # --------------------------------------------------------------------------------- recurrence
-# What fp32 may lose. EXP2, RCP: half-step counts of the hardware's exp2 and reciprocal (1 ulp
-# each); t = exp(-g) further takes the rounding of g log2(e), |g| log2(e) 2^-24 (bf16 tensors; fp32
-# ones add it back and keep two roundings). a = 1 / (1 + t) and c = t a then follow.
+# What fp32 may lose, in half steps U of relative error. t = exp(-g): 2 for the hardware's exp2 (one
+# step); the rounding of log2(e) itself, 0.23 |g|; and the rounding of g log2(e), |g| log2(e) for
+# bf16 tensors, put back with two more roundings for fp32 ones. a = 1 / (1 + t): t's error times
+# 1 - a, the sum's rounding and one step of the reciprocal; c = t a: both and a rounding.
 U = 2.0 ** -24
 
 
 def gate_bounds(g, bf16):
     """Relative error bounds of a and c = 1 - a."""
-    et = 2 * U + 4 * U + (np.abs(g) * 1.4427 * U * 2 if bf16 else 0)
+    et = (2 + 0.23 * np.abs(g) + (1.4427 * np.abs(g) if bf16 else 2)) * U
     one_minus_a = 1 / (1 + np.exp(g))
     ea = one_minus_a * et + U + 2 * U
     return ea, ea + et + U

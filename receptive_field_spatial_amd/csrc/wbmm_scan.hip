@@ -5,9 +5,9 @@
 // row), form their pieces' affine maps in registers, pass them through LDS, and each applies the
 // state that reaches its piece: g and u are read once, h written once. The next tile's loads are
 // issued before the exchange of the current one. Only where the columns are too few to fill the
-// chip is the axis cut into segments over several workgroups; a first launch then forms the
-// segments' maps (reading g and u a second time), and every workgroup of the second one joins the
-// maps before its own, in order.
+// chip is the axis cut into segments over several workgroups; a first launch then forms the maps of
+// the segments, or of finer parts of them (reading g and u a second time), and every workgroup of the
+// second one joins the maps before its own, in order.
 #include "wbmm_scan.hpp"
 
 #include <algorithm>
@@ -19,7 +19,8 @@ namespace {
 // ------------------------------------------------------------------ columns
 // CK: u is a checkpoint. Without out0 only the states (and the last one) are formed.
 template <typename T, bool CK, typename OFF>
-__global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
+__global__ void __launch_bounds__(64 * scan_col_waves(false, CK))
+k_scan_cols(ScanArgs a) {
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sm[];
   const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
@@ -28,14 +29,13 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
   const int seg = blockIdx.y, sbeg = seg * a.seg_len;
   const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
   const int tile = NW * cl.subs * K, lofs = (wv * cl.subs + cl.sub) * K;
-  const T pad = scan_narrow<T>(kScanPad);
 
   float carry = 0.f;
   if (seg == 0) {
     const float* ci = a.segs > 1 ? a.carry_copy : a.carry_in;
     if (ci) carry = ci[cl.col];
   } else {
-    for (int j = 0; j < seg; ++j) {
+    for (int j = 0; j < seg * a.fine; ++j) {
       const float2 m = a.agg[(size_t)j * a.cols + cl.col];
       carry = fmaf(m.x, carry, m.y);
     }
@@ -43,25 +43,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
 
   T rg[K];
   ScanRaw<T, CK> ru[K];
-  auto load = [&](int s) {
-    if (__all(s + K <= cl.n)) {
-      OFF o = cl.at(s);
-#pragma unroll
-      for (int k = 0; k < K; ++k, o += cl.stride) {
-        rg[k] = cl.load(a.g, o);
-        ru[k].load(a, o);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const OFF o = cl.held(s + k);
-        const T g = cl.load(a.g, o);
-        ru[k].load(a, o);
-        rg[k] = s + k < cl.n ? g : pad;
-        if (s + k >= cl.n) ru[k].clear();
-      }
-    }
-  };
+  auto load = [&](int s) { scan_load<T, CK, OFF, false>(a, cl, s, rg, rg, ru); };
   load(sbeg + lofs);
   int buf = 0;
   for (int t0 = sbeg; t0 < send; t0 += tile, buf ^= 1) {
@@ -70,7 +52,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float c;
-      scan_gate(scan_widen<T>(rg[k]), av[k], c);
+      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], c);
       bv[k] = c * ru[k].widen(a);
       H = fmaf(av[k], H, bv[k]);
       P *= av[k];
@@ -122,37 +104,30 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols(ScanArgs a) {
     a.carry_out[cl.col] = carry;
 }
 
-// Maps of segments 0 .. segs - 2; segment 0's has the initial state folded in (P = 0).
+// The maps before the last segment's; the first has the initial state folded in (P = 0).
 template <typename T, bool CK, typename OFF>
-__global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols_agg(ScanArgs a) {
+__global__ void __launch_bounds__(64 * scan_map_waves(CK)) k_scan_cols_agg(ScanArgs a) {
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sm[];
   const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanCol<T, OFF> cl(a, lane);
-  const int seg = blockIdx.y, part = a.seg_len / (NW * cl.subs);   // a multiple of K
-  const int sbeg = seg * a.seg_len + (wv * cl.subs + cl.sub) * part;
-  const T pad = scan_narrow<T>(kScanPad);
+  const int seg = blockIdx.y, flen = a.seg_len / a.fine, part = flen / (NW * cl.subs);   // K's multiple
+  const int sbeg = seg * flen + (wv * cl.subs + cl.sub) * part;
   float P = 1.f, H = 0.f;
+  T rg[K];
+  ScanRaw<T, CK> ru[K];
+  scan_load<T, CK, OFF, false>(a, cl, sbeg, rg, rg, ru);
   for (int it = 0; it < part; it += K) {
-    const int s = sbeg + it;
-    T rg[K];
-    ScanRaw<T, CK> ru[K];
+    float gv[K], uv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) gv[k] = scan_widen<T>(rg[k]), uv[k] = ru[k].widen(a);
+    if (it + K < part) scan_load<T, CK, OFF, false>(a, cl, sbeg + it + K, rg, rg, ru);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const OFF o = cl.held(s + k);
-      rg[k] = cl.load(a.g, o);
-      ru[k].load(a, o);
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (s + k >= cl.n) {
-        rg[k] = pad;
-        ru[k].clear();
-      }
       float aa, c;
-      scan_gate(scan_widen<T>(rg[k]), aa, c);
-      H = fmaf(aa, H, c * ru[k].widen(a));
+      scan_gate<sizeof(T) == 4>(gv[k], aa, c);
+      H = fmaf(aa, H, c * uv[k]);
       P *= aa;
     }
   }
@@ -179,7 +154,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_cols_agg(ScanArgs a) {
 // ------------------------------------------------------------------ rows
 // LANES = 64: the waves of the workgroup take consecutive 512-step pieces of one row; LANES = 0:
 // a.lanes lanes per row (the row fits in a.lanes * kScanE steps) and 64 / a.lanes rows per wave.
-// AGG: only the maps of segments 0 .. segs - 2 (as k_scan_cols_agg).
+// AGG: only the maps (as k_scan_cols_agg).
 template <typename T, bool REV, int LANES, bool CK, bool AGG>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
   constexpr int E = kScanE;
@@ -195,8 +170,9 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
   const int n = scan_steps(a, row);
   const ScanRow<T, REV> rw(row, a.len, n);
   const ScanRow<uint8_t, REV> rwc(row, a.len, n);
-  const int seg = LANES ? blockIdx.y : 0, sbeg = seg * a.seg_len;
-  const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
+  const int slen = AGG ? a.seg_len / a.fine : a.seg_len;
+  const int seg = LANES ? blockIdx.y : 0, sbeg = seg * slen;
+  const int send = sbeg + slen < a.len ? sbeg + slen : a.len;
   const int tile = LANES ? NW * 64 * E : 64 * E;
   const int lofs = LANES ? (wv * 64 + lane) * E : li * E;
   const T* gp = (const T*)a.g;
@@ -207,7 +183,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
     c0 = ci ? ci[row] : 0.f;
     carry = c0;
   } else if (!AGG) {
-    for (int j = 0; j < seg; ++j) {
+    for (int j = 0; j < seg * a.fine; ++j) {
       const float2 m = a.agg[(size_t)j * a.cols + row];
       carry = fmaf(m.x, carry, m.y);
     }
@@ -224,7 +200,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
 #pragma unroll
     for (int k = 0; k < E; ++k) {
       float c;
-      scan_gate(scan_widen<T>(rg[k]), av[k], c);
+      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], c);
       bv[k] *= c;
       H = fmaf(av[k], H, bv[k]);
       P *= av[k];
@@ -291,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(ScanArgs a) {
   if (c >= a.cols) return;
   const float h0 = a.carry_in ? a.carry_in[c] : 0.f;
   float aa, cc;
-  scan_gate(scan_widen<T>(((const T*)a.g)[c]), aa, cc);
+  scan_gate<sizeof(T) == 4>(scan_widen<T>(((const T*)a.g)[c]), aa, cc);
   const float h = fmaf(aa, h0, cc * scan_widen<T>(((const T*)a.u)[c]));
   const bool live = scan_steps(a, (uint32_t)(c / a.inner)) > 0;
   ((T*)a.out0)[c] = scan_narrow<T>(live ? h : 0.f);
@@ -308,7 +284,7 @@ hipError_t launch_rows(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     return hipGetLastError();
   }
   if (p.segs > 1) {
-    k_scan_rows<T, REV, 64, CK, true><<<dim3(a.cols, p.segs - 1), block, 0, st>>>(a);
+    k_scan_rows<T, REV, 64, CK, true><<<dim3(a.cols, (p.segs - 1) * p.fine), block, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -321,8 +297,8 @@ hipError_t launch_cols(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   const uint32_t groups = (a.cols + a.cw - 1) / a.cw;
   const unsigned lds = a.cw * sizeof(float2);
   if (p.segs > 1) {
-    k_scan_cols_agg<T, CK, OFF><<<dim3(groups, p.segs - 1), 64 * kScanAggWaves,
-                                  kScanAggWaves * lds, st>>>(a);
+    constexpr int mw = scan_map_waves(CK);
+    k_scan_cols_agg<T, CK, OFF><<<dim3(groups, (p.segs - 1) * p.fine), 64 * mw, mw * lds, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -368,7 +344,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   p.rows = inner == 1;
   p.segs = 1;
   p.lanes = 64;
-  p.cw = p.run = 1;
+  p.cw = p.run = p.fine = 1;
   p.wide = cols * len * es >= (1ll << 32);
   long long piece, units;   // steps of a wave's tile; workgroups without segments
   int least = 1, most = kScanWaves;
@@ -383,15 +359,17 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     piece = 64 * kScanE;
     units = outer;
   } else {
-    // Columns per wave: 64, or down to 32 bytes of a row where that still leaves CUs without a
-    // workgroup, and no more than there are.
-    int low = scan_pow2(std::min<int64_t>(cols, 32 / es));
+    // Columns per wave: 64, fewer where that leaves CUs without a workgroup: down to a memory line of
+    // 128 bytes (with 32 bytes the address units were the limit, 490 against 400 us for the backward
+    // of 4 x 32768 x 1024 bf16), or to 32 bytes where little data makes latency the limit.
+    const int bytes = cols * len <= (1 << 22) ? 32 : 128;
+    const int low = scan_pow2(std::min<int64_t>(cols, bytes / es));
     p.cw = scan_pow2(std::min<int64_t>(cols, 64));
     while (p.cw > low && (cols + p.cw - 1) / p.cw < kCus && 64 / p.cw * kScanK < len) p.cw /= 2;
     p.run = std::max(1, 128 / (p.cw * es));
     piece = (64 / p.cw) * kScanK;
     units = (cols + p.cw - 1) / p.cw;
-    if (kind) most = scan_bwd_waves(ck || p.wide);
+    most = scan_col_waves(kind, ck || (kind && p.wide));
     if (kind && p.cw == 64) least = 2;   // waves pair up for the kept states
   }
   const long long pieces = (len + piece - 1) / piece;
@@ -401,14 +379,17 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   if (least == 2) p.waves += p.waves & 1;
   p.self = pieces <= p.waves;
   if (units < kCus * 3 / 4) {
-    // segments of whole kScanAggWaves pieces, which the tiles of 8 or 16 waves divide
-    const long long step = kScanAggWaves * piece, steps = (len + step - 1) / step;
+    // segments of whole 16 pieces, which the tiles of 8 or 16 waves divide
+    const long long step = 16 * piece, steps = (len + step - 1) / step;
     const long long segs = std::min<long long>({(kCus + units - 1) / units, steps, 64});
     if (segs > 1) {
       const long long per = (steps + segs - 1) / segs;
       p.segs = (int)((steps + per - 1) / per);
       p.seg_len = (int)(per * step);
-      p.waves = p.rows || !kind ? 16 : 8;
+      p.waves = most == 16 ? 16 : 8;
+      // workgroups for the maps' launch: up to a dozen per CU (383 against 413 us with one map per
+      // segment, the backward of 4 x 32768 x 1024 bf16)
+      while (per % (2 * p.fine) == 0 && units * (p.segs - 1) * p.fine < 6 * kCus) p.fine *= 2;
       p.self = false;
       return p;
     }
@@ -419,7 +400,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
 }
 
 namespace {
-size_t maps_bytes(const ScanPlan& p, size_t cols) { return p.segs > 1 ? cols * (8 * p.segs + 4) : 0; }
+size_t maps_bytes(const ScanPlan& p, size_t cols) { return p.segs > 1 ? cols * (8 * p.segs * p.fine + 4) : 0; }
 }  // namespace
 
 size_t scan_workspace(int64_t outer, int64_t len, int64_t inner) {
@@ -465,12 +446,14 @@ ScanArgs scan_args(const ScanRequest& r, const ScanPlan& p) {
   a.cols = (uint32_t)(r.outer * r.inner);
   a.rows_per_len = r.lens ? (uint32_t)(r.outer / r.n_lens) : 1;
   a.segs = p.segs;
+  a.fine = p.fine;
+  a.maps = p.segs * p.fine;
   a.seg_len = p.seg_len;
   a.lanes = p.lanes;
   a.cw = p.cw;
   a.run = p.run;
   a.agg = (float2*)r.ws;
-  a.carry_copy = r.ws ? (float*)r.ws + (size_t)2 * p.segs * a.cols : nullptr;
+  a.carry_copy = r.ws ? (float*)r.ws + (size_t)2 * a.maps * a.cols : nullptr;
   return a;
 }
 

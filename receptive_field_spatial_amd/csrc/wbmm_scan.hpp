@@ -26,10 +26,10 @@ constexpr int kScanChunk = 32;    // steps between two kept states
 constexpr int kScanK = 16;        // steps per lane and tile of the column kernels
 constexpr int kScanE = 8;         // steps per lane and tile of the row kernels
 constexpr int kScanWaves = 16;    // waves of a workgroup at most
-// The same for the columns' backward: 3 waves per SIMD, 2 where a checkpoint or 64-bit offsets take
-// more registers.
-constexpr int scan_bwd_waves(bool more) { return more ? 8 : 12; }
-constexpr int kScanAggWaves = 16; // waves of a workgroup that forms a segment's map
+// The same for the column kernels, by their registers: forward 4 waves per SIMD, backward 3, each 2
+// from a checkpoint (and the backward with 64-bit offsets).
+constexpr int scan_col_waves(bool backward, bool more) { return more ? 8 : (backward ? 12 : 16); }
+constexpr int scan_map_waves(bool ck) { return ck ? 8 : 16; }   // of a workgroup that forms a map
 constexpr float kScanPad = 100.f; // a gate that leaves the state alone (a = 1 exactly)
 
 struct ScanArgs {
@@ -44,29 +44,32 @@ struct ScanArgs {
   void* out1;                 // du (backward)
   float* carry_out;           // h_last, or dh0, or null
   float* states;              // [outer][chunks][inner]
-  float2* agg;                // [segs][cols] maps of the segments
+  float2* agg;                // [maps][cols]
   float* carry_copy;          // [cols] carry_in, kept for the second launch
   int len, chunks, reverse, fmt;
   uint32_t inner, cols, rows_per_len;   // cols = outer * inner; lens[outer index / rows_per_len]
   int segs, seg_len;          // seg_len: a multiple of the workgroup's tile
+  int fine, maps;             // maps per segment (of seg_len / fine steps each), maps in all
   int lanes;                  // row kernels: lanes per row (64: the workgroup's waves share a row)
   int cw;                     // column kernels: columns of a wave
   int run;                    // column kernels: neighbour groups that share memory lines
 };
 
 // a = sigmoid(g) and c = 1 - a = sigmoid(-g), each with its own relative accuracy (c from 1 - a
-// would lose what a long memory lives on): with t = exp(-g), a = 1 / (1 + t) and c = t a. t takes
-// the rounding of g log2(e) back in, which otherwise costs |g| half steps; the reciprocal gets one
-// Newton step: over hundreds of steps near a = 1 its last bit shows in the fp32 states. g is held
-// to [-87, 87], where a or c is the least normal number and t finite; a NaN passes.
+// would lose what a long memory lives on): with t = exp(-g), a = 1 / (1 + t) and c = t a. The
+// reciprocal gets one Newton step: over hundreds of steps near a = 1 its last bit shows in the fp32
+// states. FINE (fp32 tensors): t takes the rounding of g log2(e) back in, |g| half steps of t; it
+// reaches only c and a's small distance from 1, and bf16 results do not show it. g is held at -87,
+// where a is the least normal number and t finite (FINE: and at 87, so that an infinity stays out of
+// the correction); the NaN-keeping forms let a NaN through.
+template <bool FINE>
 __device__ __forceinline__ void scan_gate(float g, float& a, float& c) {
-  constexpr float kL = 1.44269502f, kLlo = 1.92596299e-8f, kLn2 = 0.693147181f;
-  float x = g < -87.f ? -87.f : g;
-  x = x > 87.f ? 87.f : x;
+  constexpr float kL = 1.44269502f, kLn2 = 0.693147181f;
+  float x = __builtin_elementwise_maximum(g, -87.f);
+  if constexpr (FINE) x = __builtin_elementwise_minimum(x, 87.f);
   const float y = x * kL;
-  const float r = fmaf(x, kLlo, fmaf(x, kL, -y));
   float t = __builtin_amdgcn_exp2f(-y);
-  t = fmaf(t, -kLn2 * r, t);
+  if constexpr (FINE) t = fmaf(t, -kLn2 * fmaf(x, kL, -y), t);
   const float d = 1.f + t;
   a = __builtin_amdgcn_rcpf(d);
   a = fmaf(a, fmaf(-d, a, 1.f), a);
@@ -216,11 +219,6 @@ struct ScanCol {
     stride = a.reverse ? (OFF)0 - row : row;
   }
   __device__ __forceinline__ OFF at(int s) const { return start + (OFF)s * stride; }
-  // the same held to the sequence's own steps (position 0 of an empty one)
-  __device__ __forceinline__ OFF held(int s) const {
-    s = s < n ? s : n - 1;
-    return at(s > 0 ? s : 0);
-  }
   __device__ __forceinline__ T load(const void* p, OFF o) const {
     return *(const T*)((const char*)p + o);
   }
@@ -229,8 +227,11 @@ struct ScanCol {
   }
   // zeros at the positions of steps s .. s + kScanK - 1 that lie past the end of the sequence
   __device__ __forceinline__ void zero(void* p, int s, int len, uint32_t inner) const {
-    for (int k = 0; k < kScanK; ++k)
-      if (s + k >= n && s + k < len) store(p, base + (OFF)(s + k) * inner * sizeof(T), 0.f);
+    const OFF row = (OFF)inner * sizeof(T);
+    OFF o = base + (OFF)s * row;
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k, o += row)
+      if (s + k >= n && s + k < len) store(p, o, 0.f);
   }
   // index of the kept state before step s
   __device__ __forceinline__ size_t kept(const ScanArgs& a, int s) const {
@@ -263,6 +264,42 @@ struct ScanRaw {
     else return scan_widen<T>(r);
   }
 };
+
+// g and u (DH: and dh) of a lane's kScanK steps from s on; past the end of the sequence a neutral gate
+// and zeros.
+template <typename T, bool CK, typename OFF, bool DH, bool U = true>
+__device__ __forceinline__ void scan_load(const ScanArgs& a, const ScanCol<T, OFF>& cl, int s,
+                                          T (&rg)[kScanK], T (&rd)[kScanK],
+                                          ScanRaw<T, CK> (&ru)[kScanK]) {
+  if (__all(s + kScanK <= cl.n)) {
+    OFF o = cl.at(s);
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k, o += cl.stride) {
+      rg[k] = cl.load(a.g, o);
+      if constexpr (DH) rd[k] = cl.load(a.dh, o);
+      if constexpr (U) ru[k].load(a, o);
+    }
+  } else {
+    // steps past the end load the last one's place (position 0 of an empty sequence) for nothing
+    const T pad = scan_narrow<T>(kScanPad);
+    const int last = cl.n > 0 ? cl.n - 1 : 0;
+    OFF o = cl.at(s < last ? s : last);
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k, o += s + k <= last ? cl.stride : OFF(0)) {
+      const bool live = s + k < cl.n;
+      const T g = cl.load(a.g, o);
+      rg[k] = live ? g : pad;
+      if constexpr (DH) {
+        const T d = cl.load(a.dh, o);
+        rd[k] = live ? d : T(0);
+      }
+      if constexpr (U) {
+        ru[k].load(a, o);
+        if (!live) ru[k].clear();
+      }
+    }
+  }
+}
 
 // Composition over a wave's pieces (lanes cw apart): inclusive prefix, or suffix.
 __device__ __forceinline__ void scan_sub_prefix(float& P, float& H, int lane, int cw) {
@@ -301,9 +338,11 @@ struct ScanRow {
       for (int k = 0; k < E; ++k) v[k] = w.v[REV ? E - 1 - k : k];
     } else {
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        v[k] = pad;
-        if (s + k < n) v[k] = p[at(s + k)];
+      for (int k = 0; k < E; ++k) v[k] = pad;
+      if (s < n) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (s + k < n) v[k] = p[at(s + k)];
       }
     }
   }
@@ -384,7 +423,7 @@ struct ScanRequest {
 struct ScanPlan {
   bool rows, wide;      // rows: inner = 1; wide: 64-bit offsets (column kernels)
   bool self;            // backward: one tile holds the axis, no states needed
-  int cw, run, lanes, waves, segs, seg_len;
+  int cw, run, lanes, waves, segs, seg_len, fine;
 };
 // kind: 0 = forward, 1 = backward from kept states, 2 = backward without; ck: u is a checkpoint.
 ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kind, bool ck);

@@ -25,7 +25,7 @@ struct RunMap {
 // waves come in pairs). CK: u is a checkpoint. SELF: one tile holds the axis and no state is kept:
 // the pieces' maps of the state are exchanged beside those of its gradient, from h0 (a.h0).
 template <typename T, bool CK, bool SELF, typename OFF>
-__global__ void __launch_bounds__(64 * scan_bwd_waves(CK || sizeof(OFF) == 8))
+__global__ void __launch_bounds__(64 * scan_col_waves(true, CK || sizeof(OFF) == 8))
 k_scan_cols_bwd(ScanArgs a) {
   constexpr int K = kScanK;
   static_assert(kScanChunk == 2 * K, "two pieces between states");
@@ -36,14 +36,13 @@ k_scan_cols_bwd(ScanArgs a) {
   const int seg = blockIdx.y, sbeg = seg * a.seg_len;
   const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
   const int tile = NW * cl.subs * K, lofs = (wv * cl.subs + cl.sub) * K;
-  const T pad = scan_narrow<T>(kScanPad);
   const bool odd = cl.subs > 1 ? cl.sub & 1 : wv & 1;
 
   float carry = 0.f;
   if (seg == a.segs - 1) {
     if (a.carry_in) carry = a.carry_in[cl.col];
   } else {
-    for (int j = a.segs - 1; j > seg; --j) {
+    for (int j = a.maps - 1; j >= (seg + 1) * a.fine; --j) {
       const float2 m = a.agg[(size_t)j * a.cols + cl.col];
       carry = fmaf(m.x, carry, m.y);
     }
@@ -54,43 +53,26 @@ k_scan_cols_bwd(ScanArgs a) {
   float rst = 0.f;
   auto load = [&](int s) {
     if (!SELF && !odd && s < a.len) rst = a.states[cl.kept(a, s)];
-    if (__all(s + K <= cl.n)) {
-      OFF o = cl.at(s);
-#pragma unroll
-      for (int k = 0; k < K; ++k, o += cl.stride) {
-        rg[k] = cl.load(a.g, o);
-        rd[k] = cl.load(a.dh, o);
-        ru[k].load(a, o);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const OFF o = cl.held(s + k);
-        const T g = cl.load(a.g, o), d = cl.load(a.dh, o);
-        ru[k].load(a, o);
-        const bool live = s + k < cl.n;
-        rg[k] = live ? g : pad;
-        rd[k] = live ? d : T(0);
-        if (!live) ru[k].clear();
-      }
-    }
+    scan_load<T, CK, OFF, true>(a, cl, s, rg, rd, ru);
   };
   int t0 = sbeg + (send - sbeg - 1) / tile * tile;
   load(t0 + lofs);
   for (int buf = 0; t0 >= sbeg; t0 -= tile, buf ^= 1) {
     const int s = t0 + lofs;
-    // ev: u, later the gradient of g up to the factor G
+    // ev: (1 - a) u, later the gradient of g up to the factor G
     float av[K], cv[K], ev[K], dv[K], P = 1.f, Rl = 0.f, H = 0.f, h = rst;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      scan_gate(scan_widen<T>(rg[k]), av[k], cv[k]);
-      ev[k] = ru[k].widen(a);
+      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], cv[k]);
+      ev[k] = cv[k] * ru[k].widen(a);
       dv[k] = scan_widen<T>(rd[k]);
       P *= av[k];
-      H = fmaf(av[k], H, cv[k] * ev[k]);
+      H = fmaf(av[k], H, ev[k]);
     }
+    Rl = dv[K - 1];
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) Rl = av[k] * (dv[k] + Rl);
+    for (int k = K - 2; k >= 0; --k) Rl = fmaf(av[k + 1], Rl, dv[k]);
+    Rl *= av[0];
     if (t0 - tile >= sbeg) load(s - tile);
     float ph = P, hend = SELF ? H : fmaf(P, h, H);   // the state's map, or where the piece ends
     if (cl.subs > 1) {
@@ -140,30 +122,29 @@ k_scan_cols_bwd(ScanArgs a) {
     }
     if constexpr (SELF) h = hs;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const float u = ev[k];
-      ev[k] = av[k] * cv[k] * (h - u);
-      h = fmaf(av[k], h, cv[k] * u);
+    for (int k = 0; k < K; ++k) {   // a c (h - u)
+      const float cu = ev[k];
+      ev[k] = av[k] * fmaf(cv[k], h, -cu);
+      h = fmaf(av[k], h, cu);
     }
     if (cl.active && s < a.len) {
       OFF o = cl.at(s + K - 1);
+      float Gt = dv[K - 1] + Rt;
       if (__all(s + K <= cl.n)) {
 #pragma unroll
         for (int k = K - 1; k >= 0; --k, o -= cl.stride) {
-          const float Gt = dv[k] + Rt;
-          Rt = av[k] * Gt;
           cl.store(a.out0, o, ev[k] * Gt);
           cl.store(a.out1, o, cv[k] * Gt);
+          if (k > 0) Gt = fmaf(av[k], Gt, dv[k > 0 ? k - 1 : 0]);
         }
       } else {
 #pragma unroll
         for (int k = K - 1; k >= 0; --k, o -= cl.stride) {
-          const float Gt = dv[k] + Rt;
-          Rt = av[k] * Gt;
           if (s + k < cl.n) {
             cl.store(a.out0, o, ev[k] * Gt);
             cl.store(a.out1, o, cv[k] * Gt);
           }
+          if (k > 0) Gt = fmaf(av[k], Gt, dv[k > 0 ? k - 1 : 0]);
         }
         cl.zero(a.out0, s, a.len, a.inner);
         cl.zero(a.out1, s, a.len, a.inner);
@@ -173,33 +154,30 @@ k_scan_cols_bwd(ScanArgs a) {
   if (seg == 0 && wv == 0 && cl.sub == 0 && cl.active && a.carry_out) a.carry_out[cl.col] = carry;
 }
 
-// Maps of segments 1 .. segs - 1 (blockIdx.y + 1); the last one's has dh_last folded in (P = 0).
+// The maps after the first segment's; the last has dh_last folded in (P = 0).
 template <typename T, typename OFF>
-__global__ void __launch_bounds__(64 * kScanAggWaves) k_scan_cols_bwd_agg(ScanArgs a) {
+__global__ void __launch_bounds__(64 * scan_map_waves(false)) k_scan_cols_bwd_agg(ScanArgs a) {
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sma[];
   const int lane = threadIdx.x & 63, NW = blockDim.x >> 6;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanCol<T, OFF> cl(a, lane);
-  const int seg = blockIdx.y + 1, part = a.seg_len / (NW * cl.subs);   // a multiple of K
-  const int sbeg = seg * a.seg_len + (wv * cl.subs + cl.sub) * part;
-  const T pad = scan_narrow<T>(kScanPad);
+  const int seg = blockIdx.y + a.fine, flen = a.seg_len / a.fine, part = flen / (NW * cl.subs);   // K's multiple
+  const int sbeg = seg * flen + (wv * cl.subs + cl.sub) * part;
   float P = 1.f, Rl = 0.f;
+  T rg[K], rd[K];
+  ScanRaw<T, false> none[K];
+  scan_load<T, false, OFF, true, false>(a, cl, sbeg + part - K, rg, rd, none);
   for (int it = part - K; it >= 0; it -= K) {
-    const int s = sbeg + it;
-    T rg[K], rd[K];
+    float gv[K], dv[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const OFF o = cl.held(s + k);
-      rg[k] = cl.load(a.g, o);
-      rd[k] = cl.load(a.dh, o);
-    }
+    for (int k = 0; k < K; ++k) gv[k] = scan_widen<T>(rg[k]), dv[k] = scan_widen<T>(rd[k]);
+    if (it > 0) scan_load<T, false, OFF, true, false>(a, cl, sbeg + it - K, rg, rd, none);
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-      const bool live = s + k < cl.n;
       float aa, c;
-      scan_gate(scan_widen<T>(live ? rg[k] : pad), aa, c);
-      Rl = aa * (scan_widen<T>(live ? rd[k] : T(0)) + Rl);
+      scan_gate<sizeof(T) == 4>(gv[k], aa, c);
+      Rl = aa * (dv[k] + Rl);
       P *= aa;
     }
   }
@@ -213,7 +191,7 @@ __global__ void __launch_bounds__(64 * kScanAggWaves) k_scan_cols_bwd_agg(ScanAr
       r = fmaf(m.x, r, m.y);
       p *= m.x;
     }
-    if (seg == a.segs - 1) {
+    if (seg == a.maps - 1) {
       r = fmaf(p, a.carry_in ? a.carry_in[cl.col] : 0.f, r);
       p = 0.f;
     }
@@ -224,7 +202,7 @@ __global__ void __launch_bounds__(64 * kScanAggWaves) k_scan_cols_bwd_agg(ScanAr
 // ------------------------------------------------------------------ rows
 // As k_scan_rows. A lane's state follows from the kept one of its 32 steps through the maps of
 // the (up to three) lanes before it, or (SELF: one tile holds the row) from h0 through the maps of
-// all lanes before it. CK: u is a checkpoint. AGG: maps of segments 1 .. segs - 1.
+// all lanes before it. CK: u is a checkpoint. AGG: only the maps.
 template <typename T, bool REV, int LANES, bool CK, bool SELF, bool AGG>
 __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   constexpr int E = kScanE;
@@ -241,18 +219,20 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   const int n = scan_steps(a, row);
   const ScanRow<T, REV> rw(row, a.len, n);
   const ScanRow<uint8_t, REV> rwc(row, a.len, n);
-  const int seg = LANES ? (int)blockIdx.y + (AGG ? 1 : 0) : 0, sbeg = seg * a.seg_len;
-  const int send = sbeg + a.seg_len < a.len ? sbeg + a.seg_len : a.len;
+  const int slen = AGG ? a.seg_len / a.fine : a.seg_len;
+  const int seg = LANES ? (int)blockIdx.y + (AGG ? a.fine : 0) : 0, sbeg = seg * slen;
+  const int send = sbeg + slen < a.len ? sbeg + slen : a.len;
+  const int nseg = AGG ? a.maps : a.segs;
   const int tile = LANES ? NW * 64 * E : 64 * E;
   const int lofs = LANES ? (wv * 64 + lane) * E : li * E;
   const T* gp = (const T*)a.g;
   const T* dp = (const T*)a.dh;
 
   float carry = 0.f, carryP = 1.f, h0 = SELF && a.h0 ? a.h0[row] : 0.f;
-  if (seg == a.segs - 1) {
+  if (seg == nseg - 1) {
     carry = a.carry_in ? a.carry_in[row] : 0.f;
   } else if (!AGG) {
-    for (int j = a.segs - 1; j > seg; --j) {
+    for (int j = a.maps - 1; j >= (seg + 1) * a.fine; --j) {
       const float2 m = a.agg[(size_t)j * a.cols + row];
       carry = fmaf(m.x, carry, m.y);
     }
@@ -276,13 +256,18 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
     if constexpr (!AGG) ru.widen(a, rw, s, ev);   // u for now
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      scan_gate(scan_widen<T>(rg[k]), av[k], cv[k]);
+      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], cv[k]);
       dv[k] = scan_widen<T>(rd[k]);
       P *= av[k];
-      if constexpr (!AGG) H = fmaf(av[k], H, cv[k] * ev[k]);
+      if constexpr (!AGG) {
+        ev[k] *= cv[k];
+        H = fmaf(av[k], H, ev[k]);
+      }
     }
+    Rl = dv[E - 1];
 #pragma unroll
-    for (int k = E - 1; k >= 0; --k) Rl = av[k] * (dv[k] + Rl);
+    for (int k = E - 2; k >= 0; --k) Rl = fmaf(av[k + 1], Rl, dv[k]);
+    Rl *= av[0];
     float h = 0.f;
     float ph = P, hh = H, pe, he;
     if constexpr (SELF) {
@@ -342,16 +327,16 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
       if (active && s < a.len) {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-          const float u = ev[k];
-          ev[k] = av[k] * cv[k] * (h - u);
-          h = fmaf(av[k], h, cv[k] * u);
+          const float cu = ev[k];   // (1 - a) u
+          ev[k] = av[k] * fmaf(cv[k], h, -cu);
+          h = fmaf(av[k], h, cu);
         }
 #pragma unroll
         for (int k = E - 1; k >= 0; --k) {
-          const float G = dv[k] + Rt;
+          const float G = k == E - 1 ? dv[k] + Rt : fmaf(av[k + 1 < E ? k + 1 : k], Rt, dv[k]);
           ev[k] *= G;
           cv[k] *= G;
-          Rt = av[k] * G;
+          Rt = G;
         }
         rw.store((T*)a.out0, s, ev);
         rw.store((T*)a.out1, s, cv);
@@ -361,7 +346,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
   const bool writer = LANES ? threadIdx.x == 0 : li == 0;
   if constexpr (AGG) {
     if (writer)
-      a.agg[(size_t)seg * a.cols + row] = make_float2(seg == a.segs - 1 ? 0.f : carryP, carry);
+      a.agg[(size_t)seg * a.cols + row] = make_float2(seg == nseg - 1 ? 0.f : carryP, carry);
   } else {
     if (writer && active && seg == 0 && a.carry_out) a.carry_out[row] = carry;
   }
@@ -376,7 +361,7 @@ hipError_t launch_rows(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     return hipGetLastError();
   }
   if (p.segs > 1) {
-    k_scan_rows_bwd<T, REV, 64, false, false, true><<<dim3(a.cols, p.segs - 1), block, 0, st>>>(a);
+    k_scan_rows_bwd<T, REV, 64, false, false, true><<<dim3(a.cols, (p.segs - 1) * p.fine), block, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -388,12 +373,13 @@ template <typename T, bool CK, bool SELF, typename OFF>
 hipError_t launch_cols(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
   const uint32_t groups = (a.cols + a.cw - 1) / a.cw;
   if (p.segs > 1) {
-    k_scan_cols_bwd_agg<T, OFF><<<dim3(groups, p.segs - 1), 64 * kScanAggWaves,
-                                  kScanAggWaves * a.cw * sizeof(float2), st>>>(a);
+    constexpr int mw = scan_map_waves(false);
+    k_scan_cols_bwd_agg<T, OFF><<<dim3(groups, (p.segs - 1) * p.fine), 64 * mw,
+                                  mw * a.cw * sizeof(float2), st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  static_assert(2 * scan_bwd_waves(false) * 64 * sizeof(RunMap) <= 64 * 1024, "LDS of a launch");
+  static_assert(2 * scan_col_waves(true, false) * 64 * sizeof(RunMap) <= 64 * 1024, "LDS of a launch");
   k_scan_cols_bwd<T, CK, SELF, OFF><<<dim3(groups, p.segs), 64 * p.waves,
                                       2 * p.waves * a.cw * sizeof(RunMap), st>>>(a);
   return hipGetLastError();

@@ -127,7 +127,8 @@ def test_scan_workspace_rules(lib):
     assert q(64 * 192, 784, 1) == 0 and q(4, 32768, 1024) >= 0
     assert q(0, 5, 5) == 0 and q(1, 1 << 31, 1) == 0
     for outer, n, inner in [(1, 1, 1), (1, 1 << 30, 1), (3, 12345, 7), (1, 1 << 20, 65)]:
-        assert q(outer, n, inner) <= 64 * 8 * outer * inner + 4 * outer * inner
+        # the maps stay a small part of the tensor: 12 workgroups per CU at most form them
+        assert q(outer, n, inner) <= (8 * 2 * 12 * 256 + 4) * outer * inner
 
 
 def test_scan_backward_workspace_rules(lib):
