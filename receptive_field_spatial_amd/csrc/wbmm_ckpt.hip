@@ -226,9 +226,10 @@ hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, size_
 }
 
 // ---------------------------------------------------------------------------- backward
-// w = 14 on whole images: the fused kernel of wbmm_ckptbwd.hip. Any other shape: the checkpoints
-// are decoded into fp32 maps in the workspace and the fp32 backward runs on them; bf16 dy and T are
-// widened exactly and dx is rounded to bf16 once at the end.
+// w = 14 on whole images: the fused kernel of wbmm_ckptbwd.hip; other maps, layouts and windows from 2
+// to 16: the one of wbmm_ckptany.hip. Windows of 1 and above 16: the checkpoints are decoded into fp32
+// maps in the workspace and the fp32 backward runs on them; bf16 dy and T are widened exactly and dx
+// is rounded to bf16 once at the end.
 namespace {
 
 bool fast_call(const BwdCkptRequest& r) {
@@ -274,14 +275,18 @@ CkptWs ckpt_ws(const BwdCkptRequest& r) {
 
 }  // namespace
 
-bool backward_ckpt_plan_ok(const BwdCkptRequest& r) { return backward_plan_ok(fp32_request(r)); }
+bool backward_ckpt_plan_ok(const BwdCkptRequest& r) {
+  return any_ckpt_shape(r.B, r.C, r.H, r.W, r.w) || backward_plan_ok(fp32_request(r));
+}
 
 size_t backward_ckpt_workspace(const BwdCkptRequest& r) {
-  return fast_call(r) ? fast_ckpt_workspace(r) : ckpt_ws(r).total;
+  if (fast_call(r)) return fast_ckpt_workspace(r);
+  return any_ckpt_shape(r.B, r.C, r.H, r.W, r.w) ? any_ckpt_workspace(r) : ckpt_ws(r).total;
 }
 
 hipError_t launch_backward_ckpt(const BwdCkptRequest& r, hipStream_t st) {
   if (fast_call(r)) return launch_backward_ckpt_fast(r, st);
+  if (any_ckpt_shape(r.B, r.C, r.H, r.W, r.w)) return launch_backward_ckpt_any(r, st);
   const CkptWs w = ckpt_ws(r);
   const size_t n = (size_t)r.B * r.C * r.H * r.W;
   unsigned char* ws = (unsigned char*)r.ws;

@@ -1,0 +1,311 @@
+// The layer backward from 8-bit checkpoints for any map size, layout and window 2 <= w <= 16 (table
+// input; fp32, or bf16 dy, T and dx), on the pieces of wbmm_ckptbwd.hpp.
+//
+// A workgroup takes some units of 32 windows of one channel, in turn: G gathered window by window
+// (with the mix: the 3 x 3 neighbourhood of every pixel read from dy, through the caches, and the
+// dWmix sums taken on the way), table blocks, dX, G and x transposed to [pixel][window], dT by row
+// pairs onto the workgroup's fp64 partial. Windows past the last, and pixels past the map's edge, are
+// zeros and are not stored.
+#include "wbmm_ckptbwd.hpp"
+
+namespace wbmm {
+
+struct CkptAnyArgs {
+  int H, W, units, per, groups;   // units per channel, units per workgroup, workgroups per channel
+  int nwx, nwin, windows;         // windows per row, per image, in all
+  size_t sb, sc;                  // elements between images, channels, rows, columns
+  int sy, sx;
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const uint8_t* zc;
+  const uint8_t* zs;
+  const void* T;
+  const void* dy;
+  const float* mixw;
+  void* dx;
+  double* partT;
+  double* partW;
+  int fmt, want_dT, want_dW;
+};
+
+namespace {
+
+template <int W>
+struct AnyLds {
+  typedef CkWin<W> C;
+  static constexpr int WP = (W + 1) / 2 * 2;       // floats of a window row
+  static constexpr int DP = W * WP;                // of a window
+  static constexpr int PIX = kWins * C::D;
+  // bytes: G | blocks then x as bf16 (T as fp32 before), or the dT operands, or the tiles | sums,
+  // windows
+  static constexpr int G = (kWins * DP + 16) * 4;  // slots past the last row are read
+  static constexpr int XL = 3 * C::BLK * 2;
+  static constexpr int XB = kWins * DP * 2 > C::L * 4 ? kWins * DP * 2 : (C::L * 4 + 15) / 16 * 16;
+  static constexpr int m2(int a, int b) { return a > b ? a : b; }
+  static constexpr int V = m2(XL + XB, m2(4 * PIX * 2, kWaves * 4 * C::TILE * 4));
+  static constexpr int RED = G + (V + 15) / 16 * 16;
+  static constexpr int WIN = RED + kWaves * 4 * 9 * 4;
+  static constexpr int TOTAL = WIN + kWins * 16;
+};
+
+struct WinAt {
+  size_t base;   // element offset of its image's channel
+  int y0, x0;    // map position of its origin (y0 = H: no such window)
+};
+
+// dX of 16 windows and the output rows of quarter QR.
+template <int W, bool F32, int QR>
+__device__ __forceinline__ void dx_any(const CkptAnyArgs& a, const float* G, const uint16_t* blk,
+                                       const WinAt* wins, int wu, int lane) {
+  constexpr int Y0 = CkWin<W>::y0(QR), NY = CkWin<W>::ny(QR);
+  if constexpr (NY > 0) {
+    const int n = wu * 16 + (lane & 15), x = 4 * (lane >> 4);
+    v4f acc[NY];
+    dx_rows<W, F32, F32 ? 3 : 2, Y0, NY, AnyLds<W>::WP>(G + n * AnyLds<W>::DP, blk, lane, acc);
+    const WinAt w = wins[n];
+#pragma unroll
+    for (int y = 0; y < NY; ++y) {
+      if (w.y0 + Y0 + y >= a.H) continue;
+      const size_t o = w.base + (size_t)(w.y0 + Y0 + y) * a.sy;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (x + r >= W || w.x0 + x + r >= a.W) continue;
+        const size_t at = o + (size_t)(w.x0 + x + r) * a.sx;
+        if constexpr (F32) ((float*)a.dx)[at] = acc[y][r];
+        else ((uint16_t*)a.dx)[at] = f2bf(acc[y][r]);
+      }
+    }
+  }
+}
+
+template <int W, bool F32>
+__global__ void __launch_bounds__(kT)
+    __attribute__((amdgpu_waves_per_eu(W > 10 ? 2 : 4, W > 10 ? 2 : 4)))
+k_bwd_ckpt_any(CkptAnyArgs a) {
+  typedef CkWin<W> C;
+  typedef AnyLds<W> S;
+  constexpr int NT = F32 ? 3 : 1;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem_a[];
+  float* G = (float*)smem_a;
+  unsigned char* V = smem_a + S::G;
+  float* red = (float*)(smem_a + S::RED);
+  WinAt* wins = (WinAt*)(smem_a + S::WIN);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = blockIdx.x / a.groups, u0 = (blockIdx.x % a.groups) * a.per;
+  const int u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
+  const bool mix = a.mixw != nullptr, wantW = mix && a.want_dW;
+  auto dy_at = [&](size_t o) {
+    return F32 ? ((const float*)a.dy)[o] : bf2f(((const uint16_t*)a.dy)[o]);
+  };
+  float wr[9], dw[9];
+#pragma unroll
+  for (int q = 0; q < 9; ++q) {
+    wr[q] = mix ? a.mixw[c * 9 + 8 - q] : 0.f;   // rotated by 180 degrees
+    dw[q] = 0.f;
+  }
+
+  for (int u = u0; u < u1; ++u) {
+    __syncthreads();   // the unit before has left LDS
+    if (tid < kWins) {
+      const int n = u * kWins + tid, b = n / a.nwin, r = n - b * a.nwin, wy = r / a.nwx;
+      WinAt w{(size_t)b * a.sb + (size_t)c * a.sc, wy * W, (r - wy * a.nwx) * W};
+      if (n >= a.windows) w = WinAt{(size_t)c * a.sc, a.H, 0};
+      wins[tid] = w;
+    }
+    float* Tf = (float*)(V + S::XL);
+    for (int q = tid; q < C::L; q += kT)
+      Tf[q] = F32 ? ((const float*)a.T)[(size_t)c * C::L + q]
+                  : bf2f(((const uint16_t*)a.T)[(size_t)c * C::L + q]);
+    __syncthreads();
+    for (int q = tid; q < S::PIX; q += kT) {
+      const int n = q / C::D, p = q - n * C::D, y = p / W, x = p - y * W;
+      const WinAt w = wins[n];
+      const int gy = w.y0 + y, gx = w.x0 + x;
+      float g = 0.f;
+      if (gy < a.H && gx < a.W) {
+        const size_t o = w.base + (size_t)gy * a.sy + (size_t)gx * a.sx;
+        if (!mix) {
+          g = dy_at(o);
+        } else {
+          float d[9];
+#pragma unroll
+          for (int k = 0; k < 9; ++k) {
+            const int dyy = k / 3 - 1, dxx = k % 3 - 1;
+            const bool in = gy + dyy >= 0 && gy + dyy < a.H && gx + dxx >= 0 && gx + dxx < a.W;
+            const float v = dy_at(in ? o + (long long)dyy * a.sy + (long long)dxx * a.sx : o);
+            d[k] = in ? v : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 9; ++k) g = fmaf(wr[k], d[k], g);
+          if (wantW) {
+            const float z = ckpt_value(a.zc, a.zs, o, a.fmt);
+#pragma unroll
+            for (int k = 0; k < 9; ++k) dw[k] = fmaf(z, d[8 - k], dw[k]);
+          }
+        }
+      }
+      G[n * S::DP + y * S::WP + x] = g;
+    }
+    if (a.dx) table_blocks<W, NT>(Tf, (uint32_t*)V, tid);
+    __syncthreads();
+    if (a.dx) {
+      const uint16_t* blk = (const uint16_t*)V;
+      switch (wave >> 1) {
+        case 0: dx_any<W, F32, 0>(a, G, blk, wins, wave & 1, lane); break;
+        case 1: dx_any<W, F32, 1>(a, G, blk, wins, wave & 1, lane); break;
+        case 2: dx_any<W, F32, 2>(a, G, blk, wins, wave & 1, lane); break;
+        default: dx_any<W, F32, 3>(a, G, blk, wins, wave & 1, lane); break;
+      }
+    }
+    if (!a.want_dT) continue;
+
+    uint16_t* xl = (uint16_t*)(V + S::XL);   // over T, which the blocks have been made of
+    for (int q = tid; q < S::PIX; q += kT) {
+      const int n = q / C::D, p = q - n * C::D, y = p / W, x = p - y * W;
+      const WinAt w = wins[n];
+      const int gy = w.y0 + y, gx = w.x0 + x;
+      float v = 0.f;
+      if (gy < a.H && gx < a.W)
+        v = ckpt_value(a.xc, a.xs, w.base + (size_t)gy * a.sy + (size_t)gx * a.sx, a.fmt);
+      xl[n * S::DP + y * S::WP + x] = (uint16_t)pk_bf16(v, 0.f);   // exact
+    }
+    __syncthreads();
+    uint16_t* ops = (uint16_t*)V;
+    constexpr int TI = (C::D * 4 + kT - 1) / kT;
+    u32x4 xt[TI];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int t = tid + i * kT, tt = t < C::D * 4 ? t : 0, g = tt / C::D, p = tt % C::D;
+      const int o = 8 * g * S::DP + p / W * S::WP + p % W;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        xt[i][j] = (uint32_t)xl[o + 2 * j * S::DP] | ((uint32_t)xl[o + (2 * j + 1) * S::DP] << 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int t = tid + i * kT, tt = t < C::D * 4 ? t : 0, g = tt / C::D, p = tt % C::D;
+      const int o = 8 * g * S::DP + p / W * S::WP + p % W;
+      u32x4 part[3];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q3[3];
+        split2<3>(G[o + 2 * j * S::DP], G[o + (2 * j + 1) * S::DP], q3);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) part[q][j] = q3[q];
+      }
+      if (t < C::D * 4) {
+        const int at = slot_of(p, g);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *(u32x4*)(ops + q * S::PIX + at) = part[q];
+        *(u32x4*)(ops + 3 * S::PIX + at) = xt[i];
+      }
+    }
+    __syncthreads();
+    v4f acc[4];
+    float* scr = (float*)V + wave * 4 * C::TILE;
+    double* pT = a.partT + (size_t)blockIdx.x * C::L;
+#define WBMM_CK_WAVE(Q)                          \
+  case Q:                                        \
+    dt_rows<W, Q, 3>(ops, lane, acc);            \
+    __syncthreads();                             \
+    dt_partial<W, Q>(scr, acc, pT, lane, u > u0); \
+    break;
+    switch (wave) {   // every wave has read its operands before the tiles go over them
+      WBMM_CK_WAVE(0) WBMM_CK_WAVE(1) WBMM_CK_WAVE(2) WBMM_CK_WAVE(3)
+      WBMM_CK_WAVE(4) WBMM_CK_WAVE(5) WBMM_CK_WAVE(6) WBMM_CK_WAVE(7)
+    }
+#undef WBMM_CK_WAVE
+  }
+  if (wantW) {
+#pragma unroll
+    for (int q = 0; q < 9; ++q) {
+      const float s = row_sum_f32_last(dw[q]);
+      if ((lane & 15) == 15) red[(wave * 4 + (lane >> 4)) * 9 + q] = s;
+    }
+    __syncthreads();
+    if (tid < 9) {
+      double s = 0.0;
+#pragma unroll
+      for (int w = 0; w < kWaves * 4; ++w) s += (double)red[w * 9 + tid];
+      a.partW[(size_t)blockIdx.x * 9 + tid] = s;
+    }
+  }
+}
+
+template <int W, bool F32>
+hipError_t launch_any_w(const CkptAnyArgs& a, int blocks, hipStream_t st) {
+  static_assert(AnyLds<W>::TOTAL <= kLdsPerCu, "one workgroup per CU at least");
+  constexpr int lds = AnyLds<W>::TOTAL;
+  auto fn = k_bwd_ckpt_any<W, F32>;
+  const hipError_t e =
+      hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  return e != hipSuccess ? e : launch_main(fn, dim3(blocks), dim3(kT), lds, st, a);
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Units per channel, and how they are dealt: about 2048 workgroups and at most 96 a channel, so that
+// the partials stay few (one thread adds a table entry's).
+void any_units(const BwdCkptRequest& r, CkptAnyArgs& a) {
+  a.nwx = (r.W + r.w - 1) / r.w;
+  a.nwin = a.nwx * ((r.H + r.w - 1) / r.w);
+  a.windows = r.B * a.nwin;
+  a.units = (a.windows + kWins - 1) / kWins;
+  const long long all = (long long)a.units * r.C;
+  const int most = (a.units + 95) / 96;
+  a.per = (int)((all + 2047) / 2048);
+  if (a.per < most) a.per = most;
+  a.groups = (a.units + a.per - 1) / a.per;
+}
+
+}  // namespace
+
+bool any_ckpt_shape(int B, int C, int H, int W, int w) {
+  const long long nwin = (long long)((W + w - 1) / w) * ((H + w - 1) / w);
+  return w >= 2 && w <= 16 && B * nwin < (1ll << 31) - kWins;
+}
+
+size_t any_ckpt_workspace(const BwdCkptRequest& r) {
+  CkptAnyArgs a{};
+  any_units(r, a);
+  const size_t L = (size_t)(2 * r.w - 1) * (2 * r.w - 1);
+  return up256((size_t)r.C * a.groups * L * 8) + up256((size_t)r.C * a.groups * 9 * 8);
+}
+
+hipError_t launch_backward_ckpt_any(const BwdCkptRequest& r, hipStream_t st) {
+  CkptAnyArgs a{};
+  any_units(r, a);
+  const int L = (2 * r.w - 1) * (2 * r.w - 1);
+  a.H = r.H;
+  a.W = r.W;
+  a.sb = (size_t)r.C * r.H * r.W;
+  a.sc = r.layout == 0 ? (size_t)r.H * r.W : 1;
+  a.sx = r.layout == 0 ? 1 : r.C;
+  a.sy = r.W * a.sx;
+  a.xc = r.xc; a.xs = r.xs; a.zc = r.zc; a.zs = r.zs;
+  a.T = r.T; a.dy = r.dy; a.mixw = r.mixw; a.dx = r.dx;
+  a.partT = (double*)r.ws;
+  a.partW = (double*)((unsigned char*)r.ws + up256((size_t)r.C * a.groups * L * 8));
+  a.fmt = r.fmt;
+  a.want_dT = r.dT != nullptr;
+  a.want_dW = r.mixw && r.dmixw;
+  const int blocks = r.C * a.groups;
+  hipError_t e = hipErrorInvalidValue;
+  switch (r.w) {
+#define WBMM_CK_W(N)                                                                  \
+  case N:                                                                             \
+    e = r.bf16 ? launch_any_w<N, false>(a, blocks, st) : launch_any_w<N, true>(a, blocks, st); \
+    break;
+    WBMM_CK_W(2) WBMM_CK_W(3) WBMM_CK_W(4) WBMM_CK_W(5) WBMM_CK_W(6) WBMM_CK_W(7) WBMM_CK_W(8)
+    WBMM_CK_W(9) WBMM_CK_W(10) WBMM_CK_W(11) WBMM_CK_W(12) WBMM_CK_W(13) WBMM_CK_W(14)
+    WBMM_CK_W(15) WBMM_CK_W(16)
+#undef WBMM_CK_W
+  }
+  if (e != hipSuccess || (!a.want_dT && !a.want_dW)) return e;
+  return launch_bwd_reduce(a.partT, a.want_dW ? a.partW : nullptr, a.groups, r.C, L, r.dT,
+                           a.want_dW ? r.dmixw : nullptr, st);
+}
+
+}  // namespace wbmm

@@ -247,6 +247,10 @@ struct BwdCkptRequest {
 bool fast_ckpt_shape(int C, int H, int W, int w, int layout);
 size_t fast_ckpt_workspace(const BwdCkptRequest& r);
 hipError_t launch_backward_ckpt_fast(const BwdCkptRequest& r, hipStream_t st);
+// The kernel for any map and layout, 2 <= w <= 16.
+bool any_ckpt_shape(int B, int C, int H, int W, int w);
+size_t any_ckpt_workspace(const BwdCkptRequest& r);
+hipError_t launch_backward_ckpt_any(const BwdCkptRequest& r, hipStream_t st);
 bool backward_ckpt_plan_ok(const BwdCkptRequest& r);
 size_t backward_ckpt_workspace(const BwdCkptRequest& r);
 hipError_t launch_backward_ckpt(const BwdCkptRequest& r, hipStream_t st);

@@ -201,9 +201,56 @@ def test_backward_ckpt_misaligned_buffers(bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("w", range(1, 18))
+def test_backward_ckpt_every_window(w, bf16):
+    """A ragged map for every window side, with windows of several images in a unit of 32."""
+    check_bwd(3, 2, 2 * w + max(1, w // 2), 3 * w - w // 3, w, True, "e4m3", bf16, seed=w)
+    check_bwd(1, 1, w, w, w, False, "int8", bf16, seed=w)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("B,C,H,W,w", [(40, 70, 17, 15, 3), (3, 1, 200, 210, 2), (64, 3, 30, 45, 7),
+                                       (2, 5, 140, 100, 14), (70, 66, 12, 12, 4)])
+def test_backward_ckpt_many_units(B, C, H, W, w, bf16):
+    """Workgroups that take several units, and channels with many workgroups."""
+    check_bwd(B, C, H, W, w, True, "int8", bf16, seed=w)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("mix", [False, True])
-def test_backward_ckpt_nhwc(bf16, mix):
-    check_bwd(2, 12, 17, 19, 7, mix, "int8", bf16, layout="NHWC")
+@pytest.mark.parametrize("B,C,H,W,w", [(2, 12, 17, 19, 7), (3, 5, 28, 28, 14), (2, 3, 5, 6, 8)])
+def test_backward_ckpt_nhwc(B, C, H, W, w, bf16, mix):
+    check_bwd(B, C, H, W, w, mix, "int8", bf16, layout="NHWC")
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("H,W,w", [(30, 45, 7), (13, 9, 5), (28, 28, 14), (20, 33, 16)])
+def test_backward_ckpt_writes_only_its_outputs(H, W, w, bf16):
+    B, C, G = 3, 2, 61
+    x, z, dy, T, Wm = bwd_inputs(B, C, H, W, w, True, "int8", bf16, "NCHW", 1)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    xc, zc = (R().wbmm_ckpt_pack(dev(a).to(dt)) for a in (x, z))
+    bufs = []
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 2 * G,), 33.0, dtype=dtype, device="cuda")
+        bufs.append(buf)
+        out = buf[G:G + n].view(shape)
+        out.fill_(float("nan"))
+        return out
+
+    L = 2 * w - 1
+    outs = (guarded(dy.shape, dt), guarded((C, L, L), torch.float32), guarded((C, 3, 3), torch.float32))
+    need = R().wbmm_backward_ckpt_workspace_bytes(B, C, H, W, w, dtype=dt, has_mix=True)
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    R().wbmm_backward_ckpt(xc, dev(dy).to(dt), w, dev(T).to(dt), mix_w=dev(Wm), z_ckpt=zc, dx=outs[0],
+                           dT=outs[1], dmix_w=outs[2], workspace=ws[:need])
+    for t in outs:
+        assert torch.isfinite(t.float()).all()
+    for b in bufs:
+        assert torch.all(b[:G] == 33) and torch.all(b[-G:] == 33)
+    assert torch.all(ws[need:] == 77)
 
 
 @pytest.mark.parametrize("bf16", [False, True])
