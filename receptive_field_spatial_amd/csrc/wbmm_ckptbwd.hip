@@ -221,6 +221,20 @@ k_bwd_ckpt(CkptBwdArgs a) {
 #pragma unroll
   for (int j = 0; j < TQ; ++j)
     if (tid + j * kT < kL) Tf[tid + j * kT] = tv[j];
+  // x's codes, in flight across dX
+  uint32_t xw[kIter], xsc[kIter];
+  if (a.want_dT) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int e = 4 * (tid + it * kT), im = e / I::PLANE;
+      const bool in = im < nimg;
+      const uint32_t o = in ? (uint32_t)(im * cp + (e - im * I::PLANE)) : 0u;
+      xw[it] = *(const uint32_t*)(xcu + o);
+      xsc[it] = xsu[(og + o) / kCkptGroup];
+      if (!in) xw[it] = 0, xsc[it] = 127;
+    }
+  }
+
   float* D = MIX ? (float*)U : G;
   uint16_t* Z = (uint16_t*)(U + kPix * 4);
 #pragma unroll
@@ -253,20 +267,6 @@ k_bwd_ckpt(CkptBwdArgs a) {
 #pragma unroll
       for (int w = 0; w < kWaves * 4; ++w) s += (double)red[w * 9 + tid];
       a.partW[(size_t)blockIdx.x * 9 + tid] = s;
-    }
-  }
-
-  // x's codes, in flight across dX
-  uint32_t xw[kIter], xsc[kIter];
-  if (a.want_dT) {
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int e = 4 * (tid + it * kT), im = e / I::PLANE;
-      const bool in = im < nimg;
-      const uint32_t o = in ? (uint32_t)(im * cp + (e - im * I::PLANE)) : 0u;
-      xw[it] = *(const uint32_t*)(xcu + o);
-      xsc[it] = xsu[(og + o) / kCkptGroup];
-      if (!in) xw[it] = 0, xsc[it] = 127;
     }
   }
 

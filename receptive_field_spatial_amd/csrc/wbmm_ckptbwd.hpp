@@ -111,7 +111,7 @@ __device__ __forceinline__ void dx_rows(const float* gw, const uint16_t* blk, in
     const int ns = C::PAIRS - s0 < 4 ? C::PAIRS - s0 : 4;
     // a run's B operands are formed here, not ahead of the quarters' branches together with the
     // other run's (the registers would not hold them)
-    asm volatile("" ::: "memory");
+    if constexpr (NG > 2) asm volatile("" ::: "memory");
     u32x4 Bf[4][NG];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
