@@ -507,11 +507,13 @@ def _opt(name, t, shape, dtype, idx):
     return None if t is None else _need(name, t, shape, dtype, idx)
 
 
-def _out(name, v, shape, dtype, idx):
-    """An output argument: True allocates it, False or None skips it, a tensor is written. Returns
-    the tensor and its address."""
+def _out(name, v, shape, dtype, idx, like=None):
+    """An output argument: True allocates it (like a dense tensor of its shape and dtype, where there
+    is one: the cheaper call), False or None skips it, a tensor is written. Returns the tensor and
+    its address."""
     if v is True:
-        v = _torch().empty(shape, dtype=dtype, device=idx)
+        torch = _torch()
+        v = torch.empty(shape, dtype=dtype, device=idx) if like is None else torch.empty_like(like)
         return v, v.data_ptr()
     if v is False or v is None:
         return None, None
@@ -614,7 +616,7 @@ def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: s
         zc = _need("z codes", z_ckpt[0], shape, u8, idx)
         zs = _need("z scales", z_ckpt[1], scales, u8, idx)
     with _on_stream(stream, idx):
-        dx, dxp = _out("dx", dx, shape, dy.dtype, idx)
+        dx, dxp = _out("dx", dx, shape, dy.dtype, idx, dy)
         dT, dTp = _out("dT", dT, (C, L, L), f32, idx)
         dmix_w, dWp = (None, None) if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), f32, idx)
         ws, wp, wb = _workspace(_backward_ckpt_bytes(B, C, H, W, w, lay, dt, int(mix_w is not None)),
@@ -675,8 +677,8 @@ def wbmm_scan_forward(g, u, dim: int, *, h0=None, lens=None, reverse: bool = Fal
     h0p = _opt("h0", h0, flat, f32, idx)
     lp, n_lens = _scan_lens(lens, idx)
     with _on_stream(stream, idx):
-        h, hp = _out("h", True if h is None else h, shape, dtype, idx)
-        h_last, hlp = _out("h_last", h_last, flat, f32, idx)
+        h, hp = _out("h", True if h is None else h, shape, dtype, idx, g)
+        h_last, hlp = _out("h_last", h_last, flat, f32, idx, h0)
         states, sp = _out("states", states, kept, f32, idx)
         ws, wp, wb = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace,
                                 idx)
@@ -710,9 +712,9 @@ def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str
     dlp = _opt("dh_last", dh_last, flat, f32, idx)
     lp, n_lens = _scan_lens(lens, idx)
     with _on_stream(stream, idx):
-        dg, dgp = _out("dg", True if dg is None else dg, shape, dtype, idx)
-        du, dup = _out("du", True if du is None else du, shape, dtype, idx)
-        dh0, d0p = _out("dh0", dh0, flat, f32, idx)
+        dg, dgp = _out("dg", True if dg is None else dg, shape, dtype, idx, g)
+        du, dup = _out("du", True if du is None else du, shape, dtype, idx, g)
+        dh0, d0p = _out("dh0", dh0, flat, f32, idx, dh_last)
         need = wbmm_scan_backward_workspace_bytes(outer, length, inner, states is not None)
         ws, wp, wb = _workspace(need, workspace, idx)
         _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode, gp,

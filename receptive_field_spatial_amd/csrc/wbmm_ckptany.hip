@@ -13,8 +13,7 @@ namespace wbmm {
 struct CkptAnyArgs {
   int H, W, units, per, groups;   // units per channel, units per workgroup, workgroups per channel
   int nwx, nwin, windows;         // windows per row, per image, in all
-  size_t sb, sc;                  // elements between images, channels, rows, columns
-  int sy, sx;
+  size_t sb, sc, sy, sx;          // elements between images, channels, rows, columns
   const uint8_t* xc;
   const uint8_t* xs;
   const uint8_t* zc;
@@ -66,11 +65,11 @@ __device__ __forceinline__ void dx_any(const CkptAnyArgs& a, const float* G, con
 #pragma unroll
     for (int y = 0; y < NY; ++y) {
       if (w.y0 + Y0 + y >= a.H) continue;
-      const size_t o = w.base + (size_t)(w.y0 + Y0 + y) * a.sy;
+      const size_t o = w.base + (w.y0 + Y0 + y) * a.sy;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (x + r >= W || w.x0 + x + r >= a.W) continue;
-        const size_t at = o + (size_t)(w.x0 + x + r) * a.sx;
+        const size_t at = o + (w.x0 + x + r) * a.sx;
         if constexpr (F32) ((float*)a.dx)[at] = acc[y][r];
         else ((uint16_t*)a.dx)[at] = f2bf(acc[y][r]);
       }
@@ -124,7 +123,7 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       const int gy = w.y0 + y, gx = w.x0 + x;
       float g = 0.f;
       if (gy < a.H && gx < a.W) {
-        const size_t o = w.base + (size_t)gy * a.sy + (size_t)gx * a.sx;
+        const size_t o = w.base + gy * a.sy + gx * a.sx;
         if (!mix) {
           g = dy_at(o);
         } else {
@@ -133,7 +132,7 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
           for (int k = 0; k < 9; ++k) {
             const int dyy = k / 3 - 1, dxx = k % 3 - 1;
             const bool in = gy + dyy >= 0 && gy + dyy < a.H && gx + dxx >= 0 && gx + dxx < a.W;
-            const float v = dy_at(in ? o + (long long)dyy * a.sy + (long long)dxx * a.sx : o);
+            const float v = dy_at(in ? o + dyy * (long long)a.sy + dxx * (long long)a.sx : o);
             d[k] = in ? v : 0.f;
           }
 #pragma unroll
@@ -167,7 +166,7 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       const int gy = w.y0 + y, gx = w.x0 + x;
       float v = 0.f;
       if (gy < a.H && gx < a.W)
-        v = ckpt_value(a.xc, a.xs, w.base + (size_t)gy * a.sy + (size_t)gx * a.sx, a.fmt);
+        v = ckpt_value(a.xc, a.xs, w.base + gy * a.sy + gx * a.sx, a.fmt);
       xl[n * S::DP + y * S::WP + x] = (uint16_t)pk_bf16(v, 0.f);   // exact
     }
     __syncthreads();

@@ -170,6 +170,15 @@ def test_scan_offsets_past_32_bits(shape):
                                          h0=st[-1:, a // 32].contiguous())
         assert same(dg[-1:, a:b][:, keep], x[:, keep]) and same(du[-1:, a:b][:, keep], y[:, keep])
     assert torch.allclose(d0[-1:], z, rtol=1e-4, atol=1e-5)
+    # the same from a checkpoint of u, whose codes and scales lie as far out
+    ck = R().wbmm_ckpt_pack(u)
+    u.copy_(R().wbmm_ckpt_unpack(*ck, dtype=torch.bfloat16))
+    want = R().wbmm_scan_backward(g, st, dh, 1, u=u, dg=dg, du=du)
+    tail = [t[-1:, -4000:].clone() for t in want[:2]]
+    dg.zero_(), du.zero_()
+    R().wbmm_scan_backward(g, st, dh, 1, u_ckpt=ck, dg=dg, du=du)
+    for t, v in zip(tail, (dg, du)):
+        assert same(t, v[-1:, -4000:])
 
 
 @pytest.mark.parametrize("bf16", [False, True])
