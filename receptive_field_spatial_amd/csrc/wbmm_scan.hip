@@ -346,6 +346,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   p.lanes = 64;
   p.cw = p.run = p.fine = 1;
   p.wide = cols * len * es >= (1ll << 32);
+  const bool small = cols * len <= (1 << 22);
   long long piece, units;   // steps of a wave's tile; workgroups without segments
   int least = 1, most = kScanWaves;
   if (p.rows) {
@@ -359,17 +360,24 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     piece = 64 * kScanE;
     units = outer;
   } else {
+    most = scan_col_waves(kind, ck || (kind && p.wide));
     // Columns per wave: 64, fewer where that leaves CUs without a workgroup: down to a memory line of
     // 128 bytes (with 32 bytes the address units were the limit, 490 against 400 us for the backward
     // of 4 x 32768 x 1024 bf16), or to 32 bytes where little data makes latency the limit.
-    const int bytes = cols * len <= (1 << 22) ? 32 : 128;
-    const int low = scan_pow2(std::min<int64_t>(cols, bytes / es));
+    const int low = scan_pow2(std::min<int64_t>(cols, (small ? 32 : 128) / es));
     p.cw = scan_pow2(std::min<int64_t>(cols, 64));
     while (p.cw > low && (cols + p.cw - 1) / p.cw < kCus && 64 / p.cw * kScanK < len) p.cw /= 2;
+    // Little data: fewer still where that leaves two tiles (one for a backward without states, which
+    // then needs no other launch).
+    if (small) {
+      const long long reach = (long long)(kind == 2 ? 1 : 2) * most * 64 * kScanK;   // at one column
+      int cw = p.cw;
+      while (cw > 1 && reach / cw < len) cw /= 2;
+      if (reach / cw >= len) p.cw = cw;
+    }
     p.run = std::max(1, 128 / (p.cw * es));
     piece = (64 / p.cw) * kScanK;
     units = (cols + p.cw - 1) / p.cw;
-    most = scan_col_waves(kind, ck || (kind && p.wide));
     if (kind && p.cw == 64) least = 2;   // waves pair up for the kept states
   }
   const long long pieces = (len + piece - 1) / piece;
@@ -378,7 +386,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   if (pieces <= 2 || (kind == 2 && pieces <= most)) p.waves = (int)std::max<long long>(least, pieces);
   if (least == 2) p.waves += p.waves & 1;
   p.self = pieces <= p.waves;
-  if (units < kCus * 3 / 4) {
+  if (units < kCus * 3 / 4 && !(small && pieces <= 4 * most)) {   // four tiles cost less than a launch
     // segments of whole 16 pieces, which the tiles of 8 or 16 waves divide
     const long long step = 16 * piece, steps = (len + step - 1) / step;
     const long long segs = std::min<long long>({(kCus + units - 1) / units, steps, 64});

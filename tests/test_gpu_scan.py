@@ -194,10 +194,19 @@ def test_scan_backward_without_states(O, L, I, reverse, lens, bf16):
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("O,L,I", [(1, 20000, 1), (2, 9001, 1), (1, 12000, 3), (1, 4097, 192)])
 def test_scan_long_few_columns(O, L, I, bf16):
-    """The axis runs in segments here."""
-    assert R().wbmm_scan_forward_workspace_bytes(O, L, I) > 0
     run_case(O, L, I, bf16, False, seed=1)
-    run_case(O, L, I, bf16, True, lens=[L - 700] * O, seed=2)
+    run_case(O, L, I, bf16, True, lens=[L - 700] * O, seed=2, recompute=True)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("O,L,I,lens", [(1, 70001, 1, None), (2, 40000, 1, [40000, 333]),
+                                        (1, 70000, 2, [50000]), (1, 33000, 130, None)])
+def test_scan_in_segments(O, L, I, lens, bf16):
+    """Long axes of few columns run in segments, with the maps' launch before the second."""
+    assert R().wbmm_scan_forward_workspace_bytes(O, L, I) > 0
+    assert R().wbmm_scan_backward_workspace_bytes(O, L, I, True) > 0
+    run_case(O, L, I, bf16, False, lens=lens, seed=1)
+    run_case(O, L, I, bf16, True, lens=lens, seed=2, ckpt="int8", recompute=True)
 
 
 def test_scan_without_initial_state_and_extreme_gates():
@@ -238,7 +247,8 @@ def test_scan_nan_stays_in_its_column():
             t[idx] = 0.0
 
 
-@pytest.mark.parametrize("O,L,I", [(8, 1, 192), (5, 37, 1), (1, 9000, 1), (1, 3000, 4), (4, 70, 3)])
+@pytest.mark.parametrize("O,L,I", [(8, 1, 192), (5, 37, 1), (1, 9000, 1), (1, 3000, 4), (4, 70, 3),
+                                   (1, 70000, 1), (1, 70000, 2)])
 def test_scan_state_updated_in_place(O, L, I):
     g, u, _, h0, _ = draw((O, L, I), False, 6)
     gd, ud = dev(g), dev(u)
@@ -273,7 +283,8 @@ def test_scan_any_dimension(dim):
 
 
 @pytest.mark.parametrize("O,L,I,bf16", [(3, 130, 1, False), (2, 70, 5, True), (3, 77, 4, True),
-                                        (1, 9000, 1, True), (1, 3000, 3, False), (4, 1, 9, True)])
+                                        (1, 9000, 1, True), (1, 3000, 3, False), (4, 1, 9, True),
+                                        (1, 70000, 1, False), (1, 66000, 2, True)])
 def test_scan_writes_only_its_outputs(O, L, I, bf16):
     dt = torch.bfloat16 if bf16 else torch.float32
     g, u, dh, h0, dl = draw((O, L, I), bf16, 5)
@@ -326,7 +337,7 @@ def test_scan_writes_only_its_outputs(O, L, I, bf16):
 
 
 def test_scan_stream_and_graph():
-    for shape in ((6, 300, 1), (2, 100, 20), (1, 9000, 2)):
+    for shape in ((6, 300, 1), (2, 100, 20), (1, 9000, 2), (1, 70000, 2), (1, 70000, 1)):
         g, u, dh, h0, dl = (dev(a) for a in draw(shape, False, 1))
 
         def both(stream=None):
