@@ -7,7 +7,6 @@ There is no CPU fallback: if the library is missing or cannot load, calls raise 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -478,28 +477,24 @@ def _fmt_code(fmt: str) -> int:
 # and hand back its address.
 def _device(name, t) -> int:
     """The device of a call, from one of its tensors: the current one."""
-    if t is None:
-        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
-    idx = t.get_device()
-    if idx < 0:
-        raise WbmmError(WBMM_E_INVALID, f"{name} must be on the GPU")
-    if idx != _torch()._C._cuda_getDevice():
-        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, which is not the current device")
+    idx = -1 if t is None else t.get_device()
+    if idx < 0 or idx != _torch()._C._cuda_getDevice():
+        why = ("is required" if t is None else "must be on the GPU" if idx < 0 else
+               f"is on {t.device}, which is not the current device")
+        raise WbmmError(WBMM_E_INVALID, f"{name} {why}")
     return idx
 
 
 def _need(name, t, shape, dtype, idx):
     """Address of a tensor argument of this shape and dtype, dense, on device idx."""
-    if t is None:
-        raise WbmmError(WBMM_E_INVALID, f"{name} is required")
-    if t.shape != shape:
-        raise WbmmError(WBMM_E_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise WbmmError(WBMM_E_INVALID, f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != idx:
-        raise WbmmError(WBMM_E_INVALID, f"{name} is on {t.device}, not on GPU {idx}")
-    if not t.is_contiguous():
-        raise WbmmError(WBMM_E_INVALID, f"{name} must be contiguous")
+    if (t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != idx
+            or not t.is_contiguous()):
+        why = ("is required" if t is None else
+               f"must have shape {tuple(shape)}, got {tuple(t.shape)}" if t.shape != shape else
+               f"must be {dtype}, got {t.dtype}" if t.dtype is not dtype else
+               f"is on {t.device}, not on GPU {idx}" if t.get_device() != idx else
+               "must be contiguous")
+        raise WbmmError(WBMM_E_INVALID, f"{name} {why}")
     return t.data_ptr()
 
 
@@ -520,15 +515,13 @@ def _out(name, v, shape, dtype, idx, like=None):
     return v, _need(name, v, shape, dtype, idx)
 
 
-def _raw_stream(stream, idx) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream)
+def _current_stream(idx) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(idx)
 
 
-def _on_stream(stream, idx):
-    """Allocations of a call belong to the stream that the call runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
-    cuda = _torch().cuda
+def _on_stream(stream, name, t):
+    """Makes the call's stream the current one, so that what it allocates belongs to that stream."""
+    idx, cuda = _device(name, t), _torch().cuda
     if not isinstance(stream, cuda.Stream):
         raw = _stream(stream)
         stream = cuda.ExternalStream(raw, device=idx) if raw else cuda.default_stream(idx)
@@ -555,27 +548,31 @@ def _ckpt_scales(n: int) -> int:
 def wbmm_ckpt_pack(x, *, fmt: str = "int8", codes=None, scales=None, stream=None):
     """Packs x (fp32 or bf16, any shape) into an 8-bit checkpoint: (codes, scales), codes uint8 in
     x's shape, scales uint8 with one entry per WBMM_CKPT_GROUP elements in memory order."""
+    if stream is not None:
+        with _on_stream(stream, "x", x):
+            return wbmm_ckpt_pack(x, fmt=fmt, codes=codes, scales=scales)
     u8 = _torch().uint8
     code, dt, idx = _fmt_code(fmt), _dtype_code(x.dtype), _device("x", x)
     xp, n = _need("x", x, x.shape, x.dtype, idx), x.numel()
-    with _on_stream(stream, idx):
-        codes, cp = _out("codes", True if codes is None else codes, x.shape, u8, idx)
-        scales, sp = _out("scales", True if scales is None else scales, (_ckpt_scales(n),), u8, idx)
-        _check(_lib().wbmm_ckpt_pack(xp, n, dt, code, cp, sp, _raw_stream(stream, idx)))
+    codes, cp = _out("codes", True if codes is None else codes, x.shape, u8, idx)
+    scales, sp = _out("scales", True if scales is None else scales, (_ckpt_scales(n),), u8, idx)
+    _check(_lib().wbmm_ckpt_pack(xp, n, dt, code, cp, sp, _current_stream(idx)))
     return codes, scales
 
 
 def wbmm_ckpt_unpack(codes, scales, *, fmt: str = "int8", dtype=None, out=None, stream=None):
     """The values of a checkpoint in `dtype` (fp32 by default, or out's)."""
+    if stream is not None:
+        with _on_stream(stream, "codes", codes):
+            return wbmm_ckpt_unpack(codes, scales, fmt=fmt, dtype=dtype, out=out)
     torch = _torch()
     code, idx = _fmt_code(fmt), _device("codes", codes)
     dtype = dtype or (torch.float32 if out is None else out.dtype)
     dt, n = _dtype_code(dtype), codes.numel()
     cp = _need("codes", codes, codes.shape, torch.uint8, idx)
     sp = _need("scales", scales, (_ckpt_scales(n),), torch.uint8, idx)
-    with _on_stream(stream, idx):
-        out, xp = _out("out", True if out is None else out, codes.shape, dtype, idx)
-        _check(_lib().wbmm_ckpt_unpack(cp, sp, n, dt, code, xp, _raw_stream(stream, idx)))
+    out, xp = _out("out", True if out is None else out, codes.shape, dtype, idx)
+    _check(_lib().wbmm_ckpt_unpack(cp, sp, n, dt, code, xp, _current_stream(idx)))
     return out
 
 
@@ -598,6 +595,10 @@ def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: s
     scales) that wbmm_ckpt_pack returned for the maps (z_ckpt exactly with mix_w). dy and T are
     both fp32 or both bf16. Returns (dx in dy's dtype, dT fp32, dmix_w fp32); an output passed as
     False is skipped."""
+    if stream is not None:
+        with _on_stream(stream, "dy", dy):
+            return wbmm_backward_ckpt(x_ckpt, dy, w, T, mix_w, z_ckpt, fmt=fmt, layout=layout, dx=dx,
+                                      dT=dT, dmix_w=dmix_w, workspace=workspace)
     torch = _torch()
     idx = _device("dy", dy)
     B, C, H, W = _bchw(dy, layout)
@@ -615,14 +616,13 @@ def wbmm_backward_ckpt(x_ckpt, dy, w: int, T, mix_w=None, z_ckpt=None, *, fmt: s
         mp = _need("mix_w", mix_w, (C, 3, 3), f32, idx)
         zc = _need("z codes", z_ckpt[0], shape, u8, idx)
         zs = _need("z scales", z_ckpt[1], scales, u8, idx)
-    with _on_stream(stream, idx):
-        dx, dxp = _out("dx", dx, shape, dy.dtype, idx, dy)
-        dT, dTp = _out("dT", dT, (C, L, L), f32, idx)
-        dmix_w, dWp = (None, None) if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), f32, idx)
-        ws, wp, wb = _workspace(_backward_ckpt_bytes(B, C, H, W, w, lay, dt, int(mix_w is not None)),
-                                workspace, idx)
-        _check(_lib().wbmm_backward_ckpt(B, C, H, W, w, lay, dt, fcode, xc, xs, Tp, mp, zc, zs, dyp,
-                                         dxp, dTp, dWp, wp, wb, _raw_stream(stream, idx)))
+    dx, dxp = _out("dx", dx, shape, dy.dtype, idx, dy)
+    dT, dTp = _out("dT", dT, (C, L, L), f32, idx)
+    dmix_w, dWp = (None, None) if mix_w is None else _out("dmix_w", dmix_w, (C, 3, 3), f32, idx)
+    ws, wp, wb = _workspace(_backward_ckpt_bytes(B, C, H, W, w, lay, dt, int(mix_w is not None)),
+                            workspace, idx)
+    _check(_lib().wbmm_backward_ckpt(B, C, H, W, w, lay, dt, fcode, xc, xs, Tp, mp, zc, zs, dyp,
+                                     dxp, dTp, dWp, wp, wb, _current_stream(idx)))
     return dx, dT, dmix_w
 
 
@@ -670,20 +670,23 @@ def wbmm_scan_forward(g, u, dim: int, *, h0=None, lens=None, reverse: bool = Fal
     states: True allocates them, a tensor is written (h_last may be h0), False skips them; states
     (fp32, `dim` divided by WBMM_SCAN_CHUNK and rounded up) is what wbmm_scan_backward starts
     from. Returns (h, h_last, states)."""
+    if stream is not None:
+        with _on_stream(stream, "g", g):
+            return wbmm_scan_forward(g, u, dim, h0=h0, lens=lens, reverse=reverse, h=h,
+                                     h_last=h_last, states=states, workspace=workspace)
     f32, dtype, shape = _torch().float32, g.dtype, g.shape
     dt, idx = _dtype_code(dtype), _device("g", g)
     outer, length, inner, flat, kept = _scan_sizes(shape, dim)
     gp, up = _need("g", g, shape, dtype, idx), _need("u", u, shape, dtype, idx)
     h0p = _opt("h0", h0, flat, f32, idx)
     lp, n_lens = _scan_lens(lens, idx)
-    with _on_stream(stream, idx):
-        h, hp = _out("h", True if h is None else h, shape, dtype, idx, g)
-        h_last, hlp = _out("h_last", h_last, flat, f32, idx, h0)
-        states, sp = _out("states", states, kept, f32, idx)
-        ws, wp, wb = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace,
-                                idx)
-        _check(_lib().wbmm_scan_forward(outer, length, inner, dt, int(bool(reverse)), gp, up, h0p,
-                                        lp, n_lens, hp, hlp, sp, wp, wb, _raw_stream(stream, idx)))
+    h, hp = _out("h", True if h is None else h, shape, dtype, idx, g)
+    h_last, hlp = _out("h_last", h_last, flat, f32, idx, h0)
+    states, sp = _out("states", states, kept, f32, idx)
+    ws, wp, wb = _workspace(wbmm_scan_forward_workspace_bytes(outer, length, inner), workspace,
+                            idx)
+    _check(_lib().wbmm_scan_forward(outer, length, inner, dt, int(bool(reverse)), gp, up, h0p,
+                                    lp, n_lens, hp, hlp, sp, wp, wb, _current_stream(idx)))
     return h, h_last, states
 
 
@@ -695,6 +698,11 @@ def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str
     u: the forward's u, or u_ckpt: its checkpoint (codes, scales) in `fmt`. dh: gradient of h;
     dh_last: fp32 gradient of h_last, or None. Returns (dg, du, dh0), dg and du in g's dtype and 0
     past a sequence's end, dh0 fp32 (False skips it)."""
+    if stream is not None:
+        with _on_stream(stream, "g", g):
+            return wbmm_scan_backward(g, states, dh, dim, u=u, u_ckpt=u_ckpt, fmt=fmt, h0=h0,
+                                      dh_last=dh_last, lens=lens, reverse=reverse, dg=dg, du=du,
+                                      dh0=dh0, workspace=workspace)
     torch = _torch()
     f32, dtype, shape = torch.float32, g.dtype, g.shape
     dt, idx = _dtype_code(dtype), _device("g", g)
@@ -711,13 +719,12 @@ def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str
     sp, h0p = _opt("states", states, kept, f32, idx), _opt("h0", h0, flat, f32, idx)
     dlp = _opt("dh_last", dh_last, flat, f32, idx)
     lp, n_lens = _scan_lens(lens, idx)
-    with _on_stream(stream, idx):
-        dg, dgp = _out("dg", True if dg is None else dg, shape, dtype, idx, g)
-        du, dup = _out("du", True if du is None else du, shape, dtype, idx, g)
-        dh0, d0p = _out("dh0", dh0, flat, f32, idx, dh_last)
-        need = wbmm_scan_backward_workspace_bytes(outer, length, inner, states is not None)
-        ws, wp, wb = _workspace(need, workspace, idx)
-        _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode, gp,
-                                         up, us, sp, h0p, dhp, dlp, lp, n_lens, dgp, dup, d0p, wp,
-                                         wb, _raw_stream(stream, idx)))
+    dg, dgp = _out("dg", True if dg is None else dg, shape, dtype, idx, g)
+    du, dup = _out("du", True if du is None else du, shape, dtype, idx, g)
+    dh0, d0p = _out("dh0", dh0, flat, f32, idx, dh_last)
+    need = wbmm_scan_backward_workspace_bytes(outer, length, inner, states is not None)
+    ws, wp, wb = _workspace(need, workspace, idx)
+    _check(_lib().wbmm_scan_backward(outer, length, inner, dt, int(bool(reverse)), fcode, gp,
+                                     up, us, sp, h0p, dhp, dlp, lp, n_lens, dgp, dup, d0p, wp,
+                                     wb, _current_stream(idx)))
     return dg, du, dh0
