@@ -354,6 +354,9 @@ wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_
  *          dT and dmix_w are fp32 in both.
  * x_codes, x_scales, z_codes, z_scales: as wbmm_ckpt_pack writes them; z_* exactly with mix_w.
  * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned.
+ * An fp32 operand enters the products as the sum of three bf16 numbers, which an infinity has not,
+ * nor has a finite magnitude of (2 - 2^-8) 2^127 or more: such entries of T, or of G (dy after the
+ * mix adjoint), make the results that they reach NaN.
  * Errors as in wbmm_backward; also WBMM_E_INVALID for an unknown fmt.
  */
 size_t wbmm_backward_ckpt_workspace_bytes(int B, int C, int H, int W, int w, int layout, int dtype,

@@ -35,16 +35,16 @@ struct AnyLds {
   static constexpr int WP = (W + 1) / 2 * 2;       // floats of a window row
   static constexpr int DP = W * WP;                // of a window
   static constexpr int PIX = kWins * C::D;
-  // bytes: G | blocks then x as bf16 (T as fp32 before), or the dT operands, or the tiles | sums,
-  // windows
+  // bytes: G | blocks then x as bf16, or the dT operands, or the tiles | sums, windows, T as fp32
   static constexpr int G = (kWins * DP + 16) * 4;  // slots past the last row are read
   static constexpr int XL = 3 * C::BLK * 2;
-  static constexpr int XB = kWins * DP * 2 > C::L * 4 ? kWins * DP * 2 : (C::L * 4 + 15) / 16 * 16;
+  static constexpr int XB = kWins * DP * 2;
   static constexpr int m2(int a, int b) { return a > b ? a : b; }
   static constexpr int V = m2(XL + XB, m2(4 * PIX * 2, kWaves * 4 * C::TILE * 4));
   static constexpr int RED = G + (V + 15) / 16 * 16;
   static constexpr int WIN = RED + kWaves * 4 * 9 * 4;
-  static constexpr int TOTAL = WIN + kWins * 16;
+  static constexpr int TF = WIN + kWins * 16;
+  static constexpr int TOTAL = TF + (C::L * 4 + 15) / 16 * 16;
 };
 
 struct WinAt {
@@ -77,9 +77,16 @@ __device__ __forceinline__ void dx_any(const CkptAnyArgs& a, const float* G, con
   }
 }
 
+// What bounds it: vector issue and the waits between the six steps of a unit, not memory (13.4 M
+// pixels, w = 3, bf16, no mix: 306 us, 3% of the copy's rate; 64 x 96 x 28 x 28, w = 7, fp32, no mix:
+// 69 us, 12%). Two workgroups of 8 waves share a CU up to w = 10: three or four at w <= 6 spilt
+// (w = 5, fp32 with the mix: 234 us, 284 and 275). Above w = 10 the LDS holds one or two, and they
+// take the registers.
+constexpr int any_waves(int w) { return w > 10 ? 2 : 4; }
+
 template <int W, bool F32>
 __global__ void __launch_bounds__(kT)
-    __attribute__((amdgpu_waves_per_eu(W > 10 ? 2 : 4, W > 10 ? 2 : 4)))
+    __attribute__((amdgpu_waves_per_eu(any_waves(W), any_waves(W))))
 k_bwd_ckpt_any(CkptAnyArgs a) {
   typedef CkWin<W> C;
   typedef AnyLds<W> S;
@@ -112,39 +119,58 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       if (n >= a.windows) w = WinAt{(size_t)c * a.sc, a.H, 0};
       wins[tid] = w;
     }
-    float* Tf = (float*)(V + S::XL);
+    float* Tf = (float*)(smem_a + S::TF);
+    uint16_t* xl = (uint16_t*)(V + S::XL);
     for (int q = tid; q < C::L; q += kT)
       Tf[q] = F32 ? ((const float*)a.T)[(size_t)c * C::L + q]
                   : bf2f(((const uint16_t*)a.T)[(size_t)c * C::L + q]);
     __syncthreads();
+    // All loads of a pixel before the first value is used, and no branches between them: one off the
+    // map reads the channel's first element instead, and is zero. With a branch around each
+    // neighbour 265 us at w = 5, 64 x 192 x 28 x 28, fp32 with the mix, so 234; two pixels at once 254
+    // (spills), and equal or worse at the other windows.
+#pragma unroll 1
     for (int q = tid; q < S::PIX; q += kT) {
       const int n = q / C::D, p = q - n * C::D, y = p / W, x = p - y * W;
+      const int at = n * S::DP + y * S::WP + x;
       const WinAt w = wins[n];
       const int gy = w.y0 + y, gx = w.x0 + x;
-      float g = 0.f;
-      if (gy < a.H && gx < a.W) {
-        const size_t o = w.base + gy * a.sy + gx * a.sx;
-        if (!mix) {
-          g = dy_at(o);
-        } else {
-          float d[9];
-#pragma unroll
-          for (int k = 0; k < 9; ++k) {
-            const int dyy = k / 3 - 1, dxx = k % 3 - 1;
-            const bool in = gy + dyy >= 0 && gy + dyy < a.H && gx + dxx >= 0 && gx + dxx < a.W;
-            const float v = dy_at(in ? o + dyy * (long long)a.sy + dxx * (long long)a.sx : o);
-            d[k] = in ? v : 0.f;
-          }
-#pragma unroll
-          for (int k = 0; k < 9; ++k) g = fmaf(wr[k], d[k], g);
-          if (wantW) {
-            const float z = ckpt_value(a.zc, a.zs, o, a.fmt);
-#pragma unroll
-            for (int k = 0; k < 9; ++k) dw[k] = fmaf(z, d[8 - k], dw[k]);
-          }
-        }
+      const bool on = gy < a.H && gx < a.W;
+      const size_t o = on ? w.base + gy * a.sy + gx * a.sx : (size_t)c * a.sc;
+      uint32_t xq, xe, zq, ze;
+      float d[9], g = 0.f;
+      if (a.want_dT) {
+        xq = a.xc[o];
+        xe = a.xs[o / kCkptGroup];
       }
-      G[n * S::DP + y * S::WP + x] = g;
+      if (wantW) {
+        zq = a.zc[o];
+        ze = a.zs[o / kCkptGroup];
+      }
+      if (mix) {
+#pragma unroll
+        for (int k = 0; k < 9; ++k) {
+          const int dyy = k / 3 - 1, dxx = k % 3 - 1;
+          const bool in = on && (unsigned)(gy + dyy) < (unsigned)a.H &&
+                          (unsigned)(gx + dxx) < (unsigned)a.W;
+          const float v = dy_at(in ? o + dyy * (long long)a.sy + dxx * (long long)a.sx : o);
+          d[k] = in ? v : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 9; ++k) g = fmaf(wr[k], d[k], g);
+      } else {
+        g = dy_at(o);
+      }
+      G[at] = on ? g : 0.f;
+      if (a.want_dT) {
+        const float v = ckpt_decode1(xq, a.fmt) * ckpt_factor(xe);
+        xl[at] = (uint16_t)pk_bf16(on ? v : 0.f, 0.f);   // exact
+      }
+      if (wantW) {
+        const float v = ckpt_decode1(zq, a.fmt) * ckpt_factor(ze), z = on ? v : 0.f;
+#pragma unroll
+        for (int k = 0; k < 9; ++k) dw[k] = fmaf(z, d[8 - k], dw[k]);
+      }
     }
     if (a.dx) table_blocks<W, NT>(Tf, (uint32_t*)V, tid);
     __syncthreads();
@@ -159,16 +185,6 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
     }
     if (!a.want_dT) continue;
 
-    uint16_t* xl = (uint16_t*)(V + S::XL);   // over T, which the blocks have been made of
-    for (int q = tid; q < S::PIX; q += kT) {
-      const int n = q / C::D, p = q - n * C::D, y = p / W, x = p - y * W;
-      const WinAt w = wins[n];
-      const int gy = w.y0 + y, gx = w.x0 + x;
-      float v = 0.f;
-      if (gy < a.H && gx < a.W)
-        v = ckpt_value(a.xc, a.xs, w.base + gy * a.sy + gx * a.sx, a.fmt);
-      xl[n * S::DP + y * S::WP + x] = (uint16_t)pk_bf16(v, 0.f);   // exact
-    }
     __syncthreads();
     uint16_t* ops = (uint16_t*)V;
     constexpr int TI = (C::D * 4 + kT - 1) / kT;

@@ -8,6 +8,10 @@
 // Every phase's LDS lies in the same 54 KB beside G's 25 KB, so two workgroups (4 waves per SIMD)
 // share a CU and one's loads and vector work run beside the other's matrix work. Partials are summed
 // in a fixed order by k_bwd_reduce.
+//
+// What bounds it: vector issue (the adjoint, the splits into parts, the fp64 partials), then the
+// matrix cores. Measured at 64 x 192 x 28 x 28 with the mix (kernel alone): fp32 65.4 us, bf16 52.4 us,
+// 115 and 144 TFLOP/s of the formula's products.
 #include "wbmm_ckptbwd.hpp"
 
 namespace wbmm {
