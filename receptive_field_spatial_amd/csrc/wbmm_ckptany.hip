@@ -43,35 +43,46 @@ struct AnyLds {
   static constexpr int V = m2(XL + XB, m2(4 * PIX * 2, kWaves * 4 * C::TILE * 4));
   static constexpr int RED = G + (V + 15) / 16 * 16;
   static constexpr int WIN = RED + kWaves * 4 * 9 * 4;
-  static constexpr int TF = WIN + kWins * 16;
+  static constexpr int TF = WIN + kWins * 16;   // (a WinAt takes 12)
   static constexpr int TOTAL = TF + (C::L * 4 + 15) / 16 * 16;
 };
 
 struct WinAt {
-  size_t base;   // element offset of its image's channel
-  int y0, x0;    // map position of its origin (y0 = H: no such window)
+  uint32_t base;   // element offset of its image's channel from the unit's base
+  int y0, x0;      // map position of its origin (y0 = H: no such window)
 };
+
+// Element o of p, by a 32-bit byte offset.
+template <typename T>
+__device__ __forceinline__ T at32(const void* p, uint32_t o) {
+  return *(const T*)((const char*)p + o * (uint32_t)sizeof(T));
+}
 
 // dX of 16 windows and the output rows of quarter QR.
 template <int W, bool F32, int QR>
-__device__ __forceinline__ void dx_any(const CkptAnyArgs& a, const float* G, const uint16_t* blk,
-                                       const WinAt* wins, int wu, int lane) {
+__device__ __forceinline__ void dx_any(const CkptAnyArgs& a, size_t ub, const float* G,
+                                       const uint16_t* blk, const WinAt* wins, int wu, int lane) {
   constexpr int Y0 = CkWin<W>::y0(QR), NY = CkWin<W>::ny(QR);
   if constexpr (NY > 0) {
     const int n = wu * 16 + (lane & 15), x = 4 * (lane >> 4);
     v4f acc[NY];
     dx_rows<W, F32, F32 ? 3 : 2, Y0, NY, AnyLds<W>::WP>(G + n * AnyLds<W>::DP, blk, lane, acc);
     const WinAt w = wins[n];
+    constexpr uint32_t ES = F32 ? 4 : 2;
+    char* dxu = (char*)a.dx + ub * ES;
+    const uint32_t sy = (uint32_t)a.sy * ES, sx = (uint32_t)a.sx * ES;
+    const uint32_t o0 = w.base * ES + (w.y0 + Y0) * sy + (w.x0 + x) * sx;
+    const int rows = a.H - w.y0 - Y0;
+    const int cols = (W < a.W - w.x0 ? W : a.W - w.x0) - x;
 #pragma unroll
     for (int y = 0; y < NY; ++y) {
-      if (w.y0 + Y0 + y >= a.H) continue;
-      const size_t o = w.base + (w.y0 + Y0 + y) * a.sy;
+      if (y >= rows) continue;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if (x + r >= W || w.x0 + x + r >= a.W) continue;
-        const size_t at = o + (w.x0 + x + r) * a.sx;
-        if constexpr (F32) ((float*)a.dx)[at] = acc[y][r];
-        else ((uint16_t*)a.dx)[at] = f2bf(acc[y][r]);
+        if (r >= cols) continue;
+        char* at = dxu + (o0 + y * sy + r * sx);
+        if constexpr (F32) *(float*)at = acc[y][r];
+        else *(uint16_t*)at = f2bf(acc[y][r]);
       }
     }
   }
@@ -101,9 +112,6 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
   const int c = blockIdx.x / a.groups, u0 = (blockIdx.x % a.groups) * a.per;
   const int u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
   const bool mix = a.mixw != nullptr, wantW = mix && a.want_dW;
-  auto dy_at = [&](size_t o) {
-    return F32 ? ((const float*)a.dy)[o] : bf2f(((const uint16_t*)a.dy)[o]);
-  };
   float wr[9], dw[9];
 #pragma unroll
   for (int q = 0; q < 9; ++q) {
@@ -113,12 +121,26 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
 
   for (int u = u0; u < u1; ++u) {
     __syncthreads();   // the unit before has left LDS
+    // the unit's base: its first image's channel, down to a group of the checkpoint; the host admits
+    // images of which 33 stay below 2^32 bytes
+    const int b0 = (int)((unsigned)(u * kWins) / (unsigned)a.nwin);
+    const size_t first = (size_t)b0 * a.sb + (size_t)c * a.sc;
+    const uint32_t rest = (uint32_t)(first % kCkptGroup);
+    const size_t ub = first - rest;
     if (tid < kWins) {
       const int n = u * kWins + tid, b = n / a.nwin, r = n - b * a.nwin, wy = r / a.nwx;
-      WinAt w{(size_t)b * a.sb + (size_t)c * a.sc, wy * W, (r - wy * a.nwx) * W};
-      if (n >= a.windows) w = WinAt{(size_t)c * a.sc, a.H, 0};
+      WinAt w{(uint32_t)(b - b0) * (uint32_t)a.sb + rest, wy * W, (r - wy * a.nwx) * W};
+      if (n >= a.windows) w = WinAt{rest, a.H, 0};
       wins[tid] = w;
     }
+    const uint8_t* xc = a.xc + ub;
+    const uint8_t* xs = a.xs + ub / kCkptGroup;
+    const uint8_t* zc = a.zc + ub;
+    const uint8_t* zs = a.zs + ub / kCkptGroup;
+    const char* dyu = (const char*)a.dy + ub * (F32 ? 4 : 2);
+    auto dy_at = [&](uint32_t o) {
+      return F32 ? at32<float>(dyu, o) : bf2f(at32<uint16_t>(dyu, o));
+    };
     float* Tf = (float*)(smem_a + S::TF);
     uint16_t* xl = (uint16_t*)(V + S::XL);
     for (int q = tid; q < C::L; q += kT)
@@ -136,25 +158,30 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       const WinAt w = wins[n];
       const int gy = w.y0 + y, gx = w.x0 + x;
       const bool on = gy < a.H && gx < a.W;
-      const size_t o = on ? w.base + gy * a.sy + gx * a.sx : (size_t)c * a.sc;
+      const uint32_t sy = (uint32_t)a.sy, sx = (uint32_t)a.sx;
+      const uint32_t oy = on ? gy * sy : 0, o = w.base + oy + (on ? gx * sx : 0);
       uint32_t xq, xe, zq, ze;
       float d[9], g = 0.f;
       if (a.want_dT) {
-        xq = a.xc[o];
-        xe = a.xs[o / kCkptGroup];
+        xq = xc[o];
+        xe = xs[o / kCkptGroup];
       }
       if (wantW) {
-        zq = a.zc[o];
-        ze = a.zs[o / kCkptGroup];
+        zq = zc[o];
+        ze = zs[o / kCkptGroup];
       }
       if (mix) {
+        const bool up = on && gy > 0, down = on && gy + 1 < a.H;
+        const bool left = on && gx > 0, right = on && gx + 1 < a.W;
+        const uint32_t oc[3] = {left ? o - sx : o, o, right ? o + sx : o};
+        const uint32_t orow[3] = {up ? 0u - sy : 0u, 0u, down ? sy : 0u};
+#pragma unroll
+        for (int k = 0; k < 9; ++k) d[k] = dy_at(oc[k % 3] + orow[k / 3]);
 #pragma unroll
         for (int k = 0; k < 9; ++k) {
-          const int dyy = k / 3 - 1, dxx = k % 3 - 1;
-          const bool in = on && (unsigned)(gy + dyy) < (unsigned)a.H &&
-                          (unsigned)(gx + dxx) < (unsigned)a.W;
-          const float v = dy_at(in ? o + dyy * (long long)a.sy + dxx * (long long)a.sx : o);
-          d[k] = in ? v : 0.f;
+          const bool in = (k / 3 == 0 ? up : k / 3 == 2 ? down : on) &&
+                          (k % 3 == 0 ? left : k % 3 == 2 ? right : on);
+          d[k] = in ? d[k] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 9; ++k) g = fmaf(wr[k], d[k], g);
@@ -177,10 +204,10 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
     if (a.dx) {
       const uint16_t* blk = (const uint16_t*)V;
       switch (wave >> 1) {
-        case 0: dx_any<W, F32, 0>(a, G, blk, wins, wave & 1, lane); break;
-        case 1: dx_any<W, F32, 1>(a, G, blk, wins, wave & 1, lane); break;
-        case 2: dx_any<W, F32, 2>(a, G, blk, wins, wave & 1, lane); break;
-        default: dx_any<W, F32, 3>(a, G, blk, wins, wave & 1, lane); break;
+        case 0: dx_any<W, F32, 0>(a, ub, G, blk, wins, wave & 1, lane); break;
+        case 1: dx_any<W, F32, 1>(a, ub, G, blk, wins, wave & 1, lane); break;
+        case 2: dx_any<W, F32, 2>(a, ub, G, blk, wins, wave & 1, lane); break;
+        default: dx_any<W, F32, 3>(a, ub, G, blk, wins, wave & 1, lane); break;
       }
     }
     if (!a.want_dT) continue;
@@ -279,7 +306,8 @@ void any_units(const BwdCkptRequest& r, CkptAnyArgs& a) {
 
 bool any_ckpt_shape(int B, int C, int H, int W, int w) {
   const long long nwin = (long long)((W + w - 1) / w) * ((H + w - 1) / w);
-  return w >= 2 && w <= 16 && B * nwin < (1ll << 31) - kWins;
+  return w >= 2 && w <= 16 && B * nwin < (1ll << 31) - kWins &&
+         (double)C * H * W * 4 * (kWins + 1) < (double)(1ll << 32);   // a unit's 32-bit offsets
 }
 
 size_t any_ckpt_workspace(const BwdCkptRequest& r) {
