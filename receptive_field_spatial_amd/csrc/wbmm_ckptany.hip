@@ -8,6 +8,8 @@
 // zeros and are not stored.
 #include "wbmm_ckptbwd.hpp"
 
+#include <algorithm>
+
 namespace wbmm {
 
 struct CkptAnyArgs {
@@ -35,7 +37,8 @@ struct AnyLds {
   static constexpr int WP = (W + 1) / 2 * 2;       // floats of a window row
   static constexpr int DP = W * WP;                // of a window
   static constexpr int PIX = kWins * C::D;
-  // bytes: G | blocks then x as bf16, or the dT operands, or the tiles | sums, windows, T as fp32
+  // bytes: G | blocks then x as bf16, or the dT operands, or the tiles | dWmix sums | windows of this
+  // unit and the next | dT so far | T as fp32
   static constexpr int G = (kWins * DP + 16) * 4;  // slots past the last row are read
   static constexpr int XL = 3 * C::BLK * 2;
   static constexpr int XB = kWins * DP * 2;
@@ -43,13 +46,15 @@ struct AnyLds {
   static constexpr int V = m2(XL + XB, m2(4 * PIX * 2, kWaves * 4 * C::TILE * 4));
   static constexpr int RED = G + (V + 15) / 16 * 16;
   static constexpr int WIN = RED + kWaves * 4 * 9 * 4;
-  static constexpr int TF = WIN + kWins * 16;   // (a WinAt takes 12)
+  static constexpr int PT = WIN + 2 * kWins * 16;
+  static constexpr int TF = PT + (C::L * 8 + 15) / 16 * 16;
   static constexpr int TOTAL = TF + (C::L * 4 + 15) / 16 * 16;
 };
 
 struct WinAt {
   uint32_t base;   // element offset of its image's channel from the unit's base
   int y0, x0;      // map position of its origin (y0 = H: no such window)
+  uint32_t pad;
 };
 
 // Element o of p, by a 32-bit byte offset.
@@ -106,7 +111,8 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
   float* G = (float*)smem_a;
   unsigned char* V = smem_a + S::G;
   float* red = (float*)(smem_a + S::RED);
-  WinAt* wins = (WinAt*)(smem_a + S::WIN);
+  double* pT = (double*)(smem_a + S::PT);
+  const float* Tf = (const float*)(smem_a + S::TF);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = blockIdx.x / a.groups, u0 = (blockIdx.x % a.groups) * a.per;
@@ -119,20 +125,35 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
     dw[q] = 0.f;
   }
 
-  for (int u = u0; u < u1; ++u) {
-    __syncthreads();   // the unit before has left LDS
-    // the unit's base: its first image's channel, down to a group of the checkpoint; the host admits
-    // images of which 33 stay below 2^32 bytes
-    const int b0 = (int)((unsigned)(u * kWins) / (unsigned)a.nwin);
+  // A unit's base: its first image's channel, down to a group of the checkpoint; the host admits
+  // images of which 33 stay below 2^32 bytes.
+  auto unit_base = [&](int u, int& b0, uint32_t& rest) {
+    b0 = (int)((unsigned)(u * kWins) / (unsigned)a.nwin);
     const size_t first = (size_t)b0 * a.sb + (size_t)c * a.sc;
-    const uint32_t rest = (uint32_t)(first % kCkptGroup);
-    const size_t ub = first - rest;
-    if (tid < kWins) {
-      const int n = u * kWins + tid, b = n / a.nwin, r = n - b * a.nwin, wy = r / a.nwx;
-      WinAt w{(uint32_t)(b - b0) * (uint32_t)a.sb + rest, wy * W, (r - wy * a.nwx) * W};
-      if (n >= a.windows) w = WinAt{rest, a.H, 0};
-      wins[tid] = w;
-    }
+    rest = (uint32_t)(first % kCkptGroup);
+    return first - rest;
+  };
+  auto find_windows = [&](int u) {
+    if (tid >= kWins || u >= u1) return;
+    int b0;
+    uint32_t rest;
+    unit_base(u, b0, rest);
+    const int n = u * kWins + tid, b = n / a.nwin, r = n - b * a.nwin, wy = r / a.nwx;
+    WinAt w{(uint32_t)(b - b0) * (uint32_t)a.sb + rest, wy * W, (r - wy * a.nwx) * W, 0};
+    if (n >= a.windows) w = WinAt{rest, a.H, 0, 0};
+    ((WinAt*)(smem_a + S::WIN))[(u & 1) * kWins + tid] = w;
+  };
+  for (int q = tid; q < C::L; q += kT)
+    ((float*)(smem_a + S::TF))[q] = F32 ? ((const float*)a.T)[(size_t)c * C::L + q]
+                                        : bf2f(((const uint16_t*)a.T)[(size_t)c * C::L + q]);
+  find_windows(u0);
+
+  for (int u = u0; u < u1; ++u) {
+    __syncthreads();   // the unit before has left LDS; this one's windows (and T) are there
+    const WinAt* wins = (const WinAt*)(smem_a + S::WIN) + (u & 1) * kWins;
+    int b0;
+    uint32_t rest;
+    const size_t ub = unit_base(u, b0, rest);
     const uint8_t* xc = a.xc + ub;
     const uint8_t* xs = a.xs + ub / kCkptGroup;
     const uint8_t* zc = a.zc + ub;
@@ -141,12 +162,7 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
     auto dy_at = [&](uint32_t o) {
       return F32 ? at32<float>(dyu, o) : bf2f(at32<uint16_t>(dyu, o));
     };
-    float* Tf = (float*)(smem_a + S::TF);
     uint16_t* xl = (uint16_t*)(V + S::XL);
-    for (int q = tid; q < C::L; q += kT)
-      Tf[q] = F32 ? ((const float*)a.T)[(size_t)c * C::L + q]
-                  : bf2f(((const uint16_t*)a.T)[(size_t)c * C::L + q]);
-    __syncthreads();
     // All loads of a pixel before the first value is used, and no branches between them: one off the
     // map reads the channel's first element instead, and is zero. With a branch around each
     // neighbour 265 us at w = 5, 64 x 192 x 28 x 28, fp32 with the mix, so 234; two pixels at once 254
@@ -200,6 +216,7 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       }
     }
     if (a.dx) table_blocks<W, NT>(Tf, (uint32_t*)V, tid);
+    find_windows(u + 1);
     __syncthreads();
     if (a.dx) {
       const uint16_t* blk = (const uint16_t*)V;
@@ -247,7 +264,6 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
     __syncthreads();
     v4f acc[4];
     float* scr = (float*)V + wave * 4 * C::TILE;
-    double* pT = a.partT + (size_t)blockIdx.x * C::L;
 #define WBMM_CK_WAVE(Q)                          \
   case Q:                                        \
     dt_rows<W, Q, 3>(ops, lane, acc);            \
@@ -259,6 +275,10 @@ k_bwd_ckpt_any(CkptAnyArgs a) {
       WBMM_CK_WAVE(4) WBMM_CK_WAVE(5) WBMM_CK_WAVE(6) WBMM_CK_WAVE(7)
     }
 #undef WBMM_CK_WAVE
+  }
+  if (a.want_dT) {
+    __syncthreads();
+    for (int q = tid; q < C::L; q += kT) a.partT[(size_t)blockIdx.x * C::L + q] = pT[q];
   }
   if (wantW) {
 #pragma unroll
@@ -288,18 +308,26 @@ hipError_t launch_any_w(const CkptAnyArgs& a, int blocks, hipStream_t st) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Units per channel, and how they are dealt: about 2048 workgroups and at most 96 a channel, so that
-// the partials stay few (one thread adds a table entry's).
+// Units per channel, and how they are dealt: the workgroups per channel (at most 96, since one
+// thread adds a table entry's partials, and about 2048 in all) that leave the least to the slot
+// which gets the most. Of equal ones the most where a CU runs two, whose starts and ends overlap
+// (64 x 192 x 24 x 24, w = 8, bf16 with the mix: 1728 workgroups of 2 units 80 us, 960 of 4 84), and the
+// fewest where it runs one (64 x 64 x 40 x 40, w = 16: 256 of 5 units 111 us, 1152 of one 124).
 void any_units(const BwdCkptRequest& r, CkptAnyArgs& a) {
   a.nwx = (r.W + r.w - 1) / r.w;
   a.nwin = a.nwx * ((r.H + r.w - 1) / r.w);
   a.windows = r.B * a.nwin;
   a.units = (a.windows + kWins - 1) / kWins;
-  const long long all = (long long)a.units * r.C;
-  const int most = (a.units + 95) / 96;
-  a.per = (int)((all + 2047) / 2048);
-  if (a.per < most) a.per = most;
-  a.groups = (a.units + a.per - 1) / a.per;
+  const long long most = std::min<long long>({96, a.units, std::max(1, 2048 / r.C)});
+  const int resident = any_waves(r.w) / 2;   // workgroups that a CU runs at a time
+  const long long slots = 256 * resident;
+  long long best = -1;
+  for (long long g = 1; g <= most; ++g) {
+    const long long per = (a.units + g - 1) / g, used = (a.units + per - 1) / per;
+    const long long turns = (r.C * used + slots - 1) / slots * per;
+    if (best < 0 || turns < best || (turns == best && resident > 1))
+      best = turns, a.per = (int)per, a.groups = (int)used;
+  }
 }
 
 }  // namespace
