@@ -24,7 +24,7 @@ namespace {
 // ------------------------------------------------------------------ columns
 // CK: u is a checkpoint. Without out0 only the states (and the last one) are formed.
 template <typename T, bool CK, typename OFF>
-__global__ void __launch_bounds__(64 * scan_col_waves(false, CK))
+__global__ void __launch_bounds__(64 * scan_col_waves(false, CK, false))
 k_scan_cols(ScanArgs a) {
   constexpr int K = kScanK;
   extern __shared__ __attribute__((aligned(16))) float2 sm[];
@@ -365,7 +365,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     piece = 64 * kScanE;
     units = outer;
   } else {
-    most = scan_col_waves(kind, ck || (kind && p.wide));
+    most = scan_col_waves(kind, ck, p.wide);
     // Columns per wave: 64, fewer where that leaves CUs without a workgroup: down to a memory line of
     // 128 bytes (with 32 bytes the address units were the limit, 490 against 400 us for the backward
     // of 4 x 32768 x 1024 bf16), or to 32 bytes where little data makes latency the limit.
@@ -373,11 +373,14 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     p.cw = scan_pow2(std::min<int64_t>(cols, 64));
     while (p.cw > low && (cols + p.cw - 1) / p.cw < kCus && 64 / p.cw * kScanK < len) p.cw /= 2;
     // Little data: fewer still where that leaves two tiles (one for a backward without states, which
-    // then needs no other launch).
+    // then needs no other launch). Down to 16 bytes, or 4 columns of a backward: below that a tile's
+    // loads take longer than the maps' launch (13 x 9025 x 11 bf16, at one column: forward 49 us, 24
+    // cut instead; backward 74 and 32; 2 x 10847 x 51 fp32: 50 and 38, 72 and 52).
     if (small) {
       const long long reach = (long long)(kind == 2 ? 1 : 2) * most * 64 * kScanK;   // at one column
+      const int lowest = kind == 0 ? 16 / es : kind == 1 ? 4 : 1;
       int cw = p.cw;
-      while (cw > 1 && reach / cw < len) cw /= 2;
+      while (cw > lowest && reach / cw < len) cw /= 2;
       if (reach / cw >= len) p.cw = cw;
     }
     p.run = std::max(1, 128 / (p.cw * es));
@@ -391,10 +394,18 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   if (pieces <= 2 || (kind == 2 && pieces <= most)) p.waves = (int)std::max<long long>(least, pieces);
   if (least == 2) p.waves += p.waves & 1;
   p.self = pieces <= p.waves;
-  if (units < kCus * 3 / 4 && !(small && pieces <= 4 * most)) {   // four tiles cost less than a launch
+  // The axis is cut where half the CUs or more would have no workgroup; the forward of an fp32 tensor,
+  // which alone keeps memory busy from fewer CUs, where that is true of 11 in 16; a short axis where
+  // it is true of three in four. Never into more parts than leave each CU one at most. Forward of
+  // 144 x 16384 x 64 bf16: 253 us whole, 340 cut; 128 x 16384 x 64: 248 and 220; 64 x 16384 x 64 fp32:
+  // 184 and 221; backward of 96 x 16384 x 64 bf16: 273 us in two parts, 358 in three; 128 x 1029 x 64:
+  // 29 us whole, 35 cut.
+  const long long full = kind == 0 && !bf16 ? kCus * 5 / 16 - 1 : kCus / 2;
+  if (units <= full && (units <= kCus / 4 || len >= 2048) &&
+      !(small && pieces <= 4 * most)) {   // four tiles cost less than a launch
     // segments of whole 16 pieces, which the tiles of 8 or 16 waves divide
     const long long step = 16 * piece, steps = (len + step - 1) / step;
-    const long long segs = std::min<long long>({(kCus + units - 1) / units, steps, 64});
+    const long long segs = std::min<long long>({kCus / units, steps, 64});
     if (segs > 1) {
       const long long per = (steps + segs - 1) / segs;
       p.segs = (int)((steps + per - 1) / per);

@@ -26,9 +26,11 @@ constexpr int kScanChunk = 32;    // steps between two kept states
 constexpr int kScanK = 16;        // steps per lane and tile of the column kernels
 constexpr int kScanE = 8;         // steps per lane and tile of the row kernels
 constexpr int kScanWaves = 16;    // waves of a workgroup at most
-// The same for the column kernels, by their registers: forward 4 waves per SIMD, backward 3, each 2
-// from a checkpoint (and the backward with 64-bit offsets).
-constexpr int scan_col_waves(bool backward, bool more) { return more ? 8 : (backward ? 12 : 16); }
+// The same for the column kernels, by their registers: forward 4 waves per SIMD, 3 from a checkpoint;
+// backward 3, and 2 from a checkpoint (at 3, 13 registers spilt: 10 % slower) and with 64-bit offsets.
+constexpr int scan_col_waves(bool backward, bool ck, bool wide) {
+  return backward ? (ck || wide ? 8 : 12) : (ck ? 12 : 16);
+}
 constexpr int scan_map_waves(bool ck) { return ck ? 8 : 16; }   // of a workgroup that forms a map
 constexpr float kScanPad = 100.f; // a gate that leaves the state alone (a = 1 exactly)
 

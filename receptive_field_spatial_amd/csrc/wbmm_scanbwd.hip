@@ -30,7 +30,7 @@ struct RunMap {
 // waves come in pairs). CK: u is a checkpoint. SELF: one tile holds the axis and no state is kept:
 // the pieces' maps of the state are exchanged beside those of its gradient, from h0 (a.h0).
 template <typename T, bool CK, bool SELF, typename OFF>
-__global__ void __launch_bounds__(64 * scan_col_waves(true, CK || sizeof(OFF) == 8))
+__global__ void __launch_bounds__(64 * scan_col_waves(true, CK, sizeof(OFF) == 8))
 k_scan_cols_bwd(ScanArgs a) {
   constexpr int K = kScanK;
   static_assert(kScanChunk == 2 * K, "two pieces between states");
@@ -384,7 +384,7 @@ hipError_t launch_cols(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  static_assert(2 * scan_col_waves(true, false) * 64 * sizeof(RunMap) <= 64 * 1024, "LDS of a launch");
+  static_assert(2 * scan_col_waves(true, false, false) * 64 * sizeof(RunMap) <= 64 * 1024, "LDS of a launch");
   k_scan_cols_bwd<T, CK, SELF, OFF><<<dim3(groups, p.segs), 64 * p.waves,
                                       2 * p.waves * a.cw * sizeof(RunMap), st>>>(a);
   return hipGetLastError();
