@@ -217,6 +217,32 @@ def test_backward_ckpt_many_units(B, C, H, W, w, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("B,C,H,W,w,layout", [(33, 60, 22, 30, 16, "NCHW"), (66, 90, 11, 19, 11, "NHWC")])
+def test_backward_ckpt_many_units_of_large_windows(B, C, H, W, w, layout, bf16):
+    """One workgroup per CU and more units than CUs: some take several."""
+    check_bwd(B, C, H, W, w, True, "int8", bf16, layout=layout, seed=w)
+
+
+@pytest.mark.parametrize("C,H,W,w", [(2, 4030, 4031, 16), (1, 5704, 5709, 5)])
+def test_backward_ckpt_largest_images(C, H, W, w):
+    """Images on either side of the size up to which a unit's offsets take 32 bits (33 images of
+    2^32 bytes): the gradients of the decoded maps.
+
+    Both sides round each of a sum's n terms by a few 2^-24 of it, in chains of fp32 and then fp64: the
+    error's norm stays below 2^-20 of the root of the terms' squares, which is what the sums of these
+    random terms measure themselves, and 2e-6 leaves twice that."""
+    assert (4 * 33 * C * H * W < 2 ** 32) == (C == 2)
+    x, z, dy, T, Wm = bwd_inputs(1, C, H, W, w, True, "int8", False, "NCHW", 5)
+    xc, zc = (R().wbmm_ckpt_pack(dev(a)) for a in (x, z))
+    xu, zu = (R().wbmm_ckpt_unpack(*c) for c in (xc, zc))
+    got = R().wbmm_backward_ckpt(xc, dev(dy), w, dev(T), mix_w=dev(Wm), z_ckpt=zc)
+    want = R().wbmm_backward(xu, dev(dy), w, T=dev(T), mix_w=dev(Wm), z_saved=zu)
+    for a, b, name in zip(got, want, ("dx", "dT", "dW")):
+        a, b = a.double(), b.double()
+        assert (a - b).norm() <= 2e-6 * b.norm(), name
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("mix", [False, True])
 @pytest.mark.parametrize("B,C,H,W,w", [(2, 12, 17, 19, 7), (3, 5, 28, 28, 14), (2, 3, 5, 6, 8)])
 def test_backward_ckpt_nhwc(B, C, H, W, w, bf16, mix):

@@ -209,6 +209,13 @@ def test_scan_in_segments(O, L, I, lens, bf16):
     run_case(O, L, I, bf16, True, lens=lens, seed=2, ckpt="int8", recompute=True)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_scan_in_finer_parts(bf16):
+    """Segments whose maps are formed from two parts each, in 15 and 29 column groups."""
+    run_case(1, 5000, 900, bf16, False, seed=1)
+    run_case(1, 5000, 900, bf16, True, lens=[4100], seed=2, ckpt="e4m3", recompute=True)
+
+
 def test_scan_without_initial_state_and_extreme_gates():
     shape = (3, 70, 2)
     arrs = draw(shape, False, 3)
