@@ -210,6 +210,19 @@ def test_scan_in_segments(O, L, I, lens, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("O,L,I,reverse,lens", [
+    (3, 40, 32, False, None), (5, 77, 96, True, [77, 0, 1, 16, 50]), (300, 300, 64, True, None),
+    (2, 700, 160, False, [700, 333]), (90, 260, 96, False, [260, 100, 17] * 30), (1, 33, 1024, True, None),
+    (1, 6000, 192, True, [5000]), (129, 17, 32, False, None),
+])
+def test_scan_backward_from_checkpoint_whole_groups(O, L, I, reverse, lens, fmt, bf16):
+    """Rows of whole groups, so that a group holds one step of 32 columns."""
+    run_case(O, L, I, bf16, reverse, lens=lens, seed=L, ckpt=fmt)
+    run_case(O, L, I, bf16, reverse, lens=lens, seed=L + 1, ckpt=fmt, recompute=True)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 def test_scan_in_finer_parts(bf16):
     """Segments whose maps are formed from two parts each, in 15 and 29 column groups."""
     run_case(1, 5000, 900, bf16, False, seed=1)
