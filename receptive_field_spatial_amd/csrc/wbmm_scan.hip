@@ -389,7 +389,16 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     if (kind && p.cw == 64) least = 2;   // waves pair up for the kept states
   }
   const long long pieces = (len + piece - 1) / piece;
-  p.waves = scan_waves(units, pieces, least, most);
+  // Column groups beyond the CUs: so few waves that a CU holds its share of the workgroups at a time,
+  // where that measured less (784 steps, 64 columns a group): forward 258 groups bf16 28 us instead of
+  // 35, 384 fp32 41 and 44, 1000 bf16 66 and 83; backward 1000 groups bf16 108 and 118, from a checkpoint
+  // 183 and 258. Not where it measured more: backward 258 groups 53 and 48, from a checkpoint 143 and
+  // 106, 1500 bf16 162 and 156; rows.
+  int cap = most;
+  const int share = std::max(1, (int)(most / ((units + kCus - 1) / kCus)));
+  if (!p.rows && units > 3 * kCus && (kind == 0 || (units <= 4 * kCus && (bf16 || ck)))) cap = share;
+  else if (!p.rows && units > kCus && units <= 3 * kCus && kind == 0 && !ck) cap = most / 2;
+  p.waves = scan_waves(units, pieces, std::min(least, cap), cap);
   // one tile: a short axis costs a barrier less, and a backward without states no second run
   if (pieces <= 2 || (kind == 2 && pieces <= most)) p.waves = (int)std::max<long long>(least, pieces);
   if (least == 2) p.waves += p.waves & 1;
