@@ -230,9 +230,9 @@ hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, size_
 
 // ---------------------------------------------------------------------------- backward
 // w = 14 on whole images: the fused kernel of wbmm_ckptbwd.hip; other maps, layouts and windows from 2
-// to 16: the one of wbmm_ckptany.hip. Windows of 1 and above 16: the checkpoints are decoded into fp32
-// maps in the workspace and the fp32 backward runs on them; bf16 dy and T are widened exactly and dx
-// is rounded to bf16 once at the end.
+// to 16: the one of wbmm_ckptany.hip. Windows of 1 and above 16, and images of which 33 pass 2^32
+// bytes: the checkpoints are decoded into fp32 maps in the workspace and the fp32 backward runs on
+// them; bf16 dy and T are widened exactly and dx is rounded to bf16 once at the end.
 namespace {
 
 bool fast_call(const BwdCkptRequest& r) {
