@@ -50,6 +50,9 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
     }
     piece = 64 * kScanE;
     units = outer;
+    // a workgroup per row: fewer waves each where the launch would have 2^32 threads (below 2^26 rows
+    // one wave always fits)
+    most = (int)std::min<long long>(most, ((1ll << 32) - 1) / (64 * units));
   } else {
     most = scan_col_waves(kind, ck, p.wide);
     // Columns per wave: 64, fewer where that leaves CUs without a workgroup: down to a memory line of
@@ -86,7 +89,7 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   else if (!p.rows && units > kCus && units <= 3 * kCus && kind == 0 && !ck) cap = most / 2;
   p.waves = scan_waves(units, pieces, std::min(least, cap), cap);
   // one tile: a short axis costs a barrier less, and a backward without states no second run
-  if (pieces <= 2 || (kind == 2 && pieces <= most)) p.waves = (int)std::max<long long>(least, pieces);
+  if (pieces <= most && (pieces <= 2 || kind == 2)) p.waves = (int)std::max<long long>(least, pieces);
   if (least == 2) p.waves += p.waves & 1;
   p.self = pieces <= p.waves;
   // The axis is cut where half the CUs or more would have no workgroup; the forward of an fp32 tensor,

@@ -181,6 +181,24 @@ def test_scan_offsets_past_32_bits(shape):
         assert same(t, v[-1:, -4000:])
 
 
+def test_scan_more_rows_than_two_waves_each():
+    """2^25 rows of two tiles: a workgroup of two waves per row would be a launch of 2^32 threads."""
+    O, L = (1 << 25) + 3, 515
+    g = torch.empty((O, L, 1), dtype=torch.bfloat16, device="cuda")
+    g.normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    rows = [0, 1, 77, 1 << 24, (1 << 25) - 1, 1 << 25, O - 2, O - 1]
+    f = g[rows].double().cpu().numpy()          # one tensor serves as g, u and dh
+    h, last, _ = R().wbmm_scan_forward(g, g, 1, h_last=True)
+    wh, wl, _, bh, bl, _ = Q.scan_forward(f, f, bf16=True)
+    close(h[rows], wh, bh, True, "h")
+    close(last[rows], wl, bl, False, "h_last")
+    del h
+    dg, du, d0 = R().wbmm_scan_backward(g, None, g, 1, u=g)
+    want = Q.scan_backward(f, f, None, f, bf16=True)
+    for t, w, b, bf16, name in zip((dg, du, d0), want[:3], want[3:], (True, True, False), ("dg", "du", "dh0")):
+        close(t[rows], w, b, bf16, name)
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("O,L,I,reverse,lens", [
     (2, 1, 1, False, None), (2, 1, 3, False, [0, 1]), (3, 20, 1, True, None), (2, 600, 1, True, [600, 5]),
