@@ -55,7 +55,7 @@ k_scan_cols(ScanArgs a) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float c;
-      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], c);
+      scan_gate<sizeof(T) == 2>(scan_widen<T>(rg[k]), av[k], c);
       bv[k] = c * ru[k].widen(a);
       H = fmaf(av[k], H, bv[k]);
       P *= av[k];
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(64 * scan_map_waves(CK)) k_scan_cols_agg(ScanA
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float aa, c;
-      scan_gate<sizeof(T) == 4>(gv[k], aa, c);
+      scan_gate<sizeof(T) == 2>(gv[k], aa, c);
       H = fmaf(aa, H, c * uv[k]);
       P *= aa;
     }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows(ScanArgs a) {
 #pragma unroll
     for (int k = 0; k < E; ++k) {
       float c;
-      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], c);
+      scan_gate<sizeof(T) == 2>(scan_widen<T>(rg[k]), av[k], c);
       bv[k] *= c;
       H = fmaf(av[k], H, bv[k]);
       P *= av[k];
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(ScanArgs a) {
   if (c >= a.cols) return;
   const float h0 = a.carry_in ? a.carry_in[c] : 0.f;
   float aa, cc;
-  scan_gate<sizeof(T) == 4>(scan_widen<T>(((const T*)a.g)[c]), aa, cc);
+  scan_gate<sizeof(T) == 2>(scan_widen<T>(((const T*)a.g)[c]), aa, cc);
   const float h = fmaf(aa, h0, cc * scan_widen<T>(((const T*)a.u)[c]));
   const bool live = scan_steps(a, (uint32_t)(c / a.inner)) > 0;
   ((T*)a.out0)[c] = scan_narrow<T>(live ? h : 0.f);

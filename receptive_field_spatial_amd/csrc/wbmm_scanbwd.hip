@@ -68,7 +68,7 @@ k_scan_cols_bwd(ScanArgs a) {
     float av[K], cv[K], ev[K], dv[K], P = 1.f, Rl = 0.f, H = 0.f, h = rst;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], cv[k]);
+      scan_gate<sizeof(T) == 2>(scan_widen<T>(rg[k]), av[k], cv[k]);
       ev[k] = cv[k] * ru[k].widen(a);
       dv[k] = scan_widen<T>(rd[k]);
       P *= av[k];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(64 * scan_map_waves(false)) k_scan_cols_bwd_ag
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
       float aa, c;
-      scan_gate<sizeof(T) == 4>(gv[k], aa, c);
+      scan_gate<sizeof(T) == 2>(gv[k], aa, c);
       Rl = aa * (dv[k] + Rl);
       P *= aa;
     }
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan_rows_bwd(ScanArgs a) {
     if constexpr (!AGG) ru.widen(a, rw, s, ev);   // u for now
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      scan_gate<sizeof(T) == 4>(scan_widen<T>(rg[k]), av[k], cv[k]);
+      scan_gate<sizeof(T) == 2>(scan_widen<T>(rg[k]), av[k], cv[k]);
       dv[k] = scan_widen<T>(rd[k]);
       P *= av[k];
       if constexpr (!AGG) {

@@ -272,6 +272,45 @@ def test_scan_gate_infinite():
         assert torch.all((h[0, 3] - 7).abs() <= 7 * (2.0 ** -23 + 2 * 2.0 ** -24))
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("kernel", ["step", "rows", "columns"])
+def test_scan_gate_accuracy(kernel, bf16):
+    """Sigmoid(g) and sigmoid(-g) as fp32 outputs show them: the state after one step from 1 with u = 0,
+    and from 0 with u = 1, is a, and 1 - a.
+
+    Relative error of t = exp(-g): one step of the hardware's exp2, 2 U with U = 2^-24 (the exponent it
+    is given is exact, or its rounding is put back), and U for the correction; with the exponent in
+    two parts (bf16) the square of the second is left out, z^2 / 2 with z below 7.2e-6 ln(2) |g|,
+    2.1e-4 g^2 U. a = 1 / (1 + t) takes (1 - a) of that, U for the sum and U for the reciprocal with
+    its Newton step (whose own residue, (2 U)^2, is nothing); c = t a takes a of it, both and U. The
+    sums around them multiply by 1 or add 0, and are exact."""
+    U = 2.0 ** -24
+    if bf16:   # every bf16 value in range, and its negative
+        g = np.arange(0x3a80, 0x42ae, dtype=np.uint32) << 16
+        g = g.view(np.float32)
+    else:
+        g = np.exp(np.linspace(np.log(1e-3), np.log(86.9), 20000)).astype(np.float32)
+    g = np.concatenate([g, -g, [0]]).astype(np.float32)
+    n = g.size
+    shape = {"step": (1, 1, n), "rows": (n, 2, 1), "columns": (1, 2, n)}[kernel]
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gd = dev(g).to(dt)
+    if kernel != "step":   # the second step leaves the state alone: a = 1, u = 0
+        gd = torch.stack([gd, torch.full_like(gd, 100.0)], 1 if kernel == "rows" else 0)
+    gd = gd.reshape(shape).contiguous()
+    u = torch.zeros(shape, dtype=dt, device="cuda")
+    u[:, 0] = 1
+    one = torch.ones(shape[0], shape[2], device="cuda")
+    c = R().wbmm_scan_forward(gd, u, 1, h_last=True)[1].double().cpu().numpy().reshape(-1)
+    a = R().wbmm_scan_forward(gd, torch.zeros_like(u), 1, h0=one, h_last=True)[1].double().cpu().numpy().reshape(-1)
+    x = g.astype(np.float64)
+    wa, wc = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x))
+    et = 3 + (2.1e-4 * x * x if bf16 else 0)
+    ra, rc = np.abs(a / wa - 1) / U, np.abs(c / wc - 1) / U
+    print(f"    a: worst {ra.max():.2f} U, c: worst {rc.max():.2f} U", flush=True)
+    assert np.all(ra <= wc * et + 2.01) and np.all(rc <= wa * et + 3.01)
+
+
 def test_scan_nan_stays_in_its_column():
     for shape in ((3, 100, 1), (1, 100, 3)):
         g = torch.zeros(shape, device="cuda")
