@@ -349,14 +349,18 @@ wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_
  * a training step keeps, x and the pre-mix z, as checkpoints in `fmt` (packed in the maps' own
  * memory order, B C H W elements). dT sums over the checkpoint's x, dmix_w over its z; dx needs
  * neither. Every other argument, output, rule and error as in wbmm_backward (table input).
- * dtype:   of T, dy and dx: WBMM_F32, or WBMM_BF16 (widened exactly; products and sums in fp32
- *          and fp64 as for fp32 maps, the mix adjoint of dy in fp32, dx rounded once, RNE). mix_w,
- *          dT and dmix_w are fp32 in both.
+ * dtype:   of T, dy and dx: WBMM_F32, or WBMM_BF16 (widened exactly). mix_w, dT and dmix_w are
+ *          fp32 in both, and so is G, dy after the mix adjoint; dT's and dmix_w's products and sums
+ *          are in fp32 and fp64 for either type, dx's in fp32. For WBMM_BF16 with the mix G enters
+ *          dx's products as the sum of two bf16 numbers, to 2^-17 of itself: an error of dx of up
+ *          to 2^-17 sum |T| |G| over its window, before the one rounding to bf16 (RNE), which is
+ *          up to 2^-8 |dx|.
  * x_codes, x_scales, z_codes, z_scales: as wbmm_ckpt_pack writes them; z_* exactly with mix_w.
  * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned.
- * An fp32 operand enters the products as the sum of three bf16 numbers, which an infinity has not,
- * nor has a finite magnitude of (2 - 2^-8) 2^127 or more: such entries of T, or of G (dy after the
- * mix adjoint), make the results that they reach NaN.
+ * For 2 <= w <= 16 (very large images, 33 C H W >= 2^30, aside) every other fp32 operand enters the
+ * products as the sum of three bf16 numbers, which an infinity has not, nor has a finite magnitude
+ * of (2 - 2^-8) 2^127 or more: such entries of T or G make the results that they reach NaN. Other
+ * windows run wbmm_backward's kernels, in fp32 throughout.
  * Errors as in wbmm_backward; also WBMM_E_INVALID for an unknown fmt.
  */
 size_t wbmm_backward_ckpt_workspace_bytes(int B, int C, int H, int W, int w, int layout, int dtype,

@@ -9,7 +9,8 @@
 //       parts: 3 products, nothing lost;
 //   dX, fp32: T and G in three parts each, the 6 products that reach 2^-24 (what is left out is
 //       below 2^-26 of each term): 6/16 of the fp32 matrix time;
-//   dX, bf16: T is exact, G in two parts (2^-17 before one rounding to 2^-9); 1 part where G is dy.
+//   dX, bf16: T is exact, G in two parts (2^-17 of G, before dx's rounding to 2^-8); where G is dy it is
+//       exact in one (the any-map kernel's second part is zero there).
 //
 // A workgroup of 8 waves takes a unit of 32 windows of one channel. dX: K runs over padded window
 // rows (two rows of 16 slots per MFMA), an output tile is one window row (16 slots). Then the block of

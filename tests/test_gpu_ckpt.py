@@ -292,6 +292,28 @@ def test_backward_ckpt_partial_outputs(bf16, B, H, w):
         assert torch.equal(part[k], whole[k])
 
 
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("B,C,H,W,w", [(5, 3, 28, 28, 14), (2, 3, 30, 45, 7), (2, 2, 30, 40, 20)])
+def test_backward_ckpt_bf16_dx_error(B, C, H, W, w, mix):
+    """dx of bf16 maps, element by element, against what may be lost, U = 2^-24: half a step of the
+    result; with the mix 2^-17 of each G, and 9 U of the adjoint's terms for its 9 sums; U for each
+    of the up to 2 w^2 products (a part of G each) that a sum takes, and one more for the two parts."""
+    x, z, dy, T, Wm = bwd_inputs(B, C, H, W, w, mix, "int8", True, "NCHW", 21)
+    pk = lambda a: R().wbmm_ckpt_pack(dev(a).to(torch.bfloat16))
+    dx = R().wbmm_backward_ckpt(pk(x), dev(dy).to(torch.bfloat16), w, dev(T).to(torch.bfloat16),
+                                mix_w=dev(Wm) if mix else None, z_ckpt=pk(z) if mix else None)[0]
+    f = lambda a: None if a is None else a.astype(np.float64)
+    b = lambda a: None if a is None else np.abs(f(a))
+    zz = f(z) if mix else None
+    want = O.layer_backward(f(x), f(dy), w, T=f(T), Wmix=f(Wm), z=zz)[0]
+    terms = O.layer_backward(f(x), b(dy), w, T=b(T), Wmix=b(Wm), z=zz)[0]
+    U = 2.0 ** -24
+    tol = 2.0 ** -8 * np.abs(want) + terms * ((2.0 ** -17 + 9 * U if mix else 0) + (2 * w * w + 1) * U)
+    err = np.abs(dx.double().cpu().numpy() - want)
+    print(f"    dx: worst error/bound {np.max(err / tol):.3f}", flush=True)
+    assert np.all(err <= tol * (1 + 2.0 ** -8))
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_backward_ckpt_is_the_backward_of_the_decoded_maps(fmt):
     """fp32: the same gradients as wbmm_backward on the unpacked maps, to rounding."""
