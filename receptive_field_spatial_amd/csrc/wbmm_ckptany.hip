@@ -313,16 +313,24 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // which gets the most. Of equal ones the most where a CU runs two, whose starts and ends overlap
 // (64 x 192 x 24 x 24, w = 8, bf16 with the mix: 1728 workgroups of 2 units 80 us, 960 of 4 84), and the
 // fewest where it runs one (64 x 64 x 40 x 40, w = 16: 256 of 5 units 111 us, 1152 of one 124).
+// A thread's dWmix sums are fp32 over its workgroup's units: more workgroups where they would pass 128
+// terms (to 2^20 workgroups in all, which only maps far smaller than their window reach). One chain over
+// 200 units of equal terms was off by 148 half steps.
 void any_units(const BwdCkptRequest& r, CkptAnyArgs& a) {
   a.nwx = (r.W + r.w - 1) / r.w;
   a.nwin = a.nwx * ((r.H + r.w - 1) / r.w);
   a.windows = r.B * a.nwin;
   a.units = (a.windows + kWins - 1) / kWins;
-  const long long most = std::min<long long>({96, a.units, std::max(1, 2048 / r.C)});
+  const long long terms = (kWins * r.w * r.w + kT - 1) / kT;   // of a thread and unit
+  const long long longest = 128 / terms;
+  const long long least = std::max<long long>(
+      1, std::min<long long>((a.units + longest - 1) / longest, (1 << 20) / r.C));
+  const long long most =
+      std::max(least, std::min<long long>({96, a.units, std::max(1, 2048 / r.C)}));
   const int resident = any_waves(r.w) / 2;   // workgroups that a CU runs at a time
   const long long slots = 256 * resident;
   long long best = -1;
-  for (long long g = 1; g <= most; ++g) {
+  for (long long g = least; g <= most; ++g) {
     const long long per = (a.units + g - 1) / g, used = (a.units + per - 1) / per;
     const long long turns = (r.C * used + slots - 1) / slots * per;
     if (best < 0 || turns < best || (turns == best && resident > 1))

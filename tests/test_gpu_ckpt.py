@@ -292,6 +292,24 @@ def test_backward_ckpt_partial_outputs(bf16, B, H, w):
         assert torch.equal(part[k], whole[k])
 
 
+@pytest.mark.parametrize("B,C,H,W,w", [(76800, 1, 28, 28, 7), (12800, 1100, 7, 7, 7), (3000, 1, 160, 160, 16)])
+def test_backward_ckpt_mix_gradient_of_many_units(B, C, H, W, w):
+    """dWmix where a workgroup takes hundreds of units (one channel, or more than a thousand), all terms
+    equal, so that every rounding of a sum falls the same way. A thread's fp32 sum holds 128 terms at
+    most, then come 4 sums of lanes, fp64 and dWmix's own rounding: 133 half steps."""
+    dy = torch.full((B, C, H, W), 1.9153239727020264, device="cuda")
+    x = R().wbmm_ckpt_pack(torch.zeros_like(dy))
+    z = R().wbmm_ckpt_pack(torch.full_like(dy, 0.75))
+    T = torch.zeros(C, 2 * w - 1, 2 * w - 1, device="cuda")
+    mix = torch.zeros(C, 3, 3, device="cuda")
+    dW = R().wbmm_backward_ckpt(x, dy, w, T, mix_w=mix, z_ckpt=z, dx=False, dT=False)[2]
+    rows = np.array([H - 1, H, H - 1], np.float64)[:, None] * np.array([W - 1, W, W - 1], np.float64)
+    want = B * rows * 0.75 * float(dy.view(-1)[0])
+    worst = np.max(np.abs(dW.double().cpu().numpy() / want - 1)) * 2.0 ** 24
+    print(f"    dW: worst {worst:.1f} half steps", flush=True)
+    assert worst <= 133
+
+
 @pytest.mark.parametrize("mix", [False, True])
 @pytest.mark.parametrize("B,C,H,W,w", [(5, 3, 28, 28, 14), (2, 3, 30, 45, 7), (2, 2, 30, 40, 20)])
 def test_backward_ckpt_bf16_dx_error(B, C, H, W, w, mix):
