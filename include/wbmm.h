@@ -395,6 +395,10 @@ wbmm_status wbmm_backward_ckpt(int B, int C, int H, int W, int w, int layout, in
  * workspace: wbmm_scan_forward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0; needed only
  *           where few columns make the axis run in segments). Calls that share one must be ordered
  *           on one stream.
+ * An infinity in h0 or u makes h from there on, in its own column, infinite or NaN (the runs of
+ * steps are joined by products of their a_t, which may underflow to 0: NaN where a product with the
+ * infinity would be one). Gates: a_t and 1 - a_t are held at 1.6e-38 from below; a NaN in g or u is
+ * a NaN in h from there on.
  * No atomics: bitwise reproducible. Errors: WBMM_E_INVALID (sizes, dtype, n_lens, NULL or
  * overlapping buffers), WBMM_E_UNSUPPORTED (outer * inner >= 2^26, len > 2^30, more than 2^38
  * elements, misaligned pointer), WBMM_E_WORKSPACE, WBMM_E_HIP.
@@ -424,6 +428,8 @@ wbmm_status wbmm_scan_forward(int64_t outer, int64_t len, int64_t inner, int dty
  * dg, du:   device maps in dtype, written; 0 past the end of a sequence. dh0: device fp32
  *           [outer][inner], written, or NULL.
  * workspace: wbmm_scan_backward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0).
+ * Infinities and NaN as in the forward: those of dh and dh_last reach the earlier steps' dg, du and
+ * dh0, those of the state only dg.
  * Errors as in the forward; also WBMM_E_INVALID for an unknown u_fmt, or h0 beside states.
  */
 size_t wbmm_scan_backward_workspace_bytes(int64_t outer, int64_t len, int64_t inner,

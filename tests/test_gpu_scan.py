@@ -324,6 +324,53 @@ def test_scan_nan_stays_in_its_column():
             t[idx] = 0.0
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("O,L,I", [(3, 1, 5), (4, 100, 1), (3, 900, 1), (2, 9000, 1), (2, 300, 5), (2, 70, 96),
+                                   (1, 70000, 2), (1, 70000, 1)])
+def test_scan_infinite_values_stay_in_their_column(O, L, I, bf16):
+    """From an infinite h0 or u on nothing finite, before it and beside it what there was without it; a
+    gradient's infinity runs the other way. Half of the gates forget so fast that products of them
+    underflow."""
+    g, u, dh, h0, dl = draw((O, L, I), bf16, 12)
+    g[:, 1::2] = -25
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gd, ud, dd, s0, sl = dev(g).to(dt), dev(u).to(dt), dev(dh).to(dt), dev(h0), dev(dl)
+    o, i, t = O - 1, I // 2, L // 3
+    inf = float("inf")
+
+    def run(u, h0):
+        h, last, st = R().wbmm_scan_forward(gd, u, 1, h0=h0, h_last=True, states=True)
+        return h, last[:, None], st
+
+    def check(got, want, first):
+        for a, b, k in zip(got, want, first):
+            mine = a[o, :, i]
+            assert torch.equal(mine[:k], b[o, :k, i]) and not torch.isfinite(mine[k:]).any()
+            a, b = a.clone(), b.clone()
+            a[o, :, i] = b[o, :, i] = 0
+            assert torch.equal(a, b)
+
+    want = run(ud, s0)
+    bad = s0.clone()
+    bad[o, i] = inf
+    check(run(ud, bad), want, (0, 0, 0))
+    bad = ud.clone()
+    bad[o, t, i] = -inf
+    check(run(bad, s0), want, (t, 0, t // 32 + 1))
+
+    def back(dh, dl):
+        dg, du, d0 = R().wbmm_scan_backward(gd, want[2], dh, 1, u=ud, dh_last=dl)
+        return dg.flip(1), du.flip(1), d0[:, None]
+
+    base = back(dd, sl)
+    bad = sl.clone()
+    bad[o, i] = -inf
+    check(back(dd, bad), base, (0, 0, 0))
+    bad = dd.clone()
+    bad[o, t, i] = inf
+    check(back(bad, sl), base, (L - 1 - t, L - 1 - t, 0))
+
+
 @pytest.mark.parametrize("O,L,I", [(8, 1, 192), (5, 37, 1), (1, 9000, 1), (1, 3000, 4), (4, 70, 3),
                                    (1, 70000, 1), (1, 70000, 2)])
 def test_scan_state_updated_in_place(O, L, I):
