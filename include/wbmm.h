@@ -321,8 +321,10 @@ wbmm_status wbmm_backward_bf16(int B, int C, int H, int W, int w, int layout, co
  *   value = q(code) * 2^(byte - 127);   byte 255: every value of the group is NaN,
  * q(code) the int8 value (WBMM_CKPT_INT8) or the OCP 8-bit float 4-3 value (WBMM_CKPT_E4M3).
  * int8 spreads its steps evenly below the group's largest magnitude, e4m3 keeps a relative error
- * of at most 2^-4 over the 15 binades below it. Decoded values are exact in bf16 and fp32 (results
- * below fp32's range aside: byte 0 to 2 with the smallest codes).
+ * of at most 2^-4 for magnitudes down to 2^-13 of it. Decoded values are exact in bf16 and fp32 (results
+ * outside their range aside: in bf16 the smallest codes under bytes 0 to 2; and the largest
+ * magnitudes, above 127/64 2^127 in int8 and from 31/16 2^127 in e4m3, whose nearest code stands
+ * for 2^128, which reads back as an infinity).
  */
 #define WBMM_CKPT_GROUP 32
 typedef enum wbmm_ckpt_format { WBMM_CKPT_INT8 = 0, WBMM_CKPT_E4M3 = 1 } wbmm_ckpt_format;

@@ -71,6 +71,23 @@ def test_pack_nonfinite_groups(fmt):
     check_pack(x, fmt, False)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("fmt,edge", [("int8", 127 / 64), ("e4m3", 31 / 16)])
+def test_pack_largest_magnitudes(fmt, edge, bf16):
+    """The largest values whose nearest code stands for a finite number, and those just above."""
+    x = np.zeros(128, np.float32)
+    top = np.float32(edge * 2.0 ** 127)
+    step = np.float32(2.0 ** (120 if bf16 else 104))    # of the type, there
+    below, above = (top, top + step) if fmt == "int8" else (top - step, top)
+    x[3], x[40], x[70], x[100] = below, above, -below, -above
+    check_pack(x, fmt, bf16)
+    t = dev(x).to(torch.bfloat16 if bf16 else torch.float32)
+    got = R().wbmm_ckpt_unpack(*R().wbmm_ckpt_pack(t, fmt=fmt), fmt=fmt).cpu().numpy()
+    assert np.isfinite(got[[3, 70]]).all() and got[40] == np.inf and got[100] == -np.inf
+    # half a step: of 127 even ones, or relative
+    assert abs(got[3] / below - 1) <= (0.5 / 63.5 if fmt == "int8" else 2.0 ** -4)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_unpack_every_code_and_scale(fmt):
     codes = np.repeat(np.arange(256, dtype=np.uint8), 32).reshape(32 * 8, 32).T.copy().reshape(-1)
