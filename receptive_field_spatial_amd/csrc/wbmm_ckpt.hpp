@@ -42,10 +42,4 @@ __device__ __forceinline__ float ckpt_decode1(uint32_t code, int fmt) {
   return fmt == kFmtInt8 ? (float)(int8_t)code : __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
 }
 
-// Element e of a checkpoint.
-__device__ __forceinline__ float ckpt_value(const uint8_t* __restrict__ codes,
-                                            const uint8_t* __restrict__ scales, size_t e, int fmt) {
-  return ckpt_decode1(codes[e], fmt) * ckpt_factor(scales[e / kCkptGroup]);
-}
-
 }  // namespace wbmm
