@@ -241,6 +241,59 @@ def test_scan_backward_from_checkpoint_whole_groups(O, L, I, reverse, lens, fmt,
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("O,L,I,reverse,lens", [
+    (5, 784, 1, False, None), (3, 37, 1, True, [37, 0, 9]), (2, 1001, 1, True, None), (2, 100, 7, False, None),
+    (2, 300, 64, True, [300, 41]), (1, 1500, 96, False, None), (1, 9000, 2, False, None), (2, 1, 40, False, None),
+])
+def test_scan_backward_from_checkpoint_and_the_forwards_states(O, L, I, reverse, lens, fmt, bf16):
+    """What a training step keeps: the states of the forward's own u, and u in 8 bits. Every run of 32
+    steps starts from its state and goes on with the decoded u."""
+    g, u, dh, s0, dl = draw((O, L, I), bf16, L + I)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gd, ud, dd = (dev(a).to(dt) for a in (g, u, dh))
+    ln = None if lens is None else dev(np.asarray(lens, np.int32))
+    n = np.full(O, L) if lens is None else np.repeat(lens, O // len(lens))
+    states = R().wbmm_scan_forward(gd, ud, 1, h0=dev(s0), lens=ln, reverse=reverse, states=True)[2]
+    ck = R().wbmm_ckpt_pack(ud, fmt=fmt)
+    got = R().wbmm_scan_backward(gd, states, dd, 1, u_ckpt=ck, fmt=fmt, dh_last=dev(dl), lens=ln, reverse=reverse)
+
+    def order(a):   # scan order, zeros past the end
+        a = a.astype(np.float64).copy()
+        for o in range(O):
+            a[o, :n[o]] = a[o, :n[o]][::-1 if reverse else 1]
+            a[o, n[o]:] = 0
+        return a
+
+    f64 = lambda t: t.double().cpu().numpy()
+    G_, U_, D_ = order(g), order(f64(R().wbmm_ckpt_unpack(*ck, fmt=fmt))), order(dh)
+    _, du, d0, _, bu, b0 = Q.scan_backward(G_, U_, None, D_, dl.astype(np.float64), n, False, bf16)
+    c = 1 / (1 + np.exp(G_))
+    ea, ec = Q.gate_bounds(G_, bf16)
+    grad = du / c                                           # of each step's state
+    gerr = bu / c - np.abs(grad) * (ec + 2 * Q.U)
+    # the state before every step, and its bound: runs of 32 steps as sequences of their own
+    K = Q.CHUNK
+    ch = -(-L // K)
+    cut = lambda a: np.pad(a, ((0, 0), (0, ch * K - L), (0, 0))).reshape(O * ch, K, I)
+    st = f64(states).reshape(O * ch, I)
+    nk = np.clip(n[:, None] - K * np.arange(ch), 0, K).reshape(-1)
+    h, _, _, hb, _, _ = Q.scan_forward(cut(G_), cut(U_), st, nk, False, bf16)
+    join = lambda first, a: np.concatenate([first[:, None], a[:, :-1]], 1).reshape(O, ch * K, I)[:, :L]
+    # c (h - u) is formed as c h less the rounded c u: U |u| beside the state's own error, which is none
+    # at a run's first step
+    prev, perr = join(st, h), join(np.zeros_like(st), hb) + Q.U * np.abs(U_)
+    x, w = prev - U_, c / (1 + np.exp(-G_))
+    inside = (np.arange(L) < n[:, None])[:, :, None]
+    dg = np.where(inside, w * x * grad, 0)
+    bg = w * (np.abs(x) * gerr + np.abs(grad) * (perr + np.abs(x) * (ea + ec + 4 * Q.U)))
+    back = lambda a: order(np.where(inside, a, 0))          # its own inverse
+    close(got[0], back(dg), back(bg), bf16, "dg")
+    close(got[1], back(du), back(bu), bf16, "du")
+    close(got[2], d0, b0, False, "dh0")
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 def test_scan_in_finer_parts(bf16):
     """Segments whose maps are formed from two parts each, in 15 and 29 column groups."""
     run_case(1, 5000, 900, bf16, False, seed=1)
