@@ -108,13 +108,16 @@ def scan_forward(g, u, h0=None, n=None, reverse=False, bf16=False):
         ga, gc, gu = a[r, p], c[r, p], u[r, p]
         nh = ga * h + gc * gu
         # every factor of every term of h is off by ea or ec and by one rounding of its product
-        # and one of the sum it enters, whatever the order of joining
+        # and one of the sum it enters, whatever the order of joining; the third U of a step is for
+        # the joins that come one after another (waves, tiles, parts of the axis): they lie 16 steps
+        # or more apart and round a term that passes at most twice, however many there are
         nE = ga * E + ga * S * (ea[r, p] + 3 * U) + gc * np.abs(gu) * (ec[r, p] + 3 * U)
         nS = ga * S + gc * np.abs(gu)
         h, E, S = np.where(m, nh, h), np.where(m, nE, E), np.where(m, nS, S)
         out[r[live], p[live]] = h[live]
-        # joining of pieces: up to 6 + 8 + 64 more roundings of terms that pass through, 40 U
-        # covers 80 roundings of half a step each
+        # the joins that come by doubling: 6 within a wave and one to the lane before, twice each
+        # for the pieces and for the waves, of two roundings: 28, and the first and last join of a
+        # term that passes fewer than 16 steps
         bound[r[live], p[live]] = (E + 40 * U * S)[live]
     return out, h, np.stack(states, 1), bound, E + 40 * U * S, np.stack(sbound, 1)
 

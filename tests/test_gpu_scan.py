@@ -300,6 +300,58 @@ def test_scan_in_finer_parts(bf16):
     run_case(1, 5000, 900, bf16, True, lens=[4100], seed=2, ckpt="e4m3", recompute=True)
 
 
+@pytest.mark.parametrize("L", [(1 << 24) - 3, (1 << 22) + 5])
+def test_scan_one_long_column(L):
+    """One column in thousands of maps (2048 of them at 2^24 steps), memories from a step to a million:
+    the oracle's sums and bounds, its loop over steps written as a doubling in fp64."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda: torch.randn(L, dtype=torch.float32, device="cuda", generator=gen)
+    g = r() + 7 + 7 * torch.sin(torch.arange(L, device="cuda") * (2e-6 * np.pi))
+    u, dh = r(), r()
+
+    def scan(a, b):   # h_t = a_t h_{t-1} + b_t
+        a, b, d = a.clone(), b.clone(), 1
+        while d < L:
+            b[d:] = b[d:] + a[d:] * b[:-d]
+            a[d:] = a[d:] * a[:-d]
+            d *= 2
+        return b
+
+    U = Q.U
+    x = g.double()
+    a, c = torch.sigmoid(x), torch.sigmoid(-x)
+    ea = c * (3 * U) + 3 * U
+    ec = ea + 4 * U
+
+    def bounds(a, b, eb, ea):   # with S the sum of magnitudes and E the error that has come up
+        h, S = scan(a, b), scan(a, b.abs())
+        before = torch.cat([S.new_zeros(1), S[:-1]])
+        E = scan(a, a * before * (ea + 3 * U) + b.abs() * eb)
+        return h, E + 40 * U * S, S
+
+    def near(got, want, bound, what):
+        err = (got.double().reshape(want.shape) - want).abs()
+        tol = bound * (1 + U) + U * want.abs() + 1e-36
+        print(f"    {what}: worst error/bound {(err / tol).max().item():.3f}", flush=True)
+        assert torch.all(err <= tol), what
+
+    col = lambda t: t.reshape(1, L, 1)
+    h, last, st = R().wbmm_scan_forward(col(g), col(u), 1, h_last=True, states=True)
+    wh, bh, _ = bounds(a, c * u.double(), ec + 3 * U, ea)
+    near(h, wh, bh, "h")
+    near(last, wh[-1:], bh[-1:], "h_last")
+    dg, du, d0 = R().wbmm_scan_backward(col(g), st, col(dh), 1, u=col(u))
+    # G_t = dh_t + a_{t+1} G_{t+1}
+    nxt = torch.cat([a[1:], a.new_zeros(1)]).flip(0)
+    eb = torch.cat([ea[1:], ea.new_zeros(1)]).flip(0)
+    G, bG, _ = (t.flip(0) for t in bounds(nxt, dh.double().flip(0), 3 * U, eb))
+    near(du, c * G, c * (bG + G.abs() * (ec + 2 * U)), "du")
+    prev, bp = (torch.cat([t.new_zeros(1), t[:-1]]) for t in (wh, bh))
+    xx, w = prev - u.double(), a * c
+    near(dg, w * xx * G, w * (xx.abs() * bG + G.abs() * (bp + U * u.double().abs() + xx.abs() * (ea + ec + 4 * U))), "dg")
+    near(d0, (a * G)[:1], (a * bG + (a * G).abs() * (ea + 3 * U))[:1], "dh0")
+
+
 def test_scan_without_initial_state_and_extreme_gates():
     shape = (3, 70, 2)
     arrs = draw(shape, False, 3)
