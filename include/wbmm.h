@@ -358,7 +358,10 @@ wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_
  *          to 2^-17 sum |T| |G| over its window, before the one rounding to bf16 (RNE), which is
  *          up to 2^-8 |dx|.
  * x_codes, x_scales, z_codes, z_scales: as wbmm_ckpt_pack writes them; z_* exactly with mix_w.
- * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned.
+ * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned. For w = 1, w > 16 and
+ * 33 C H W >= 2^30 it holds the decoded maps beside wbmm_backward's own: 4 bytes an element for x,
+ * for z with the mix, and for WBMM_BF16 for dy and dx as well, so that a call needs more memory
+ * than the checkpoints save.
  * For 2 <= w <= 16 (very large images, 33 C H W >= 2^30, aside) every other fp32 operand enters the
  * products as the sum of three bf16 numbers, which an infinity has not, nor has a finite magnitude
  * of (2 - 2^-8) 2^127 or more: such entries of T or G make the results that they reach NaN. Other

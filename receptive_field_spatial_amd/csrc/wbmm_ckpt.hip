@@ -11,9 +11,9 @@
 //
 // Both directions are bound by memory: one lane takes 8 elements (16 or 32 bytes in, 8 out), four
 // lanes a group, whose maximum takes two quad moves; each lane has two such pieces in flight.
-// Measured (kernel alone; a large copy reaches 5.05 TB/s): 64 x 192 x 28 x 28 fp32 packed to int8 in
-// 8.8 us and unpacked in 11.4 us (5.5 and 4.3 TB/s, partly out of the last-level cache); 128 x 96 x
-// 56 x 56 bf16 to e4m3 and back 18.0 and 16.8 us (6.5 and 6.9 TB/s).
+// Measured (kernel alone; a large copy reaches 5.05 to 5.18 TB/s): 64 x 192 x 28 x 28 fp32 packed to
+// int8 in 9.0 us and unpacked in 11.6 us (5.4 and 4.2 TB/s, partly out of the last-level cache); 128 x
+// 96 x 56 x 56 bf16 to e4m3 and back 20.0 and 18.8 us (5.8 and 6.2 TB/s).
 #include "wbmm_ckpt.hpp"
 #include "wbmm_launch.hpp"
 
@@ -232,7 +232,9 @@ hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, size_
 // w = 14 on whole images: the fused kernel of wbmm_ckptbwd.hip; other maps, layouts and windows from 2
 // to 16: the one of wbmm_ckptany.hip. Windows of 1 and above 16, and images of which 33 pass 2^32
 // bytes: the checkpoints are decoded into fp32 maps in the workspace and the fp32 backward runs on
-// them; bf16 dy and T are widened exactly and dx is rounded to bf16 once at the end.
+// them; bf16 dy and T are widened exactly and dx is rounded to bf16 once at the end. The workspace is
+// then larger than what the checkpoints save (64 x 192 x 28 x 28, w = 28, with the mix: 184 MiB fp32, 260
+// bf16, for 110 and 91 on plain maps; 856 and 889 us, 830 and 530 there).
 namespace {
 
 bool fast_call(const BwdCkptRequest& r) {

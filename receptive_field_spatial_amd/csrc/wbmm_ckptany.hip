@@ -95,7 +95,7 @@ __device__ __forceinline__ void dx_any(const CkptAnyArgs& a, size_t ub, const fl
 
 // What bounds it: vector issue and the waits between the six steps of a unit, not memory (64 x 192 x
 // 33 x 33, w = 3, bf16, no mix: 272 us, 5% of the copy's rate; 64 x 96 x 28 x 28, w = 7, fp32, no mix:
-// 64 us, 13%; with the mix 320 and 87). Two workgroups of 8 waves share a CU up to w = 10: three or four
+// 60 us, 14%; with the mix 318 and 78 to 83). Two workgroups of 8 waves share a CU up to w = 10: three or four
 // at w <= 6 spilt (w = 5, fp32 with the mix, 284 and 275 us where two took 234). Above w = 10 one runs,
 // with twice the registers.
 constexpr int any_waves(int w) { return w > 10 ? 2 : 4; }

@@ -10,8 +10,8 @@
 // in a fixed order by k_bwd_reduce.
 //
 // What bounds it: vector issue (the adjoint, the splits into parts, the fp64 partials), then the
-// matrix cores. Measured at 64 x 192 x 28 x 28 with the mix (kernel alone): fp32 65.4 us, bf16 52.4 us,
-// 115 and 144 TFLOP/s of the formula's products.
+// matrix cores. Measured at 64 x 192 x 28 x 28 with the mix (kernel alone): fp32 66.0 us, bf16 52.8 us,
+// 114 and 143 TFLOP/s of the formula's products.
 #include "wbmm_ckptbwd.hpp"
 
 namespace wbmm {

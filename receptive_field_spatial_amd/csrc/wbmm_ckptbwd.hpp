@@ -7,8 +7,8 @@
 // bf16 at 16 times their fp32 rate (1131 against 154 TFLOP/s in a large library product). So:
 //   dT: x comes from a checkpoint and is exact in bf16, G (the mix adjoint of dy) takes its three
 //       parts: 3 products, nothing lost;
-//   dX, fp32: T and G in three parts each, the 6 products that reach 2^-24 (what is left out is
-//       below 2^-26 of each term): 6/16 of the fp32 matrix time;
+//   dX, fp32: T and G in three parts each, the 6 largest products (of the others two are up to 2^-25
+//       of the term, one 2^-34): 6/16 of the fp32 matrix time;
 //   dX, bf16: T is exact, G in two parts (2^-17 of G, before dx's rounding to 2^-8); where G is dy it is
 //       exact in one (the any-map kernel's second part is zero there).
 //

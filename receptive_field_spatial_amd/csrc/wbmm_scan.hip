@@ -11,8 +11,8 @@
 //
 // What bounds it: memory on large tensors, one launch and its chain of loads and exchanges on small
 // ones. Measured (kernel alone; rates of the bytes that have to move, a large copy reaches 5.05 TB/s):
-// k_scan_cols 64 x 784 x 192 bf16 18 us, 3.2 TB/s; k_scan_rows 256 x 16384 fp32, reversed, 13.2 us,
-// 3.8 TB/s; k_scan_cols 13 x 1531 x 97 fp32, ragged, 14.8 us; k_scan_step 8 x 192 bf16 2.2 us.
+// k_scan_cols 64 x 784 x 192 bf16 20 us, 3.0 TB/s; k_scan_rows 256 x 16384 fp32, reversed, 13.6 us,
+// 3.7 TB/s; k_scan_cols 13 x 1531 x 97 fp32, ragged, 16 us; k_scan_step 8 x 192 bf16 2.3 us.
 #include "wbmm_scan.hpp"
 
 namespace wbmm {

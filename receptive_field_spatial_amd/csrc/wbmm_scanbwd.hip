@@ -9,8 +9,8 @@
 //
 // What bounds it: memory, less where the axis is cut (the maps' launch reads g and dh before), vector
 // issue along rows (the exponential and the reciprocal of each gate). Measured (kernel alone, rates of the bytes that have to move; a large copy reaches
-// 5.05 TB/s): k_scan_cols_bwd 4 x 32768 x 1024 bf16 268 us, 5.1 TB/s, and its maps 110 us, 4.9 TB/s;
-// k_scan_rows_bwd 12288 x 784 fp32 with u in 8 bits and no states 41 us, 4.0 TB/s.
+// 5.05 TB/s): k_scan_cols_bwd 4 x 32768 x 1024 bf16 271 us, 5.0 TB/s, and its maps 113 us, 4.8 TB/s;
+// k_scan_rows_bwd 12288 x 784 fp32 with u in 8 bits and no states 42 us, 3.9 TB/s.
 #include "wbmm_scan.hpp"
 
 #include <type_traits>

@@ -79,10 +79,13 @@ ScanPlan scan_plan(int64_t outer, int64_t len, int64_t inner, bool bf16, int kin
   }
   const long long pieces = (len + piece - 1) / piece;
   // Column groups beyond the CUs: so few waves that a CU holds its share of the workgroups at a time,
-  // where that measured less (784 steps, 64 columns a group): forward 258 groups bf16 28 us instead of
-  // 35, 384 fp32 41 and 44, 1000 bf16 66 and 83; backward 1000 groups bf16 108 and 118, from a checkpoint
-  // 183 and 258. Not where it measured more: backward 258 groups 53 and 48, from a checkpoint 143 and
-  // 106, 1500 bf16 162 and 156; rows.
+  // where that measured less (784 steps, 64 columns a group): forward 258 groups bf16 27 us instead of
+  // 35, 384 fp32 38 and 43, 1000 bf16 65 and 87; backward 1000 groups bf16 107 and 123, from a checkpoint
+  // 185 and 263. Not where it measured more: backward 258 groups 53 and 48, from a checkpoint 143 and
+  // 106, 1500 bf16 162 and 156; rows. The same from 200 to 3200 steps: 1000 groups bf16, forward 22 and
+  // 32 us at 200 steps, 251 and 331 at 3200, backward 26 and 42, 430 and 442; up to 128 steps, one tile,
+  // nothing changes. It loses up to 7 % in forwards of 1500 groups bf16 at 200 and 400 steps (31 and 30,
+  // 50 and 46), and gains that at 784 and 1600.
   int cap = most;
   const int share = std::max(1, (int)(most / ((units + kCus - 1) / kCus)));
   if (!p.rows && units > 3 * kCus && (kind == 0 || (units <= 4 * kCus && (bf16 || ck)))) cap = share;
