@@ -321,10 +321,10 @@ wbmm_status wbmm_backward_bf16(int B, int C, int H, int W, int w, int layout, co
  *   value = q(code) * 2^(byte - 127);   byte 255: every value of the group is NaN,
  * q(code) the int8 value (WBMM_CKPT_INT8) or the OCP 8-bit float 4-3 value (WBMM_CKPT_E4M3).
  * int8 spreads its steps evenly below the group's largest magnitude, e4m3 keeps a relative error
- * of at most 2^-4 for magnitudes down to 2^-13 of it. Decoded values are exact in bf16 and fp32 (results
- * outside their range aside: in bf16 the smallest codes under bytes 0 to 2; and the largest
+ * of at most 2^-4 for magnitudes down to 2^-13 of it. Decoded values are exact in bf16 and fp32,
+ * results outside their range aside: in bf16 the smallest codes under bytes 0 to 2; and the largest
  * magnitudes, above 127/64 2^127 in int8 and from 31/16 2^127 in e4m3, whose nearest code stands
- * for 2^128, which reads back as an infinity).
+ * for 2^128, which reads back as an infinity.
  */
 #define WBMM_CKPT_GROUP 32
 typedef enum wbmm_ckpt_format { WBMM_CKPT_INT8 = 0, WBMM_CKPT_E4M3 = 1 } wbmm_ckpt_format;
@@ -359,7 +359,7 @@ wbmm_status wbmm_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int64_
  *          up to 2^-8 |dx|.
  * x_codes, x_scales, z_codes, z_scales: as wbmm_ckpt_pack writes them; z_* exactly with mix_w.
  * dx, dT, dmix_w: written, or NULL to skip. workspace: 256-byte aligned. For w = 1, w > 16 and
- * 33 C H W >= 2^30 it holds the decoded maps beside wbmm_backward's own: 4 bytes an element for x,
+ * most maps of 33 C H W >= 2^30 it holds the decoded maps beside wbmm_backward's own: 4 bytes an element for x,
  * for z with the mix, and for WBMM_BF16 for dy and dx as well, so that a call needs more memory
  * than the checkpoints save.
  * For 2 <= w <= 16 (very large images, 33 C H W >= 2^30, aside) every other fp32 operand enters the
@@ -423,6 +423,8 @@ wbmm_status wbmm_scan_forward(int64_t outer, int64_t len, int64_t inner, int dty
  * g, reverse, lens, sizes: as in the forward.
  * u:        the forward's u, or its checkpoint's codes when u_scales is given (u_fmt: the
  *           checkpoint's format; ignored without u_scales).
+ *           A checkpoint's groups run through the whole tensor: with lens, the padding that was
+ *           packed has to be finite, or its group's other values read back as NaN.
  * states:   as the forward wrote them, or NULL: the call then runs the recurrence for them first,
  *           on the u that it is given, from h0 (device fp32 [outer][inner], or NULL for zeros; NULL
  *           with states), into its workspace, reading g and u a second time. With a checkpointed u
