@@ -46,11 +46,11 @@ def listed():
         dict(name="adamw_layer_f32", op="adamw", state="f32", grad="f32", copy=False, layers=1,
              C=192, w=14),
         # a whole backbone, mixed precision, states in 8 bits
-        dict(name="adamw_model_e4m3", op="adamw", state="e4m3", grad="bf16", copy=True, layers=12,
-             C=768, w=14),
+        dict(name="adamw_model_e4m3", op="adamw", state="e4m3", grad="bf16", copy=True, layers=14,
+             C=640, w=14),
         # the same backbone with fp32 states
-        dict(name="adamw_model_f32", op="adamw", state="f32", grad="f32", copy=False, layers=12,
-             C=768, w=14),
+        dict(name="adamw_model_f32", op="adamw", state="f32", grad="f32", copy=False, layers=14,
+             C=640, w=14),
         # serving: one new position per sequence, the state updated
         dict(name="delta_step_bf16", op="delta_fwd", dtype="bf16", B=8, L=1, Hk=3, H=6, dk=64,
              dv=64, reverse=False, ragged=False, states=False),
