@@ -449,6 +449,104 @@ wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inner, int dt
                                void* stream);
 
 /*
+ * wbmm_rmsnorm_forward — root-mean-square norm along one axis with the residual's addition in front:
+ * what stands before a mixer. Tensors are dense (outer, len, inner) and normed over len, for every
+ * (outer, inner): the channels of a map are (B, C, H W) in NCHW, (B H W, C, 1) in NHWC.
+ *   t = x + residual,   y = t weight / sqrt(mean_len(t^2) + eps).
+ * Computed in fp32 from the sum as it is; s and y are rounded once (RNE). Squares are fp32: |t| beyond
+ * about 1.8e19 makes their mean infinite and y zero there. An infinity or NaN in t reaches its own
+ * (outer, inner) only.
+ * dtype:    of x, residual, s and y: WBMM_F32 or WBMM_BF16.
+ * residual: device tensor, or NULL. weight: device fp32 [len], or NULL for ones.
+ * s:        device tensor, t in dtype (what the backward takes), or NULL. May be x or residual itself.
+ * y:        device tensor, written.
+ * codes, scales: the checkpoint of y in `fmt`, exactly what wbmm_ckpt_pack makes of it (n bytes and
+ *           ceil(n / WBMM_CKPT_GROUP) bytes), or both NULL (fmt ignored). In the same launch where the
+ *           groups do not run across rows (len a multiple of 32 at inner = 1, or inner a multiple of 32)
+ *           and addresses are aligned to 16 bytes (codes to 8), else by a second launch over y.
+ * Any pointer alignment down to the element works. No workspace, no atomics: bitwise reproducible.
+ * Errors: WBMM_E_INVALID (sizes, dtype, fmt, eps, NULL or overlapping buffers), WBMM_E_UNSUPPORTED (len >
+ * 2^20, outer * inner > 2^25 (2^23 for inner = 1 and len > 1536), more than 2^35 elements, misaligned
+ * pointer), WBMM_E_HIP.
+ */
+wbmm_status wbmm_rmsnorm_forward(int64_t outer, int64_t len, int64_t inner, int dtype, float eps,
+                                 const void* x, const void* residual, const float* weight, void* s,
+                                 void* y, int fmt, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * wbmm_rmsnorm_backward_workspace_bytes / wbmm_rmsnorm_backward — gradients of wbmm_rmsnorm_forward at
+ * the sum that it stored:
+ *   r = 1 / sqrt(mean(s^2) + eps),   h = s r,
+ *   dx = ds + r (weight dy - h mean(weight dy h)),   dweight = sum over (outer, inner) of dy h.
+ * s:       the forward's s (its x where there was no residual). dy: gradient of y.
+ * ds:      gradient of s from elsewhere (the residual's further way), or NULL for zeros.
+ * dx:      device tensor in dtype, the gradient of x and of residual alike, or NULL to skip.
+ * dweight: device fp32 [len], or NULL to skip. Summed in a fixed order, in fp32 with the roundings
+ *          carried along, then in fp64.
+ * workspace: wbmm_rmsnorm_backward_workspace_bytes(...) bytes, 16-byte aligned; not needed without
+ *          dweight. Calls that share one must be ordered on one stream.
+ * Errors as in the forward, and WBMM_E_WORKSPACE.
+ */
+size_t wbmm_rmsnorm_backward_workspace_bytes(int64_t outer, int64_t len, int64_t inner);
+wbmm_status wbmm_rmsnorm_backward(int64_t outer, int64_t len, int64_t inner, int dtype, float eps,
+                                  const void* s, const float* weight, const void* dy,
+                                  const void* ds, void* dx, float* dweight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * wbmm_adamw_plan / wbmm_adamw_step — one AdamW step over all parameters of a model in one launch, from
+ * the gradients that the backward calls write. For every element, with t the step's number:
+ *   g = grad_factor grad,   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = (1 - lr wd) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * Everything is fp32 and rounded operation by operation; the factors of lr, beta and t are formed in
+ * fp64 and rounded once.
+ * A wbmm_adamw_tensor is one parameter, dense, all pointers to device memory:
+ *   p:        fp32, updated. g: fp32 or bf16 (g_dtype), read. n: elements. weight_decay: wd.
+ *   m, v:     fp32, updated; or, with m_scales and v_scales, 8-bit states: m and the root of v as
+ *             checkpoints in WBMM_CKPT_E4M3 (n code bytes and ceil(n / WBMM_CKPT_GROUP) scale bytes each;
+ *             all zero bytes are zero states). They are read as wbmm_ckpt_unpack gives them. What is
+ *             stored is rounded to one of the two neighbouring code values at random, to the value
+ *             itself on average, a root above zero never to 0; random words are Philox 4x32 with 7
+ *             rounds, counter (index / 4 as 64 bits, tensor, t), key `seed`, word index % 4, its low
+ *             16 bits for m and its high ones for the root. A group that holds an infinity or a NaN
+ *             becomes NaN, as in wbmm_ckpt_pack.
+ *   p_bf16:   a copy of p in bf16 (RNE), written, or NULL: what a bf16 forward reads.
+ * wbmm_adamw_plan checks `count` such tensors and lays out a table for them in HOST memory (table_bytes
+ *   at least wbmm_adamw_plan_bytes(...), 8-byte aligned); the caller copies it to the device and keeps
+ *   both it and the tensors where they are. *chunks is what the step wants back. No GPU work.
+ *   Overlapping buffers are refused, two gradients aside.
+ * wbmm_adamw_step: table: the device copy, 8-byte aligned; count, chunks: the plan's (a table of other
+ *   counts is left alone: nothing is written).
+ *   step:     t, from 1 to 2^31 - 1; with step_dev, a device int32 read by the kernel, `step` is ignored
+ *             (a captured graph counts on the device; it must hold at least 1).
+ *   lr_factor, grad_factor: device fp32 that lr and the gradients are multiplied by, or NULL.
+ * 1 <= t; 0 <= beta < 1; eps >= 0. Any alignment down to the element works; 16 bytes (codes 8) takes the
+ * wide accesses. Bitwise reproducible, and the same for any alignment.
+ * Errors: WBMM_E_INVALID, WBMM_E_UNSUPPORTED (more than 2^36 elements, misaligned pointers),
+ * WBMM_E_WORKSPACE (table too small), WBMM_E_HIP.
+ */
+typedef struct wbmm_adamw_tensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* m_scales;
+  uint8_t* v_scales;
+  uint16_t* p_bf16;
+  int64_t n;
+  double weight_decay;
+  int32_t g_dtype;
+  int32_t reserved;
+} wbmm_adamw_tensor;
+size_t wbmm_adamw_plan_bytes(const wbmm_adamw_tensor* tensors, int64_t count);
+wbmm_status wbmm_adamw_plan(const wbmm_adamw_tensor* tensors, int64_t count, void* table,
+                            size_t table_bytes, int64_t* chunks);
+wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, double lr,
+                            double beta1, double beta2, double eps, int64_t step,
+                            const int32_t* step_dev, const float* lr_factor,
+                            const float* grad_factor, uint64_t seed, void* stream);
+
+/*
  * wbmm_probe_mfma — measurement aid, not part of the method: a matrix-core peak probe. Launches
  * `blocks` workgroups of 4 waves; every wave runs `iters` rounds of 8 independent MFMA
  * accumulation chains on register operands (dtype WBMM_F32: v_mfma_f32_16x16x4f32, WBMM_BF16:

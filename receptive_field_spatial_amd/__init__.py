@@ -27,6 +27,8 @@ __all__ = [
     "wbmm_ckpt_pack", "wbmm_ckpt_unpack", "wbmm_backward_ckpt",
     "wbmm_backward_ckpt_workspace_bytes", "wbmm_scan_forward", "wbmm_scan_backward",
     "wbmm_scan_forward_workspace_bytes", "wbmm_scan_backward_workspace_bytes", "WBMM_CKPT_GROUP", "WBMM_SCAN_CHUNK",
+    "wbmm_rmsnorm_forward", "wbmm_rmsnorm_backward", "wbmm_rmsnorm_backward_workspace_bytes",
+    "wbmm_adamw_plan", "wbmm_adamw_step", "WbmmAdamwPlan",
     "WBMM_OK", "WBMM_E_INVALID", "WBMM_E_UNSUPPORTED", "WBMM_E_WORKSPACE", "WBMM_E_HIP",
 ]
 
@@ -53,9 +55,15 @@ def lib_path() -> str:
     return os.path.join(_PKG_DIR, "libwbmm.so")
 
 
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scales", "v_scales", "p_bf16")]
+    _fields_ += [("n", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                 ("g_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def _declare(lib):
     c_int, c_size, vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
-    c_i64 = ctypes.c_int64
+    c_i64, c_f, c_d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     sigs = {
         "wbmm_abi_version": (c_int, []),
         "wbmm_last_error": (ctypes.c_char_p, []),
@@ -91,6 +99,14 @@ def _declare(lib):
                               [c_size, vp]),
         "wbmm_scan_backward": (c_int, [c_i64] * 3 + [c_int] * 3 + [vp] * 8 + [c_i64] + [vp] * 4 +
                                [c_size, vp]),
+        "wbmm_rmsnorm_forward": (c_int, [c_i64] * 3 + [c_int, c_f] + [vp] * 5 + [c_int] + [vp] * 3),
+        "wbmm_rmsnorm_backward_workspace_bytes": (c_size, [c_i64] * 3),
+        "wbmm_rmsnorm_backward": (c_int, [c_i64] * 3 + [c_int, c_f] + [vp] * 7 + [c_size, vp]),
+        "wbmm_adamw_plan_bytes": (c_size, [ctypes.POINTER(_AdamwTensor), c_i64]),
+        "wbmm_adamw_plan": (c_int, [ctypes.POINTER(_AdamwTensor), c_i64, vp, c_size,
+                                    ctypes.POINTER(c_i64)]),
+        "wbmm_adamw_step": (c_int, [vp, c_i64, c_i64] + [c_d] * 4 + [c_i64] + [vp] * 3 +
+                            [ctypes.c_uint64, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -728,3 +744,149 @@ def wbmm_scan_backward(g, states, dh, dim: int, *, u=None, u_ckpt=None, fmt: str
                                      up, us, sp, h0p, dhp, dlp, lp, n_lens, dgp, dup, d0p, wp,
                                      wb, _current_stream(idx)))
     return dg, du, dh0
+
+
+# ----------------------------------------------------------------------------- RMS norm
+@functools.lru_cache(maxsize=256)
+def wbmm_rmsnorm_backward_workspace_bytes(outer: int, length: int, inner: int) -> int:
+    return int(_lib().wbmm_rmsnorm_backward_workspace_bytes(int(outer), int(length), int(inner)))
+
+
+def wbmm_rmsnorm_forward(x, dim: int, *, residual=None, weight=None, eps: float = 1e-6, s=None,
+                         y=None, fmt: Optional[str] = None, codes=None, scales=None, stream=None):
+    """RMS norm over dimension `dim` of t = x + residual (fp32 or bf16, dense, same shape):
+    y = t weight / sqrt(mean(t^2) + eps); weight fp32 of dim's size, or None for ones.
+
+    s: the sum in x's dtype; None allocates it where there is a residual, False skips it, a tensor is
+    written (it may be x or residual itself). fmt: "int8" or "e4m3" gives y's checkpoint too, as
+    wbmm_ckpt_pack would. Returns (y, s, ckpt): s is x itself without a residual (what
+    wbmm_rmsnorm_backward takes), ckpt is (codes, scales) or None."""
+    if stream is not None:
+        with _on_stream(stream, "x", x):
+            return wbmm_rmsnorm_forward(x, dim, residual=residual, weight=weight, eps=eps, s=s, y=y,
+                                        fmt=fmt, codes=codes, scales=scales)
+    torch = _torch()
+    dtype, shape = x.dtype, x.shape
+    dt, idx = _dtype_code(dtype), _device("x", x)
+    outer, length, inner = _scan_sizes(shape, dim)[:3]
+    xp, rp = _need("x", x, shape, dtype, idx), _opt("residual", residual, shape, dtype, idx)
+    wp = _opt("weight", weight, (length,), torch.float32, idx)
+    s, sp = _out("s", residual is not None if s is None else s, shape, dtype, idx, x)
+    y, yp = _out("y", True if y is None else y, shape, dtype, idx, x)
+    fcode = cp = scp = 0
+    if fmt is not None:
+        fcode, u8 = _fmt_code(fmt), torch.uint8
+        codes, cp = _out("codes", True if codes is None else codes, shape, u8, idx)
+        scales, scp = _out("scales", True if scales is None else scales, (_ckpt_scales(x.numel()),),
+                           u8, idx)
+    elif codes is not None or scales is not None:
+        raise WbmmError(WBMM_E_INVALID, "codes and scales go with fmt")
+    _check(_lib().wbmm_rmsnorm_forward(outer, length, inner, dt, eps, xp, rp, wp, sp, yp, fcode,
+                                       cp or None, scp or None, _current_stream(idx)))
+    return y, x if s is None and residual is None else s, (codes, scales) if fmt is not None else None
+
+
+def wbmm_rmsnorm_backward(s, dy, dim: int, *, weight=None, ds=None, eps: float = 1e-6, dx=True,
+                          dweight=True, workspace=None, stream=None):
+    """Gradients of wbmm_rmsnorm_forward at the sum s that it returned. ds: gradient of s from
+    elsewhere, or None. Returns (dx, dweight): dx in s's dtype is the gradient of x and of the
+    residual, dweight fp32 (None without a weight); an output passed as False is skipped."""
+    if stream is not None:
+        with _on_stream(stream, "s", s):
+            return wbmm_rmsnorm_backward(s, dy, dim, weight=weight, ds=ds, eps=eps, dx=dx,
+                                         dweight=dweight, workspace=workspace)
+    f32, dtype, shape = _torch().float32, s.dtype, s.shape
+    dt, idx = _dtype_code(dtype), _device("s", s)
+    outer, length, inner = _scan_sizes(shape, dim)[:3]
+    sp, dyp = _need("s", s, shape, dtype, idx), _need("dy", dy, shape, dtype, idx)
+    wp, dsp = _opt("weight", weight, (length,), f32, idx), _opt("ds", ds, shape, dtype, idx)
+    dx, dxp = _out("dx", dx, shape, dtype, idx, s)
+    dweight, dwp = _out("dweight", dweight if weight is not None else None, (length,), f32, idx,
+                        weight)
+    need = 0 if dwp is None else wbmm_rmsnorm_backward_workspace_bytes(outer, length, inner)
+    ws, wsp, wsb = _workspace(need, workspace, idx)
+    _check(_lib().wbmm_rmsnorm_backward(outer, length, inner, dt, eps, sp, wp, dyp, dsp, dxp, dwp,
+                                        wsp, wsb, _current_stream(idx)))
+    return dx, dweight
+
+
+# ----------------------------------------------------------------------------- AdamW
+class WbmmAdamwPlan:
+    """What wbmm_adamw_plan returns: the table on the GPU, and the tensors, which have to stay where
+    they are as long as the plan is stepped."""
+
+    def __init__(self, table, count, chunks, tensors):
+        self.table, self.count, self.chunks, self.tensors = table, count, chunks, tensors
+        self.ptr, self.idx = table.data_ptr(), table.get_device()
+
+
+def wbmm_adamw_plan(params, grads, m, v, *, copies=None, weight_decay=0.0) -> WbmmAdamwPlan:
+    """Plan of an AdamW step over many tensors (lists of equal length, all on the current GPU).
+
+    params: fp32, updated by the steps. grads: fp32 or bf16 in the parameters' shapes, read where they
+    are. m, v: per parameter an fp32 tensor of its shape, or a pair (codes, scales) for 8-bit states:
+    uint8 in its shape and uint8 of ceil(n / WBMM_CKPT_GROUP), of v the root is kept (zeros to begin
+    with). copies: bf16 tensors (or None) that receive the parameters. weight_decay: a number, or one
+    per parameter. Copies a table to the GPU and waits for it; not for a graph's capture."""
+    torch = _torch()
+    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    count = len(params)
+    copies = [None] * count if copies is None else list(copies)
+    decays = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * count
+    if count == 0:
+        raise WbmmError(WBMM_E_INVALID, "no tensors")
+    if not count == len(grads) == len(m) == len(v) == len(copies) == len(decays):
+        raise WbmmError(WBMM_E_INVALID, "the lists differ in length")
+    idx = _device("params[0]", params[0])
+    table = (_AdamwTensor * count)()
+    for i, (p, g, mi, vi, c) in enumerate(zip(params, grads, m, v, copies)):
+        t, sh = table[i], p.shape
+        t.p, t.n, t.weight_decay = _need(f"params[{i}]", p, sh, f32, idx), p.numel(), decays[i]
+        if g is None or g.dtype not in (f32, bf16):
+            raise WbmmError(WBMM_E_INVALID, f"grads[{i}] must be fp32 or bf16")
+        t.g, t.g_dtype = _need(f"grads[{i}]", g, sh, g.dtype, idx), _dtype_code(g.dtype)
+        t.p_bf16 = _opt(f"copies[{i}]", c, sh, bf16, idx)
+        small = isinstance(mi, (tuple, list))
+        if small != isinstance(vi, (tuple, list)):
+            raise WbmmError(WBMM_E_INVALID, f"m[{i}] and v[{i}] must both be in 8 bits, or neither")
+        if small:
+            sc = (_ckpt_scales(p.numel()),)
+            t.m, t.v = _need(f"m[{i}] codes", mi[0], sh, u8, idx), _need(f"v[{i}] codes", vi[0], sh, u8, idx)
+            t.m_scales = _need(f"m[{i}] scales", mi[1], sc, u8, idx)
+            t.v_scales = _need(f"v[{i}] scales", vi[1], sc, u8, idx)
+        else:
+            t.m, t.v = _need(f"m[{i}]", mi, sh, f32, idx), _need(f"v[{i}]", vi, sh, f32, idx)
+    size = _lib().wbmm_adamw_plan_bytes(table, count)
+    host = torch.zeros(max(size, 8) // 8 + 1, dtype=torch.int64)
+    chunks = ctypes.c_int64()
+    _check(_lib().wbmm_adamw_plan(table, count, host.data_ptr(), host.numel() * 8,
+                                  ctypes.byref(chunks)))
+    dev = host.to(torch.device("cuda", idx))
+    torch.cuda.current_stream(idx).synchronize()
+    return WbmmAdamwPlan(dev, count, chunks.value, (params, grads, m, v, copies))
+
+
+def wbmm_adamw_step(plan: WbmmAdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+                    step=1, lr_factor=None, grad_factor=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over the plan's tensors. step: the step's number from 1, or an int32 tensor of one
+    element on the GPU, read there (a captured graph counts on). lr_factor, grad_factor: fp32 tensors
+    of one element on the GPU that lr and the gradients are multiplied by. seed: of the 8-bit states'
+    rounding."""
+    if stream is not None:
+        with _on_stream(stream, "plan", plan.table):
+            return wbmm_adamw_step(plan, lr=lr, betas=betas, eps=eps, step=step, lr_factor=lr_factor,
+                                   grad_factor=grad_factor, seed=seed)
+    torch = _torch()
+    idx = plan.idx
+    if idx != torch._C._cuda_getDevice():
+        _device("plan", plan.table)
+    stp = None
+    if isinstance(step, torch.Tensor):
+        stp, step = _need("step", step, step.shape if step.numel() == 1 else (1,), torch.int32, idx), 0
+    f32 = torch.float32
+    lp, gp = (None if t is None else _need(n, t, t.shape if t.numel() == 1 else (1,), f32, idx)
+              for n, t in (("lr_factor", lr_factor), ("grad_factor", grad_factor)))
+    _check(_lib().wbmm_adamw_step(plan.ptr, plan.count, plan.chunks, lr, betas[0], betas[1], eps,
+                                  step, stp, lp, gp, seed & 0xffffffffffffffff,
+                                  _current_stream(idx)))

@@ -2,14 +2,21 @@
 // error message, and dispatch to the kernel launchers.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "../../include/wbmm.h"
+#include "wbmm_adamw.hpp"
 #include "wbmm_launch.hpp"
+#include "wbmm_norm.hpp"
 #include "wbmm_scan.hpp"
 
 #define WBMM_API extern "C" __attribute__((visibility("default")))
@@ -869,4 +876,242 @@ WBMM_API wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inne
                      workspace_bytes);
   if (st != WBMM_OK) return st;
   return hip_status(wbmm::launch_scan_backward(r, (hipStream_t)stream), "wbmm_scan_backward");
+}
+
+// ---------------------------------------------------------------------------- RMS norm
+namespace {
+
+// A row takes up to 64 lanes, one longer than a wave's registers 256, and grids hold 2^32 threads.
+constexpr int64_t kMaxNormRows = 1ll << 25;
+
+wbmm_status check_norm(int64_t outer, int64_t len, int64_t inner, int dtype, double eps) {
+  if (outer < 1 || len < 1 || inner < 1)
+    return fail(WBMM_E_INVALID, "sizes must be >= 1 (outer=%lld len=%lld inner=%lld)",
+                (long long)outer, (long long)len, (long long)inner);
+  if (len > kMaxDim) return fail(WBMM_E_UNSUPPORTED, "len=%lld exceeds 2^20", (long long)len);
+  if (outer > kMaxNormRows || inner > kMaxNormRows || outer * inner > kMaxNormRows)
+    return fail(WBMM_E_UNSUPPORTED, "outer * inner exceeds 2^25");
+  if (outer * inner > kMaxCkpt / len) return fail(WBMM_E_UNSUPPORTED, "tensor too large");
+  if (inner == 1 && len > wbmm::kNormWaveLen && outer > kMaxNormRows / 4)
+    return fail(WBMM_E_UNSUPPORTED, "more than 2^23 rows of over %d elements", wbmm::kNormWaveLen);
+  if (!valid_dtype(dtype)) return fail(WBMM_E_INVALID, "unknown dtype %d", dtype);
+  if (!(eps >= 0) || eps > 3e38) return fail(WBMM_E_INVALID, "eps must be finite and not negative");
+  return WBMM_OK;
+}
+
+}  // namespace
+
+WBMM_API wbmm_status wbmm_rmsnorm_forward(int64_t outer, int64_t len, int64_t inner, int dtype,
+                                          float eps, const void* x, const void* residual,
+                                          const float* weight, void* s, void* y, int fmt,
+                                          uint8_t* codes, uint8_t* scales, void* stream) {
+  wbmm_status st = check_norm(outer, len, inner, dtype, eps);
+  if (st != WBMM_OK) return st;
+  if (!x || !y) return fail(WBMM_E_INVALID, "x and y must be non-NULL");
+  if ((codes == nullptr) != (scales == nullptr))
+    return fail(WBMM_E_INVALID, "codes and scales go together");
+  if (codes && !valid_fmt(fmt)) return fail(WBMM_E_INVALID, "unknown checkpoint format %d", fmt);
+  const size_t es = dtype_size(dtype);
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, 4) || !aligned(s, es) ||
+      !aligned(y, es))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const size_t n = (size_t)outer * len * inner;
+  // s may be x or the residual itself: an element is written after it has been read
+  const Span in[] = {{x == s ? nullptr : x, n * es, "x"},
+                     {residual == s ? nullptr : residual, n * es, "residual"},
+                     {weight, (size_t)len * 4, "weight"}};
+  const Span out[] = {{s, n * es, "s"}, {y, n * es, "y"}, {codes, n, "codes"},
+                      {scales, ckpt_scales((int64_t)n), "scales"}};
+  st = check_spans(in, 3, out, 4);
+  if (st != WBMM_OK) return st;
+  wbmm::NormRequest r{};
+  r.outer = outer; r.len = len; r.inner = inner;
+  r.bf16 = dtype == WBMM_BF16;
+  r.fmt = fmt; r.eps = eps;
+  r.x = x; r.res = residual; r.w = weight; r.s = s; r.y = y; r.codes = codes; r.scales = scales;
+  return hip_status(wbmm::launch_norm_forward(r, (hipStream_t)stream), "wbmm_rmsnorm_forward");
+}
+
+WBMM_API size_t wbmm_rmsnorm_backward_workspace_bytes(int64_t outer, int64_t len, int64_t inner) {
+  if (check_norm(outer, len, inner, WBMM_F32, 0) != WBMM_OK) return 0;
+  return wbmm::norm_backward_workspace(outer, len, inner);
+}
+
+WBMM_API wbmm_status wbmm_rmsnorm_backward(int64_t outer, int64_t len, int64_t inner, int dtype,
+                                           float eps, const void* s, const float* weight,
+                                           const void* dy, const void* ds, void* dx,
+                                           float* dweight, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  wbmm_status st = check_norm(outer, len, inner, dtype, eps);
+  if (st != WBMM_OK) return st;
+  if (!s || !dy) return fail(WBMM_E_INVALID, "s and dy must be non-NULL");
+  const size_t es = dtype_size(dtype);
+  if (!aligned(s, es) || !aligned(dy, es) || !aligned(ds, es) || !aligned(dx, es) ||
+      !aligned(weight, 4) || !aligned(dweight, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const size_t n = (size_t)outer * len * inner * es;
+  const Span in[] = {{s, n, "s"}, {dy, n, "dy"}, {ds, n, "ds"}, {weight, (size_t)len * 4, "weight"}};
+  const Span out[] = {{dx, n, "dx"}, {dweight, (size_t)len * 4, "dweight"}};
+  st = check_spans(in, 4, out, 2);
+  if (st != WBMM_OK) return st;
+  if (!dx && !dweight) return ok();
+  const size_t need = dweight ? wbmm::norm_backward_workspace(outer, len, inner) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(WBMM_E_WORKSPACE, "workspace of %zu bytes required, %zu given", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 16))
+    return fail(WBMM_E_UNSUPPORTED, "workspace not 16-byte aligned");
+  wbmm::NormRequest r{};
+  r.outer = outer; r.len = len; r.inner = inner;
+  r.bf16 = dtype == WBMM_BF16;
+  r.eps = eps;
+  r.x = s; r.res = ds; r.w = weight; r.dy = dy; r.y = dx; r.dw = dweight; r.ws = workspace;
+  return hip_status(wbmm::launch_norm_backward(r, (hipStream_t)stream), "wbmm_rmsnorm_backward");
+}
+
+// ---------------------------------------------------------------------------- AdamW
+namespace {
+
+constexpr int64_t kMaxAdamChunks = (1ll << 24) - 1;   // grids hold 2^32 threads
+
+int64_t adam_chunks(int64_t n) { return (n + wbmm::kAdamChunk - 1) / wbmm::kAdamChunk; }
+
+wbmm_status adam_sizes(const wbmm_adamw_tensor* t, int64_t count, int64_t* chunks) {
+  if (!t) return fail(WBMM_E_INVALID, "tensors must be non-NULL");
+  if (count < 1) return fail(WBMM_E_INVALID, "count=%lld must be >= 1", (long long)count);
+  if (count > kMaxAdamChunks) return fail(WBMM_E_UNSUPPORTED, "more than 2^24 - 1 tensors");
+  int64_t sum = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n < 1)
+      return fail(WBMM_E_INVALID, "tensor %lld: n=%lld must be >= 1", (long long)i,
+                  (long long)t[i].n);
+    if (t[i].n > kMaxAdamChunks * wbmm::kAdamChunk ||
+        (sum += adam_chunks(t[i].n)) > kMaxAdamChunks)
+      return fail(WBMM_E_UNSUPPORTED, "more than 2^36 elements");
+  }
+  *chunks = sum;
+  return WBMM_OK;
+}
+
+size_t adam_bytes(int64_t count, int64_t chunks) {
+  return sizeof(wbmm::AdamHead) + (size_t)count * sizeof(wbmm::AdamEntry) + (size_t)chunks * 4;
+}
+
+wbmm_status adam_tensor(const wbmm_adamw_tensor& t, long long i) {
+  if (!t.p || !t.g || !t.m || !t.v)
+    return fail(WBMM_E_INVALID, "tensor %lld: p, g, m and v must be non-NULL", i);
+  if ((t.m_scales == nullptr) != (t.v_scales == nullptr))
+    return fail(WBMM_E_INVALID, "tensor %lld: m_scales and v_scales go together", i);
+  if (!valid_dtype(t.g_dtype))
+    return fail(WBMM_E_INVALID, "tensor %lld: unknown gradient dtype %d", i, t.g_dtype);
+  if (!std::isfinite(t.weight_decay) || t.weight_decay < 0)
+    return fail(WBMM_E_INVALID, "tensor %lld: weight_decay must be finite and not negative", i);
+  const bool small = t.m_scales != nullptr;
+  if (!aligned(t.p, 4) || !aligned(t.g, dtype_size(t.g_dtype)) || !aligned(t.p_bf16, 2) ||
+      (!small && (!aligned(t.m, 4) || !aligned(t.v, 4))))
+    return fail(WBMM_E_UNSUPPORTED, "tensor %lld: pointer not aligned to its element size", i);
+  return WBMM_OK;
+}
+
+}  // namespace
+
+WBMM_API size_t wbmm_adamw_plan_bytes(const wbmm_adamw_tensor* tensors, int64_t count) {
+  int64_t chunks = 0;
+  return adam_sizes(tensors, count, &chunks) == WBMM_OK ? adam_bytes(count, chunks) : 0;
+}
+
+WBMM_API wbmm_status wbmm_adamw_plan(const wbmm_adamw_tensor* tensors, int64_t count, void* table,
+                                     size_t table_bytes, int64_t* chunks) {
+  int64_t total = 0;
+  wbmm_status st = adam_sizes(tensors, count, &total);
+  if (st != WBMM_OK) return st;
+  if (!table || !chunks) return fail(WBMM_E_INVALID, "table and chunks must be non-NULL");
+  if (table_bytes < adam_bytes(count, total))
+    return fail(WBMM_E_WORKSPACE, "table of %zu bytes required, %zu given",
+                adam_bytes(count, total), table_bytes);
+  if (!aligned(table, 8)) return fail(WBMM_E_UNSUPPORTED, "table not 8-byte aligned");
+  // nothing that a step writes may be another tensor's, or its own gradient
+  struct Range { uintptr_t a, b; int64_t i; bool written; };
+  try {
+    std::vector<Range> all;
+    all.reserve((size_t)count * 7);
+    for (int64_t i = 0; i < count; ++i) {
+      const wbmm_adamw_tensor& t = tensors[i];
+      st = adam_tensor(t, (long long)i);
+      if (st != WBMM_OK) return st;
+      const size_t n = (size_t)t.n, e = t.m_scales ? 1 : 4, sc = ckpt_scales(t.n);
+      auto add = [&](const void* p, size_t bytes, bool written) {
+        if (p) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, i, written});
+      };
+      add(t.p, n * 4, true);
+      add(t.g, n * dtype_size(t.g_dtype), false);
+      add(t.m, n * e, true);
+      add(t.v, n * e, true);
+      add(t.m_scales, sc, true);
+      add(t.v_scales, sc, true);
+      add(t.p_bf16, n * 2, true);
+    }
+    std::sort(all.begin(), all.end(), [](const Range& x, const Range& y) { return x.a < y.a; });
+    uintptr_t end = 0, wend = 0;       // of all ranges so far, and of the written ones
+    int64_t at = 0, wat = 0;
+    for (const Range& r : all) {
+      if (r.a < wend || (r.written && r.a < end))
+        return fail(WBMM_E_INVALID, "tensors %lld and %lld overlap",
+                    (long long)(r.a < wend ? wat : at), (long long)r.i);
+      if (r.b > end) end = r.b, at = r.i;
+      if (r.written && r.b > wend) wend = r.b, wat = r.i;
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(WBMM_E_UNSUPPORTED, "out of host memory for %lld tensors", (long long)count);
+  }
+  wbmm::AdamHead* head = (wbmm::AdamHead*)table;
+  *head = {wbmm::kAdamMagic, (uint64_t)count, (uint64_t)total, 0};
+  wbmm::AdamEntry* entries = (wbmm::AdamEntry*)(head + 1);
+  uint32_t* owner = (uint32_t*)(entries + count);
+  uint32_t first = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const wbmm_adamw_tensor& t = tensors[i];
+    const bool small = t.m_scales != nullptr;
+    wbmm::AdamEntry e{};
+    e.p = t.p; e.g = t.g; e.m = t.m; e.v = t.v; e.ms = t.m_scales; e.vs = t.v_scales;
+    e.copy = t.p_bf16; e.n = t.n; e.decay = t.weight_decay; e.first = first;
+    const size_t sa = small ? 8 : 16;
+    if (t.g_dtype == WBMM_BF16) e.flags |= wbmm::kAdamG16;
+    if (small) e.flags |= wbmm::kAdam8;
+    if (aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.m, sa) && aligned(t.v, sa) &&
+        aligned(t.p_bf16, 16))
+      e.flags |= wbmm::kAdamWide;
+    entries[i] = e;
+    const uint32_t c = (uint32_t)adam_chunks(t.n);
+    for (uint32_t k = 0; k < c; ++k) owner[first + k] = (uint32_t)i;
+    first += c;
+  }
+  *chunks = total;
+  return ok();
+}
+
+WBMM_API wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, double lr,
+                                     double beta1, double beta2, double eps, int64_t step,
+                                     const int32_t* step_dev, const float* lr_factor,
+                                     const float* grad_factor, uint64_t seed, void* stream) {
+  if (!table) return fail(WBMM_E_INVALID, "table must be non-NULL");
+  if (count < 1 || chunks < count || chunks > kMaxAdamChunks)
+    return fail(WBMM_E_INVALID, "count=%lld and chunks=%lld are not a plan's", (long long)count,
+                (long long)chunks);
+  if (!std::isfinite(lr)) return fail(WBMM_E_INVALID, "lr must be finite");
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1))
+    return fail(WBMM_E_INVALID, "beta1 and beta2 must lie in [0, 1)");
+  if (!(eps >= 0) || !std::isfinite(eps))
+    return fail(WBMM_E_INVALID, "eps must be finite and not negative");
+  if (!step_dev && (step < 1 || step > INT32_MAX))
+    return fail(WBMM_E_INVALID, "step=%lld outside [1, 2^31)", (long long)step);
+  if (!aligned(table, 8) || !aligned(step_dev, 4) || !aligned(lr_factor, 4) ||
+      !aligned(grad_factor, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  wbmm::AdamRequest r{};
+  r.table = table; r.count = (uint32_t)count; r.chunks = (uint32_t)chunks;
+  r.lr = lr; r.beta1 = beta1; r.beta2 = beta2; r.eps = eps;
+  r.step = step; r.step_dev = step_dev; r.lr_factor = lr_factor; r.grad_factor = grad_factor;
+  r.seed = seed;
+  return hip_status(wbmm::launch_adamw(r, (hipStream_t)stream), "wbmm_adamw_step");
 }

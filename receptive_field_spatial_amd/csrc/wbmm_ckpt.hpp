@@ -42,4 +42,36 @@ __device__ __forceinline__ float ckpt_decode1(uint32_t code, int fmt) {
   return fmt == kFmtInt8 ? (float)(int8_t)code : __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
 }
 
+// Scale byte of a group whose largest magnitude has the bits m (finite): e + 127 with e the least
+// integer >= -126 such that m <= top 2^e.
+__device__ __forceinline__ int ckpt_scale_byte(uint32_t m, int fmt) {
+  const uint32_t over = fmt == kFmtInt8 ? 0x7e0000u : 0x600000u;
+  const int byte = (int)(m >> 23) - (fmt == kFmtInt8 ? 6 : 8) + ((m & 0x7fffffu) > over ? 1 : 0);
+  return byte < 1 ? 1 : byte;
+}
+// 2^(127 - byte), for byte from 1 to 253.
+__device__ __forceinline__ float ckpt_inverse(int byte) {
+  return __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+// The larger of x over the lane's quad.
+__device__ __forceinline__ uint32_t ckpt_quad_max(uint32_t x) {
+  const uint32_t a = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xf, 0xf, true);
+  x = x > a ? x : a;
+  const uint32_t b = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xf, 0xf, true);
+  return x > b ? x : b;
+}
+
+// Codes of four scaled values, to the nearest.
+__device__ __forceinline__ uint32_t ckpt_encode4(const float (&s)[4], int fmt) {
+  if (fmt == kFmtInt8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= ((uint32_t)(int)rintf(s[j]) & 0xffu) << (8 * j);
+    return w;
+  }
+  const int p = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], p, true);
+}
+
 }  // namespace wbmm
