@@ -547,6 +547,73 @@ wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, do
                             const float* grad_factor, uint64_t seed, void* stream);
 
 /*
+ * wbmm_delta_forward_workspace_bytes / wbmm_delta_forward — gated delta rule: the recurrence beside
+ * wbmm_scan_forward whose state is a matrix S (dk x dv) per head, for long sequences, maps in raster
+ * order (a map in NHWC is (B, H W, heads, channels of a head) as it lies) and single steps:
+ *   a_t = sigmoid(g_t),   b_t = sigmoid(beta_t),
+ *   S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,   o_t = scale S_t^T q_t,   S_{-1} = s0.
+ * Keys are taken as they are; the rule contracts for |k| <= 1 (wbmm_rmsnorm_forward over a key's entries,
+ * with weights of dk^-1/2, gives length 1).
+ * Sizes:    B, L, Hk, H >= 1, Hk dividing H; 1 <= dk, dv <= 128.
+ * dtype:    of q, k, v, g, beta and o: WBMM_F32 or WBMM_BF16. Sums and the state are fp32, products good
+ *           to 2^-24 of their factors; bf16 outputs to 2^-17 of theirs before they are rounded (RNE).
+ * reverse:  nonzero: sequences run from their last position to their first.
+ * q, k:     device [B][L][Hk][dk]; head h uses key head h / (H / Hk). v: device [B][L][H][dv].
+ * g, beta:  device [B][L][H]. g is held to [-87, 87].
+ * s0:       device fp32 [B][H][dk][dv], or NULL for zeros.
+ * lens:     device int32 [B], or NULL: sequence b has lens[b] positions, held to [0, L]. Positions past
+ *           it are not used, whatever they hold, and o is 0 there; a reversed sequence starts at its own
+ *           last position.
+ * o:        device [B][L][H][dv], written.
+ * s_last:   device fp32 [B][H][dk][dv], or NULL: the state after the last step (s0 for an empty
+ *           sequence). May be s0 itself (updated in place).
+ * states:   device fp32 [B][H][ceil(L / WBMM_DELTA_CHUNK)][dk][dv], or NULL: the state before steps 0,
+ *           WBMM_DELTA_CHUNK, ... in the order the sequence runs (its last state past its end).
+ * workspace: wbmm_delta_forward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0: up to 8
+ *           steps). Calls that share one must be ordered on one stream.
+ * An infinity or NaN in q reaches its own o; in k, v, g, beta or the state it makes o of the head NaN from
+ * the chunk of WBMM_DELTA_CHUNK steps on that it lies in (in v and in a column of the state: in its own
+ * column). No atomics: bitwise reproducible.
+ * Errors: WBMM_E_INVALID (sizes, dtype, scale, NULL or overlapping buffers), WBMM_E_UNSUPPORTED (dk or dv >
+ * 128, more than 2^22 chunks over all heads, L > 2^28, misaligned pointer), WBMM_E_WORKSPACE, WBMM_E_HIP.
+ */
+#define WBMM_DELTA_CHUNK 64
+size_t wbmm_delta_forward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv);
+wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype,
+                               int reverse, float scale, const void* q, const void* k,
+                               const void* v, const void* g, const void* beta, const float* s0,
+                               const int32_t* lens, void* o, float* s_last, float* states,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * wbmm_delta_backward_workspace_bytes / wbmm_delta_backward — gradients of wbmm_delta_forward. With D_t
+ * the gradient of S_t (D of the last step has ds_last added), e_t = v_t - a_t S_{t-1}^T k_t:
+ *   D_t += scale q_t do_t^T,   dq_t = scale S_t do_t,   dv_t = b_t D_t^T k_t,
+ *   dk_t = b_t (D_t e_t - a_t S_{t-1} D_t^T k_t),   D_{t-1} = a_t (I - b_t k_t k_t^T) D_t,
+ *   db_t = (D_t^T k_t) . e_t,   da_t = <(I - b_t k_t k_t^T) S_{t-1}, D_t>,   ds0 = D_{-1},
+ * dg and dbeta through the sigmoids. dq and dk of a shared key head are the sums over its heads, in order.
+ * q, k, v, g, beta, lens, reverse, scale, sizes: as in the forward.
+ * states:   as the forward wrote them, or NULL: the call then forms them first, from s0 (device fp32
+ *           [B][H][dk][dv], or NULL for zeros; NULL with states), in its workspace.
+ * dout:     device [B][L][H][dv], gradient of o. ds_last: device fp32 [B][H][dk][dv], gradient of s_last,
+ *           or NULL for zeros.
+ * dq, dk, dv, dg, dbeta: device tensors in dtype, written; 0 past the end of a sequence. ds0: device fp32
+ *           [B][H][dk][dv], written, or NULL; may be ds_last itself.
+ * workspace: wbmm_delta_backward_workspace_bytes(...) bytes, 16-byte aligned.
+ * An infinity or NaN makes the gradients of its head NaN where they depend on it, in whole chunks.
+ * Errors as in the forward; also WBMM_E_INVALID for s0 beside states.
+ */
+size_t wbmm_delta_backward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
+                                           int has_states);
+wbmm_status wbmm_delta_backward(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype,
+                                int reverse, float scale, const void* q, const void* k,
+                                const void* v, const void* g, const void* beta,
+                                const float* states, const float* s0, const void* dout,
+                                const float* ds_last, const int32_t* lens, void* dq, void* dkey,
+                                void* dval, void* dg, void* dbeta, float* ds0, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
  * wbmm_probe_mfma — measurement aid, not part of the method: a matrix-core peak probe. Launches
  * `blocks` workgroups of 4 waves; every wave runs `iters` rounds of 8 independent MFMA
  * accumulation chains on register operands (dtype WBMM_F32: v_mfma_f32_16x16x4f32, WBMM_BF16:

@@ -28,7 +28,9 @@ __all__ = [
     "wbmm_backward_ckpt_workspace_bytes", "wbmm_scan_forward", "wbmm_scan_backward",
     "wbmm_scan_forward_workspace_bytes", "wbmm_scan_backward_workspace_bytes", "WBMM_CKPT_GROUP", "WBMM_SCAN_CHUNK",
     "wbmm_rmsnorm_forward", "wbmm_rmsnorm_backward", "wbmm_rmsnorm_backward_workspace_bytes",
-    "wbmm_adamw_plan", "wbmm_adamw_step", "WbmmAdamwPlan",
+    "wbmm_adamw_plan", "wbmm_adamw_step", "WbmmAdamwPlan", "wbmm_delta_forward",
+    "wbmm_delta_backward", "wbmm_delta_forward_workspace_bytes",
+    "wbmm_delta_backward_workspace_bytes", "WBMM_DELTA_CHUNK",
     "WBMM_OK", "WBMM_E_INVALID", "WBMM_E_UNSUPPORTED", "WBMM_E_WORKSPACE", "WBMM_E_HIP",
 ]
 
@@ -38,6 +40,7 @@ WBMM_NCHW, WBMM_NHWC = 0, 1
 WBMM_CKPT_INT8, WBMM_CKPT_E4M3 = 0, 1
 WBMM_CKPT_GROUP = 32   # elements per scale of an 8-bit checkpoint
 WBMM_SCAN_CHUNK = 32   # steps between two states that the recurrence's forward keeps
+WBMM_DELTA_CHUNK = 64  # steps between two states that the delta rule's forward keeps
 WBMM_NOALLOC_SCRATCH_BYTES = 32 << 20  # the library's fixed scratch for wbmm_backward_noalloc
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -107,6 +110,12 @@ def _declare(lib):
                                     ctypes.POINTER(c_i64)]),
         "wbmm_adamw_step": (c_int, [vp, c_i64, c_i64] + [c_d] * 4 + [c_i64] + [vp] * 3 +
                             [ctypes.c_uint64, vp]),
+        "wbmm_delta_forward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 4),
+        "wbmm_delta_backward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 5),
+        "wbmm_delta_forward": (c_int, [c_i64] * 2 + [c_int] * 6 + [c_f] + [vp] * 11 +
+                               [c_size, vp]),
+        "wbmm_delta_backward": (c_int, [c_i64] * 2 + [c_int] * 6 + [c_f] + [vp] * 17 +
+                                [c_size, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -890,3 +899,101 @@ def wbmm_adamw_step(plan: WbmmAdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: 
     _check(_lib().wbmm_adamw_step(plan.ptr, plan.count, plan.chunks, lr, betas[0], betas[1], eps,
                                   step, stp, lp, gp, seed & 0xffffffffffffffff,
                                   _current_stream(idx)))
+
+
+# ----------------------------------------------------------------------------- delta rule
+@functools.lru_cache(maxsize=256)
+def wbmm_delta_forward_workspace_bytes(B: int, L: int, Hk: int, H: int, dk: int, dv: int) -> int:
+    return int(_lib().wbmm_delta_forward_workspace_bytes(int(B), int(L), int(Hk), int(H), int(dk),
+                                                         int(dv)))
+
+
+@functools.lru_cache(maxsize=256)
+def wbmm_delta_backward_workspace_bytes(B: int, L: int, Hk: int, H: int, dk: int, dv: int,
+                                        has_states: bool = True) -> int:
+    return int(_lib().wbmm_delta_backward_workspace_bytes(int(B), int(L), int(Hk), int(H), int(dk),
+                                                          int(dv), int(bool(has_states))))
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_sizes(qs, vs):
+    """(B, L, Hk, H, dk, dv) of the shapes of q and v, and the shapes of g, of a state and of states."""
+    if len(qs) != 4 or len(vs) != 4 or qs[:2] != vs[:2]:
+        raise WbmmError(WBMM_E_INVALID, f"q (B, L, Hk, dk) and v (B, L, H, dv) do not go together: "
+                                        f"{tuple(qs)}, {tuple(vs)}")
+    B, L, Hk, dk = qs
+    H, dv = vs[2], vs[3]
+    return (B, L, Hk, H, dk, dv), (B, L, H), (B, H, dk, dv), (B, H, -(-L // WBMM_DELTA_CHUNK), dk, dv)
+
+
+def _delta_inputs(q, k, v, g, beta, lens, scale):
+    dtype = q.dtype
+    dt, idx = _dtype_code(dtype), _device("q", q)
+    sizes, gs, flat, kept = _delta_sizes(q.shape, v.shape)
+    ptrs = (_need("q", q, q.shape, dtype, idx), _need("k", k, q.shape, dtype, idx),
+            _need("v", v, v.shape, dtype, idx), _need("g", g, gs, dtype, idx),
+            _need("beta", beta, gs, dtype, idx))
+    lp = _opt("lens", lens, (sizes[0],), _torch().int32, idx)
+    scale = sizes[4] ** -0.5 if scale is None and sizes[4] else 1.0 if scale is None else scale
+    return dt, idx, sizes, gs, flat, kept, ptrs, lp, scale
+
+
+def wbmm_delta_forward(q, k, v, g, beta, *, scale: Optional[float] = None, s0=None, lens=None,
+                       reverse: bool = False, o=None, s_last=False, states=False, workspace=None,
+                       stream=None):
+    """Gated delta rule: S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T, o_t = scale S_t^T q_t,
+    with a_t = sigmoid(g_t), b_t = sigmoid(beta_t).
+
+    q, k: (B, L, Hk, dk); v: (B, L, H, dv), Hk dividing H; g, beta: (B, L, H); all fp32 or all bf16,
+    dense. scale: dk^-1/2 by default. s0: fp32 (B, H, dk, dv), or None for zeros. lens: int32 (B) on the
+    GPU; o is 0 past a sequence's end. reverse: from each sequence's last position to its first. s_last
+    and states: True allocates them, a tensor is written (s_last may be s0), False skips them; states
+    (fp32, (B, H, ceil(L / WBMM_DELTA_CHUNK), dk, dv)) is what wbmm_delta_backward starts from.
+    Returns (o, s_last, states)."""
+    if stream is not None:
+        with _on_stream(stream, "q", q):
+            return wbmm_delta_forward(q, k, v, g, beta, scale=scale, s0=s0, lens=lens,
+                                      reverse=reverse, o=o, s_last=s_last, states=states,
+                                      workspace=workspace)
+    f32 = _torch().float32
+    dt, idx, sizes, gs, flat, kept, ptrs, lp, scale = _delta_inputs(q, k, v, g, beta, lens, scale)
+    s0p = _opt("s0", s0, flat, f32, idx)
+    o, op = _out("o", True if o is None else o, v.shape, q.dtype, idx, v)
+    s_last, slp = _out("s_last", s_last, flat, f32, idx, s0)
+    states, stp = _out("states", states, kept, f32, idx)
+    ws, wp, wb = _workspace(wbmm_delta_forward_workspace_bytes(*sizes), workspace, idx)
+    _check(_lib().wbmm_delta_forward(*sizes, dt, int(bool(reverse)), scale, *ptrs, s0p, lp, op, slp,
+                                     stp, wp, wb, _current_stream(idx)))
+    return o, s_last, states
+
+
+def wbmm_delta_backward(q, k, v, g, beta, do, *, states=None, s0=None, ds_last=None,
+                        scale: Optional[float] = None, lens=None, reverse: bool = False, dq=None,
+                        dk=None, dv=None, dg=None, dbeta=None, ds0=True, workspace=None,
+                        stream=None):
+    """Gradients of wbmm_delta_forward (same q, k, v, g, beta, scale, lens and reverse; states as it
+    wrote them; without states (None) they are formed again from s0). do: gradient of o; ds_last: fp32
+    gradient of s_last, or None. Returns (dq, dk, dv, dg, dbeta, ds0), ds0 fp32 (False skips it), the
+    others in q's dtype and 0 past a sequence's end."""
+    if stream is not None:
+        with _on_stream(stream, "q", q):
+            return wbmm_delta_backward(q, k, v, g, beta, do, states=states, s0=s0, ds_last=ds_last,
+                                       scale=scale, lens=lens, reverse=reverse, dq=dq, dk=dk, dv=dv,
+                                       dg=dg, dbeta=dbeta, ds0=ds0, workspace=workspace)
+    f32, dtype = _torch().float32, q.dtype
+    dt, idx, sizes, gs, flat, kept, ptrs, lp, scale = _delta_inputs(q, k, v, g, beta, lens, scale)
+    stp, s0p = _opt("states", states, kept, f32, idx), _opt("s0", s0, flat, f32, idx)
+    dop = _need("do", do, v.shape, dtype, idx)
+    dlp = _opt("ds_last", ds_last, flat, f32, idx)
+    dq, dqp = _out("dq", True if dq is None else dq, q.shape, dtype, idx, q)
+    dk, dkp = _out("dk", True if dk is None else dk, q.shape, dtype, idx, k)
+    dv, dvp = _out("dv", True if dv is None else dv, v.shape, dtype, idx, v)
+    dg, dgp = _out("dg", True if dg is None else dg, gs, dtype, idx, g)
+    dbeta, dbp = _out("dbeta", True if dbeta is None else dbeta, gs, dtype, idx, beta)
+    ds0, d0p = _out("ds0", ds0, flat, f32, idx, ds_last)
+    ws, wp, wb = _workspace(wbmm_delta_backward_workspace_bytes(*sizes, states is not None),
+                            workspace, idx)
+    _check(_lib().wbmm_delta_backward(*sizes, dt, int(bool(reverse)), scale, *ptrs, stp, s0p, dop,
+                                      dlp, lp, dqp, dkp, dvp, dgp, dbp, d0p, wp, wb,
+                                      _current_stream(idx)))
+    return dq, dk, dv, dg, dbeta, ds0

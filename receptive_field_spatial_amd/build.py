@@ -20,7 +20,7 @@ SOURCES = ["wbmm_api.cpp", "wbmm_aux.hip", "wbmm_fwd.hip", "wbmm_bwd.hip", "wbmm
            "wbmm_fast28.hip", "wbmm_fast7.hip", "wbmm_fasttab.hip", "wbmm_hiergen.cpp",
            "wbmm_bwdwide.hip", "wbmm_ckpt.hip", "wbmm_ckptbwd.hip", "wbmm_ckptany.hip",
            "wbmm_scan.hip", "wbmm_scanbwd.hip", "wbmm_scanplan.cpp", "wbmm_norm.hip",
-           "wbmm_adamw.hip"]
+           "wbmm_adamw.hip", "wbmm_delta.hip", "wbmm_deltabwd.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

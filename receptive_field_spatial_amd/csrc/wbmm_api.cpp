@@ -15,6 +15,7 @@
 
 #include "../../include/wbmm.h"
 #include "wbmm_adamw.hpp"
+#include "wbmm_delta.hpp"
 #include "wbmm_launch.hpp"
 #include "wbmm_norm.hpp"
 #include "wbmm_scan.hpp"
@@ -1114,4 +1115,139 @@ WBMM_API wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t c
   r.step = step; r.step_dev = step_dev; r.lr_factor = lr_factor; r.grad_factor = grad_factor;
   r.seed = seed;
   return hip_status(wbmm::launch_adamw(r, (hipStream_t)stream), "wbmm_adamw_step");
+}
+
+// ---------------------------------------------------------------------------- delta rule
+namespace {
+
+constexpr int64_t kMaxDeltaChunks = 1ll << 22;   // chunks of heads: grids hold 2^32 threads
+
+wbmm_status check_delta(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype) {
+  if (B < 1 || L < 1 || Hk < 1 || H < 1 || dk < 1 || dv < 1)
+    return fail(WBMM_E_INVALID, "sizes must be >= 1 (B=%lld L=%lld Hk=%d H=%d dk=%d dv=%d)",
+                (long long)B, (long long)L, Hk, H, dk, dv);
+  if (H % Hk != 0) return fail(WBMM_E_INVALID, "Hk=%d must divide H=%d", Hk, H);
+  if (dk > 128 || dv > 128)
+    return fail(WBMM_E_UNSUPPORTED, "dk=%d and dv=%d must not exceed 128", dk, dv);
+  if (L > (1ll << 28) || B > kMaxDeltaChunks || H > kMaxDeltaChunks ||
+      B * H > kMaxDeltaChunks ||
+      B * H * ((L + WBMM_DELTA_CHUNK - 1) / WBMM_DELTA_CHUNK) > kMaxDeltaChunks)
+    return fail(WBMM_E_UNSUPPORTED, "more than 2^22 chunks of %d steps of a head, or L > 2^28",
+                WBMM_DELTA_CHUNK);
+  if (!valid_dtype(dtype)) return fail(WBMM_E_INVALID, "unknown dtype %d", dtype);
+  return WBMM_OK;
+}
+
+wbmm_status check_delta_ws(size_t need, const void* ws, size_t bytes) {
+  if (need > 0 && (!ws || bytes < need))
+    return fail(WBMM_E_WORKSPACE, "workspace of %zu bytes required, %zu given", need,
+                ws ? bytes : (size_t)0);
+  if (need > 0 && !aligned(ws, 16))
+    return fail(WBMM_E_UNSUPPORTED, "workspace not 16-byte aligned");
+  return WBMM_OK;
+}
+
+// Byte sizes of the tensors of a call.
+struct DeltaBytes {
+  size_t qk, v, gate, state, states;
+  DeltaBytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype) {
+    const size_t es = dtype_size(dtype), t = (size_t)B * L;
+    qk = t * Hk * dk * es;
+    v = t * H * dv * es;
+    gate = t * H * es;
+    state = (size_t)B * H * dk * dv * 4;
+    states = state * ((L + WBMM_DELTA_CHUNK - 1) / WBMM_DELTA_CHUNK);
+  }
+};
+
+}  // namespace
+
+WBMM_API size_t wbmm_delta_forward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk,
+                                                   int dv) {
+  if (check_delta(B, L, Hk, H, dk, dv, WBMM_F32) != WBMM_OK) return 0;
+  return wbmm::delta_forward_workspace(B, L, H, dk, dv);
+}
+
+WBMM_API wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
+                                        int dtype, int reverse, float scale, const void* q,
+                                        const void* k, const void* v, const void* g,
+                                        const void* beta, const float* s0, const int32_t* lens,
+                                        void* o, float* s_last, float* states, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  wbmm_status st = check_delta(B, L, Hk, H, dk, dv, dtype);
+  if (st != WBMM_OK) return st;
+  if (!std::isfinite(scale)) return fail(WBMM_E_INVALID, "scale must be finite");
+  if (!q || !k || !v || !g || !beta || !o)
+    return fail(WBMM_E_INVALID, "q, k, v, g, beta and o must be non-NULL");
+  const size_t es = dtype_size(dtype);
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(g, es) ||
+      !aligned(beta, es) || !aligned(o, es) || !aligned(s0, 4) || !aligned(lens, 4) ||
+      !aligned(s_last, 4) || !aligned(states, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const DeltaBytes n(B, L, Hk, H, dk, dv, dtype);
+  const Span in[] = {{q, n.qk, "q"}, {k, n.qk, "k"}, {v, n.v, "v"}, {g, n.gate, "g"},
+                     {beta, n.gate, "beta"}, {lens, (size_t)B * 4, "lens"},
+                     {s0 == s_last ? nullptr : s0, n.state, "s0"}};   // in place: exactly the same
+  const Span out[] = {{o, n.v, "o"}, {s_last, n.state, "s_last"}, {states, n.states, "states"}};
+  st = check_spans(in, 7, out, 3);
+  if (st != WBMM_OK) return st;
+  st = check_delta_ws(wbmm::delta_forward_workspace(B, L, H, dk, dv), workspace, workspace_bytes);
+  if (st != WBMM_OK) return st;
+  wbmm::DeltaRequest r{};
+  r.B = B; r.L = L; r.Hk = Hk; r.H = H; r.dk = dk; r.dv = dv;
+  r.bf16 = dtype == WBMM_BF16;
+  r.reverse = reverse != 0;
+  r.scale = scale;
+  r.q = q; r.k = k; r.v = v; r.g = g; r.beta = beta; r.s0 = s0; r.lens = lens;
+  r.o = o; r.s_last = s_last; r.states = states; r.ws = workspace;
+  return hip_status(wbmm::launch_delta_forward(r, (hipStream_t)stream), "wbmm_delta_forward");
+}
+
+WBMM_API size_t wbmm_delta_backward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk,
+                                                    int dv, int has_states) {
+  if (check_delta(B, L, Hk, H, dk, dv, WBMM_F32) != WBMM_OK) return 0;
+  return wbmm::delta_backward_workspace(B, L, H, dk, dv, has_states != 0);
+}
+
+WBMM_API wbmm_status wbmm_delta_backward(
+    int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype, int reverse, float scale,
+    const void* q, const void* k, const void* v, const void* g, const void* beta,
+    const float* states, const float* s0, const void* dout, const float* ds_last,
+    const int32_t* lens, void* dq, void* dkey, void* dval, void* dg, void* dbeta, float* ds0,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  wbmm_status st = check_delta(B, L, Hk, H, dk, dv, dtype);
+  if (st != WBMM_OK) return st;
+  if (!std::isfinite(scale)) return fail(WBMM_E_INVALID, "scale must be finite");
+  if (!q || !k || !v || !g || !beta || !dout || !dq || !dkey || !dval || !dg || !dbeta)
+    return fail(WBMM_E_INVALID,
+                "q, k, v, g, beta, do, dq, dk, dv, dg and dbeta must be non-NULL");
+  if (states && s0) return fail(WBMM_E_INVALID, "s0 goes with states == NULL only");
+  const size_t es = dtype_size(dtype);
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(g, es) ||
+      !aligned(beta, es) || !aligned(dout, es) || !aligned(dq, es) || !aligned(dkey, es) ||
+      !aligned(dval, es) || !aligned(dg, es) || !aligned(dbeta, es) || !aligned(s0, 4) ||
+      !aligned(lens, 4) || !aligned(ds_last, 4) || !aligned(ds0, 4) || !aligned(states, 4))
+    return fail(WBMM_E_UNSUPPORTED, "pointer not aligned to its element size");
+  const DeltaBytes n(B, L, Hk, H, dk, dv, dtype);
+  const Span in[] = {{q, n.qk, "q"}, {k, n.qk, "k"}, {v, n.v, "v"}, {g, n.gate, "g"},
+                     {beta, n.gate, "beta"}, {lens, (size_t)B * 4, "lens"},
+                     {states, n.states, "states"}, {s0, n.state, "s0"}, {dout, n.v, "do"},
+                     {ds_last == ds0 ? nullptr : ds_last, n.state, "ds_last"}};
+  const Span out[] = {{dq, n.qk, "dq"}, {dkey, n.qk, "dk"}, {dval, n.v, "dv"}, {dg, n.gate, "dg"},
+                      {dbeta, n.gate, "dbeta"}, {ds0, n.state, "ds0"}};
+  st = check_spans(in, 10, out, 6);
+  if (st != WBMM_OK) return st;
+  st = check_delta_ws(wbmm::delta_backward_workspace(B, L, H, dk, dv, states != nullptr), workspace,
+                      workspace_bytes);
+  if (st != WBMM_OK) return st;
+  wbmm::DeltaRequest r{};
+  r.B = B; r.L = L; r.Hk = Hk; r.H = H; r.dk = dk; r.dv = dv;
+  r.bf16 = dtype == WBMM_BF16;
+  r.reverse = reverse != 0;
+  r.scale = scale;
+  r.q = q; r.k = k; r.v = v; r.g = g; r.beta = beta; r.dout = dout; r.lens = lens;
+  r.states = const_cast<float*>(states); r.s0 = s0; r.ds_last = ds_last;
+  r.dq = dq; r.dkey = dkey; r.dval = dval; r.dg = dg; r.dbeta = dbeta; r.ds0 = ds0;
+  r.ws = workspace;
+  return hip_status(wbmm::launch_delta_backward(r, (hipStream_t)stream), "wbmm_delta_backward");
 }

@@ -42,25 +42,6 @@ struct CkWin {
   static constexpr int y0(int q) { return q * (W / 4) + (q < W % 4 ? q : W % 4); }
 };
 
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
-}
-// The NS leading bf16 parts of a pair of fp32 numbers, packed.
-template <int NS>
-__device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[NS]) {
-#pragma unroll
-  for (int q = 0; q < NS; ++q) {
-    p[q] = pk_bf16(a, b);
-    if (q + 1 < NS) {
-      a -= __uint_as_float(p[q] << 16);
-      b -= __uint_as_float(p[q] & 0xffff0000u);
-    }
-  }
-}
-
 // Sums over the lane's row of 16 lanes, left in its last lane.
 template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float x) {

@@ -1,0 +1,100 @@
+// Gated delta rule: a recurrence whose state is a matrix S (dk x dv) for every head of a sequence,
+//   S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,   o_t = scale S_t^T q_t,
+//   a_t = sigmoid(g_t),   b_t = sigmoid(beta_t).
+//
+// In chunks of C = 64 steps, with S0 the state before the chunk, y_i = a_1 ... a_i, K, Q, V the
+// chunk's rows and u_i = b_i (v_i - a_i S_{i-1}^T k_i) what step i adds (S_i = a_i S_{i-1} + k_i u_i^T):
+//   A_ij = b_i (y_i / y_j) k_i.k_j (j < i),   P_ij = (y_i / y_j) q_i.k_j (j <= i),   T = (I + A)^-1 diag(b),
+//   U = T (V - diag(y) K S0),   o = scale (diag(y) Q S0 + P U),   S_C = y_C S0 + sum_j (y_C / y_j) k_j u_j^T.
+// A, P and T depend on no state: one launch forms them for all chunks at once. What is left for the
+// walk along the chunks are products of 64 x dk, 64 x 64 and dk x 64 matrices with 64 or dk x dv ones,
+// and every column of S, U and o goes its own way: 16 columns are a workgroup's.
+//
+// Backward, with D the gradient of the state after a chunk and G = scale do:
+//   dU = P^T G + diag(y_C / y) K D,   R = T^T dU = dv,   D0 = y_C D + Q^T diag(y) G - K^T diag(y) R,
+// again a walk over columns (last chunk to first); then, for all chunks at once,
+//   dP = (G U^T) . (y_i / y_j) (j <= i),   N = -(R U^T) . (y_i / y_j) (j < i),
+//   dq = diag(y) G S0^T + dP K,   row = N K - diag(y) R S0^T,
+//   col = dP^T Q + N^T K + diag(y_C / y) U D^T,   dk = row + col.
+// y_i enters o, A and P as a factor of q_i, of k_i as the row of A, and as 1 / y_j of k_j elsewhere, b_i
+// as a factor of k_i's row and of v_i. So the gradients of the gates are dot products of rows,
+//   d log y_i = q_i.dq_i + k_i.row_i - k_i.col_i  (+ <S_C, D> for the last),
+//   d log a_t = sum_{i >= t} d log y_i,   dg = (1 - a) d log a,   dbeta = (1 - b)(v.R + k.row).
+//
+// Products run on the bf16 matrix cores at fp32 accuracy. An fp32 number is the sum of three bf16
+// numbers to 2^-25, so the states, T, X, U and D are taken in three parts and the products that matter
+// (up to 2^-24) are formed; bf16 tensors are one part as they are. What only reaches a bf16 output (o, dq,
+// dk, dg, dbeta) takes two parts, 2^-17, before its rounding to 2^-8. Sums are fp32, running sums of
+// log a and of d log y fp64.
+//
+// Layouts. v_mfma_f32_16x16x32_bf16: with l the lane, an A operand is row l % 16 and 8 terms of the sum, a
+// B operand column l % 16 and the same 8, a result column l % 16 and rows 4 (l / 16) + r. The order of
+// the terms is free where A and B agree: slot j of lane group q stands for term 4 q + j of the first
+// 16 (j < 4) or second 16 (j >= 4) of 32. Then two results on top of each other are a B operand as they lie
+// in the registers, and two side by side a transposed A operand: "frag" below is such an operand, 64
+// lanes of 16 bytes for each part.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace wbmm {
+
+constexpr int kDeltaChunk = 64;
+constexpr int kDeltaTiles = 10;              // 16 x 16 tiles on and below the diagonal of 64 x 64
+constexpr int kDeltaTri = kDeltaTiles * 256; // floats of T, or of P
+
+struct DeltaRequest {
+  int64_t B, L;
+  int Hk, H, dk, dv, bf16, reverse;
+  float scale;
+  const void *q, *k, *v, *g, *beta, *dout;
+  const float* s0;
+  const float* ds_last;
+  const int32_t* lens;
+  void* o;
+  float* s_last;
+  float* states;               // written by the forward, read by the backward (null: formed again)
+  void *dq, *dkey, *dval, *dg, *dbeta;
+  float* ds0;
+  void* ws;
+};
+
+size_t delta_forward_workspace(int64_t B, int64_t L, int H, int dk, int dv);
+size_t delta_backward_workspace(int64_t B, int64_t L, int H, int dk, int dv, bool has_states);
+hipError_t launch_delta_forward(const DeltaRequest& r, hipStream_t st);
+hipError_t launch_delta_backward(const DeltaRequest& r, hipStream_t st);
+
+// The gates of a chunk: log y (fp64), y, y_C / y, b and 1 - a.
+struct DeltaGates {
+  double cum[kDeltaChunk];
+  float gam[kDeltaChunk], end[kDeltaChunk], b[kDeltaChunk], na[kDeltaChunk];
+};
+
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta, *dout;
+  const float* s0;
+  const float* ds_last;
+  const int32_t* lens;
+  void* o;
+  float* s_last;
+  float* states;
+  void *dq, *dkey, *dval, *dg, *dbeta;
+  float* ds0;
+  float* T;                    // [B H chunks][kDeltaTri]
+  float* P;
+  DeltaGates* gates;           // [B H chunks]
+  float* D;                    // [B H chunks][dk][dv]
+  float* R;                    // [B H chunks][64][dv]
+  int B, L, Hk, H, dk, dv, rep, chunks, reverse;
+  float scale;
+};
+
+DeltaArgs delta_args(const DeltaRequest& r);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
+hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
+// 4 elements at a time of everything that lies in rows of dk or dv.
+bool delta_vec(const DeltaRequest& r);
+
+}  // namespace wbmm

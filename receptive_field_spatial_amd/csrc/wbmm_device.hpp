@@ -65,6 +65,26 @@ __device__ __forceinline__ v4f mfma_bf16(u32x4 a, u32x4 b, v4f c) {
                                                  __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+// ---------------------------------------------------------------------------- bf16 parts
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+// The NS leading bf16 parts of a pair of fp32 numbers, packed.
+template <int NS>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[NS]) {
+#pragma unroll
+  for (int q = 0; q < NS; ++q) {
+    p[q] = pk_bf16(a, b);
+    if (q + 1 < NS) {
+      a -= __uint_as_float(p[q] << 16);
+      b -= __uint_as_float(p[q] & 0xffff0000u);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------- wave sums
 // x of lane (i - n) within the lane's row of 16 (ROW_SHR), or of the broadcast source lane; 0
 // where there is none or the row is masked off. Both 32-bit halves move the same way.
