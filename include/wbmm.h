@@ -575,10 +575,12 @@ wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, do
  * the chunk of WBMM_DELTA_CHUNK steps on that it lies in (in v and in a column of the state: in its own
  * column). No atomics: bitwise reproducible.
  * Errors: WBMM_E_INVALID (sizes, dtype, scale, NULL or overlapping buffers), WBMM_E_UNSUPPORTED (dk or dv >
- * 128, more than 2^22 chunks over all heads, L > 2^28, misaligned pointer), WBMM_E_WORKSPACE, WBMM_E_HIP.
+ * 128, Hk dk or H dv > 2^22, more than 2^22 chunks over all heads, L > 2^28, misaligned pointer),
+ * WBMM_E_WORKSPACE, WBMM_E_HIP.
  */
 #define WBMM_DELTA_CHUNK 64
-size_t wbmm_delta_forward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv);
+size_t wbmm_delta_forward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
+                                          int dtype);
 wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype,
                                int reverse, float scale, const void* q, const void* k,
                                const void* v, const void* g, const void* beta, const float* s0,
@@ -604,7 +606,7 @@ wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int 
  * Errors as in the forward; also WBMM_E_INVALID for s0 beside states.
  */
 size_t wbmm_delta_backward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
-                                           int has_states);
+                                           int dtype, int has_states);
 wbmm_status wbmm_delta_backward(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int dtype,
                                 int reverse, float scale, const void* q, const void* k,
                                 const void* v, const void* g, const void* beta,

@@ -110,8 +110,8 @@ def _declare(lib):
                                     ctypes.POINTER(c_i64)]),
         "wbmm_adamw_step": (c_int, [vp, c_i64, c_i64] + [c_d] * 4 + [c_i64] + [vp] * 3 +
                             [ctypes.c_uint64, vp]),
-        "wbmm_delta_forward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 4),
-        "wbmm_delta_backward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 5),
+        "wbmm_delta_forward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 5),
+        "wbmm_delta_backward_workspace_bytes": (c_size, [c_i64] * 2 + [c_int] * 6),
         "wbmm_delta_forward": (c_int, [c_i64] * 2 + [c_int] * 6 + [c_f] + [vp] * 11 +
                                [c_size, vp]),
         "wbmm_delta_backward": (c_int, [c_i64] * 2 + [c_int] * 6 + [c_f] + [vp] * 17 +
@@ -903,16 +903,21 @@ def wbmm_adamw_step(plan: WbmmAdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: 
 
 # ----------------------------------------------------------------------------- delta rule
 @functools.lru_cache(maxsize=256)
-def wbmm_delta_forward_workspace_bytes(B: int, L: int, Hk: int, H: int, dk: int, dv: int) -> int:
-    return int(_lib().wbmm_delta_forward_workspace_bytes(int(B), int(L), int(Hk), int(H), int(dk),
-                                                         int(dv)))
+def _delta_bytes(sizes, dt: int, states) -> int:
+    """Workspace of a forward (states None) or a backward call."""
+    if states is None:
+        return int(_lib().wbmm_delta_forward_workspace_bytes(*sizes, dt))
+    return int(_lib().wbmm_delta_backward_workspace_bytes(*sizes, dt, int(states)))
 
 
-@functools.lru_cache(maxsize=256)
-def wbmm_delta_backward_workspace_bytes(B: int, L: int, Hk: int, H: int, dk: int, dv: int,
-                                        has_states: bool = True) -> int:
-    return int(_lib().wbmm_delta_backward_workspace_bytes(int(B), int(L), int(Hk), int(H), int(dk),
-                                                          int(dv), int(bool(has_states))))
+def wbmm_delta_forward_workspace_bytes(B, L, Hk, H, dk, dv, dtype=None) -> int:
+    code = WBMM_F32 if dtype is None else _dtype_code(dtype)
+    return _delta_bytes((int(B), int(L), int(Hk), int(H), int(dk), int(dv)), code, None)
+
+
+def wbmm_delta_backward_workspace_bytes(B, L, Hk, H, dk, dv, dtype=None, has_states=True) -> int:
+    code = WBMM_F32 if dtype is None else _dtype_code(dtype)
+    return _delta_bytes((int(B), int(L), int(Hk), int(H), int(dk), int(dv)), code, bool(has_states))
 
 
 @functools.lru_cache(maxsize=256)
@@ -961,7 +966,7 @@ def wbmm_delta_forward(q, k, v, g, beta, *, scale: Optional[float] = None, s0=No
     o, op = _out("o", True if o is None else o, v.shape, q.dtype, idx, v)
     s_last, slp = _out("s_last", s_last, flat, f32, idx, s0)
     states, stp = _out("states", states, kept, f32, idx)
-    ws, wp, wb = _workspace(wbmm_delta_forward_workspace_bytes(*sizes), workspace, idx)
+    ws, wp, wb = _workspace(_delta_bytes(sizes, dt, None), workspace, idx)
     _check(_lib().wbmm_delta_forward(*sizes, dt, int(bool(reverse)), scale, *ptrs, s0p, lp, op, slp,
                                      stp, wp, wb, _current_stream(idx)))
     return o, s_last, states
@@ -991,8 +996,7 @@ def wbmm_delta_backward(q, k, v, g, beta, do, *, states=None, s0=None, ds_last=N
     dg, dgp = _out("dg", True if dg is None else dg, gs, dtype, idx, g)
     dbeta, dbp = _out("dbeta", True if dbeta is None else dbeta, gs, dtype, idx, beta)
     ds0, d0p = _out("ds0", ds0, flat, f32, idx, ds_last)
-    ws, wp, wb = _workspace(wbmm_delta_backward_workspace_bytes(*sizes, states is not None),
-                            workspace, idx)
+    ws, wp, wb = _workspace(_delta_bytes(sizes, dt, states is not None), workspace, idx)
     _check(_lib().wbmm_delta_backward(*sizes, dt, int(bool(reverse)), scale, *ptrs, stp, s0p, dop,
                                       dlp, lp, dqp, dkp, dvp, dgp, dbp, d0p, wp, wb,
                                       _current_stream(idx)))

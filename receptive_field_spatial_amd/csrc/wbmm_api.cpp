@@ -1129,6 +1129,8 @@ wbmm_status check_delta(int64_t B, int64_t L, int Hk, int H, int dk, int dv, int
   if (H % Hk != 0) return fail(WBMM_E_INVALID, "Hk=%d must divide H=%d", Hk, H);
   if (dk > 128 || dv > 128)
     return fail(WBMM_E_UNSUPPORTED, "dk=%d and dv=%d must not exceed 128", dk, dv);
+  if ((int64_t)Hk * dk > (1 << 22) || (int64_t)H * dv > (1 << 22))
+    return fail(WBMM_E_UNSUPPORTED, "rows of more than 2^22 elements");
   if (L > (1ll << 28) || B > kMaxDeltaChunks || H > kMaxDeltaChunks ||
       B * H > kMaxDeltaChunks ||
       B * H * ((L + WBMM_DELTA_CHUNK - 1) / WBMM_DELTA_CHUNK) > kMaxDeltaChunks)
@@ -1163,9 +1165,9 @@ struct DeltaBytes {
 }  // namespace
 
 WBMM_API size_t wbmm_delta_forward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk,
-                                                   int dv) {
-  if (check_delta(B, L, Hk, H, dk, dv, WBMM_F32) != WBMM_OK) return 0;
-  return wbmm::delta_forward_workspace(B, L, H, dk, dv);
+                                                   int dv, int dtype) {
+  if (check_delta(B, L, Hk, H, dk, dv, dtype) != WBMM_OK) return 0;
+  return wbmm::delta_forward_workspace(B, L, H, dtype == WBMM_BF16);
 }
 
 WBMM_API wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
@@ -1191,7 +1193,8 @@ WBMM_API wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int
   const Span out[] = {{o, n.v, "o"}, {s_last, n.state, "s_last"}, {states, n.states, "states"}};
   st = check_spans(in, 7, out, 3);
   if (st != WBMM_OK) return st;
-  st = check_delta_ws(wbmm::delta_forward_workspace(B, L, H, dk, dv), workspace, workspace_bytes);
+  st = check_delta_ws(wbmm::delta_forward_workspace(B, L, H, dtype == WBMM_BF16), workspace,
+                      workspace_bytes);
   if (st != WBMM_OK) return st;
   wbmm::DeltaRequest r{};
   r.B = B; r.L = L; r.Hk = Hk; r.H = H; r.dk = dk; r.dv = dv;
@@ -1204,9 +1207,9 @@ WBMM_API wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int
 }
 
 WBMM_API size_t wbmm_delta_backward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk,
-                                                    int dv, int has_states) {
-  if (check_delta(B, L, Hk, H, dk, dv, WBMM_F32) != WBMM_OK) return 0;
-  return wbmm::delta_backward_workspace(B, L, H, dk, dv, has_states != 0);
+                                                    int dv, int dtype, int has_states) {
+  if (check_delta(B, L, Hk, H, dk, dv, dtype) != WBMM_OK) return 0;
+  return wbmm::delta_backward_workspace(B, L, H, dk, dv, dtype == WBMM_BF16, has_states != 0);
 }
 
 WBMM_API wbmm_status wbmm_delta_backward(
@@ -1237,8 +1240,9 @@ WBMM_API wbmm_status wbmm_delta_backward(
                       {dbeta, n.gate, "dbeta"}, {ds0, n.state, "ds0"}};
   st = check_spans(in, 10, out, 6);
   if (st != WBMM_OK) return st;
-  st = check_delta_ws(wbmm::delta_backward_workspace(B, L, H, dk, dv, states != nullptr), workspace,
-                      workspace_bytes);
+  st = check_delta_ws(wbmm::delta_backward_workspace(B, L, H, dk, dv, dtype == WBMM_BF16,
+                                                     states != nullptr),
+                      workspace, workspace_bytes);
   if (st != WBMM_OK) return st;
   wbmm::DeltaRequest r{};
   r.B = B; r.L = L; r.Hk = Hk; r.H = H; r.dk = dk; r.dv = dv;

@@ -22,96 +22,122 @@ __device__ __forceinline__ v4f mm16(const v4f& a, const v4f& b, v4f acc) {
 template <typename T>
 __device__ __forceinline__ float elem(const void* p, size_t i) { return load_f32<T>((const T*)p, i); }
 
-template <typename T, int DK, bool VEC>
+// 16 x 16 tile (i, j), j <= i, of a triangular matrix in LDS: rows of 20 floats.
+__device__ __forceinline__ constexpr int lds_tile(int i, int j) { return (i * (i + 1) / 2 + j) * 320; }
+
+template <typename T, int DK, bool VEC, DeltaPrep MODE>
 __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
-  constexpr int PI = DeltaType<T>::PI, KS = DK / 32;
-  using Quad = typename DeltaType<T>::Quad;
+  using Ty = DeltaType<T, VEC>;
+  constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32;
+  constexpr bool WANTP = MODE != kPrepStates;
   __shared__ double s_cum[kDeltaChunk];
   __shared__ float s_b[kDeltaChunk];
-  __shared__ float s_n[6][16][20];      // N_ij, j < i
-  __shared__ float s_t[4][16][20];      // T_ii
+  __shared__ __attribute__((aligned(16))) float s_n[10 * 320];   // N below the diagonal, then P
+  __shared__ __attribute__((aligned(16))) float s_t[10 * 320];   // T
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, gq = lane >> 4;
   const int ch = blockIdx.x, bh = ch / a.chunks, c = ch - bh * a.chunks;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
-  const int t0 = c * kDeltaChunk;
-  if (t0 >= sq.n) return;
+  if (c * kDeltaChunk >= sq.n) return;
+  const DeltaRows rows = delta_rows(sq, c);
+  const size_t low = delta_low(a, sq, b, c);
+  const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
+  const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
+  const uint32_t stride = (uint32_t)(a.Hk * a.dk) * sizeof(T);
+
+  // rows of tiles w .. 3
+  typename Ty::Raw kr[4][KS][2], qr[4][KS][2];
+  const uint32_t goff = rows.off(lane, (uint32_t)a.H * sizeof(T));
+  float g = wide(buf_load<T>(delta_buf((const T*)a.g + low * a.H + h), goff));
+  const float x = wide(buf_load<T>(delta_buf((const T*)a.beta + low * a.H + h), goff));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i >= w) {
+      const uint32_t off = rows.off(16 * i + row, stride);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          kr[i][s][e] = raw4<T, VEC>(kbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
+    }
+  if (WANTP && PI == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i >= w) {
+        const uint32_t off = rows.off(16 * i + row, stride);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qr[i][s][e] = raw4<T, VEC>(qbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
+      }
+  }
 
   // gates: lane = step. log a = min(g, 0) - log(1 + exp(-|g|)), g held to [-87, 87] (NaN passes)
   double cum;
-  float be, na;
   {
-    const int t = t0 + lane;
-    const size_t at = ((size_t)b * a.L + sq.pos(t)) * a.H + h;
-    float g = elem<T>(a.g, at);
-    const float x = elem<T>(a.beta, at);
     g = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -87.f), 87.f);
     const float e = expf(-fabsf(g));
     const float la = fminf(g, 0.f) - log1pf(e);
-    na = (g > 0.f ? e : 1.f) / (1.f + e);
-    be = 1.f / (1.f + expf(-x));
-    const bool live = sq.live(t);
+    const bool live = rows.live(lane);
+    const float na = live ? (g > 0.f ? e : 1.f) / (1.f + e) : 0.f;
+    const float be = live ? 1.f / (1.f + expf(-x)) : 0.f;
     cum = live ? (double)(g == g ? la : g) : 0.0;
-    na = live ? na : 0.f;
-    be = live ? be : 0.f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const double o = __shfl_up(cum, d);
       cum += lane >= d ? o : 0.0;
     }
-  }
-  if (w == 0) {
-    s_cum[lane] = cum;
-    s_b[lane] = be;
-    DeltaGates& gt = a.gates[ch];
-    gt.cum[lane] = cum;
-    gt.gam[lane] = expf((float)cum);
-    gt.end[lane] = expf((float)(__shfl(cum, 63) - cum));
-    gt.b[lane] = be;
-    gt.na[lane] = na;
+    if (w == 3) {   // the wave with the fewest tiles
+      s_cum[lane] = cum;
+      s_b[lane] = be;
+      DeltaGates& gt = a.gates[ch];
+      gt.cum[lane] = cum;
+      gt.gam[lane] = expf((float)cum);
+      gt.end[lane] = expf((float)(__shfl(cum, 63) - cum));
+      gt.b[lane] = be;
+      gt.na[lane] = na;
+    }
   }
 
   // K_i K_w^T and Q_i K_w^T for row tiles i >= w
-  auto tile_of = [&](const void* src, int i, Frag<PI> (&f)[KS]) {
-    const int t = t0 + 16 * i + row;
-    const T* p = (const T*)src + (((size_t)b * a.L + sq.pos(t)) * a.Hk + hk) * a.dk;
-    const bool live = sq.live(t);
-    Quad x[KS][2];
+  auto frags = [&](const typename Ty::Raw (&r)[KS][2], Frag<PI> (&f)[KS]) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) x[s][e] = load4<VEC>(p, 32 * s + 16 * e + 4 * gq, a.dk, live);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) f[s] = join<PI>(to_half(x[s][0]), to_half(x[s][1]));
+    for (int s = 0; s < KS; ++s) f[s] = operand<PI>(r[s][0], r[s][1]);
   };
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
   v4f kk[4], qk[4];
   {
     Frag<PI> kw[KS];
-    tile_of(a.k, w, kw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i == w) frags(kr[i], kw);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       kk[i] = qk[i] = zero;
       if (i < w) continue;
       Frag<PI> f[KS];
-      if (i == w) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) f[s] = kw[s];
-      } else {
-        tile_of(a.k, i, f);
-      }
+      frags(kr[i], f);
 #pragma unroll
       for (int s = 0; s < KS; ++s) kk[i] = mma<PI, PI>(f[s], kw[s], kk[i]);
-      tile_of(a.q, i, f);
+      if (WANTP) {
+        if (PI != 1) {
+          const uint32_t off = rows.off(16 * i + row, stride);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) qk[i] = mma<PI, PI>(f[s], kw[s], qk[i]);
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qr[i][s][e] = raw4<T, VEC>(qbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
+        }
+        frags(qr[i], f);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qk[i] = mma<PI, PI>(f[s], kw[s], qk[i]);
+      }
     }
   }
   __syncthreads();
 
-  float* Pm = a.P + (size_t)ch * kDeltaTri;
-  float* Tm = a.T + (size_t)ch * kDeltaTri;
   const double cc = s_cum[16 * w + row];
   const float bc = s_b[16 * w + row];
   v4f n, nt;        // N_ww and its transpose
@@ -123,12 +149,13 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
       const int m = 4 * gq + r;
       const double d = s_cum[16 * i + m] - cc;
       const float dec = expf((float)(i == w && m < row ? -d : d));   // the transpose's above the diagonal
-      Pm[tri(i, w) + m * 16 + row] = i > w || m >= row ? dec * qk[i][r] : 0.f;
+      qk[i][r] = i > w || m >= row ? dec * qk[i][r] : 0.f;
+      const float f = dec * kk[i][r];
       if (i == w) {
-        n[r] = m > row ? -(s_b[16 * i + m] * dec * kk[i][r]) : 0.f;
-        nt[r] = m < row ? -(bc * dec * kk[i][r]) : 0.f;
+        n[r] = m > row ? -(s_b[16 * i + m] * f) : 0.f;
+        nt[r] = m < row ? -(bc * f) : 0.f;
       } else {
-        s_n[i * (i - 1) / 2 + w][m][row] = -(s_b[16 * i + m] * dec * kk[i][r]);
+        s_n[lds_tile(i, w) + m * 20 + row] = -(s_b[16 * i + m] * f);
       }
     }
   }
@@ -150,7 +177,7 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
     tt = ut;
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) s_t[w][4 * gq + r][row] = t[r];
+  for (int r = 0; r < 4; ++r) s_t[lds_tile(w, w) + (4 * gq + r) * 20 + row] = t[r];
   __syncthreads();
 
   v4f col[4];
@@ -161,28 +188,85 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
     if (i < w) continue;
     if (i == w) {
       col[i] = t;
-    } else {
-      v4f y = zero;
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (k >= w && k < i) y = mm16(*(const v4f*)&s_n[i * (i - 1) / 2 + k][row][4 * gq], col[k], y);
-      col[i] = mm16(*(const v4f*)&s_t[i][row][4 * gq], y, zero);
+      continue;
     }
+    v4f y = zero;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) Tm[tri(i, w) + (4 * gq + r) * 16 + row] = col[i][r] * bc;
+    for (int k = 0; k < 3; ++k)
+      if (k >= w && k < i) y = mm16(*(const v4f*)&s_n[lds_tile(i, k) + row * 20 + 4 * gq], col[k], y);
+    col[i] = mm16(*(const v4f*)&s_t[lds_tile(i, i) + row * 20 + 4 * gq], y, zero);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) col[i] *= bc;
+  if (MODE == kPrepBackward) {       // results one above the other: operands of the transposes
+    unsigned char *Tt = a.Tt + ch * kDeltaTtBytes, *Pt = a.Pt + ch * kDeltaTtBytes;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (2 * s + 1 >= w) {
+        const Frag<3> ft = join<3>(split4<3>(col[2 * s][0], col[2 * s][1], col[2 * s][2], col[2 * s][3]),
+                                   split4<3>(col[2 * s + 1][0], col[2 * s + 1][1], col[2 * s + 1][2],
+                                             col[2 * s + 1][3]));
+        const Frag<3> fp = join<3>(split4<3>(qk[2 * s][0], qk[2 * s][1], qk[2 * s][2], qk[2 * s][3]),
+                                   split4<3>(qk[2 * s + 1][0], qk[2 * s + 1][1], qk[2 * s + 1][2],
+                                             qk[2 * s + 1][3]));
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const int at = (trit_frag(w, s) * 3 + p) * 1024 + lane * 16;
+          *(u32x4*)(Tt + at) = ft.p[p];
+          *(u32x4*)(Pt + at) = fp.p[p];
+        }
+      }
+  }
+  __syncthreads();                   // N and the diagonal tiles have been read
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i >= w)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s_t[lds_tile(i, w) + (4 * gq + r) * 20 + row] = col[i][r];
+        if (MODE == kPrepForward) s_n[lds_tile(i, w) + (4 * gq + r) * 20 + row] = qk[i][r];
+      }
+  __syncthreads();
+  constexpr int PT = MODE == kPrepBackward ? PO : 3;
+  unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, MODE == kPrepBackward);
+  unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
+  auto rows_of = [&](const float* m, int s, float (&v)[8]) {   // row tile w, terms 32 s ..
+    const v4f x = *(const v4f*)&m[lds_tile(w, 2 * s) + row * 20 + 4 * gq];
+    v4f y = zero;
+    if (2 * s + 1 <= w) y = *(const v4f*)&m[lds_tile(w, 2 * s + 1) + row * 20 + 4 * gq];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = x[j], v[4 + j] = y[j];
+  };
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (2 * s <= w) {
+      float v[8];
+      rows_of(s_t, s, v);
+      const Frag<PT> f = split8<PT>(v);
+#pragma unroll
+      for (int p = 0; p < PT; ++p)
+        *(u32x4*)(Tm + (tri_frag(w, s) * PT + p) * 1024 + lane * 16) = f.p[p];
+      if (MODE == kPrepForward) {
+        rows_of(s_n, s, v);
+        const Frag<PO> fp = split8<PO>(v);
+#pragma unroll
+        for (int p = 0; p < PO; ++p)
+          *(u32x4*)(Pm + (tri_frag(w, s) * PO + p) * 1024 + lane * 16) = fp.p[p];
+      }
+    }
 }
 
 // ---------------------------------------------------------------------------- the walk
 // One workgroup per head and 16 columns of dv; the 4 waves share a chunk's work: wave w has row tile w of
 // the 64 steps and OWN of the state's row tiles. Three hand-overs per chunk, each through LDS: the state
-// (as B operands of K S and Q S), X = V - diag(y) K S, and U.
-template <typename T, int DK, bool VEC>
+// (as B operands of K S and Q S), X = V - diag(y) K S, and U. Everything that a chunk reads is requested
+// one chunk ahead, and row addresses are offsets within a chunk, formed anew only for a last, short one.
+template <typename T, int DK, bool VEC, bool OUT>
 __global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
-  constexpr int PI = DeltaType<T>::PI, PO = DeltaType<T>::PO;
+  using Ty = DeltaType<T, VEC>;
+  constexpr int PI = Ty::PI, PO = Ty::PO;
   constexpr int KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4, BLK = 64 * DK / 16 / 256;
   constexpr int BLKS = BLK < 1 ? 1 : BLK;
-  using Quad = typename DeltaType<T>::Quad;
   constexpr int kTileB = 2 * PI * 1024 + 16;    // of K^T: two frags, staggered over the banks
   __shared__ __attribute__((aligned(16))) unsigned char s_s[KS * 3 * 1024];
   __shared__ __attribute__((aligned(16))) unsigned char s_x[2 * 3 * 1024];
@@ -199,31 +283,26 @@ __global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
   const bool in = col < a.dv;
   const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+  const uint32_t kstride = (uint32_t)(a.Hk * a.dk) * sizeof(T), vstride = (uint32_t)(a.H * a.dv) * sizeof(T);
 
   const size_t sdim = (size_t)a.dk * a.dv;
   v4f S[OWN];
+  uint32_t soff[OWN][4];      // of the state's entries that this lane holds
 #pragma unroll
-  for (int i = 0; i < OWN; ++i) {
-    S[i] = zero;
-    const int tile = w * OWN + i;
-    if (tile < NT && a.s0 && in)
+  for (int i = 0; i < OWN; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = 16 * tile + 4 * gq + r;
-        if (k < a.dk) S[i][r] = a.s0[bh * sdim + (size_t)k * a.dv + col];
-      }
-  }
-  auto put_state = [&](float* to) {
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int tile = w * OWN + i;
-      if (tile < NT && in)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int k = 16 * tile + 4 * gq + r;
-          if (k < a.dk) to[(size_t)k * a.dv + col] = S[i][r];
-        }
+    for (int r = 0; r < 4; ++r) {
+      const int k = 16 * (w * OWN + i) + 4 * gq + r;
+      const bool own = w * OWN + i < NT && k < a.dk && in;
+      soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
+      S[i][r] = a.s0 ? buf_load<float>(delta_buf(a.s0 + bh * sdim), soff[i][r]) : 0.f;
     }
+  auto put_state = [&](float* to) {
+    const auto buf = delta_buf(to);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], S[i][r], 0.f);
   };
   auto share_state = [&] {
 #pragma unroll
@@ -235,80 +314,98 @@ __global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
   };
   share_state();
 
-  // of a chunk, loaded while the one before is computed
   struct Chunk {
-    Quad k[KS][2], q[KS][2], kb[BLKS][4];
-    float t[2][8], p[2][8], v[4], gam[4], end[4], last;
+    typename Ty::Raw k[KS][2], q[OUT ? KS : 1][2], kb[BLKS][4];
+    Frag<3> t[2];
+    Frag<PO> p[2];
+    T v[4];
+    float gam[4], end[4], last;
+  } x;
+  uint32_t koff = 0, boff[BLKS][4], voff[4];
+  auto offsets = [&](const DeltaRows& rows) {
+    koff = rows.off(16 * w + row, kstride);
+#pragma unroll
+    for (int m = 0; m < BLKS; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        boff[m][j] = rows.off(4 * ((threadIdx.x + 256 * m) / (DK / 4)) + j, kstride);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      voff[r] = in ? rows.off(16 * w + 4 * gq + r, vstride) + col * sizeof(T) : kNowhere;
   };
-  const bool out = a.o != nullptr;
-  auto load = [&](int c, Chunk& x) {
-    const int ch = bh * a.chunks + c, t0 = c * kDeltaChunk;
-    {
-      const int t = t0 + 16 * w + row;
-      const size_t at = (((size_t)b * a.L + sq.pos(t)) * a.Hk + hk) * a.dk;
-      const bool live = sq.live(t);
+  // each part of the next chunk is requested as soon as the same part of this one has been used
+  auto load_rows = [&](int c) {
+    const size_t low = delta_low(a, sq, b, c);
+    const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
+    const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
+    const auto vbuf = delta_buf((const T*)a.v + (low * a.H + h) * a.dv);
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x.k[s][e] = load4<VEC>((const T*)a.k + at, 32 * s + 16 * e + 4 * gq, a.dk, live);
-          if (out) x.q[s][e] = load4<VEC>((const T*)a.q + at, 32 * s + 16 * e + 4 * gq, a.dk, live);
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m) {
-      const int id = threadIdx.x + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
-      if (BLK >= 1 || tg < 16)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = t0 + 4 * tg + j;
-          const size_t at = (((size_t)b * a.L + sq.pos(t)) * a.Hk + hk) * a.dk;
-          x.kb[m][j] = load4<VEC>((const T*)a.k + at, 4 * dg, a.dk, sq.live(t));
-        }
-    }
-    const float *Tm = a.T + (size_t)ch * kDeltaTri, *Pm = a.P + (size_t)ch * kDeltaTri;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (2 * s <= w) {
-        tri_rows(Tm, w, s, lane, x.t[s]);
-        if (out) tri_rows(Pm, w, s, lane, x.p[s]);
+      for (int e = 0; e < 2; ++e) {
+        x.k[s][e] = raw4<T, VEC>(kbuf, koff, 32 * s + 16 * e + 4 * gq, a.dk);
+        if constexpr (OUT) x.q[s][e] = raw4<T, VEC>(qbuf, koff, 32 * s + 16 * e + 4 * gq, a.dk);
       }
-    const DeltaGates& gt = a.gates[ch];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int m = 16 * w + 4 * gq + r, t = t0 + m;
-      x.gam[r] = gt.gam[m];
-      x.end[r] = gt.end[m];
-      const float v = elem<T>(a.v, (((size_t)b * a.L + sq.pos(t)) * a.H + h) * a.dv + (in ? col : 0));
-      x.v[r] = in && sq.live(t) ? v : 0.f;
+    for (int r = 0; r < 4; ++r) x.v[r] = buf_load<T>(vbuf, voff[r]);
+    *(v4f*)x.gam = *(const v4f*)&a.gates[bh * a.chunks + c].gam[16 * w + 4 * gq];
+#pragma unroll
+    for (int m = 0; m < BLKS; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x.kb[m][j] = raw4<T, VEC>(kbuf, boff[m][j], 4 * ((threadIdx.x + 256 * m) % (DK / 4)), a.dk);
+  };
+  // T and P of row tiles 0 and 1 have terms below 32 only: they load the first frag twice, as loads in a
+  // branch would make every wait for an older one wait for them all
+  const int second = w >= 2 ? 1 : 0;
+  auto load_t = [&](int c) {
+    const size_t ch = (size_t)bh * a.chunks + c;
+    const unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, false);
+    x.t[0] = mem_frag<3>(Tm, tri_frag(w, 0), lane);
+    x.t[1] = mem_frag<3>(Tm, tri_frag(w, second), lane);
+    *(v4f*)x.end = *(const v4f*)&a.gates[ch].end[16 * w + 4 * gq];
+  };
+  auto load_p = [&](int c) {
+    const size_t ch = (size_t)bh * a.chunks + c;
+    x.last = a.gates[ch].gam[kDeltaChunk - 1];
+    if constexpr (OUT) {
+      const unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
+      x.p[0] = mem_frag<PO>(Pm, tri_frag(w, 0), lane);
+      x.p[1] = mem_frag<PO>(Pm, tri_frag(w, second), lane);
     }
-    x.last = gt.gam[kDeltaChunk - 1];
   };
 
-  Chunk x, y;
-  if (nch > 0) load(0, x);
+  if (nch > 0) {
+    offsets(delta_rows(sq, 0));
+    load_rows(0);
+    load_t(0);
+    load_p(0);
+  }
   __syncthreads();
   for (int c = 0; c < nch; ++c) {
-    if (c + 1 < nch) load(c + 1, y);
+    const int next = c + 1 < nch ? c + 1 : c;    // the last chunk loads itself again
     if (a.states) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
     // K S and Q S; K^T for the update
     v4f ks = zero, qs = zero;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const Frag<3> f = lds_frag<3>(s_s, s, lane);
-      ks = mma<PI, 3>(join<PI>(to_half(x.k[s][0]), to_half(x.k[s][1])), f, ks);
-      if (out)
-        qs = mma<PI, PO>(join<PI>(to_half(x.q[s][0]), to_half(x.q[s][1])), lead<PO>(f), qs);
+      ks = mma<PI, 3>(operand<PI>(x.k[s][0], x.k[s][1]), f, ks);
+      if constexpr (OUT) qs = mma<PI, PO>(operand<PI>(x.q[s][0], x.q[s][1]), lead<PO>(f), qs);
     }
-    lds_half<3>(s_x, w >> 1, lane, w & 1,
-                split4<3>(x.v[0] - x.gam[0] * ks[0], x.v[1] - x.gam[1] * ks[1],
-                          x.v[2] - x.gam[2] * ks[2], x.v[3] - x.gam[3] * ks[3]));
+    float d[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) d[r] = wide(x.v[r]) - x.gam[r] * ks[r];
+    lds_half<3>(s_x, w >> 1, lane, w & 1, split4<3>(d[0], d[1], d[2], d[3]));
 #pragma unroll
     for (int m = 0; m < BLKS; ++m) {
       const int id = threadIdx.x + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
       if (BLK >= 1 || tg < 16) {
+        typename Ty::Quad q[4];
         Half<PI> cl[4];
-        transpose4(x.kb[m], cl);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = quad(x.kb[m][j]);
+        transpose4(q, cl);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int k = 4 * dg + j;
@@ -317,14 +414,19 @@ __global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
         }
       }
     }
-    __syncthreads();
-    v4f u = zero;
+    uint32_t ooff[4];
+    float ogam[4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (2 * s <= w) u = mma<3, 3>(split8<3>(x.t[s]), lds_frag<3>(s_x, s, lane), u);
-    if (out) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
+    for (int r = 0; r < 4; ++r) ooff[r] = voff[r], ogam[r] = x.gam[r];
+    if (next == nch - 1) offsets(delta_rows(sq, next));
+    load_rows(next);
+    __syncthreads();
+    v4f u = mma<3, 3>(x.t[0], lds_frag<3>(s_x, 0, lane), zero);
+    if (w >= 2) u = mma<3, 3>(x.t[1], lds_frag<3>(s_x, 1, lane), u);
+    if constexpr (OUT) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
     lds_half<3>(s_e, w >> 1, lane, w & 1,
                 split4<3>(x.end[0] * u[0], x.end[1] * u[1], x.end[2] * u[2], x.end[3] * u[3]));
+    load_t(next);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
@@ -338,26 +440,22 @@ __global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
       }
     }
     share_state();
-    if (out) {
-      v4f pu = zero;
+    if constexpr (OUT) {
+      v4f pu = mma<PO, PO>(x.p[0], lds_frag<PO>(s_u, 0, lane), zero);
+      if (w >= 2) pu = mma<PO, PO>(x.p[1], lds_frag<PO>(s_u, 1, lane), pu);
+      const auto obuf = delta_buf((T*)a.o + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (2 * s <= w) pu = mma<PO, PO>(split8<PO>(x.p[s]), lds_frag<PO>(s_u, s, lane), pu);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = c * kDeltaChunk + 16 * w + 4 * gq + r;
-        if (in && sq.live(t))
-          put1((T*)a.o + (((size_t)b * a.L + sq.pos(t)) * a.H + h) * a.dv + col,
-               a.scale * fmaf(x.gam[r], qs[r], pu[r]));
-      }
+      for (int r = 0; r < 4; ++r)
+        buf_store(obuf, ooff[r], a.scale * fmaf(ogam[r], qs[r], pu[r]), T());
     }
-    x = y;
+    load_p(next);
     __syncthreads();
   }
+
   if (a.s_last) put_state(a.s_last + bh * sdim);
   if (a.states)
     for (int c = nch; c < a.chunks; ++c) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
-  if (out && in)
+  if (OUT && in)
     for (int t = sq.n + (threadIdx.x >> 4); t < a.L; t += 16)
       put1((T*)a.o + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
 }
@@ -475,19 +573,28 @@ void with_dk(int dk, bool vec, F f) {
   else go(std::integral_constant<int, 128>());
 }
 
-template <typename T>
+template <typename T, DeltaPrep MODE>
 void prep_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   with_dk<T>(a.dk, vec, [&](auto d, auto v) {
-    k_delta_prep<T, decltype(d)::value, decltype(v)::value>
+    k_delta_prep<T, decltype(d)::value, decltype(v)::value, MODE>
         <<<dim3(a.B * a.H * a.chunks), 256, 0, st>>>(a);
   });
+}
+template <typename T>
+void prep_mode(const DeltaArgs& a, bool vec, DeltaPrep mode, hipStream_t st) {
+  if (mode == kPrepForward) prep_t<T, kPrepForward>(a, vec, st);
+  else if (mode == kPrepStates) prep_t<T, kPrepStates>(a, vec, st);
+  else prep_t<T, kPrepBackward>(a, vec, st);
 }
 template <typename T>
 void walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   // heads side by side in steps of 8: a head's columns then lie on one XCD and share its L2
   const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 15) / 16);
   with_dk<T>(a.dk, vec, [&](auto d, auto v) {
-    k_delta_walk<T, decltype(d)::value, decltype(v)::value><<<grid, 256, 0, st>>>(a);
+    constexpr int DK = decltype(d)::value;
+    constexpr bool VEC = decltype(v)::value;
+    if (a.o) k_delta_walk<T, DK, VEC, true><<<grid, 256, 0, st>>>(a);
+    else k_delta_walk<T, DK, VEC, false><<<grid, 256, 0, st>>>(a);
   });
 }
 template <typename T>
@@ -508,11 +615,6 @@ DeltaArgs delta_args(const DeltaRequest& r) {
   a.dbeta = r.dbeta; a.ds0 = r.ds0;
   a.B = (int)r.B; a.L = (int)r.L; a.Hk = r.Hk; a.H = r.H; a.dk = r.dk; a.dv = r.dv;
   a.rep = r.H / r.Hk; a.chunks = (int)chunks_of(r.L); a.reverse = r.reverse; a.scale = r.scale;
-  const size_t n = (size_t)r.B * r.H * a.chunks;
-  unsigned char* ws = (unsigned char*)r.ws;
-  a.T = (float*)ws;
-  a.P = a.T + n * kDeltaTri;
-  a.gates = (DeltaGates*)(a.P + n * kDeltaTri);
   return a;
 }
 
@@ -523,9 +625,9 @@ bool delta_vec(const DeltaRequest& r) {
          al(r.dout, m) && al(r.states, 15);
 }
 
-hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st) {
-  if (bf16) prep_t<uint16_t>(a, vec, st);
-  else prep_t<float>(a, vec, st);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st) {
+  if (bf16) prep_mode<uint16_t>(a, vec, mode, st);
+  else prep_mode<float>(a, vec, mode, st);
   return hipGetLastError();
 }
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st) {
@@ -534,20 +636,40 @@ hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_
   return hipGetLastError();
 }
 
-size_t delta_forward_workspace(int64_t B, int64_t L, int H, int dk, int dv) {
-  if (L <= kDeltaSteps) return 0;
-  return (size_t)B * H * chunks_of(L) * (2 * kDeltaTri * 4 + sizeof(DeltaGates));
+namespace {
+
+struct FwdWs {
+  size_t P, gates, total;
+};
+FwdWs fwd_ws(int64_t B, int64_t L, int H, bool bf16) {
+  const size_t n = (size_t)B * H * chunks_of(L);
+  FwdWs w;
+  w.P = n * delta_t_bytes(bf16, false);
+  w.gates = w.P + n * delta_p_bytes(bf16);
+  w.total = w.gates + n * sizeof(DeltaGates);
+  return w;
+}
+
+}  // namespace
+
+size_t delta_forward_workspace(int64_t B, int64_t L, int H, bool bf16) {
+  return L <= kDeltaSteps ? 0 : fwd_ws(B, L, H, bf16).total;
 }
 
 hipError_t launch_delta_forward(const DeltaRequest& r, hipStream_t st) {
-  const DeltaArgs a = delta_args(r);
+  DeltaArgs a = delta_args(r);
   if (r.L <= kDeltaSteps) {
     if (r.bf16) step_t<uint16_t>(a, st);
     else step_t<float>(a, st);
     return hipGetLastError();
   }
+  const FwdWs w = fwd_ws(r.B, r.L, r.H, r.bf16);
+  unsigned char* ws = (unsigned char*)r.ws;
+  a.T = ws;
+  a.P = ws + w.P;
+  a.gates = (DeltaGates*)(ws + w.gates);
   const bool vec = delta_vec(r);
-  const hipError_t e = launch_delta_prep(a, r.bf16, vec, st);
+  const hipError_t e = launch_delta_prep(a, r.bf16, vec, kPrepForward, st);
   return e != hipSuccess ? e : launch_delta_walk(a, r.bf16, vec, st);
 }
 

@@ -42,8 +42,7 @@
 namespace wbmm {
 
 constexpr int kDeltaChunk = 64;
-constexpr int kDeltaTiles = 10;              // 16 x 16 tiles on and below the diagonal of 64 x 64
-constexpr int kDeltaTri = kDeltaTiles * 256; // floats of T, or of P
+constexpr int kDeltaFrags = 6;               // operands of a triangular 64 x 64 matrix, 1024 bytes a part
 
 struct DeltaRequest {
   int64_t B, L;
@@ -61,8 +60,8 @@ struct DeltaRequest {
   void* ws;
 };
 
-size_t delta_forward_workspace(int64_t B, int64_t L, int H, int dk, int dv);
-size_t delta_backward_workspace(int64_t B, int64_t L, int H, int dk, int dv, bool has_states);
+size_t delta_forward_workspace(int64_t B, int64_t L, int H, bool bf16);
+size_t delta_backward_workspace(int64_t B, int64_t L, int H, int dk, int dv, bool bf16, bool has_states);
 hipError_t launch_delta_forward(const DeltaRequest& r, hipStream_t st);
 hipError_t launch_delta_backward(const DeltaRequest& r, hipStream_t st);
 
@@ -82,8 +81,9 @@ struct DeltaArgs {
   float* states;
   void *dq, *dkey, *dval, *dg, *dbeta;
   float* ds0;
-  float* T;                    // [B H chunks][kDeltaTri]
-  float* P;
+  // per chunk of a head, kDeltaFrags operands each: T and P for the walk along the chunks, T for the
+  // gradients, the transposes for the walk back
+  unsigned char *T, *P, *Tt, *Pt;
   DeltaGates* gates;           // [B H chunks]
   float* D;                    // [B H chunks][dk][dv]
   float* R;                    // [B H chunks][64][dv]
@@ -91,8 +91,18 @@ struct DeltaArgs {
   float scale;
 };
 
+// What of a chunk's own matrices a launch of launch_delta_prep forms.
+enum DeltaPrep { kPrepForward, kPrepStates, kPrepBackward };
+// Bytes per chunk of a head: T in three parts (backward: as many as the outputs need), P in as many as
+// the outputs need, the transposes in three.
+constexpr size_t delta_t_bytes(bool bf16, bool backward) {
+  return (size_t)kDeltaFrags * 1024 * (bf16 && backward ? 2 : 3);
+}
+constexpr size_t delta_p_bytes(bool bf16) { return (size_t)kDeltaFrags * 1024 * (bf16 ? 2 : 3); }
+constexpr size_t kDeltaTtBytes = (size_t)kDeltaFrags * 1024 * 3;
+
 DeltaArgs delta_args(const DeltaRequest& r);
-hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
 // 4 elements at a time of everything that lies in rows of dk or dv.
 bool delta_vec(const DeltaRequest& r);

@@ -5,25 +5,34 @@
 #include "wbmm_delta.hpp"
 #include "wbmm_device.hpp"
 
+#include <type_traits>
+
 namespace wbmm {
 
 template <int P>
 struct Frag {
   u32x4 p[P];
 };
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 template <int P>
 struct Half {                  // the four terms of one 16: half a frag
-  uint2 p[P];
+  u32x2 p[P];
 };
 
 template <int P>
 __device__ __forceinline__ Half<P> split4(float a, float b, float c, float d) {
-  uint32_t lo[P], hi[P];
-  split2<P>(a, b, lo);
-  split2<P>(c, d, hi);
   Half<P> h;
 #pragma unroll
-  for (int i = 0; i < P; ++i) h.p[i] = make_uint2(lo[i], hi[i]);
+  for (int i = 0; i < P; ++i) {
+    const uint32_t lo = pk_bf16(a, b), hi = pk_bf16(c, d);
+    h.p[i] = u32x2{lo, hi};
+    if (i + 1 < P) {
+      a -= __uint_as_float(lo << 16);
+      b -= __uint_as_float(lo & 0xffff0000u);
+      c -= __uint_as_float(hi << 16);
+      d -= __uint_as_float(hi & 0xffff0000u);
+    }
+  }
   return h;
 }
 template <int P>
@@ -69,7 +78,7 @@ template <int P>
 __device__ __forceinline__ void lds_half(unsigned char* base, int f, int lane, int half,
                                          const Half<P>& h) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) *(uint2*)(base + (f * P + i) * 1024 + lane * 16 + half * 8) = h.p[i];
+  for (int i = 0; i < P; ++i) *(u32x2*)(base + (f * P + i) * 1024 + lane * 16 + half * 8) = h.p[i];
 }
 
 // The steps of one sequence: step t < n takes position t, or n - 1 - t when reversed.
@@ -91,60 +100,113 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs& a, int b) {
   return s;
 }
 
-// Four neighbouring entries i .. i + 3 of a row of `len`; 0 past its end and in a row that is not
-// live, whatever stands there.
+// Types of a tensor's elements: parts of an input, parts of what only reaches an output, a quad of
+// entries, and a quad as it is loaded (nothing is done to it before it is used: the loads of a chunk are
+// in flight while the chunk before it is computed).
+struct Raw16 {
+  uint32_t e[4];
+};
+template <typename T, bool VEC>
+struct DeltaType;
 template <bool VEC>
-__device__ __forceinline__ Half<1> load4(const uint16_t* row, int i, int len, bool live) {
-  uint2 u;
-  if (VEC) {
-    const bool in = live && i < len;
-    u = *(const uint2*)(row + (i < len ? i : 0));
-    u.x = in ? u.x : 0;
-    u.y = in ? u.y : 0;
+struct DeltaType<uint16_t, VEC> {
+  static constexpr int PI = 1, PO = 2;
+  using Quad = Half<1>;
+  using Raw = typename std::conditional<VEC, u32x2, Raw16>::type;
+};
+template <bool VEC>
+struct DeltaType<float, VEC> {
+  static constexpr int PI = 3, PO = 3;
+  using Quad = v4f;
+  using Raw = v4f;
+};
+
+// Buffers: loads at offsets from kNowhere on read 0, stores there are dropped. So what lies past the
+// end of a sequence or a row is zero whatever memory holds, without a branch or a select. An offset
+// counts from the lowest position of a chunk: at most 64 rows of 2^24 bytes.
+constexpr uint32_t kNowhere = 0x7fffff00u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t delta_buf(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)kNowhere,
+                                           0x00020000);
+}
+template <typename T>
+__device__ __forceinline__ T buf_load(__amdgpu_buffer_rsrc_t r, uint32_t off);
+template <>
+__device__ __forceinline__ uint16_t buf_load<uint16_t>(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+}
+template <>
+__device__ __forceinline__ float buf_load<float>(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+}
+template <>
+__device__ __forceinline__ u32x2 buf_load<u32x2>(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+}
+template <>
+__device__ __forceinline__ v4f buf_load<v4f>(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, uint32_t off, float v, float) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, (int)off, 0, 0);
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, uint32_t off, float v, uint16_t) {
+  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, (int)off, 0, 0);
+}
+__device__ __forceinline__ float wide(float v) { return v; }
+__device__ __forceinline__ float wide(uint16_t v) { return bf2f(v); }
+
+// Entries i .. i + 3 of a row of `len` at `off` (kNowhere: a row of zeros). VEC: len is a multiple of 4.
+template <typename T, bool VEC>
+__device__ __forceinline__ typename DeltaType<T, VEC>::Raw raw4(__amdgpu_buffer_rsrc_t r, uint32_t off,
+                                                                int i, int len) {
+  typename DeltaType<T, VEC>::Raw u;
+  if constexpr (VEC) {
+    u = buf_load<typename DeltaType<T, VEC>::Raw>(r, i < len ? off + i * sizeof(T) : kNowhere);
   } else {
-    uint32_t e[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = row[i + j < len ? i + j : 0];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = live && i + j < len ? e[j] : 0;
-    u = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    for (int j = 0; j < 4; ++j) {
+      const T x = buf_load<T>(r, i + j < len ? off + (i + j) * sizeof(T) : kNowhere);
+      if constexpr (sizeof(T) == 2) u.e[j] = x;
+      else u[j] = x;
+    }
   }
+  return u;
+}
+__device__ __forceinline__ Half<1> quad(u32x2 u) {
   Half<1> h;
   h.p[0] = u;
   return h;
 }
-template <bool VEC>
-__device__ __forceinline__ v4f load4(const float* row, int i, int len, bool live) {
-  v4f u;
-  if (VEC) {
-    const bool in = live && i < len;
-    u = *(const v4f*)(row + (i < len ? i : 0));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = in ? u[j] : 0.f;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = row[i + j < len ? i + j : 0];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = live && i + j < len ? u[j] : 0.f;
-  }
-  return u;
+__device__ __forceinline__ Half<1> quad(const Raw16& u) {
+  return quad(u32x2{u.e[0] | (u.e[1] << 16), u.e[2] | (u.e[3] << 16)});
 }
-__device__ __forceinline__ Half<1> to_half(Half<1> h) { return h; }
-__device__ __forceinline__ Half<3> to_half(v4f v) { return split4<3>(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ v4f quad(const v4f& u) { return u; }
+__device__ __forceinline__ Half<1> to_half(const Half<1>& h) { return h; }
+__device__ __forceinline__ Half<3> to_half(const v4f& v) { return split4<3>(v[0], v[1], v[2], v[3]); }
+template <int P, typename R>
+__device__ __forceinline__ Frag<P> operand(const R& a, const R& b) {
+  return join<P>(to_half(quad(a)), to_half(quad(b)));
+}
 
-// Types of a tensor's elements: parts of an input, parts of what only reaches an output, raw quads.
-template <typename T>
-struct DeltaType;
-template <>
-struct DeltaType<uint16_t> {
-  static constexpr int PI = 1, PO = 2;
-  using Quad = Half<1>;
+// Rows of one chunk of a sequence, as offsets from its lowest position.
+struct DeltaRows {
+  int cnt, reverse;      // live steps
+  __device__ __forceinline__ bool live(int m) const { return m < cnt; }
+  __device__ __forceinline__ uint32_t off(int m, uint32_t stride) const {
+    return m < cnt ? (uint32_t)(reverse ? cnt - 1 - m : m) * stride : kNowhere;
+  }
 };
-template <>
-struct DeltaType<float> {
-  static constexpr int PI = 3, PO = 3;
-  using Quad = v4f;
-};
+__device__ __forceinline__ DeltaRows delta_rows(const DeltaSeq& s, int c) {
+  const int left = s.n - c * kDeltaChunk;
+  return {left < kDeltaChunk ? left : kDeltaChunk, s.reverse};
+}
+// Lowest position of chunk c, counted over the batch.
+__device__ __forceinline__ size_t delta_low(const DeltaArgs& a, const DeltaSeq& s, int b, int c) {
+  const int t0 = c * kDeltaChunk, left = s.n - t0;
+  const int cnt = left < kDeltaChunk ? left : kDeltaChunk;
+  return (size_t)b * a.L + (s.reverse ? s.n - t0 - cnt : t0);
+}
 
 // A 4 x 4 block, rows r[0..3] of four entries, as its four columns of four.
 __device__ __forceinline__ void transpose4(const Half<1> (&r)[4], Half<1> (&c)[4]) {
@@ -153,7 +215,7 @@ __device__ __forceinline__ void transpose4(const Half<1> (&r)[4], Half<1> (&c)[4
     const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;   // the upper or lower halves of two words
     const uint32_t a = j < 2 ? r[0].p[0].x : r[0].p[0].y, b = j < 2 ? r[1].p[0].x : r[1].p[0].y;
     const uint32_t d = j < 2 ? r[2].p[0].x : r[2].p[0].y, e = j < 2 ? r[3].p[0].x : r[3].p[0].y;
-    c[j].p[0] = make_uint2(__builtin_amdgcn_perm(b, a, sel), __builtin_amdgcn_perm(e, d, sel));
+    c[j].p[0] = u32x2{__builtin_amdgcn_perm(b, a, sel), __builtin_amdgcn_perm(e, d, sel)};
   }
 }
 __device__ __forceinline__ void transpose4(const v4f (&r)[4], Half<3> (&c)[4]) {
@@ -166,29 +228,17 @@ __device__ __forceinline__ void put1(uint16_t* p, float v) {
   *p = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// Tile (i, j), j <= i, of T or P: 16 rows of 16 floats.
-__device__ __forceinline__ constexpr int tri(int i, int j) { return (i * (i + 1) / 2 + j) * 256; }
-
-// A operand of row tile i over terms 32 s ..: rows of a lower triangular matrix.
-__device__ __forceinline__ void tri_rows(const float* m, int i, int s, int lane, float (&v)[8]) {
-  const int at = (lane & 15) * 16 + (lane >> 4) * 4;
-  const v4f x = *(const v4f*)(m + tri(i, 2 * s) + at);
-  v4f y = v4f{0.f, 0.f, 0.f, 0.f};
-  if (2 * s + 1 <= i) y = *(const v4f*)(m + tri(i, 2 * s + 1) + at);
+// Frags of a lower triangular 64 x 64 matrix M in memory, 6 of them, as A operands: row tile i over
+// terms 32 s .. (2 s <= i), and of its transpose row tile j over terms 32 s .. (2 s + 1 >= j).
+__device__ __forceinline__ constexpr int tri_frag(int i, int s) { return s == 0 ? i : 2 + i; }
+__device__ __forceinline__ constexpr int trit_frag(int j, int s) { return j < 2 ? 2 * j + s : 2 + j; }
+template <int P>
+__device__ __forceinline__ Frag<P> mem_frag(const unsigned char* base, int f, int lane) {
+  Frag<P> r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = x[j], v[4 + j] = y[j];
-}
-// The same of its transpose: row tile j, terms 32 s .. (2 s + 1 >= j).
-__device__ __forceinline__ void tri_cols(const float* m, int j, int s, int lane, float (&v)[8]) {
-  const int at = (lane >> 4) * 64 + (lane & 15);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] = 0.f;
-  if (2 * s >= j) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = m[tri(2 * s, j) + at + 16 * r];
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) v[4 + r] = m[tri(2 * s + 1, j) + at + 16 * r];
+  for (int i = 0; i < P; ++i)
+    r.p[i] = *(const u32x4*)(base + (uint32_t)((f * P + i) * 1024 + lane * 16));
+  return r;
 }
 
 }  // namespace wbmm
