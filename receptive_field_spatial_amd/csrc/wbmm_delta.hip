@@ -30,10 +30,14 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
   constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32;
   constexpr bool WANTP = MODE != kPrepStates;
+  constexpr int kRows = 4 * KS * PI * 1024;               // K (or Q) as operands
+  constexpr int kMats = 2 * 10 * 320 * 4;                 // N below the diagonal (then P), and T
+  constexpr int kShared = (WANTP ? 2 : 1) * kRows > kMats ? (WANTP ? 2 : 1) * kRows : kMats;
   __shared__ double s_cum[kDeltaChunk];
   __shared__ float s_b[kDeltaChunk];
-  __shared__ __attribute__((aligned(16))) float s_n[10 * 320];   // N below the diagonal, then P
-  __shared__ __attribute__((aligned(16))) float s_t[10 * 320];   // T
+  __shared__ __attribute__((aligned(16))) unsigned char s_all[kShared];
+  float* s_n = (float*)s_all;
+  float* s_t = s_n + 10 * 320;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, gq = lane >> 4;
   const int ch = blockIdx.x, bh = ch / a.chunks, c = ch - bh * a.chunks;
@@ -44,52 +48,44 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
   const size_t low = delta_low(a, sq, b, c);
   const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
   const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
-  const uint32_t stride = (uint32_t)(a.Hk * a.dk) * sizeof(T);
 
-  // rows of tiles w .. 3
-  typename Ty::Raw kr[4][KS][2], qr[4][KS][2];
-  const uint32_t goff = rows.off(lane, (uint32_t)a.H * sizeof(T));
-  float g = wide(buf_load<T>(delta_buf((const T*)a.g + low * a.H + h), goff));
-  const float x = wide(buf_load<T>(delta_buf((const T*)a.beta + low * a.H + h), goff));
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i >= w) {
-      const uint32_t off = rows.off(16 * i + row, stride);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          kr[i][s][e] = raw4<T, VEC>(kbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
-    }
-  if (WANTP && PI == 1) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i >= w) {
-        const uint32_t off = rows.off(16 * i + row, stride);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            qr[i][s][e] = raw4<T, VEC>(qbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
-      }
-  }
-
-  // gates: lane = step. log a = min(g, 0) - log(1 + exp(-|g|)), g held to [-87, 87] (NaN passes)
-  double cum;
+  // each wave's 16 rows of K and Q, shared as operands
   {
-    g = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -87.f), 87.f);
-    const float e = expf(-fabsf(g));
-    const float la = fminf(g, 0.f) - log1pf(e);
-    const bool live = rows.live(lane);
-    const float na = live ? (g > 0.f ? e : 1.f) / (1.f + e) : 0.f;
-    const float be = live ? 1.f / (1.f + expf(-x)) : 0.f;
-    cum = live ? (double)(g == g ? la : g) : 0.0;
+    const uint32_t off = rows.off(16 * w + row, (uint32_t)(a.Hk * a.dk) * sizeof(T));
+    Raw8<T, VEC> kr[KS], qr[KS];
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const double o = __shfl_up(cum, d);
-      cum += lane >= d ? o : 0.0;
-    }
-    if (w == 3) {   // the wave with the fewest tiles
+    for (int s = 0; s < KS; ++s) kr[s] = raw8<T, VEC>(kbuf, off, 32 * s + 8 * gq, a.dk);
+    if (WANTP)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) qr[s] = raw8<T, VEC>(qbuf, off, 32 * s + 8 * gq, a.dk);
+    auto share = [&](const Raw8<T, VEC> (&r)[KS], unsigned char* to) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        Half<PI> lo, hi;
+        halves<PI>(r[s], lo, hi);
+        const Frag<PI> f = join<PI>(lo, hi);
+#pragma unroll
+        for (int p = 0; p < PI; ++p)
+          *(u32x4*)(to + ((w * KS + s) * PI + p) * 1024 + lane * 16) = f.p[p];
+      }
+    };
+    // gates, by the wave that has the fewest products below: lane = step. log a = min(g, 0) - log(1 +
+    // exp(-|g|)), g held to [-87, 87] (NaN passes)
+    if (w == 3) {
+      const uint32_t goff = rows.off(lane, (uint32_t)a.H * sizeof(T));
+      float g = wide(buf_load<T>(delta_buf((const T*)a.g + low * a.H + h), goff));
+      const float x = wide(buf_load<T>(delta_buf((const T*)a.beta + low * a.H + h), goff));
+      g = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -87.f), 87.f);
+      const float e = expf(-fabsf(g));
+      const float la = fminf(g, 0.f) - log1pf(e);
+      const bool live = rows.live(lane);
+      const float be = live ? 1.f / (1.f + expf(-x)) : 0.f;
+      double cum = live ? (double)(g == g ? la : g) : 0.0;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double o = __shfl_up(cum, d);
+        cum += lane >= d ? o : 0.0;
+      }
       s_cum[lane] = cum;
       s_b[lane] = be;
       DeltaGates& gt = a.gates[ch];
@@ -97,46 +93,29 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
       gt.gam[lane] = expf((float)cum);
       gt.end[lane] = expf((float)(__shfl(cum, 63) - cum));
       gt.b[lane] = be;
-      gt.na[lane] = na;
+      gt.na[lane] = live ? (g > 0.f ? e : 1.f) / (1.f + e) : 0.f;
     }
-  }
-
-  // K_i K_w^T and Q_i K_w^T for row tiles i >= w
-  auto frags = [&](const typename Ty::Raw (&r)[KS][2], Frag<PI> (&f)[KS]) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) f[s] = operand<PI>(r[s][0], r[s][1]);
-  };
-  const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
-  v4f kk[4], qk[4];
-  {
-    Frag<PI> kw[KS];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i == w) frags(kr[i], kw);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kk[i] = qk[i] = zero;
-      if (i < w) continue;
-      Frag<PI> f[KS];
-      frags(kr[i], f);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) kk[i] = mma<PI, PI>(f[s], kw[s], kk[i]);
-      if (WANTP) {
-        if (PI != 1) {
-          const uint32_t off = rows.off(16 * i + row, stride);
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              qr[i][s][e] = raw4<T, VEC>(qbuf, off, 32 * s + 16 * e + 4 * gq, a.dk);
-        }
-        frags(qr[i], f);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) qk[i] = mma<PI, PI>(f[s], kw[s], qk[i]);
-      }
-    }
+    share(kr, s_all);
+    if (WANTP) share(qr, s_all + kRows);
   }
   __syncthreads();
+
+  // K_i K_w^T and Q_i K_w^T for row tiles i >= w
+  const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f kk[4], qk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = zero;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const Frag<PI> kw = lds_frag<PI>(s_all, w * KS + s, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i >= w) {
+        kk[i] = mma<PI, PI>(lds_frag<PI>(s_all, i * KS + s, lane), kw, kk[i]);
+        if (WANTP) qk[i] = mma<PI, PI>(lds_frag<PI>(s_all + kRows, i * KS + s, lane), kw, qk[i]);
+      }
+  }
+  __syncthreads();                   // K and Q have been read: their place is N's and T's
 
   const double cc = s_cum[16 * w + row];
   const float bc = s_b[16 * w + row];
@@ -257,209 +236,243 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------- the walk
-// One workgroup per head and 16 columns of dv; the 4 waves share a chunk's work: wave w has row tile w of
-// the 64 steps and OWN of the state's row tiles. Three hand-overs per chunk, each through LDS: the state
-// (as B operands of K S and Q S), X = V - diag(y) K S, and U. Everything that a chunk reads is requested
-// one chunk ahead, and row addresses are offsets within a chunk, formed anew only for a last, short one.
+// One workgroup per head and 16 columns of dv, of 8 waves: the first four walk the state along the chunks,
+// wave w with row tile w of the 64 steps and OWN of the state's row tiles; the other four fetch K for
+// them, one chunk ahead, and form the outputs. Three hand-overs per chunk, each through LDS:
+//        walkers                                    helpers
+//   A    X = V - diag(y) K S                        Q S
+//   B    U = T X
+//   C    S = y_C S + K^T diag(y_C / y) U            o = scale (diag(y) Q S + P U); K of the next chunk
+// Loads are issued a chunk before their use, right after the last use of their registers.
+// LDS of a workgroup. Two chunks' K^T, where they fit (all but fp32 with 96 < dk): the next one is then
+// written while this one is read, and K is loaded a whole chunk ahead.
+template <typename T, int DK>
+struct WalkLds {
+  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO, KS = DK / 32;
+  static constexpr int rows = 4 * KS * PI * 1024, cols = (DK / 16) * kTileBytes<PI>;
+  static constexpr int rest = (KS * 3 + 12 + 2 * PO) * 1024 + rows;
+  static constexpr bool two = rest + 2 * cols <= 160 * 1024;
+  static constexpr int bytes = rest + (two ? 2 : 1) * cols;
+};
+
 template <typename T, int DK, bool VEC, bool OUT>
-__global__ void __launch_bounds__(256) k_delta_walk(DeltaArgs a) {
+__global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
-  constexpr int PI = Ty::PI, PO = Ty::PO;
-  constexpr int KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4, BLK = 64 * DK / 16 / 256;
-  constexpr int BLKS = BLK < 1 ? 1 : BLK;
-  constexpr int kTileB = 2 * PI * 1024 + 16;    // of K^T: two frags, staggered over the banks
-  __shared__ __attribute__((aligned(16))) unsigned char s_s[KS * 3 * 1024];
-  __shared__ __attribute__((aligned(16))) unsigned char s_x[2 * 3 * 1024];
-  __shared__ __attribute__((aligned(16))) unsigned char s_u[2 * PO * 1024];
-  __shared__ __attribute__((aligned(16))) unsigned char s_e[2 * 3 * 1024];
-  __shared__ __attribute__((aligned(16))) unsigned char s_kt[NT * kTileB];
+  constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
+  constexpr bool TWO = WalkLds<T, DK>::two;
+  constexpr int kRows = WalkLds<T, DK>::rows, kCols = TWO ? WalkLds<T, DK>::cols : 0;
+  extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
+  unsigned char* const s_s = sm;                          // the state
+  unsigned char* const s_x = s_s + KS * 3 * 1024;         // X
+  unsigned char* const s_e = s_x + 2 * 3 * 1024;          // diag(y_C / y) U
+  unsigned char* const s_u = s_e + 2 * 3 * 1024;          // U
+  unsigned char* const s_k = s_u + 2 * PO * 1024;         // K, and K^T
+  unsigned char* const s_kt = s_k + kRows;
   const int bh = blockIdx.x;
   if (bh >= a.B * a.H) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = lane & 15, gq = lane >> 4;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wid & 3, row = lane & 15, gq = lane >> 4;
+  const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
   const int col = blockIdx.y * 16 + row;
   const bool in = col < a.dv;
-  const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk;
+  const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
   const uint32_t kstride = (uint32_t)(a.Hk * a.dk) * sizeof(T), vstride = (uint32_t)(a.H * a.dv) * sizeof(T);
-
   const size_t sdim = (size_t)a.dk * a.dv;
-  v4f S[OWN];
-  uint32_t soff[OWN][4];      // of the state's entries that this lane holds
-#pragma unroll
-  for (int i = 0; i < OWN; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int k = 16 * (w * OWN + i) + 4 * gq + r;
-      const bool own = w * OWN + i < NT && k < a.dk && in;
-      soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
-      S[i][r] = a.s0 ? buf_load<float>(delta_buf(a.s0 + bh * sdim), soff[i][r]) : 0.f;
-    }
-  auto put_state = [&](float* to) {
-    const auto buf = delta_buf(to);
-#pragma unroll
-    for (int i = 0; i < OWN; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], S[i][r], 0.f);
-  };
-  auto share_state = [&] {
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int tile = w * OWN + i;
-      if (tile < NT)
-        lds_half<3>(s_s, tile >> 1, lane, tile & 1, split4<3>(S[i][0], S[i][1], S[i][2], S[i][3]));
-    }
-  };
-  share_state();
-
-  struct Chunk {
-    typename Ty::Raw k[KS][2], q[OUT ? KS : 1][2], kb[BLKS][4];
-    Frag<3> t[2];
-    Frag<PO> p[2];
-    T v[4];
-    float gam[4], end[4], last;
-  } x;
-  uint32_t koff = 0, boff[BLKS][4], voff[4];
-  auto offsets = [&](const DeltaRows& rows) {
-    koff = rows.off(16 * w + row, kstride);
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        boff[m][j] = rows.off(4 * ((threadIdx.x + 256 * m) / (DK / 4)) + j, kstride);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      voff[r] = in ? rows.off(16 * w + 4 * gq + r, vstride) + col * sizeof(T) : kNowhere;
-  };
-  // each part of the next chunk is requested as soon as the same part of this one has been used
-  auto load_rows = [&](int c) {
-    const size_t low = delta_low(a, sq, b, c);
-    const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
-    const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
-    const auto vbuf = delta_buf((const T*)a.v + (low * a.H + h) * a.dv);
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x.k[s][e] = raw4<T, VEC>(kbuf, koff, 32 * s + 16 * e + 4 * gq, a.dk);
-        if constexpr (OUT) x.q[s][e] = raw4<T, VEC>(qbuf, koff, 32 * s + 16 * e + 4 * gq, a.dk);
-      }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x.v[r] = buf_load<T>(vbuf, voff[r]);
-    *(v4f*)x.gam = *(const v4f*)&a.gates[bh * a.chunks + c].gam[16 * w + 4 * gq];
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x.kb[m][j] = raw4<T, VEC>(kbuf, boff[m][j], 4 * ((threadIdx.x + 256 * m) % (DK / 4)), a.dk);
-  };
   // T and P of row tiles 0 and 1 have terms below 32 only: they load the first frag twice, as loads in a
   // branch would make every wait for an older one wait for them all
   const int second = w >= 2 ? 1 : 0;
-  auto load_t = [&](int c) {
-    const size_t ch = (size_t)bh * a.chunks + c;
-    const unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, false);
-    x.t[0] = mem_frag<3>(Tm, tri_frag(w, 0), lane);
-    x.t[1] = mem_frag<3>(Tm, tri_frag(w, second), lane);
-    *(v4f*)x.end = *(const v4f*)&a.gates[ch].end[16 * w + 4 * gq];
-  };
-  auto load_p = [&](int c) {
-    const size_t ch = (size_t)bh * a.chunks + c;
-    x.last = a.gates[ch].gam[kDeltaChunk - 1];
-    if constexpr (OUT) {
-      const unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
-      x.p[0] = mem_frag<PO>(Pm, tri_frag(w, 0), lane);
-      x.p[1] = mem_frag<PO>(Pm, tri_frag(w, second), lane);
-    }
+  // this lane's entries of V and o, as a result lies; rows past a last chunk's end: nowhere
+  auto value_offsets = [&](const DeltaRows& rows, uint32_t (&off)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      off[r] = in ? rows.off(16 * w + 4 * gq + r, vstride) + col * sizeof(T) : kNowhere;
   };
 
-  if (nch > 0) {
-    offsets(delta_rows(sq, 0));
-    load_rows(0);
-    load_t(0);
-    load_p(0);
-  }
-  __syncthreads();
-  for (int c = 0; c < nch; ++c) {
-    const int next = c + 1 < nch ? c + 1 : c;    // the last chunk loads itself again
-    if (a.states) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
-    // K S and Q S; K^T for the update
-    v4f ks = zero, qs = zero;
+  if (walker) {
+    v4f S[OWN];
+    uint32_t soff[OWN][4], voff[4];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const Frag<3> f = lds_frag<3>(s_s, s, lane);
-      ks = mma<PI, 3>(operand<PI>(x.k[s][0], x.k[s][1]), f, ks);
-      if constexpr (OUT) qs = mma<PI, PO>(operand<PI>(x.q[s][0], x.q[s][1]), lead<PO>(f), qs);
-    }
-    float d[4];
+    for (int i = 0; i < OWN; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) d[r] = wide(x.v[r]) - x.gam[r] * ks[r];
-    lds_half<3>(s_x, w >> 1, lane, w & 1, split4<3>(d[0], d[1], d[2], d[3]));
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m) {
-      const int id = threadIdx.x + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
-      if (BLK >= 1 || tg < 16) {
-        typename Ty::Quad q[4];
-        Half<PI> cl[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = quad(x.kb[m][j]);
-        transpose4(q, cl);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 4 * dg + j;
-          lds_half<PI>(s_kt + (k >> 4) * kTileB, tg >> 3, (tg & 3) * 16 + (k & 15), (tg >> 2) & 1,
-                       cl[j]);
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int k = walk_entry(w * OWN + i, 4 * gq + r);
+        const bool own = w * OWN + i < NT && k < a.dk && in;
+        soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
+        S[i][r] = a.s0 ? buf_load<float>(delta_buf(a.s0 + bh * sdim), soff[i][r]) : 0.f;
       }
-    }
-    uint32_t ooff[4];
-    float ogam[4];
+    auto put_state = [&](float* to) {
+      const auto buf = delta_buf(to);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) ooff[r] = voff[r], ogam[r] = x.gam[r];
-    if (next == nch - 1) offsets(delta_rows(sq, next));
-    load_rows(next);
-    __syncthreads();
-    v4f u = mma<3, 3>(x.t[0], lds_frag<3>(s_x, 0, lane), zero);
-    if (w >= 2) u = mma<3, 3>(x.t[1], lds_frag<3>(s_x, 1, lane), u);
-    if constexpr (OUT) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
-    lds_half<3>(s_e, w >> 1, lane, w & 1,
-                split4<3>(x.end[0] * u[0], x.end[1] * u[1], x.end[2] * u[2], x.end[3] * u[3]));
-    load_t(next);
-    __syncthreads();
+      for (int i = 0; i < OWN; ++i)
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int tile = w * OWN + i;
-      if (tile < NT) {
-        S[i] *= x.last;
+        for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], S[i][r], 0.f);
+    };
+    auto share_state = [&] {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          S[i] = mma<PI, 3>(lds_frag<PI>(s_kt + tile * kTileB, s, lane), lds_frag<3>(s_e, s, lane),
-                            S[i]);
+      for (int i = 0; i < OWN; ++i) {
+        const int tile = w * OWN + i;
+        if (tile < NT)
+          lds_half<3>(s_s, tile >> 1, lane, tile & 1, split4<3>(S[i][0], S[i][1], S[i][2], S[i][3]));
       }
+    };
+    Frag<3> t[2];
+    uint32_t v[4];
+    v4f gam, end;
+    float last = 1.f;
+    auto load_v = [&](int c) {
+      if (c == endc) value_offsets(delta_rows(sq, c), voff);
+      const auto vbuf = delta_buf((const T*)a.v + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = raw1<T>(vbuf, voff[r]);
+      gam = *(const v4f*)&a.gates[(size_t)bh * a.chunks + c].gam[16 * w + 4 * gq];
+    };
+    auto load_t = [&](int c) {
+      const size_t ch = (size_t)bh * a.chunks + c;
+      const unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, false);
+      t[0] = mem_frag<3>(Tm, tri_frag(w, 0), lane);
+      t[1] = mem_frag<3>(Tm, tri_frag(w, second), lane);
+      end = *(const v4f*)&a.gates[ch].end[16 * w + 4 * gq];
+    };
+    auto load_last = [&](int c) {
+      last = a.gates[(size_t)bh * a.chunks + c].gam[kDeltaChunk - 1];
+    };
+    if (nch > 0) {
+      value_offsets(delta_rows(sq, 0), voff);
+      load_v(0);
+      load_t(0);
+      load_last(0);
     }
     share_state();
-    if constexpr (OUT) {
-      v4f pu = mma<PO, PO>(x.p[0], lds_frag<PO>(s_u, 0, lane), zero);
-      if (w >= 2) pu = mma<PO, PO>(x.p[1], lds_frag<PO>(s_u, 1, lane), pu);
-      const auto obuf = delta_buf((T*)a.o + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        buf_store(obuf, ooff[r], a.scale * fmaf(ogam[r], qs[r], pu[r]), T());
-    }
-    load_p(next);
     __syncthreads();
+    for (int c = 0; c < nch; ++c) {
+      const int next = c < endc ? c + 1 : c;
+      if (a.states) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
+      v4f ks = zero;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        ks = mma<PI, 3>(lds_frag<PI>(s_k, w * KS + s, lane), lds_frag<3>(s_s, s, lane), ks);
+      lds_half<3>(s_x, w >> 1, lane, w & 1,
+                  split4<3>(wide1<T>(v[0]) - gam[0] * ks[0], wide1<T>(v[1]) - gam[1] * ks[1],
+                            wide1<T>(v[2]) - gam[2] * ks[2], wide1<T>(v[3]) - gam[3] * ks[3]));
+      load_v(next);
+      __syncthreads();
+      v4f u = mma<3, 3>(t[0], lds_frag<3>(s_x, 0, lane), zero);
+      if (w >= 2) u = mma<3, 3>(t[1], lds_frag<3>(s_x, 1, lane), u);
+      lds_half<3>(s_e, w >> 1, lane, w & 1,
+                  split4<3>(end[0] * u[0], end[1] * u[1], end[2] * u[2], end[3] * u[3]));
+      if constexpr (OUT) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
+      load_t(next);
+      __syncthreads();
+      const unsigned char* kt = s_kt + (c & 1) * kCols;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) S[i] *= last;
+      load_last(next);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag<3> e = lds_frag<3>(s_e, s, lane);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+          if (w * OWN + i < NT)
+            S[i] = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), e, S[i]);
+      }
+      share_state();
+      __syncthreads();
+    }
+    if (a.s_last) put_state(a.s_last + bh * sdim);
+    if (a.states)
+      for (int c = nch; c < a.chunks; ++c) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
+  } else {
+    const int id = threadIdx.x - 256, dg = id % (DK / 8), tg = id / (DK / 8);
+    const bool block = tg < 16;      // a 4 x 8 block of K
+    Raw8<T, VEC> kb[4], q[OUT ? KS : 1];
+    Frag<PO> p[2];
+    v4f gam = zero;
+    uint32_t boff[4], qoff = 0, ooff[4];
+    auto block_offsets = [&](const DeltaRows& rows) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) boff[j] = block ? rows.off(4 * tg + j, kstride) : kNowhere;
+    };
+    auto load_k = [&](int c) {
+      if (c == endc) block_offsets(delta_rows(sq, c));
+      const auto kbuf = delta_buf((const T*)a.k + (delta_low(a, sq, b, c) * a.Hk + hk) * a.dk);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kb[j] = raw8<T, VEC>(kbuf, boff[j], 8 * dg, a.dk);
+    };
+    auto share_k = [&](int c, bool as_rows, bool as_cols) {
+      Half<PI> lo[4], hi[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) halves<PI>(kb[j], lo[j], hi[j]);
+      if (block && as_rows) lds_rows<PI, KS>(s_k, tg, dg, lo, hi);
+      if (block && as_cols) lds_cols<PI>(s_kt + (c & 1) * kCols, tg, dg, lo, hi);
+    };
+    auto load_q = [&](int c) {
+      if constexpr (OUT) {
+        if (c == endc) qoff = delta_rows(sq, c).off(16 * w + row, kstride);
+        const auto qbuf = delta_buf((const T*)a.q + (delta_low(a, sq, b, c) * a.Hk + hk) * a.dk);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) q[s] = raw8<T, VEC>(qbuf, qoff, 32 * s + 8 * gq, a.dk);
+      }
+    };
+    auto load_p = [&](int c) {
+      if constexpr (OUT) {
+        const size_t ch = (size_t)bh * a.chunks + c;
+        const unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
+        p[0] = mem_frag<PO>(Pm, tri_frag(w, 0), lane);
+        p[1] = mem_frag<PO>(Pm, tri_frag(w, second), lane);
+        gam = *(const v4f*)&a.gates[ch].gam[16 * w + 4 * gq];
+      }
+    };
+    if (nch > 0) {
+      block_offsets(delta_rows(sq, 0));
+      load_k(0);
+      qoff = delta_rows(sq, 0).off(16 * w + row, kstride);
+      value_offsets(delta_rows(sq, 0), ooff);
+      load_q(0);
+      load_p(0);
+      share_k(0, true, TWO);
+      if (TWO) load_k(endc > 0 ? 1 : 0);
+    }
+    __syncthreads();
+    for (int c = 0; c < nch; ++c) {
+      const int next = c < endc ? c + 1 : c;
+      v4f qs = zero;
+      if constexpr (OUT) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          Half<PI> lo, hi;
+          halves<PI>(q[s], lo, hi);
+          qs = mma<PI, PO>(join<PI>(lo, hi), lead<PO>(lds_frag<3>(s_s, s, lane)), qs);
+        }
+      }
+      load_q(next);
+      if (!TWO) {
+        share_k(c, false, true);
+        load_k(next);
+      }
+      __syncthreads();
+      __syncthreads();
+      share_k(c + 1, true, TWO);
+      if (TWO) load_k(c + 2 < nch ? c + 2 : endc);
+      if constexpr (OUT) {
+        v4f pu = mma<PO, PO>(p[0], lds_frag<PO>(s_u, 0, lane), zero);
+        if (w >= 2) pu = mma<PO, PO>(p[1], lds_frag<PO>(s_u, 1, lane), pu);
+        if (c == endc) value_offsets(delta_rows(sq, c), ooff);
+        const auto obuf = delta_buf((T*)a.o + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          buf_store(obuf, ooff[r], a.scale * fmaf(gam[r], qs[r], pu[r]), T());
+        load_p(next);
+      }
+      __syncthreads();
+    }
+    if (OUT && in)
+      for (int t = sq.n + (id >> 4); t < a.L; t += 16)
+        put1((T*)a.o + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
   }
-
-  if (a.s_last) put_state(a.s_last + bh * sdim);
-  if (a.states)
-    for (int c = nch; c < a.chunks; ++c) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
-  if (OUT && in)
-    for (int t = sq.n + (threadIdx.x >> 4); t < a.L; t += 16)
-      put1((T*)a.o + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
 }
-
 // ---------------------------------------------------------------------------- single steps
 // A wave per head and 16 columns: lane 4 i + c has rows i, i + 16, ... of four of them in registers.
 template <typename T, int RW>
@@ -586,16 +599,27 @@ void prep_mode(const DeltaArgs& a, bool vec, DeltaPrep mode, hipStream_t st) {
   else if (mode == kPrepStates) prep_t<T, kPrepStates>(a, vec, st);
   else prep_t<T, kPrepBackward>(a, vec, st);
 }
+template <typename T, int DK, bool VEC, bool OUT>
+hipError_t walk_one(const DeltaArgs& a, dim3 grid, hipStream_t st) {
+  constexpr int bytes = WalkLds<T, DK>::bytes;
+  static_assert(bytes <= 160 * 1024, "LDS of a CU");
+  const hipError_t e = hipFuncSetAttribute((const void*)k_delta_walk<T, DK, VEC, OUT>,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  k_delta_walk<T, DK, VEC, OUT><<<grid, 512, bytes, st>>>(a);
+  return hipGetLastError();
+}
 template <typename T>
-void walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
+hipError_t walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   // heads side by side in steps of 8: a head's columns then lie on one XCD and share its L2
   const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 15) / 16);
+  hipError_t e = hipSuccess;
   with_dk<T>(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;
     constexpr bool VEC = decltype(v)::value;
-    if (a.o) k_delta_walk<T, DK, VEC, true><<<grid, 256, 0, st>>>(a);
-    else k_delta_walk<T, DK, VEC, false><<<grid, 256, 0, st>>>(a);
+    e = a.o ? walk_one<T, DK, VEC, true>(a, grid, st) : walk_one<T, DK, VEC, false>(a, grid, st);
   });
+  return e;
 }
 template <typename T>
 void step_t(const DeltaArgs& a, hipStream_t st) {
@@ -619,9 +643,9 @@ DeltaArgs delta_args(const DeltaRequest& r) {
 }
 
 bool delta_vec(const DeltaRequest& r) {
-  const uintptr_t m = r.bf16 ? 7 : 15;
+  const uintptr_t m = 15;
   auto al = [](const void* p, uintptr_t mask) { return ((uintptr_t)p & mask) == 0; };
-  return r.dk % 4 == 0 && r.dv % 4 == 0 && al(r.q, m) && al(r.k, m) && al(r.v, m) &&
+  return r.dk % 8 == 0 && r.dv % 4 == 0 && al(r.q, m) && al(r.k, m) && al(r.v, m) &&
          al(r.dout, m) && al(r.states, 15);
 }
 
@@ -631,9 +655,7 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep 
   return hipGetLastError();
 }
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st) {
-  if (bf16) walk_t<uint16_t>(a, vec, st);
-  else walk_t<float>(a, vec, st);
-  return hipGetLastError();
+  return bf16 ? walk_t<uint16_t>(a, vec, st) : walk_t<float>(a, vec, st);
 }
 
 namespace {

@@ -104,7 +104,7 @@ constexpr size_t kDeltaTtBytes = (size_t)kDeltaFrags * 1024 * 3;
 DeltaArgs delta_args(const DeltaRequest& r);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
-// 4 elements at a time of everything that lies in rows of dk or dv.
+// 16 bytes at a time of everything that lies in rows of dk or dv.
 bool delta_vec(const DeltaRequest& r);
 
 }  // namespace wbmm

@@ -163,10 +163,10 @@ __global__ void __launch_bounds__(256) k_delta_walk_bwd(DeltaArgs a) {
     for (int m = 0; m < BLKS; ++m) {
       const int id = threadIdx.x + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
       if (BLK >= 1 || tg < 16) {
-        typename Ty::Quad qk[4], qq[4];
-        Half<PI> ck[4], cq[4];
+        Half<PI> qk[4], qq[4], ck[4], cq[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qk[j] = quad(x.kb[m][j]), qq[j] = quad(x.qb[m][j]);
+        for (int j = 0; j < 4; ++j)
+          qk[j] = to_half(quad(x.kb[m][j])), qq[j] = to_half(quad(x.qb[m][j]));
         transpose4(qk, ck);
         transpose4(qq, cq);
 #pragma unroll
@@ -486,10 +486,9 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
     for (int m = 0; m < kBlk; ++m) {
       const int id = (tid & 255) + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
       if (tg < 16) {
-        typename Ty::Quad q[4];
-        Half<PI> cl[4];
+        Half<PI> q[4], cl[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) q[r] = quad(mb[m][r]);
+        for (int r = 0; r < 4; ++r) q[r] = to_half(quad(mb[m][r]));
         transpose4(q, cl);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {

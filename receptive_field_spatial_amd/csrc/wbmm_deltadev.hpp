@@ -156,6 +156,17 @@ __device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, uint32_t off
 __device__ __forceinline__ float wide(float v) { return v; }
 __device__ __forceinline__ float wide(uint16_t v) { return bf2f(v); }
 
+// One entry as it is loaded, in a register of its own.
+template <typename T>
+__device__ __forceinline__ uint32_t raw1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  if constexpr (sizeof(T) == 2) return buf_load<uint16_t>(r, off);
+  return __float_as_uint(buf_load<float>(r, off));
+}
+template <typename T>
+__device__ __forceinline__ float wide1(uint32_t v) {
+  return __uint_as_float(sizeof(T) == 2 ? v << 16 : v);
+}
+
 // Entries i .. i + 3 of a row of `len` at `off` (kNowhere: a row of zeros). VEC: len is a multiple of 4.
 template <typename T, bool VEC>
 __device__ __forceinline__ typename DeltaType<T, VEC>::Raw raw4(__amdgpu_buffer_rsrc_t r, uint32_t off,
@@ -189,6 +200,38 @@ __device__ __forceinline__ Frag<P> operand(const R& a, const R& b) {
   return join<P>(to_half(quad(a)), to_half(quad(b)));
 }
 
+// Eight neighbouring entries. VEC: len is a multiple of 8.
+template <typename T, bool VEC>
+struct Raw8 {
+  typename DeltaType<T, VEC>::Raw a, b;
+};
+template <>
+struct Raw8<uint16_t, true> {
+  u32x4 a;
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T, VEC> raw8(__amdgpu_buffer_rsrc_t r, uint32_t off, int i, int len) {
+  Raw8<T, VEC> u;
+  if constexpr (sizeof(T) == 2 && VEC) {
+    u.a = __builtin_bit_cast(u32x4, buf_load<v4f>(r, i < len ? off + i * sizeof(T) : kNowhere));
+  } else {
+    u.a = raw4<T, VEC>(r, off, i, len);
+    u.b = raw4<T, VEC>(r, off, i + 4, len);
+  }
+  return u;
+}
+// Its two quads in parts.
+template <int P>
+__device__ __forceinline__ void halves(const Raw8<uint16_t, true>& u, Half<P>& lo, Half<P>& hi) {
+  lo.p[0] = u32x2{u.a[0], u.a[1]};
+  hi.p[0] = u32x2{u.a[2], u.a[3]};
+}
+template <int P, typename R>
+__device__ __forceinline__ void halves(const R& u, Half<P>& lo, Half<P>& hi) {
+  lo = to_half(quad(u.a));
+  hi = to_half(quad(u.b));
+}
+
 // Rows of one chunk of a sequence, as offsets from its lowest position.
 struct DeltaRows {
   int cnt, reverse;      // live steps
@@ -208,19 +251,54 @@ __device__ __forceinline__ size_t delta_low(const DeltaArgs& a, const DeltaSeq& 
   return (size_t)b * a.L + (s.reverse ? s.n - t0 - cnt : t0);
 }
 
-// A 4 x 4 block, rows r[0..3] of four entries, as its four columns of four.
-__device__ __forceinline__ void transpose4(const Half<1> (&r)[4], Half<1> (&c)[4]) {
+// A 4 x 4 block, rows r[0..3] of four entries, as its four columns of four, part by part.
+template <int P>
+__device__ __forceinline__ void transpose4(const Half<P> (&r)[4], Half<P> (&c)[4]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;   // upper or lower halves of two words
+      c[j].p[p] = u32x2{__builtin_amdgcn_perm(r[1].p[p][j >> 1], r[0].p[p][j >> 1], sel),
+                        __builtin_amdgcn_perm(r[3].p[p][j >> 1], r[2].p[p][j >> 1], sel)};
+    }
+}
+
+// Operands of the rows of a 64 x DK matrix in LDS. Rows as terms lie along DK (row tile i, terms 32 s ..)
+// at (i KS + s), in the order of the walk: slot j of lane group q is entry 32 s + 8 q + j, so that a lane's 8
+// are neighbours. A state's row tile t then has entry 32 (t / 2) + 8 q + 4 (t % 2) + r in row 4 q + r.
+__device__ __forceinline__ int walk_entry(int tile, int m) {   // of row m of a state's tile
+  return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3);
+}
+// 4 rows (steps 4 tg ..) of 8 entries (8 dg ..): as rows ...
+template <int P, int KS>
+__device__ __forceinline__ void lds_rows(unsigned char* to, int tg, int dg, const Half<P> (&lo)[4],
+                                         const Half<P> (&hi)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;   // the upper or lower halves of two words
-    const uint32_t a = j < 2 ? r[0].p[0].x : r[0].p[0].y, b = j < 2 ? r[1].p[0].x : r[1].p[0].y;
-    const uint32_t d = j < 2 ? r[2].p[0].x : r[2].p[0].y, e = j < 2 ? r[3].p[0].x : r[3].p[0].y;
-    c[j].p[0] = u32x2{__builtin_amdgcn_perm(b, a, sel), __builtin_amdgcn_perm(e, d, sel)};
+    const Frag<P> f = join<P>(lo[j], hi[j]);
+    unsigned char* at = to + ((tg >> 2) * KS + (dg >> 2)) * P * 1024 +
+                        ((dg & 3) * 16 + 4 * (tg & 3) + j) * 16;
+#pragma unroll
+    for (int p = 0; p < P; ++p) *(u32x4*)(at + p * 1024) = f.p[p];
   }
 }
-__device__ __forceinline__ void transpose4(const v4f (&r)[4], Half<3> (&c)[4]) {
+// ... and transposed, as operands of the state's row tiles over the steps; a tile's two frags lie
+// 2 P KB + 16 bytes from the next tile's, staggered over the banks.
+template <int P>
+constexpr int kTileBytes = 2 * P * 1024 + 16;
+template <int P>
+__device__ __forceinline__ void lds_cols(unsigned char* to, int tg, int dg, const Half<P> (&lo)[4],
+                                         const Half<P> (&hi)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = split4<3>(r[0][j], r[1][j], r[2][j], r[3][j]);
+  for (int e = 0; e < 2; ++e) {
+    Half<P> c[4];
+    transpose4(e ? hi : lo, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      lds_half<P>(to + (2 * (dg >> 2) + e) * kTileBytes<P>, tg >> 3,
+                  (tg & 3) * 16 + 4 * (dg & 3) + j, (tg >> 2) & 1, c[j]);
+  }
 }
 
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
