@@ -25,10 +25,139 @@ __device__ __forceinline__ float elem(const void* p, size_t i) { return load_f32
 // 16 x 16 tile (i, j), j <= i, of a triangular matrix in LDS: rows of 20 floats.
 __device__ __forceinline__ constexpr int lds_tile(int i, int j) { return (i * (i + 1) / 2 + j) * 320; }
 
+// A wave's share of a chunk: column tile W, all of whose loops are then of known length.
+template <typename T, DeltaPrep MODE>
+struct DeltaOwn {
+  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO;   // parts
+  static constexpr bool WANTP = MODE != kPrepStates;
+  unsigned char* s_all;
+  const double* s_cum;
+  const float* s_b;
+  int lane;
+  unsigned char *T_, *P_, *Tt_, *Pt_;
+
+  static __device__ __forceinline__ Frag<3> above(const v4f& x, const v4f& y) {
+    return join<3>(split4<3>(x[0], x[1], x[2], x[3]), split4<3>(y[0], y[1], y[2], y[3]));
+  }
+  template <int P>
+  __device__ __forceinline__ void put(unsigned char* to, int f, const Frag<P>& v) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) *(u32x4*)(to + (f * P + p) * 1024 + lane * 16) = v.p[p];
+  }
+
+  template <int W, int KS>
+  __device__ __forceinline__ void column() const {
+    constexpr int kRows = 4 * KS * PI * 1024, M = 4 - W;   // row tiles W .. 3
+    const int row = lane & 15, gq = lane >> 4;
+    float* s_n = (float*)s_all;
+    float* s_t = s_n + 10 * 320;
+    const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+    v4f kk[M], qk[M];      // K_i K_W^T and Q_i K_W^T
+#pragma unroll
+    for (int i = 0; i < M; ++i) kk[i] = qk[i] = zero;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const Frag<PI> kw = lds_frag<PI>(s_all, W * KS + s, lane);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        kk[i] = mma<PI, PI>(i == 0 ? kw : lds_frag<PI>(s_all, (W + i) * KS + s, lane), kw, kk[i]);
+        if (WANTP) qk[i] = mma<PI, PI>(lds_frag<PI>(s_all + kRows, (W + i) * KS + s, lane), kw, qk[i]);
+      }
+    }
+    const double cc = s_cum[16 * W + row];
+    const float bc = s_b[16 * W + row];
+    __syncthreads();                 // K and Q have been read: their place is N's and T's
+    v4f n, nt;                       // N_WW and its transpose
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int m = 4 * gq + r;
+        float d = (float)(s_cum[16 * (W + i) + m] - cc);
+        if (i == 0) d = m < row ? -d : d;            // the transpose's above the diagonal
+        const float dec = __builtin_amdgcn_exp2f(d), f = dec * kk[i][r];
+        const float bm = s_b[16 * (W + i) + m];
+        qk[i][r] = i > 0 || m >= row ? dec * qk[i][r] : 0.f;
+        if (i == 0) {
+          n[r] = m > row ? -(bm * f) : 0.f;
+          nt[r] = m < row ? -(bc * f) : 0.f;
+        } else {
+          s_n[lds_tile(W + i, W) + m * 20 + row] = -(bm * f);
+        }
+      }
+    v4f t, tt;                       // T_WW and its transpose
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float one = 4 * gq + r == row ? 1.f : 0.f;
+      t[r] = one + n[r];
+      tt[r] = one + nt[r];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {    // T (I + N^2), (I + N^4), (I + N^8)
+      const v4f n2 = mm16(nt, n, zero), n2t = mm16(n, nt, zero);
+      n = n2;
+      nt = n2t;
+      const v4f u = mm16(tt, n, t);
+      if (k < 2) tt = mm16(n, tt, tt);
+      t = u;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s_t[lds_tile(W, W) + (4 * gq + r) * 20 + row] = t[r];
+    __syncthreads();
+    v4f col[M];
+    col[0] = t;
+#pragma unroll
+    for (int i = 1; i < M; ++i) {
+      v4f y = zero;
+#pragma unroll
+      for (int k = 0; k < i; ++k)
+        y = mm16(*(const v4f*)&s_n[lds_tile(W + i, W + k) + row * 20 + 4 * gq], col[k], y);
+      col[i] = mm16(*(const v4f*)&s_t[lds_tile(W + i, W + i) + row * 20 + 4 * gq], y, zero);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) col[i] *= bc;
+    if (MODE == kPrepBackward) {     // results one above the other: operands of the transposes
+#pragma unroll
+      for (int s = W / 2; s < 2; ++s) {
+        const bool odd = 2 * s < W;  // the upper tile lies above the diagonal
+        put<3>(Tt_, trit_frag(W, s), above(odd ? zero : col[odd ? 0 : 2 * s - W], col[2 * s + 1 - W]));
+        put<3>(Pt_, trit_frag(W, s), above(odd ? zero : qk[odd ? 0 : 2 * s - W], qk[2 * s + 1 - W]));
+      }
+    }
+    __syncthreads();                 // N and the diagonal tiles have been read
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s_t[lds_tile(W + i, W) + (4 * gq + r) * 20 + row] = col[i][r];
+        if (MODE == kPrepForward) s_n[lds_tile(W + i, W) + (4 * gq + r) * 20 + row] = qk[i][r];
+      }
+    __syncthreads();
+    constexpr int PT = MODE == kPrepBackward ? PO : 3;
+    auto rows_of = [&](const float* m, int s, float (&v)[8]) {   // row tile W, terms 32 s ..
+      const v4f x = *(const v4f*)&m[lds_tile(W, 2 * s) + row * 20 + 4 * gq];
+      v4f y = zero;
+      if (2 * s + 1 <= W) y = *(const v4f*)&m[lds_tile(W, 2 * s + 1) + row * 20 + 4 * gq];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = x[j], v[4 + j] = y[j];
+    };
+#pragma unroll
+    for (int s = 0; 2 * s <= W; ++s) {
+      float v[8];
+      rows_of(s_t, s, v);
+      put<PT>(T_, tri_frag(W, s), split8<PT>(v));
+      if (MODE == kPrepForward) {
+        rows_of(s_n, s, v);
+        put<PO>(P_, tri_frag(W, s), split8<PO>(v));
+      }
+    }
+  }
+};
+
 template <typename T, int DK, bool VEC, DeltaPrep MODE>
-__global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
+__global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 128 ? 2 : 1)) k_delta_prep(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
-  constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32;
+  constexpr int PI = Ty::PI, KS = DK / 32;
   constexpr bool WANTP = MODE != kPrepStates;
   constexpr int kRows = 4 * KS * PI * 1024;               // K (or Q) as operands
   constexpr int kMats = 2 * 10 * 320 * 4;                 // N below the diagonal (then P), and T
@@ -36,8 +165,6 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
   __shared__ double s_cum[kDeltaChunk];
   __shared__ float s_b[kDeltaChunk];
   __shared__ __attribute__((aligned(16))) unsigned char s_all[kShared];
-  float* s_n = (float*)s_all;
-  float* s_t = s_n + 10 * 320;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, gq = lane >> 4;
   const int ch = blockIdx.x, bh = ch / a.chunks, c = ch - bh * a.chunks;
@@ -80,7 +207,7 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
       const float la = fminf(g, 0.f) - log1pf(e);
       const bool live = rows.live(lane);
       const float be = live ? 1.f / (1.f + expf(-x)) : 0.f;
-      double cum = live ? (double)(g == g ? la : g) : 0.0;
+      double cum = live ? (double)(g == g ? la : g) * 1.4426950408889634 : 0.0;   // base 2
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double o = __shfl_up(cum, d);
@@ -90,8 +217,8 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
       s_b[lane] = be;
       DeltaGates& gt = a.gates[ch];
       gt.cum[lane] = cum;
-      gt.gam[lane] = expf((float)cum);
-      gt.end[lane] = expf((float)(__shfl(cum, 63) - cum));
+      gt.gam[lane] = __builtin_amdgcn_exp2f((float)cum);
+      gt.end[lane] = __builtin_amdgcn_exp2f((float)(__shfl(cum, 63) - cum));
       gt.b[lane] = be;
       gt.na[lane] = live ? (g > 0.f ? e : 1.f) / (1.f + e) : 0.f;
     }
@@ -100,139 +227,15 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
   }
   __syncthreads();
 
-  // K_i K_w^T and Q_i K_w^T for row tiles i >= w
-  const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
-  v4f kk[4], qk[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) kk[i] = qk[i] = zero;
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const Frag<PI> kw = lds_frag<PI>(s_all, w * KS + s, lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i >= w) {
-        kk[i] = mma<PI, PI>(lds_frag<PI>(s_all, i * KS + s, lane), kw, kk[i]);
-        if (WANTP) qk[i] = mma<PI, PI>(lds_frag<PI>(s_all + kRows, i * KS + s, lane), kw, qk[i]);
-      }
-  }
-  __syncthreads();                   // K and Q have been read: their place is N's and T's
-
-  const double cc = s_cum[16 * w + row];
-  const float bc = s_b[16 * w + row];
-  v4f n, nt;        // N_ww and its transpose
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < w) continue;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int m = 4 * gq + r;
-      const double d = s_cum[16 * i + m] - cc;
-      const float dec = expf((float)(i == w && m < row ? -d : d));   // the transpose's above the diagonal
-      qk[i][r] = i > w || m >= row ? dec * qk[i][r] : 0.f;
-      const float f = dec * kk[i][r];
-      if (i == w) {
-        n[r] = m > row ? -(s_b[16 * i + m] * f) : 0.f;
-        nt[r] = m < row ? -(bc * f) : 0.f;
-      } else {
-        s_n[lds_tile(i, w) + m * 20 + row] = -(s_b[16 * i + m] * f);
-      }
-    }
-  }
-
-  v4f t, tt;        // T_ww and its transpose
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float one = 4 * gq + r == row ? 1.f : 0.f;
-    t[r] = one + n[r];
-    tt[r] = one + nt[r];
-  }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {      // T (I + N^2), (I + N^4), (I + N^8)
-    const v4f n2 = mm16(nt, n, zero), n2t = mm16(n, nt, zero);
-    n = n2;
-    nt = n2t;
-    const v4f u = mm16(tt, n, t), ut = mm16(n, tt, tt);
-    t = u;
-    tt = ut;
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) s_t[lds_tile(w, w) + (4 * gq + r) * 20 + row] = t[r];
-  __syncthreads();
-
-  v4f col[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) col[i] = zero;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < w) continue;
-    if (i == w) {
-      col[i] = t;
-      continue;
-    }
-    v4f y = zero;
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (k >= w && k < i) y = mm16(*(const v4f*)&s_n[lds_tile(i, k) + row * 20 + 4 * gq], col[k], y);
-    col[i] = mm16(*(const v4f*)&s_t[lds_tile(i, i) + row * 20 + 4 * gq], y, zero);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) col[i] *= bc;
-  if (MODE == kPrepBackward) {       // results one above the other: operands of the transposes
-    unsigned char *Tt = a.Tt + ch * kDeltaTtBytes, *Pt = a.Pt + ch * kDeltaTtBytes;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (2 * s + 1 >= w) {
-        const Frag<3> ft = join<3>(split4<3>(col[2 * s][0], col[2 * s][1], col[2 * s][2], col[2 * s][3]),
-                                   split4<3>(col[2 * s + 1][0], col[2 * s + 1][1], col[2 * s + 1][2],
-                                             col[2 * s + 1][3]));
-        const Frag<3> fp = join<3>(split4<3>(qk[2 * s][0], qk[2 * s][1], qk[2 * s][2], qk[2 * s][3]),
-                                   split4<3>(qk[2 * s + 1][0], qk[2 * s + 1][1], qk[2 * s + 1][2],
-                                             qk[2 * s + 1][3]));
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const int at = (trit_frag(w, s) * 3 + p) * 1024 + lane * 16;
-          *(u32x4*)(Tt + at) = ft.p[p];
-          *(u32x4*)(Pt + at) = fp.p[p];
-        }
-      }
-  }
-  __syncthreads();                   // N and the diagonal tiles have been read
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i >= w)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s_t[lds_tile(i, w) + (4 * gq + r) * 20 + row] = col[i][r];
-        if (MODE == kPrepForward) s_n[lds_tile(i, w) + (4 * gq + r) * 20 + row] = qk[i][r];
-      }
-  __syncthreads();
-  constexpr int PT = MODE == kPrepBackward ? PO : 3;
-  unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, MODE == kPrepBackward);
-  unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
-  auto rows_of = [&](const float* m, int s, float (&v)[8]) {   // row tile w, terms 32 s ..
-    const v4f x = *(const v4f*)&m[lds_tile(w, 2 * s) + row * 20 + 4 * gq];
-    v4f y = zero;
-    if (2 * s + 1 <= w) y = *(const v4f*)&m[lds_tile(w, 2 * s + 1) + row * 20 + 4 * gq];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = x[j], v[4 + j] = y[j];
-  };
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (2 * s <= w) {
-      float v[8];
-      rows_of(s_t, s, v);
-      const Frag<PT> f = split8<PT>(v);
-#pragma unroll
-      for (int p = 0; p < PT; ++p)
-        *(u32x4*)(Tm + (tri_frag(w, s) * PT + p) * 1024 + lane * 16) = f.p[p];
-      if (MODE == kPrepForward) {
-        rows_of(s_n, s, v);
-        const Frag<PO> fp = split8<PO>(v);
-#pragma unroll
-        for (int p = 0; p < PO; ++p)
-          *(u32x4*)(Pm + (tri_frag(w, s) * PO + p) * 1024 + lane * 16) = fp.p[p];
-      }
-    }
+  DeltaOwn<T, MODE> own{s_all, s_cum, s_b, lane};
+  own.T_ = a.T + ch * delta_t_bytes(PI == 1, MODE == kPrepBackward);
+  own.P_ = a.P + ch * delta_p_bytes(PI == 1);
+  own.Tt_ = a.Tt + ch * kDeltaTtBytes;
+  own.Pt_ = a.Pt + ch * kDeltaTtBytes;
+  if (w == 0) own.template column<0, KS>();
+  else if (w == 1) own.template column<1, KS>();
+  else if (w == 2) own.template column<2, KS>();
+  else own.template column<3, KS>();
 }
 
 // ---------------------------------------------------------------------------- the walk

@@ -65,7 +65,7 @@ size_t delta_backward_workspace(int64_t B, int64_t L, int H, int dk, int dv, boo
 hipError_t launch_delta_forward(const DeltaRequest& r, hipStream_t st);
 hipError_t launch_delta_backward(const DeltaRequest& r, hipStream_t st);
 
-// The gates of a chunk: log y (fp64), y, y_C / y, b and 1 - a.
+// The gates of a chunk: log2 y (fp64), y, y_C / y, b and 1 - a.
 struct DeltaGates {
   double cum[kDeltaChunk];
   float gam[kDeltaChunk], end[kDeltaChunk], b[kDeltaChunk], na[kDeltaChunk];

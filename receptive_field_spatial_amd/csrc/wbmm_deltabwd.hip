@@ -8,215 +8,299 @@ namespace wbmm {
 namespace {
 
 // ---------------------------------------------------------------------------- the walk back
-// As the forward's walk: one workgroup per head and 16 columns of dv, wave w with row tile w of the 64
-// steps and OWN row tiles of D. Hand-overs per chunk: D, then dU (with diag(y) G beside it), then
-// diag(y) R. D after each chunk and R stay in the workspace for k_delta_grads.
+// As the forward's walk: one workgroup per head and 16 columns of dv, four walkers and four helpers.
+//        walkers                                         helpers
+//   A    dU = P^T G + diag(y_C / y) K D                  M = Q^T diag(y) G
+//   B    R = T^T dU (= dv)                               P^T G of the next chunk
+//   C    D = y_C D + M - K^T diag(y) R                   K, K^T, Q^T and G of the next chunk
+// D after each chunk and R stay in the workspace for k_delta_grads.
+template <typename T, int DK>
+struct BackLds {
+  static constexpr int PI = DeltaType<T, true>::PI, KS = DK / 32, NT = DK / 16;
+  static constexpr int d = 0;                              // D
+  static constexpr int x = d + KS * 3 * 1024;              // dU
+  static constexpr int r = x + 2 * 3 * 1024;               // -diag(y) R
+  static constexpr int g = r + 2 * 3 * 1024;               // diag(y) G
+  static constexpr int o = g + 2 * 3 * 1024;               // do
+  static constexpr int m = o + 2 * PI * 1024;              // M, as results lie
+  static constexpr int pg = m + NT * 1024;                 // P^T G, as results lie
+  static constexpr int qt = pg + 4 * 1024;                 // Q^T
+  static constexpr int cols = NT * kTileBytes<PI>;
+  static constexpr int kt = qt + cols;                     // K^T, of two chunks where they fit
+  static constexpr int rows = 4 * KS * PI * 1024;
+  // fp32 with 96 < dk: the walkers load K's rows themselves
+  static constexpr bool direct = kt + cols + rows > 160 * 1024;
+  static constexpr bool two = !direct && kt + 2 * cols + rows <= 160 * 1024;
+  static constexpr int k = kt + (two ? 2 : 1) * cols;      // K
+  static constexpr int bytes = k + (direct ? 0 : rows);
+};
+
 template <typename T, int DK, bool VEC>
-__global__ void __launch_bounds__(256) k_delta_walk_bwd(DeltaArgs a) {
+__global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
-  constexpr int PI = Ty::PI;
-  constexpr int KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4, BLK = 64 * DK / 16 / 256;
-  constexpr int BLKS = BLK < 1 ? 1 : BLK;
-  constexpr int kTileB = 2 * PI * 1024 + 16;
-  __shared__ __attribute__((aligned(16))) unsigned char s_d[KS * 3 * 1024];
-  __shared__ __attribute__((aligned(16))) unsigned char s_o[2 * PI * 1024];  // do
-  __shared__ __attribute__((aligned(16))) unsigned char s_x[2 * 3 * 1024];   // dU
-  __shared__ __attribute__((aligned(16))) unsigned char s_g[2 * 3 * 1024];   // diag(y) G
-  __shared__ __attribute__((aligned(16))) unsigned char s_r[2 * 3 * 1024];   // -diag(y) R
-  __shared__ __attribute__((aligned(16))) unsigned char s_kt[NT * kTileB];
-  __shared__ __attribute__((aligned(16))) unsigned char s_qt[NT * kTileB];
+  using Lds = BackLds<T, DK>;
+  constexpr int PI = Ty::PI, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
+  constexpr bool TWO = Lds::two, DIRECT = Lds::direct;
+  extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   const int bh = blockIdx.x;
   if (bh >= a.B * a.H) return;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = lane & 15, gq = lane >> 4;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wid & 3, row = lane & 15, gq = lane >> 4;
+  const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
   const int col = blockIdx.y * 16 + row;
   const bool in = col < a.dv;
-  const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk;
+  const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
   const uint32_t kstride = (uint32_t)(a.Hk * a.dk) * sizeof(T), vstride = (uint32_t)(a.H * a.dv) * sizeof(T);
-
   const size_t sdim = (size_t)a.dk * a.dv;
-  v4f D[OWN];
-  uint32_t soff[OWN][4], roff[4];
+  // frags of row tiles 2 and 3 have terms from 32 on only (loaded twice, as in the forward)
+  const int first = w >= 2 ? 1 : 0;
+  auto value_offsets = [&](const DeltaRows& rows, uint32_t (&off)[4]) {
 #pragma unroll
-  for (int i = 0; i < OWN; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int k = 16 * (w * OWN + i) + 4 * gq + r;
-      const bool own = w * OWN + i < NT && k < a.dk && in;
-      soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
-      D[i][r] = a.ds_last ? buf_load<float>(delta_buf(a.ds_last + bh * sdim), soff[i][r]) : 0.f;
-    }
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    roff[r] = in ? (uint32_t)((16 * w + 4 * gq + r) * a.dv + col) * 4 : kNowhere;
-  auto put_state = [&](float* to) {
-    const auto buf = delta_buf(to);
+    for (int r = 0; r < 4; ++r)
+      off[r] = in ? rows.off(16 * w + 4 * gq + r, vstride) + col * sizeof(T) : kNowhere;
+  };
+
+  if (walker) {
+    v4f D[OWN];
+    uint32_t soff[OWN][4], roff[4], voff[4], koff = 0;
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], D[i][r], 0.f);
-  };
-  auto share_state = [&] {
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int tile = w * OWN + i;
-      if (tile < NT)
-        lds_half<3>(s_d, tile >> 1, lane, tile & 1, split4<3>(D[i][0], D[i][1], D[i][2], D[i][3]));
-    }
-  };
-  share_state();
-
-  struct Chunk {
-    typename Ty::Raw k[KS][2], kb[BLKS][4], qb[BLKS][4];
-    Frag<3> t[2], p[2];
-    T g[4];
-    float gam[4], end[4], last;
-  } x;
-  uint32_t koff = 0, boff[BLKS][4], voff[4];
-  auto offsets = [&](const DeltaRows& rows) {
-    koff = rows.off(16 * w + row, kstride);
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        boff[m][j] = rows.off(4 * ((threadIdx.x + 256 * m) / (DK / 4)) + j, kstride);
+      for (int r = 0; r < 4; ++r) {
+        const int k = walk_entry(w * OWN + i, 4 * gq + r);
+        const bool own = w * OWN + i < NT && k < a.dk && in;
+        soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
+        D[i][r] = a.ds_last ? buf_load<float>(delta_buf(a.ds_last + bh * sdim), soff[i][r]) : 0.f;
+      }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      voff[r] = in ? rows.off(16 * w + 4 * gq + r, vstride) + col * sizeof(T) : kNowhere;
-  };
-  // frags of row tiles 2 and 3 have terms from 32 on only (loaded twice, as in the forward)
-  const int first = w >= 2 ? 1 : 0;
-  auto load_rows = [&](int c) {
-    const size_t low = delta_low(a, sq, b, c), ch = (size_t)bh * a.chunks + c;
-    const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
-    const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
-    const auto obuf = delta_buf((const T*)a.dout + (low * a.H + h) * a.dv);
+      roff[r] = in ? (uint32_t)((16 * w + 4 * gq + r) * a.dv + col) * 4 : kNowhere;
+    auto put_state = [&](float* to) {
+      const auto buf = delta_buf(to);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x.g[r] = buf_load<T>(obuf, voff[r]);
-    const unsigned char* Pm = a.Pt + ch * kDeltaTtBytes;
-    x.p[0] = mem_frag<3>(Pm, trit_frag(w, first), lane);
-    x.p[1] = mem_frag<3>(Pm, trit_frag(w, 1), lane);
-    const DeltaGates& gt = a.gates[ch];
-    *(v4f*)x.gam = *(const v4f*)&gt.gam[16 * w + 4 * gq];
-    *(v4f*)x.end = *(const v4f*)&gt.end[16 * w + 4 * gq];
+      for (int i = 0; i < OWN; ++i)
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+        for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], D[i][r], 0.f);
+    };
+    auto share_state = [&] {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        x.k[s][e] = raw4<T, VEC>(kbuf, koff, 32 * s + 16 * e + 4 * gq, a.dk);
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = 4 * ((threadIdx.x + 256 * m) % (DK / 4));
-        x.kb[m][j] = raw4<T, VEC>(kbuf, boff[m][j], at, a.dk);
-        x.qb[m][j] = raw4<T, VEC>(qbuf, boff[m][j], at, a.dk);
+      for (int i = 0; i < OWN; ++i) {
+        const int tile = w * OWN + i;
+        if (tile < NT)
+          lds_half<3>(sm + Lds::d, tile >> 1, lane, tile & 1,
+                      split4<3>(D[i][0], D[i][1], D[i][2], D[i][3]));
       }
-  };
-  auto load_t = [&](int c) {
-    const unsigned char* Tm = a.Tt + ((size_t)bh * a.chunks + c) * kDeltaTtBytes;
-    x.t[0] = mem_frag<3>(Tm, trit_frag(w, first), lane);
-    x.t[1] = mem_frag<3>(Tm, trit_frag(w, 1), lane);
-  };
-  auto load_last = [&](int c) {
-    x.last = a.gates[(size_t)bh * a.chunks + c].gam[kDeltaChunk - 1];
-  };
-  auto share_do = [&] {
-    lds_half<PI>(s_o, w >> 1, lane, w & 1,
-                 split4<PI>(wide(x.g[0]), wide(x.g[1]), wide(x.g[2]), wide(x.g[3])));
-  };
-
-  if (nch > 0) {
-    offsets(delta_rows(sq, nch - 1));
-    load_rows(nch - 1);
-    load_t(nch - 1);
-    load_last(nch - 1);
-    share_do();
-  }
-  __syncthreads();
-  for (int c = nch - 1; c >= 0; --c) {
-    const size_t ch = (size_t)bh * a.chunks + c;
-    const int next = c > 0 ? c - 1 : 0;         // the last one loads itself again
-    put_state(a.D + ch * sdim);
-    v4f kd = zero, pg = zero;
+    };
+    Frag<3> t[2];
+    Raw8<T, VEC> k[DIRECT ? KS : 1];
+    v4f gam = zero, end = zero;
+    float last = 1.f;
+    auto load_k = [&](int c) {
+      if constexpr (DIRECT) {
+        if (c == endc || c == endc - 1) koff = delta_rows(sq, c).off(16 * w + row, kstride);
+        const auto kbuf = delta_buf((const T*)a.k + (delta_low(a, sq, b, c) * a.Hk + hk) * a.dk);
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      kd = mma<PI, 3>(operand<PI>(x.k[s][0], x.k[s][1]), lds_frag<3>(s_d, s, lane), kd);
-    if (w < 2) pg = mma<3, PI>(x.p[0], lds_frag<PI>(s_o, 0, lane), pg);
-    pg = mma<3, PI>(x.p[1], lds_frag<PI>(s_o, 1, lane), pg);
-    lds_half<3>(s_x, w >> 1, lane, w & 1,
-                split4<3>(fmaf(a.scale, pg[0], x.end[0] * kd[0]), fmaf(a.scale, pg[1], x.end[1] * kd[1]),
-                          fmaf(a.scale, pg[2], x.end[2] * kd[2]), fmaf(a.scale, pg[3], x.end[3] * kd[3])));
-    float gam[4], gy[4];
-    uint32_t voff0[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      gam[r] = x.gam[r];
-      gy[r] = a.scale * gam[r] * wide(x.g[r]);
-      voff0[r] = voff[r];
-    }
-    lds_half<3>(s_g, w >> 1, lane, w & 1, split4<3>(gy[0], gy[1], gy[2], gy[3]));
-#pragma unroll
-    for (int m = 0; m < BLKS; ++m) {
-      const int id = threadIdx.x + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
-      if (BLK >= 1 || tg < 16) {
-        Half<PI> qk[4], qq[4], ck[4], cq[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qk[j] = to_half(quad(x.kb[m][j])), qq[j] = to_half(quad(x.qb[m][j]));
-        transpose4(qk, ck);
-        transpose4(qq, cq);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 4 * dg + j, at = (k >> 4) * kTileB, ln = (tg & 3) * 16 + (k & 15);
-          lds_half<PI>(s_kt + at, tg >> 3, ln, (tg >> 2) & 1, ck[j]);
-          lds_half<PI>(s_qt + at, tg >> 3, ln, (tg >> 2) & 1, cq[j]);
-        }
+        for (int s = 0; s < KS; ++s) k[s] = raw8<T, VEC>(kbuf, koff, 32 * s + 8 * gq, a.dk);
       }
-    }
-    if (c == nch - 1) offsets(delta_rows(sq, next));
-    load_rows(next);
-    __syncthreads();
-    v4f rr = zero;
-    if (w < 2) rr = mma<3, 3>(x.t[0], lds_frag<3>(s_x, 0, lane), rr);
-    rr = mma<3, 3>(x.t[1], lds_frag<3>(s_x, 1, lane), rr);
-    lds_half<3>(s_r, w >> 1, lane, w & 1,
-                split4<3>(-gam[0] * rr[0], -gam[1] * rr[1], -gam[2] * rr[2], -gam[3] * rr[3]));
-    load_t(next);
-    const auto rbuf = delta_buf(a.R + ch * kDeltaChunk * a.dv);
-    const auto vbuf = delta_buf((T*)a.dval + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      buf_store(rbuf, roff[r], rr[r], 0.f);
-      buf_store(vbuf, voff0[r], rr[r], T());
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-      const int tile = w * OWN + i;
-      if (tile < NT) {
-        D[i] *= x.last;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          D[i] = mma<PI, 3>(lds_frag<PI>(s_qt + tile * kTileB, s, lane), lds_frag<3>(s_g, s, lane),
-                            D[i]);
-          D[i] = mma<PI, 3>(lds_frag<PI>(s_kt + tile * kTileB, s, lane), lds_frag<3>(s_r, s, lane),
-                            D[i]);
-        }
-      }
+      end = *(const v4f*)&a.gates[(size_t)bh * a.chunks + c].end[16 * w + 4 * gq];
+    };
+    auto load_t = [&](int c) {
+      const size_t ch = (size_t)bh * a.chunks + c;
+      const unsigned char* Tm = a.Tt + ch * kDeltaTtBytes;
+      t[0] = mem_frag<3>(Tm, trit_frag(w, first), lane);
+      t[1] = mem_frag<3>(Tm, trit_frag(w, 1), lane);
+      gam = *(const v4f*)&a.gates[ch].gam[16 * w + 4 * gq];
+    };
+    auto load_last = [&](int c) {
+      last = a.gates[(size_t)bh * a.chunks + c].gam[kDeltaChunk - 1];
+    };
+    if (nch > 0) {
+      value_offsets(delta_rows(sq, endc), voff);
+      load_k(endc);
+      load_t(endc);
+      load_last(endc);
     }
     share_state();
-    load_last(next);
-    share_do();
     __syncthreads();
+    __syncthreads();
+    __syncthreads();
+    for (int c = endc; c >= 0; --c) {
+      const size_t ch = (size_t)bh * a.chunks + c;
+      const int next = c > 0 ? c - 1 : 0;
+      put_state(a.D + ch * sdim);
+      v4f kd = zero;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        Frag<PI> f;
+        if constexpr (DIRECT) {
+          Half<PI> lo, hi;
+          halves<PI>(k[s], lo, hi);
+          f = join<PI>(lo, hi);
+        } else {
+          f = lds_frag<PI>(sm + Lds::k, w * KS + s, lane);
+        }
+        kd = mma<PI, 3>(f, lds_frag<3>(sm + Lds::d, s, lane), kd);
+      }
+      const v4f pg = *(const v4f*)(sm + Lds::pg + w * 1024 + lane * 16);
+      lds_half<3>(sm + Lds::x, w >> 1, lane, w & 1,
+                  split4<3>(fmaf(end[0], kd[0], pg[0]), fmaf(end[1], kd[1], pg[1]),
+                            fmaf(end[2], kd[2], pg[2]), fmaf(end[3], kd[3], pg[3])));
+      load_k(next);
+      __syncthreads();
+      v4f rr = zero;
+      if (w < 2) rr = mma<3, 3>(t[0], lds_frag<3>(sm + Lds::x, 0, lane), rr);
+      rr = mma<3, 3>(t[1], lds_frag<3>(sm + Lds::x, 1, lane), rr);
+      lds_half<3>(sm + Lds::r, w >> 1, lane, w & 1,
+                  split4<3>(-gam[0] * rr[0], -gam[1] * rr[1], -gam[2] * rr[2], -gam[3] * rr[3]));
+      load_t(next);
+      const auto rbuf = delta_buf(a.R + ch * kDeltaChunk * a.dv);
+      const auto vbuf = delta_buf((T*)a.dval + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        buf_store(rbuf, roff[r], rr[r], 0.f);
+        buf_store(vbuf, voff[r], rr[r], T());
+      }
+      if (c == endc) value_offsets(delta_rows(sq, next), voff);
+      __syncthreads();
+      const unsigned char* kt = sm + Lds::kt + (TWO ? c & 1 : 0) * Lds::cols;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i)
+        if (w * OWN + i < NT)
+          D[i] = last * D[i] + *(const v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16);
+      load_last(next);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag<3> f = lds_frag<3>(sm + Lds::r, s, lane);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+          if (w * OWN + i < NT)
+            D[i] = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), f, D[i]);
+      }
+      share_state();
+      __syncthreads();
+    }
+    if (a.ds0) put_state(a.ds0 + bh * sdim);
+  } else {
+    const int id = threadIdx.x - 256, dg = id % (DK / 8), tg = id / (DK / 8);
+    const bool block = tg < 16;      // a 4 x 8 block of K and of Q
+    Raw8<T, VEC> kb[4], qb[4];
+    Frag<3> p[2];
+    uint32_t g[4], g2[4];            // do of the next chunk and of the one after
+    v4f gam = zero;
+    uint32_t boff[4], goff[4];
+    auto load_kq = [&](int c) {
+      if (c == endc || c == endc - 1) {
+        const DeltaRows rows = delta_rows(sq, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) boff[j] = block ? rows.off(4 * tg + j, kstride) : kNowhere;
+      }
+      const size_t at = (delta_low(a, sq, b, c) * a.Hk + hk) * a.dk;
+      const auto kbuf = delta_buf((const T*)a.k + at), qbuf = delta_buf((const T*)a.q + at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kb[j] = raw8<T, VEC>(kbuf, boff[j], 8 * dg, a.dk);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qb[j] = raw8<T, VEC>(qbuf, boff[j], 8 * dg, a.dk);
+      gam = *(const v4f*)&a.gates[(size_t)bh * a.chunks + c].gam[16 * w + 4 * gq];
+    };
+    auto load_g = [&](int c, uint32_t (&to)[4]) {
+      if (c == endc || c == endc - 1) value_offsets(delta_rows(sq, c), goff);
+      const auto obuf = delta_buf((const T*)a.dout + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[r] = raw1<T>(obuf, goff[r]);
+    };
+    auto load_p = [&](int c) {
+      const unsigned char* Pm = a.Pt + ((size_t)bh * a.chunks + c) * kDeltaTtBytes;
+      p[0] = mem_frag<3>(Pm, trit_frag(w, first), lane);
+      p[1] = mem_frag<3>(Pm, trit_frag(w, 1), lane);
+    };
+    auto share_k = [&](int c, bool as_rows, bool as_cols) {
+      Half<PI> lo[4], hi[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) halves<PI>(kb[j], lo[j], hi[j]);
+      if (block && as_rows && !DIRECT) lds_rows<PI, KS>(sm + Lds::k, tg, dg, lo, hi);
+      if (block && as_cols) lds_cols<PI>(sm + Lds::kt + (TWO ? c & 1 : 0) * Lds::cols, tg, dg, lo, hi);
+    };
+    auto share_q = [&] {
+      Half<PI> lo[4], hi[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) halves<PI>(qb[j], lo[j], hi[j]);
+      if (block) lds_cols<PI>(sm + Lds::qt, tg, dg, lo, hi);
+    };
+    auto share_g = [&] {             // diag(y) G
+      lds_half<3>(sm + Lds::g, w >> 1, lane, w & 1,
+                  split4<3>(a.scale * gam[0] * wide1<T>(g[0]), a.scale * gam[1] * wide1<T>(g[1]),
+                            a.scale * gam[2] * wide1<T>(g[2]), a.scale * gam[3] * wide1<T>(g[3])));
+    };
+    auto share_o = [&](const uint32_t (&o)[4]) {
+      lds_half<PI>(sm + Lds::o, w >> 1, lane, w & 1,
+                   split4<PI>(wide1<T>(o[0]), wide1<T>(o[1]), wide1<T>(o[2]), wide1<T>(o[3])));
+    };
+    auto form_pg = [&] {
+      v4f pg = zero;
+      if (w < 2) pg = mma<3, PI>(p[0], lds_frag<PI>(sm + Lds::o, 0, lane), pg);
+      pg = mma<3, PI>(p[1], lds_frag<PI>(sm + Lds::o, 1, lane), pg);
+      *(v4f*)(sm + Lds::pg + w * 1024 + lane * 16) = pg * a.scale;
+    };
+    auto back = [&](int c, int by) { return c >= by ? c - by : 0; };
+    if (nch > 0) {
+      load_kq(endc);
+      load_g(endc, g);
+      load_p(endc);
+      load_g(back(endc, 1), g2);
+      share_k(endc, true, TWO);
+      share_q();
+      share_g();
+      share_o(g);
+    }
+    __syncthreads();
+    if (nch > 0) form_pg();
+    __syncthreads();
+    if (nch > 0) {
+      share_o(g2);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[r] = g2[r];
+      load_p(back(endc, 1));
+      load_g(back(endc, 2), g2);
+      if (TWO) load_kq(back(endc, 1));
+    }
+    __syncthreads();
+    for (int c = endc; c >= 0; --c) {
+      // M: its row tiles over the four waves
+#pragma unroll
+      for (int i = 0; i < OWN; ++i)
+        if (w * OWN + i < NT) {
+          v4f m = zero;
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            m = mma<PI, 3>(lds_frag<PI>(sm + Lds::qt + (w * OWN + i) * kTileBytes<PI>, s, lane),
+                           lds_frag<3>(sm + Lds::g, s, lane), m);
+          *(v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16) = m;
+        }
+      if (!TWO) {
+        share_k(c, false, true);
+        load_kq(back(c, 1));
+      }
+      __syncthreads();
+      form_pg();
+      load_p(back(c, 2));
+      __syncthreads();
+      share_k(c - 1, true, TWO);
+      share_q();
+      share_g();
+      if (TWO) load_kq(back(c, 2));
+      share_o(g2);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[r] = g2[r];
+      load_g(back(c, 3), g2);
+      __syncthreads();
+    }
+    if (in)
+      for (int t = sq.n + (id >> 4); t < a.L; t += 16)
+        put1((T*)a.dval + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
   }
-  if (a.ds0) put_state(a.ds0 + bh * sdim);
-  if (in)
-    for (int t = sq.n + (threadIdx.x >> 4); t < a.L; t += 16)
-      put1((T*)a.dval + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
 }
 
 // ---------------------------------------------------------------------------- chunks on their own
@@ -476,7 +560,7 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
           for (int r = 0; r < 4; ++r) {
             const int m = 16 * w + 4 * gq + r, nn = 16 * i + row;
             const bool low_ = hf == 0 ? nn <= m : nn < m;
-            const float dec = expf(low_ ? (float)(cm[r] - cc) : 0.f);
+            const float dec = __builtin_amdgcn_exp2f(low_ ? (float)(cm[r] - cc) : 0.f);
             mat[hf * 64 * 68 + m * 68 + nn] = low_ ? one * dec * pn[i][r] : 0.f;
           }
         }
@@ -624,7 +708,12 @@ hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   with_dk(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;
     constexpr bool VEC = decltype(v)::value;
-    k_delta_walk_bwd<T, DK, VEC><<<grid, 256, 0, st>>>(a);
+    constexpr int back = BackLds<T, DK>::bytes;
+    static_assert(back <= 160 * 1024, "LDS of a CU");
+    e = hipFuncSetAttribute((const void*)k_delta_walk_bwd<T, DK, VEC>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, back);
+    if (e != hipSuccess) return;
+    k_delta_walk_bwd<T, DK, VEC><<<grid, 512, back, st>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return;
     constexpr int bytes = GradLds<T, DK, VEC>::bytes;
