@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
         const Frag<PI> f = join<PI>(lo, hi);
 #pragma unroll
         for (int p = 0; p < PI; ++p)
-          *(u32x4*)(to + ((w * KS + s) * PI + p) * 1024 + lane * 16) = f.p[p];
+          *(u32x4*)(to + ((w * KS + s) * PI + p) * 1024 + slot(lane) * 16) = f.p[p];
       }
     };
     // gates, by the wave that has the fewest products below: lane = step. log a = min(g, 0) - log(1 +
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 // them, one chunk ahead, and form the outputs. Three hand-overs per chunk, each through LDS:
 //        walkers                                    helpers
 //   A    X = V - diag(y) K S                        Q S
-//   B    U = T X
-//   C    S = y_C S + K^T diag(y_C / y) U            o = scale (diag(y) Q S + P U); K of the next chunk
+//   B    U = T X                                    K of the next chunk
+//   C    S = y_C S + K^T diag(y_C / y) U            o = scale (diag(y) Q S + P U)
 // Loads are issued a chunk before their use, right after the last use of their registers.
 // LDS of a workgroup. Two chunks' K^T, where they fit (all but fp32 with 96 < dk): the next one is then
 // written while this one is read, and K is loaded a whole chunk ahead.
@@ -353,34 +353,41 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
     for (int c = 0; c < nch; ++c) {
       const int next = c < endc ? c + 1 : c;
       if (a.states) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
-      v4f ks = zero;
+      v4f ks = zero, kp[KS];         // a chain of products for each 32 terms
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        ks = mma<PI, 3>(lds_frag<PI>(s_k, w * KS + s, lane), lds_frag<3>(s_s, s, lane), ks);
+        kp[s] = mma<PI, 3>(lds_frag<PI>(s_k, w * KS + s, lane), lds_frag<3>(s_s, s, lane), zero);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) ks += kp[s];
       lds_half<3>(s_x, w >> 1, lane, w & 1,
                   split4<3>(wide1<T>(v[0]) - gam[0] * ks[0], wide1<T>(v[1]) - gam[1] * ks[1],
                             wide1<T>(v[2]) - gam[2] * ks[2], wide1<T>(v[3]) - gam[3] * ks[3]));
       load_v(next);
       __syncthreads();
-      v4f u = mma<3, 3>(t[0], lds_frag<3>(s_x, 0, lane), zero);
-      if (w >= 2) u = mma<3, 3>(t[1], lds_frag<3>(s_x, 1, lane), u);
+      v4f u = mma_short(t[0], lds_frag<3>(s_x, 0, lane));
+      if (w >= 2) u += mma_short(t[1], lds_frag<3>(s_x, 1, lane));
       lds_half<3>(s_e, w >> 1, lane, w & 1,
                   split4<3>(end[0] * u[0], end[1] * u[1], end[2] * u[2], end[3] * u[3]));
       if constexpr (OUT) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
       load_t(next);
       __syncthreads();
       const unsigned char* kt = s_kt + (c & 1) * kCols;
+      v4f more[OWN];
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) S[i] *= last;
+      for (int i = 0; i < OWN; ++i) S[i] *= last, more[i] = zero;
       load_last(next);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const Frag<3> e = lds_frag<3>(s_e, s, lane);
 #pragma unroll
         for (int i = 0; i < OWN; ++i)
-          if (w * OWN + i < NT)
-            S[i] = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), e, S[i]);
+          if (w * OWN + i < NT) {
+            v4f& to = s ? more[i] : S[i];
+            to = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), e, to);
+          }
       }
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) S[i] += more[i];
       share_state();
       __syncthreads();
     }
@@ -456,9 +463,9 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
         load_k(next);
       }
       __syncthreads();
-      __syncthreads();
-      share_k(c + 1, true, TWO);
+      share_k(c + 1, true, TWO);     // this chunk's rows have been read
       if (TWO) load_k(c + 2 < nch ? c + 2 : endc);
+      __syncthreads();
       if constexpr (OUT) {
         v4f pu = mma<PO, PO>(p[0], lds_frag<PO>(s_u, 0, lane), zero);
         if (w >= 2) pu = mma<PO, PO>(p[1], lds_frag<PO>(s_u, 1, lane), pu);

@@ -11,8 +11,8 @@ namespace {
 // As the forward's walk: one workgroup per head and 16 columns of dv, four walkers and four helpers.
 //        walkers                                         helpers
 //   A    dU = P^T G + diag(y_C / y) K D                  M = Q^T diag(y) G
-//   B    R = T^T dU (= dv)                               P^T G of the next chunk
-//   C    D = y_C D + M - K^T diag(y) R                   K, K^T, Q^T and G of the next chunk
+//   B    R = T^T dU (= dv)                               P^T G, K, K^T, Q^T and diag(y) G of the next chunk
+//   C    D = y_C D + M - K^T diag(y) R                   do of the one after
 // D after each chunk and R stay in the workspace for k_delta_grads.
 template <typename T, int DK>
 struct BackLds {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       const size_t ch = (size_t)bh * a.chunks + c;
       const int next = c > 0 ? c - 1 : 0;
       put_state(a.D + ch * sdim);
-      v4f kd = zero;
+      v4f kd = zero, kp[KS];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         Frag<PI> f;
@@ -142,17 +142,18 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
         } else {
           f = lds_frag<PI>(sm + Lds::k, w * KS + s, lane);
         }
-        kd = mma<PI, 3>(f, lds_frag<3>(sm + Lds::d, s, lane), kd);
+        kp[s] = mma<PI, 3>(f, lds_frag<3>(sm + Lds::d, s, lane), zero);
       }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) kd += kp[s];
       const v4f pg = *(const v4f*)(sm + Lds::pg + w * 1024 + lane * 16);
       lds_half<3>(sm + Lds::x, w >> 1, lane, w & 1,
                   split4<3>(fmaf(end[0], kd[0], pg[0]), fmaf(end[1], kd[1], pg[1]),
                             fmaf(end[2], kd[2], pg[2]), fmaf(end[3], kd[3], pg[3])));
       load_k(next);
       __syncthreads();
-      v4f rr = zero;
-      if (w < 2) rr = mma<3, 3>(t[0], lds_frag<3>(sm + Lds::x, 0, lane), rr);
-      rr = mma<3, 3>(t[1], lds_frag<3>(sm + Lds::x, 1, lane), rr);
+      v4f rr = mma_short(t[1], lds_frag<3>(sm + Lds::x, 1, lane));
+      if (w < 2) rr += mma_short(t[0], lds_frag<3>(sm + Lds::x, 0, lane));
       lds_half<3>(sm + Lds::r, w >> 1, lane, w & 1,
                   split4<3>(-gam[0] * rr[0], -gam[1] * rr[1], -gam[2] * rr[2], -gam[3] * rr[3]));
       load_t(next);
@@ -166,19 +167,25 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       if (c == endc) value_offsets(delta_rows(sq, next), voff);
       __syncthreads();
       const unsigned char* kt = sm + Lds::kt + (TWO ? c & 1 : 0) * Lds::cols;
+      v4f more[OWN];
 #pragma unroll
-      for (int i = 0; i < OWN; ++i)
-        if (w * OWN + i < NT)
-          D[i] = last * D[i] + *(const v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16);
+      for (int i = 0; i < OWN; ++i) {
+        D[i] *= last;
+        more[i] = w * OWN + i < NT ? *(const v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16) : zero;
+      }
       load_last(next);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const Frag<3> f = lds_frag<3>(sm + Lds::r, s, lane);
 #pragma unroll
         for (int i = 0; i < OWN; ++i)
-          if (w * OWN + i < NT)
-            D[i] = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), f, D[i]);
+          if (w * OWN + i < NT) {
+            v4f& to = s ? more[i] : D[i];
+            to = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), f, to);
+          }
       }
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) D[i] += more[i];
       share_state();
       __syncthreads();
     }
@@ -286,11 +293,11 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       __syncthreads();
       form_pg();
       load_p(back(c, 2));
-      __syncthreads();
-      share_k(c - 1, true, TWO);
+      share_k(c - 1, true, TWO);     // this chunk's rows, Q^T and G have been read
       share_q();
       share_g();
       if (TWO) load_kq(back(c, 2));
+      __syncthreads();
       share_o(g2);
 #pragma unroll
       for (int r = 0; r < 4; ++r) g[r] = g2[r];
@@ -317,7 +324,7 @@ struct GradLds {
   static constexpr int uf = xf + 4 * PO * 1024;           // U as rows: 4
   static constexpr int walk = uf + 4 * PO * 1024;
   static constexpr int kt = 0;                            // afterwards: K^T and Q^T, NT x 2 each
-  static constexpr int kTileB = 2 * PI * 1024 + 16;
+  static constexpr int kTileB = 2 * PI * 1024;
   static constexpr int qt = kt + NT * kTileB;
   static constexpr int after = qt + NT * kTileB;
   static constexpr int mat = walk > after ? walk : after; // dP and N: 64 rows of 68 floats each
@@ -497,12 +504,12 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
         const Half<PO> uh = split4<PO>(u[0], u[1], u[2], u[3]);
 #pragma unroll
         for (int p = 0; p < PO; ++p) {
-          unsigned char* to = sm + Lds::uf + (w * PO + p) * 1024 + ((row >> 2) * 16 + 4 * gq) * 16 +
-                              hf * 8 + (row & 3) * 2;
-          *(uint16_t*)(to) = (uint16_t)uh.p[p].x;
-          *(uint16_t*)(to + 16) = (uint16_t)(uh.p[p].x >> 16);
-          *(uint16_t*)(to + 32) = (uint16_t)uh.p[p].y;
-          *(uint16_t*)(to + 48) = (uint16_t)(uh.p[p].y >> 16);
+          unsigned char* to = sm + Lds::uf + (w * PO + p) * 1024 + hf * 8 + (row & 3) * 2;
+          const int l = (row >> 2) * 16 + 4 * gq;
+          *(uint16_t*)(to + slot(l) * 16) = (uint16_t)uh.p[p].x;
+          *(uint16_t*)(to + slot(l + 1) * 16) = (uint16_t)(uh.p[p].x >> 16);
+          *(uint16_t*)(to + slot(l + 2) * 16) = (uint16_t)uh.p[p].y;
+          *(uint16_t*)(to + slot(l + 3) * 16) = (uint16_t)(uh.p[p].y >> 16);
         }
       }
       __syncthreads();

@@ -58,6 +58,17 @@ __device__ __forceinline__ v4f mma(const Frag<PA>& a, const Frag<PB>& b, v4f acc
       if (s - i >= 0 && s - i < PB) acc = mfma_bf16(a.p[i], b.p[s - i], acc);
   return acc;
 }
+// A B for three parts each, in two chains of three products (a product waits twice as long for the one
+// before it in its chain as the matrix core takes).
+__device__ __forceinline__ v4f mma_short(const Frag<3>& a, const Frag<3>& b) {
+  const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f lo = mfma_bf16(a.p[0], b.p[2], zero), hi = mfma_bf16(a.p[0], b.p[1], zero);
+  lo = mfma_bf16(a.p[1], b.p[1], lo);
+  hi = mfma_bf16(a.p[1], b.p[0], hi);
+  lo = mfma_bf16(a.p[2], b.p[0], lo);
+  hi = mfma_bf16(a.p[0], b.p[0], hi);
+  return hi + lo;
+}
 template <int P, int N>
 __device__ __forceinline__ Frag<P> lead(const Frag<N>& f) {   // the P leading parts
   Frag<P> r;
@@ -66,19 +77,23 @@ __device__ __forceinline__ Frag<P> lead(const Frag<N>& f) {   // the P leading p
   return r;
 }
 
-// Frags in LDS: part p of frag f at base + (f * P + p) * 1024, lane's 16 bytes, half h 8 of them.
+// Frags in LDS: part p of frag f at base + (f * P + p) * 1024, a lane's 16 bytes in slot(lane), half h 8 of
+// them. Operands are read by lane in any case without bank conflicts; writes of transposed blocks run
+// over rows 4 apart and over lane groups, which the slot's low bits spread over the banks (without: 55 % of
+// the walk's LDS cycles were conflicts).
+__device__ __forceinline__ int slot(int lane) { return lane ^ ((lane >> 4) & 3); }
 template <int P>
 __device__ __forceinline__ Frag<P> lds_frag(const unsigned char* base, int f, int lane) {
   Frag<P> r;
 #pragma unroll
-  for (int i = 0; i < P; ++i) r.p[i] = *(const u32x4*)(base + (f * P + i) * 1024 + lane * 16);
+  for (int i = 0; i < P; ++i) r.p[i] = *(const u32x4*)(base + (f * P + i) * 1024 + slot(lane) * 16);
   return r;
 }
 template <int P>
 __device__ __forceinline__ void lds_half(unsigned char* base, int f, int lane, int half,
                                          const Half<P>& h) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) *(u32x2*)(base + (f * P + i) * 1024 + lane * 16 + half * 8) = h.p[i];
+  for (int i = 0; i < P; ++i) *(u32x2*)(base + (f * P + i) * 1024 + slot(lane) * 16 + half * 8) = h.p[i];
 }
 
 // The steps of one sequence: step t < n takes position t, or n - 1 - t when reversed.
@@ -278,15 +293,14 @@ __device__ __forceinline__ void lds_rows(unsigned char* to, int tg, int dg, cons
   for (int j = 0; j < 4; ++j) {
     const Frag<P> f = join<P>(lo[j], hi[j]);
     unsigned char* at = to + ((tg >> 2) * KS + (dg >> 2)) * P * 1024 +
-                        ((dg & 3) * 16 + 4 * (tg & 3) + j) * 16;
+                        slot((dg & 3) * 16 + 4 * (tg & 3) + j) * 16;
 #pragma unroll
     for (int p = 0; p < P; ++p) *(u32x4*)(at + p * 1024) = f.p[p];
   }
 }
-// ... and transposed, as operands of the state's row tiles over the steps; a tile's two frags lie
-// 2 P KB + 16 bytes from the next tile's, staggered over the banks.
+// ... and transposed, as operands of the state's row tiles over the steps, two frags a tile.
 template <int P>
-constexpr int kTileBytes = 2 * P * 1024 + 16;
+constexpr int kTileBytes = 2 * P * 1024;
 template <int P>
 __device__ __forceinline__ void lds_cols(unsigned char* to, int tg, int dg, const Half<P> (&lo)[4],
                                          const Half<P> (&hi)[4]) {
