@@ -332,6 +332,32 @@ struct GradLds {
   static constexpr int bytes = red + 7 * 64 * 4;
 };
 
+// x, as a value that the compiler forms where it is used: offsets derived from it are not kept in registers
+// over a whole loop.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// The sum of the products of this lane's 8 entries.
+template <int P>
+__device__ __forceinline__ float dot(const Frag<P>& a, const Frag<P>& b) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x = 0.f, y = 0.f, z = 0.f, t = 0.f;
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p) {
+      x += __uint_as_float(a.p[p][j] << 16);
+      y += __uint_as_float(b.p[p][j] << 16);
+      z += __uint_as_float(a.p[p][j] & 0xffff0000u);
+      t += __uint_as_float(b.p[p][j] & 0xffff0000u);
+    }
+    s = fmaf(x, y, fmaf(z, t, s));
+  }
+  return s;
+}
+
 // Sum over the 16 lanes of a row of lanes, in its last one.
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float x) {
@@ -344,8 +370,8 @@ __device__ __forceinline__ float sum16_last(float x) {
   return dpp_add<0x118>(x);
 }
 
-template <typename T, int DK, bool VEC>
-__global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
+template <typename T, int DK, bool VEC, bool ONE>
+__global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ? 4 : 2)) k_delta_grads(DeltaArgs a) {
   using Lds = GradLds<T, DK, VEC>;
   using Ty = DeltaType<T, VEC>;
   using Fy = DeltaType<float, VEC>;
@@ -384,7 +410,7 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
   const uint32_t kstride = (uint32_t)(a.Hk * a.dk) * sizeof(T), vstride = (uint32_t)(a.H * a.dv) * sizeof(T);
   const auto kbuf = delta_buf((const T*)a.k + (low * a.Hk + hk) * a.dk);
   const auto qbuf = delta_buf((const T*)a.q + (low * a.Hk + hk) * a.dk);
-  const uint32_t krow = rows.off(16 * w + row, kstride), vrow = rows.off(16 * w + row, vstride);
+  const uint32_t krow = rows.off(16 * w + row, kstride);
 
   Frag<PI> kf[KS];
   {
@@ -400,7 +426,7 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
 #pragma unroll
   for (int i = 0; i < NTH; ++i) dqs[i] = dks[i] = zero;
 
-  for (int j = 0; j < a.rep; ++j) {
+  for (int j = 0; j < (ONE ? 1 : a.rep); ++j) {
     const int h = hk * a.rep + j;
     const size_t ch = (size_t)(b * a.H + h) * a.chunks + c;
     const DeltaGates& gt = a.gates[ch];
@@ -424,78 +450,80 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
     for (int i = 0; i < 4; ++i) pn[i] = zero;
     float rv[4] = {0.f, 0.f, 0.f, 0.f}, sd = 0.f;     // v.R of this lane's rows; <S0, D>
 
-    for (int n0 = 0; n0 < a.dv; n0 += 32) {
-      // 4 x 4 blocks of S0 (threads below 256) and of D (the others); rows of do and R as operands; v and
-      // R as results lie
-      constexpr int kBlk = (DK * 2 + 255) / 256;
-      const bool second = tid >= 256;
-      typename Fy::Raw ms[kBlk][4], md[kBlk][4];
+    // Of a piece: 4 x 4 blocks of S0 (threads below 256) or of D (the others), rows of do and R as
+    // operands, v and R as results lie. The next piece's loads are issued once this one's are in LDS.
+    constexpr int kBlk = (DK * 2 + 255) / 256;
+    const bool second = tid >= 256;
+    const auto mbuf = second ? dbuf : sbuf;
+    typename Fy::Raw ms[kBlk][4];
+    typename Ty::Raw g0, g1;
+    v4f r0, r1;
+    uint32_t v[4];
+    float rd[4];
+    auto load_piece = [&](int n0) {
+      const int tid = here(threadIdx.x), lane = tid & 63, row = lane & 15, gq = lane >> 4;
+      const uint32_t vrow = rows.off(16 * w + row, vstride);
 #pragma unroll
       for (int m = 0; m < kBlk; ++m) {
         const int id = (tid & 255) + 256 * m, n4 = id & 7, k4 = id >> 3;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int k = 4 * k4 + r;
-          const uint32_t off = k < a.dk ? (uint32_t)(k * a.dv) * 4 : kNowhere;
-          ms[m][r] = raw4<float, VEC>(sbuf, off, n0 + 4 * n4, a.dv);
-          if (second) md[m][r] = raw4<float, VEC>(dbuf, off, n0 + 4 * n4, a.dv);
+          ms[m][r] = raw4<float, VEC>(mbuf, k < a.dk ? (uint32_t)(k * a.dv) * 4 : kNowhere, n0 + 4 * n4,
+                                      a.dv);
         }
       }
-      const auto g0 = raw4<T, VEC>(gbuf, vrow, n0 + 4 * gq, a.dv);
-      const auto g1 = raw4<T, VEC>(gbuf, vrow, n0 + 16 + 4 * gq, a.dv);
+      g0 = raw4<T, VEC>(gbuf, vrow, n0 + 4 * gq, a.dv);
+      g1 = raw4<T, VEC>(gbuf, vrow, n0 + 16 + 4 * gq, a.dv);
       const uint32_t rrow = (uint32_t)((16 * w + row) * a.dv) * 4;
-      const v4f r0 = raw4<float, VEC>(rbuf, rrow, n0 + 4 * gq, a.dv);
-      const v4f r1 = raw4<float, VEC>(rbuf, rrow, n0 + 16 + 4 * gq, a.dv);
+      r0 = raw4<float, VEC>(rbuf, rrow, n0 + 4 * gq, a.dv);
+      r1 = raw4<float, VEC>(rbuf, rrow, n0 + 16 + 4 * gq, a.dv);
       const int n = n0 + 16 * hf + row;
-      T v[4];
-      float rd[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int m = 16 * w + 4 * gq + r;
-        v[r] = buf_load<T>(vbuf, n < a.dv ? rows.off(m, vstride) + n * sizeof(T) : kNowhere);
+        v[r] = raw1<T>(vbuf, n < a.dv ? rows.off(m, vstride) + n * sizeof(T) : kNowhere);
         rd[r] = buf_load<float>(rbuf, n < a.dv ? (uint32_t)(m * a.dv + n) * 4 : kNowhere);
       }
+    };
+    for (int n0 = 0; n0 < a.dv; n0 += 32) {
+      const int tid = here(threadIdx.x), lane = tid & 63, row = lane & 15, gq = lane >> 4;
+      load_piece(n0);
       __syncthreads();            // the last piece's (or head's) operands have been read
 #pragma unroll
       for (int m = 0; m < kBlk; ++m) {
         const int id = (tid & 255) + 256 * m, n4 = id & 7, k4 = id >> 3;
         if (DK * 2 % 256 == 0 || id < DK * 2) {
-          if (second) {
+          unsigned char* to = sm + (second ? Lds::dn : Lds::sn);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const v4f d = md[m][r], s = ms[m][r];
-              lds_half<PO>(sm + Lds::dn, k4 >> 2, (n4 & 3) * 16 + 4 * (k4 & 3) + r, n4 >> 2,
-                           split4<PO>(d[0], d[1], d[2], d[3]));
-              sd += s[0] * d[0] + s[1] * d[1] + s[2] * d[2] + s[3] * d[3];
-            }
-          } else {
+          for (int r = 0; r < 4; ++r)
+            lds_half<PO>(to, k4 >> 2, (n4 & 3) * 16 + 4 * (k4 & 3) + r, n4 >> 2,
+                         split4<PO>(ms[m][r][0], ms[m][r][1], ms[m][r][2], ms[m][r][3]));
+          if (!second)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const v4f s = ms[m][r];
-              lds_half<PO>(sm + Lds::sn, k4 >> 2, (n4 & 3) * 16 + 4 * (k4 & 3) + r, n4 >> 2,
-                           split4<PO>(s[0], s[1], s[2], s[3]));
+            for (int r = 0; r < 4; ++r)
               lds_half<PO>(sm + Lds::sk, (k4 >> 3) * 2 + (n4 >> 2), (k4 & 3) * 16 + 4 * (n4 & 3) + r,
                            (k4 >> 2) & 1,
                            split4<PO>(ms[m][0][r], ms[m][1][r], ms[m][2][r], ms[m][3][r]));
-            }
-          }
         }
       }
       const Frag<PI> gf = operand<PI>(g0, g1);
       const Frag<PO> rf = join<PO>(split4<PO>(r0[0], r0[1], r0[2], r0[3]),
                                    split4<PO>(r1[0], r1[1], r1[2], r1[3]));
+      float x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = wide1<T>(v[r]);
+        rv[r] = fmaf(rd[r], x[r], rv[r]);
+      }
       __syncthreads();
       // X = V - diag(y) K S0, this wave's 16 rows and 16 columns
       v4f ks = zero;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         ks = mma<PI, PO>(kf[s], lds_frag<PO>(sm + Lds::sk, 2 * s + hf, lane), ks);
-      float x[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = wide(v[r]) - gam[r] * ks[r];
-        rv[r] = fmaf(rd[r], wide(v[r]), rv[r]);
-      }
+      for (int r = 0; r < 4; ++r) x[r] -= gam[r] * ks[r];
       lds_half<PO>(sm + Lds::xf, (w >> 1) * 2 + hf, lane, w & 1, split4<PO>(x[0], x[1], x[2], x[3]));
       __syncthreads();
       v4f u = mma<PO, PO>(tf0, lds_frag<PO>(sm + Lds::xf, hf, lane), zero);
@@ -524,21 +552,24 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
 #pragma unroll
       for (int i = 0; i < NTH; ++i) {
         const Frag<PO> sf = lds_frag<PO>(sm + Lds::sn, hf * NTH + i, lane);
+        const Frag<PO> df = lds_frag<PO>(sm + Lds::dn, hf * NTH + i, lane);
         dq[i] = mma<PI, PO>(gf, sf, dq[i]);
         rowg[i] = mma<PO, PO>(rf, sf, rowg[i]);
-        colg[i] = mma<PO, PO>(uw, lds_frag<PO>(sm + Lds::dn, hf * NTH + i, lane), colg[i]);
+        colg[i] = mma<PO, PO>(uw, df, colg[i]);
+        if (w == (i & 3)) sd += dot(sf, df);      // <S0, D>, each tile by one wave
       }
     }
 
     // K and Q by 4 x 4 blocks, for their transposes; as results lie
-    constexpr int kBlk = (DK * 4 + 255) / 256;
-    typename Ty::Raw mb[kBlk][4];
+    constexpr int kRowBlk = (DK * 4 + 255) / 256;
+    const int tid = here(threadIdx.x), lane = tid & 63, row = lane & 15, gq = lane >> 4;
+    typename Ty::Raw mb[kRowBlk][4];
 #pragma unroll
-    for (int m = 0; m < kBlk; ++m) {
+    for (int m = 0; m < kRowBlk; ++m) {
       const int id = (tid & 255) + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        mb[m][r] = raw4<T, VEC>(tid >= 256 ? qbuf : kbuf,
+        mb[m][r] = raw4<T, VEC>(second ? qbuf : kbuf,
                                 tg < 16 ? rows.off(4 * tg + r, kstride) : kNowhere, 4 * dg, a.dk);
     }
     T kr[NTH][4], qr[NTH][4];
@@ -574,7 +605,7 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
     }
     __syncthreads();              // the pieces' operands have been read
 #pragma unroll
-    for (int m = 0; m < kBlk; ++m) {
+    for (int m = 0; m < kRowBlk; ++m) {
       const int id = (tid & 255) + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
       if (tg < 16) {
         Half<PI> q[4], cl[4];
@@ -660,10 +691,18 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) red[(2 * e + hf) * 64 + 16 * w + 4 * gq + r] = z[e][r];
     if (lane == 0) red[6 * 64 + wid] = tot;
+    if (ONE) {
 #pragma unroll
-    for (int i = 0; i < NTH; ++i) {
-      dqs[i] += dq[i];
-      dks[i] += rowg[i] + colg[i];
+      for (int i = 0; i < NTH; ++i) {
+        dqs[i] = dq[i];
+        dks[i] = rowg[i] + colg[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NTH; ++i) {
+        dqs[i] += dq[i];
+        dks[i] += rowg[i] + colg[i];
+      }
     }
     __syncthreads();
     if (wid == 0) {
@@ -682,15 +721,16 @@ __global__ void __launch_bounds__(512) k_delta_grads(DeltaArgs a) {
                 (red[4 * 64 + lane] + red[5 * 64 + lane] + rowk) * (1.f - gt.b[lane]), T());
     }
   }
+  const int tidl = here(threadIdx.x), gql = (tidl & 63) >> 4, rowl = tidl & 15;
   const auto dqbuf = delta_buf((T*)a.dq + (low * a.Hk + hk) * a.dk);
   const auto dkbuf = delta_buf((T*)a.dkey + (low * a.Hk + hk) * a.dk);
 #pragma unroll
   for (int i = 0; i < NTH; ++i) {
-    const int k = 16 * (hf * NTH + i) + row;
+    const int k = 16 * (hf * NTH + i) + rowl;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const uint32_t off =
-          k < a.dk ? rows.off(16 * w + 4 * gq + r, kstride) + k * sizeof(T) : kNowhere;
+          k < a.dk ? rows.off(16 * w + 4 * gql + r, kstride) + k * sizeof(T) : kNowhere;
       buf_store(dqbuf, off, dqs[i][r], T());
       buf_store(dkbuf, off, dks[i][r], T());
     }
@@ -725,11 +765,16 @@ hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
     if (e != hipSuccess) return;
     constexpr int bytes = GradLds<T, DK, VEC>::bytes;
     static_assert(bytes <= 160 * 1024, "LDS of a CU");
-    e = hipFuncSetAttribute((const void*)k_delta_grads<T, DK, VEC>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return;
-    k_delta_grads<T, DK, VEC><<<dim3(a.B * a.Hk * a.chunks), 512, bytes, st>>>(a);
-    e = hipGetLastError();
+    auto grads = [&](auto one) {
+      constexpr bool ONE = decltype(one)::value;   // every head has a key head of its own
+      e = hipFuncSetAttribute((const void*)k_delta_grads<T, DK, VEC, ONE>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != hipSuccess) return;
+      k_delta_grads<T, DK, VEC, ONE><<<dim3(a.B * a.Hk * a.chunks), 512, bytes, st>>>(a);
+      e = hipGetLastError();
+    };
+    if (a.rep == 1) grads(std::true_type());
+    else grads(std::false_type());
   });
   return e;
 }
