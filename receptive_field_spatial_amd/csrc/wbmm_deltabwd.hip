@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
     // Of a piece: 4 x 4 blocks of S0 (threads below 256) or of D (the others), rows of do and R as
     // operands, v and R as results lie. The next piece's loads are issued once this one's are in LDS.
     constexpr int kBlk = (DK * 2 + 255) / 256;
-    const bool second = tid >= 256;
+    const bool second = hf == 1;     // the same for a whole wave, and known to be
     const auto mbuf = second ? dbuf : sbuf;
     typename Fy::Raw ms[kBlk][4];
     typename Ty::Raw g0, g1;
@@ -598,8 +598,8 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
           for (int r = 0; r < 4; ++r) {
             const int m = 16 * w + 4 * gq + r, nn = 16 * i + row;
             const bool low_ = hf == 0 ? nn <= m : nn < m;
-            const float dec = __builtin_amdgcn_exp2f(low_ ? (float)(cm[r] - cc) : 0.f);
-            mat[hf * 64 * 68 + m * 68 + nn] = low_ ? one * dec * pn[i][r] : 0.f;
+            const float d = (float)(cm[r] - cc), p = one * __builtin_amdgcn_exp2f(d > 0.f ? 0.f : d);
+            mat[hf * 64 * 68 + m * 68 + nn] = low_ ? p * pn[i][r] : 0.f;
           }
         }
     }
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int k = 4 * dg + r;
-          lds_half<PI>(sm + (tid >= 256 ? Lds::qt : Lds::kt) + (k >> 4) * Lds::kTileB, tg >> 3,
+          lds_half<PI>(sm + (second ? Lds::qt : Lds::kt) + (k >> 4) * Lds::kTileB, tg >> 3,
                        (tg & 3) * 16 + (k & 15), (tg >> 2) & 1, cl[r]);
         }
       }
