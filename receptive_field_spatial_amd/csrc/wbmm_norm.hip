@@ -11,7 +11,7 @@
 //   rows    (inner = 1): a row belongs to LPR lanes (4 to 64, or the 256 of a workgroup) that hold K
 //           pieces of 8 elements each; several rows per wave where rows are short. Rows whose length or
 //           address does not allow 16-byte accesses go element by element, 64 lanes side by side.
-//   columns (inner > 1): a lane holds VW neighbouring positions and a wave every NW-th entry of len
+//   columns (inner > 1): a lane holds one position (the bf16 forward: two neighbours) and a wave every NW-th entry of len
 //           there; the waves' sums meet in LDS.
 // Longer axes than the registers hold are read twice, the second time from a cache.
 //
@@ -26,7 +26,8 @@ namespace wbmm {
 namespace {
 
 constexpr int kP = 8;              // elements of a row piece
-constexpr int kDwGroups = 512;     // workgroups of a backward with dw: two per CU
+// Workgroups of a backward with dw: two per CU (50176 rows of 192 bf16: 20.9 us; one 24.5, four 23.7).
+constexpr int kDwGroups = 512;
 // Values of each tensor that a lane of the column kernels keeps (the forward keeps one tensor, the
 // backward three): what 16 waves of a workgroup have registers for.
 constexpr int kColFwd = 32, kColBwd = 16;
@@ -357,45 +358,21 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_long_bwd(NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------- columns
+// A lane's VW positions: one, or two of bf16.
 template <typename T, int VW>
 __device__ __forceinline__ void load_n(const T* p, float (&v)[VW]) {
-  if constexpr (sizeof(T) == 4) {
-    typedef float vec __attribute__((ext_vector_type(VW)));
-    if constexpr (VW == 1) {
-      v[0] = *p;
-    } else {
-      const vec a = *(const vec*)p;
-#pragma unroll
-      for (int j = 0; j < VW; ++j) v[j] = a[j];
-    }
-  } else if constexpr (VW == 1) {
-    v[0] = bf2f(*p);
+  if constexpr (VW == 1) {
+    v[0] = load_f32<T>(p, 0);
   } else {
-    uint32_t a[VW / 2];
-    __builtin_memcpy(a, __builtin_assume_aligned(p, 2 * VW), 2 * VW);
-#pragma unroll
-    for (int j = 0; j < VW / 2; ++j) {
-      v[2 * j] = __uint_as_float(a[j] << 16);
-      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-    }
+    const uint32_t a = *(const uint32_t*)p;
+    v[0] = __uint_as_float(a << 16);
+    v[1] = __uint_as_float(a & 0xffff0000u);
   }
 }
 template <typename T, int VW>
 __device__ __forceinline__ void store_n(T* p, const float (&v)[VW]) {
-  if constexpr (VW == 1) {
-    put(p, v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    typedef float vec __attribute__((ext_vector_type(VW)));
-    vec a;
-#pragma unroll
-    for (int j = 0; j < VW; ++j) a[j] = v[j];
-    *(vec*)p = a;
-  } else {
-    uint32_t a[VW / 2];
-#pragma unroll
-    for (int j = 0; j < VW / 2; ++j) a[j] = bf_bits(v[2 * j]) | (bf_bits(v[2 * j + 1]) << 16);
-    __builtin_memcpy(__builtin_assume_aligned(p, 2 * VW), a, 2 * VW);
-  }
+  if constexpr (VW == 1) put(p, v[0]);
+  else *(uint32_t*)p = bf_bits(v[0]) | (bf_bits(v[1]) << 16);
 }
 
 // Sum over the workgroup's waves of each lane's VW values, in every wave; sm: NW * 64 * VW floats.
@@ -485,7 +462,6 @@ __device__ __forceinline__ void col_codes(const NormArgs& a, size_t at, float (&
   for (int j = 0; j < VW; ++j) s[j] = bad ? 0.f : y[j] * inv;
   const uint32_t w = ckpt_encode4(s, a.fmt);
   if (!live) return;
-  if constexpr (VW == 4) *(uint32_t*)(a.codes + at) = w;
   if constexpr (VW == 2) *(uint16_t*)(a.codes + at) = (uint16_t)w;
   if constexpr (VW == 1) a.codes[at] = (uint8_t)w;
   if ((threadIdx.x & (32 / VW - 1)) == 0) a.scales[at / kCkptGroup] = (uint8_t)(bad ? 255 : byte);
@@ -577,8 +553,9 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
 // Backward: a workgroup takes every gridDim.x-th tile. N > 0: dw's sums of the lane's positions
 // stay in registers and are added across the wave at the end. N = 0: the wave adds them per tile into
 // its workgroup's partial.
-template <typename T, int VW, int N, bool DW>
+template <typename T, int N, bool DW>
 __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
+  constexpr int VW = 1;
   extern __shared__ __attribute__((aligned(16))) float sm[];
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   const int lane = threadIdx.x & 63;
@@ -737,41 +714,36 @@ bool rows_vec(const NormRequest& r) {
          al(r.y, 16) && al(r.w, 16);
 }
 
-// Lanes of a row and pieces per lane: the fewest idle lanes, then the fewest pieces. K <= 3 keeps a
-// backward (three tensors and dw with its carry, 40 registers a piece) at two workgroups per SIMD.
+// Lanes of a row and pieces per lane: a piece each as long as a wave's lanes suffice, idle ones or not. Against
+// the fewest idle lanes (50176 rows of bf16, 192 entries: 8 lanes x 3 pieces): 19.1 us for 20.9 backward, 8 rows
+// 4.7 for 6.6; 264 entries, half of whose lanes idle: 8.5 for 7.5 forward. A workgroup's 256 lanes only
+// where a wave's 3 pieces end: 20000 rows of 768 in 16.4 us with 64 x 2, 22.4 with 256 x 1. More than 3 pieces
+// would not leave a backward (three tensors and dw with its carry, 40 registers a piece) two
+// workgroups per SIMD.
 struct RowShape { int lpr, k; };
 RowShape row_shape(int64_t len) {
   const int64_t pieces = (len + kP - 1) / kP;
-  RowShape best{0, 0};
-  int64_t cost = 0;
-  for (int lpr : {4, 8, 16, 32, 64, 256})
-    for (int k = 1; k <= 3; ++k) {
-      const int64_t cap = (int64_t)lpr * k;
-      if (cap < pieces) continue;
-      if (best.lpr == 0 || cap < cost) best = {lpr, k}, cost = cap;
-    }
-  return best;
+  for (int lpr : {4, 8, 16, 32})
+    if (lpr >= pieces) return {lpr, 1};
+  for (int lpr : {64, 256})
+    for (int k = 1; k <= 3; ++k)
+      if ((int64_t)lpr * k >= pieces) return {lpr, k};
+  return {0, 0};
 }
 
-// Columns: positions per lane, waves, entries per wave.
+// Columns: positions per lane, waves, entries per wave. 4 bytes a lane: 32 x 192 x 784 bf16 forward 9.0 us,
+// with 2 bytes 10.7; 16 bytes (fp32) are slower, 128 x 96 x 3136 94 for 90 us forward and 131 for 119
+// backward, 4 x 192 x 784 8.4 for 5.9. The backward with three tensors to keep takes one position: bf16
+// 128 x 96 x 3136 68.8 us, two 71.5.
 struct ColShape { int vw, nw, n; };
 ColShape col_shape(const NormRequest& r, bool backward) {
-  const size_t es = r.bf16 ? 2 : 4;
-  int vw = 4;
-  auto fits = [&](int v) {
-    return r.inner % v == 0 && al(r.x, v * es) && al(r.res, v * es) && al(r.dy, v * es) &&
-           al(r.s, v * es) && al(r.y, v * es) && al(r.codes, v);
-  };
-  while (vw > 1 && !fits(vw)) vw /= 2;
-  const int64_t rows = r.outer * r.inner;
+  const bool two = !backward && r.bf16 && r.inner % 2 == 0 && al(r.x, 4) && al(r.res, 4) && al(r.s, 4) &&
+                   al(r.y, 4) && al(r.codes, 2);
   const int cap = backward ? kColBwd : kColFwd;
-  for (; vw >= 1; vw /= 2) {
-    // fewer positions per lane where the CUs would not all have a tile
-    if (vw > 1 && rows < 256ll * 64 * vw) continue;
+  for (int vw = two ? 2 : 1; vw >= 1; --vw)
     for (int nw : {4, 8, 16})
       for (int n : {4, 6, 8, 12, 16, 24, 32})
         if ((int64_t)nw * n >= r.len && n * vw <= cap) return {vw, nw, n};
-  }
   return {1, 16, 0};
 }
 
@@ -809,15 +781,16 @@ void rows_bwd(NormArgs a, bool vec, bool dw, hipStream_t st, int& groups) {
 // Calls f with the shape as compile-time constants.
 template <typename F>
 void with_rows(RowShape s, F f) {
+  using One = std::integral_constant<int, 1>;
   auto ks = [&](auto lpr) {
-    if (s.k == 1) f(lpr, std::integral_constant<int, 1>());
+    if (s.k == 1) f(lpr, One());
     else if (s.k == 2) f(lpr, std::integral_constant<int, 2>());
     else f(lpr, std::integral_constant<int, 3>());
   };
-  if (s.lpr == 4) ks(std::integral_constant<int, 4>());
-  else if (s.lpr == 8) ks(std::integral_constant<int, 8>());
-  else if (s.lpr == 16) ks(std::integral_constant<int, 16>());
-  else if (s.lpr == 32) ks(std::integral_constant<int, 32>());
+  if (s.lpr == 4) f(std::integral_constant<int, 4>(), One());
+  else if (s.lpr == 8) f(std::integral_constant<int, 8>(), One());
+  else if (s.lpr == 16) f(std::integral_constant<int, 16>(), One());
+  else if (s.lpr == 32) f(std::integral_constant<int, 32>(), One());
   else if (s.lpr == 64) ks(std::integral_constant<int, 64>());
   else ks(std::integral_constant<int, 256>());
 }
@@ -833,8 +806,7 @@ void with_cols(ColShape s, F f) {
     else if (s.n == 32) f(vw, std::integral_constant<int, 32>());
     else f(vw, std::integral_constant<int, 0>());
   };
-  if (s.vw == 4) ns(std::integral_constant<int, 4>());
-  else if (s.vw == 2) ns(std::integral_constant<int, 2>());
+  if (s.vw == 2) ns(std::integral_constant<int, 2>());
   else ns(std::integral_constant<int, 1>());
 }
 
@@ -861,7 +833,7 @@ bool forward_t(const NormRequest& r, hipStream_t st) {   // whether the codes we
   a.tiles = cdiv(a.rows, 64 * s.vw);
   with_cols(s, [&](auto vw, auto n) {
     constexpr int VW = decltype(vw)::value, N = decltype(n)::value;
-    if constexpr (N * VW <= kColFwd)
+    if constexpr (N * VW <= kColFwd && (VW == 1 || (sizeof(T) == 2 && N > 0)))
       k_norm_cols<T, VW, N><<<dim3(a.tiles), 64 * s.nw, s.nw * 64 * VW * 4, st>>>(a);
   });
   return a.codes != nullptr;
@@ -891,11 +863,11 @@ void backward_t(const NormRequest& r, hipStream_t st) {
     with_cols(s, [&](auto vw, auto n) {
       constexpr int VW = decltype(vw)::value, N = decltype(n)::value;
       const size_t lds = (size_t)2 * s.nw * 2 * VW * 64 * 4;
-      if constexpr (N * VW <= kColBwd) {
+      if constexpr (N <= kColBwd && VW == 1) {
         if (dw)
-          k_norm_cols_bwd<T, VW, N, true><<<dim3(groups), 64 * s.nw, lds, st>>>(a);
+          k_norm_cols_bwd<T, N, true><<<dim3(groups), 64 * s.nw, lds, st>>>(a);
         else
-          k_norm_cols_bwd<T, VW, N, false><<<dim3(groups), 64 * s.nw, lds, st>>>(a);
+          k_norm_cols_bwd<T, N, false><<<dim3(groups), 64 * s.nw, lds, st>>>(a);
       }
     });
   }
