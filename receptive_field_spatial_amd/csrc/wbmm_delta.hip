@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 }
 
 // ---------------------------------------------------------------------------- the walk
-// One workgroup per head and 16 columns of dv, of 8 waves: the first four walk the state along the chunks,
+// One workgroup per head and NC tiles of 16 columns of dv, of 8 waves: the first four walk the state along the chunks,
 // wave w with row tile w of the 64 steps and OWN of the state's row tiles; the other four fetch K for
 // them, one chunk ahead, and form the outputs. Three hand-overs per chunk, each through LDS:
 //        walkers                                    helpers
@@ -251,27 +251,28 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 // Loads are issued a chunk before their use, right after the last use of their registers.
 // LDS of a workgroup. Two chunks' K^T, where they fit (all but fp32 with 96 < dk): the next one is then
 // written while this one is read, and K is loaded a whole chunk ahead.
-template <typename T, int DK>
+template <typename T, int DK, int NC>
 struct WalkLds {
   static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO, KS = DK / 32;
   static constexpr int rows = 4 * KS * PI * 1024, cols = (DK / 16) * kTileBytes<PI>;
-  static constexpr int rest = (KS * 3 + 12 + 2 * PO) * 1024 + rows;
+  static constexpr int rest = NC * (KS * 3 + 12 + 2 * PO) * 1024 + rows;
   static constexpr bool two = rest + 2 * cols <= 160 * 1024;
   static constexpr int bytes = rest + (two ? 2 : 1) * cols;
 };
 
-template <typename T, int DK, bool VEC, bool OUT>
-__global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
+template <typename T, int DK, bool VEC, bool OUT, int NC>
+__global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>::PI == 1 ? 4 : 2)) k_delta_walk(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
   constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
-  constexpr bool TWO = WalkLds<T, DK>::two;
-  constexpr int kRows = WalkLds<T, DK>::rows, kCols = TWO ? WalkLds<T, DK>::cols : 0;
+  constexpr bool TWO = WalkLds<T, DK, NC>::two;
+  constexpr int kRows = WalkLds<T, DK, NC>::rows, kCols = TWO ? WalkLds<T, DK, NC>::cols : 0;
+  constexpr int kS = KS * 3 * 1024, kX = 2 * 3 * 1024, kU = 2 * PO * 1024;   // of a column tile
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   unsigned char* const s_s = sm;                          // the state
-  unsigned char* const s_x = s_s + KS * 3 * 1024;         // X
-  unsigned char* const s_e = s_x + 2 * 3 * 1024;          // diag(y_C / y) U
-  unsigned char* const s_u = s_e + 2 * 3 * 1024;          // U
-  unsigned char* const s_k = s_u + 2 * PO * 1024;         // K, and K^T
+  unsigned char* const s_x = s_s + NC * kS;               // X
+  unsigned char* const s_e = s_x + NC * kX;               // diag(y_C / y) U
+  unsigned char* const s_u = s_e + NC * kX;               // U
+  unsigned char* const s_k = s_u + NC * kU;               // K, and K^T
   unsigned char* const s_kt = s_k + kRows;
   const int bh = blockIdx.x;
   if (bh >= a.B * a.H) return;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
   const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
-  const int col = blockIdx.y * 16 + row;
+  const int col = blockIdx.y * (16 * NC) + row;     // NC = 2: and the 16th after it
   const bool in = col < a.dv;
   const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
   };
 
   if (walker) {
-    v4f S[OWN];
+    v4f S[NC][OWN];
     uint32_t soff[OWN][4], voff[4];
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
@@ -306,32 +307,41 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
         const int k = walk_entry(w * OWN + i, 4 * gq + r);
         const bool own = w * OWN + i < NT && k < a.dk && in;
         soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
-        S[i][r] = a.s0 ? buf_load<float>(delta_buf(a.s0 + bh * sdim), soff[i][r]) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          S[n][i][r] = a.s0 ? buf_load<float>(delta_buf(a.s0 + bh * sdim), soff[i][r] + 64 * n) : 0.f;
       }
     auto put_state = [&](float* to) {
       const auto buf = delta_buf(to);
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], S[i][r], 0.f);
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) buf_store(buf, soff[i][r] + 64 * n, S[n][i][r], 0.f);
     };
     auto share_state = [&] {
 #pragma unroll
       for (int i = 0; i < OWN; ++i) {
         const int tile = w * OWN + i;
         if (tile < NT)
-          lds_half<3>(s_s, tile >> 1, lane, tile & 1, split4<3>(S[i][0], S[i][1], S[i][2], S[i][3]));
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            lds_half<3>(s_s + n * kS, tile >> 1, lane, tile & 1,
+                        split4<3>(S[n][i][0], S[n][i][1], S[n][i][2], S[n][i][3]));
       }
     };
     Frag<3> t[2];
-    uint32_t v[4];
+    uint32_t v[NC][4];
     v4f gam, end;
     float last = 1.f;
     auto load_v = [&](int c) {
       if (c == endc) value_offsets(delta_rows(sq, c), voff);
       const auto vbuf = delta_buf((const T*)a.v + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = raw1<T>(vbuf, voff[r]);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) v[n][r] = raw1<T>(vbuf, voff[r] + 16 * n * sizeof(T));
       gam = *(const v4f*)&a.gates[(size_t)bh * a.chunks + c].gam[16 * w + 4 * gq];
     };
     auto load_t = [&](int c) {
@@ -355,41 +365,66 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
     for (int c = 0; c < nch; ++c) {
       const int next = c < endc ? c + 1 : c;
       if (a.states) put_state(a.states + ((size_t)bh * a.chunks + c) * sdim);
-      v4f ks = zero, kp[KS];         // a chain of products for each 32 terms
+      v4f kp[NC][KS];                // a chain of products for each 32 terms
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-        kp[s] = mma<PI, 3>(lds_frag<PI>(s_k, w * KS + s, lane), lds_frag<3>(s_s, s, lane), zero);
+      for (int s = 0; s < KS; ++s) {
+        const Frag<PI> kf = lds_frag<PI>(s_k, w * KS + s, lane);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) ks += kp[s];
-      lds_half<3>(s_x, w >> 1, lane, w & 1,
-                  split4<3>(wide1<T>(v[0]) - gam[0] * ks[0], wide1<T>(v[1]) - gam[1] * ks[1],
-                            wide1<T>(v[2]) - gam[2] * ks[2], wide1<T>(v[3]) - gam[3] * ks[3]));
+        for (int n = 0; n < NC; ++n) kp[n][s] = mma<PI, 3>(kf, lds_frag<3>(s_s + n * kS, s, lane), zero);
+      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        v4f ks = zero;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) ks += kp[n][s];
+        lds_half<3>(s_x + n * kX, w >> 1, lane, w & 1,
+                    split4<3>(wide1<T>(v[n][0]) - gam[0] * ks[0], wide1<T>(v[n][1]) - gam[1] * ks[1],
+                              wide1<T>(v[n][2]) - gam[2] * ks[2], wide1<T>(v[n][3]) - gam[3] * ks[3]));
+      }
       load_v(next);
       __syncthreads();
-      v4f u = mma_short(t[0], lds_frag<3>(s_x, 0, lane));
-      if (w >= 2) u += mma_short(t[1], lds_frag<3>(s_x, 1, lane));
-      lds_half<3>(s_e, w >> 1, lane, w & 1,
-                  split4<3>(end[0] * u[0], end[1] * u[1], end[2] * u[2], end[3] * u[3]));
-      if constexpr (OUT) lds_half<PO>(s_u, w >> 1, lane, w & 1, split4<PO>(u[0], u[1], u[2], u[3]));
+      v4f u[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) u[n] = mma_short(t[0], lds_frag<3>(s_x + n * kX, 0, lane));
+      if (w >= 2)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) u[n] += mma_short(t[1], lds_frag<3>(s_x + n * kX, 1, lane));
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        lds_half<3>(s_e + n * kX, w >> 1, lane, w & 1,
+                    split4<3>(end[0] * u[n][0], end[1] * u[n][1], end[2] * u[n][2], end[3] * u[n][3]));
+        if constexpr (OUT)
+          lds_half<PO>(s_u + n * kU, w >> 1, lane, w & 1, split4<PO>(u[n][0], u[n][1], u[n][2], u[n][3]));
+      }
       load_t(next);
       __syncthreads();
       const unsigned char* kt = s_kt + (c & 1) * kCols;
-      v4f more[OWN];
+      v4f more[NC][OWN];
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) S[i] *= last, more[i] = zero;
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) S[n][i] *= last, more[n][i] = zero;
       load_last(next);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const Frag<3> e = lds_frag<3>(s_e, s, lane);
+        Frag<3> e[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) e[n] = lds_frag<3>(s_e + n * kX, s, lane);
 #pragma unroll
         for (int i = 0; i < OWN; ++i)
           if (w * OWN + i < NT) {
-            v4f& to = s ? more[i] : S[i];
-            to = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), e, to);
+            const Frag<PI> kf = lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              v4f& to = s ? more[n][i] : S[n][i];
+              to = mma<PI, 3>(kf, e[n], to);
+            }
           }
       }
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) S[i] += more[i];
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) S[n][i] += more[n][i];
       share_state();
       __syncthreads();
     }
@@ -450,13 +485,17 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
     __syncthreads();
     for (int c = 0; c < nch; ++c) {
       const int next = c < endc ? c + 1 : c;
-      v4f qs = zero;
+      v4f qs[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) qs[n] = zero;
       if constexpr (OUT) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           Half<PI> lo, hi;
           halves<PI>(q[s], lo, hi);
-          qs = mma<PI, PO>(join<PI>(lo, hi), lead<PO>(lds_frag<3>(s_s, s, lane)), qs);
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            qs[n] = mma<PI, PO>(join<PI>(lo, hi), lead<PO>(lds_frag<3>(s_s + n * kS, s, lane)), qs[n]);
         }
       }
       load_q(next);
@@ -469,20 +508,28 @@ __global__ void __launch_bounds__(512) k_delta_walk(DeltaArgs a) {
       if (TWO) load_k(c + 2 < nch ? c + 2 : endc);
       __syncthreads();
       if constexpr (OUT) {
-        v4f pu = mma<PO, PO>(p[0], lds_frag<PO>(s_u, 0, lane), zero);
-        if (w >= 2) pu = mma<PO, PO>(p[1], lds_frag<PO>(s_u, 1, lane), pu);
+        v4f pu[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) pu[n] = mma<PO, PO>(p[0], lds_frag<PO>(s_u + n * kU, 0, lane), zero);
+        if (w >= 2)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) pu[n] = mma<PO, PO>(p[1], lds_frag<PO>(s_u + n * kU, 1, lane), pu[n]);
         if (c == endc) value_offsets(delta_rows(sq, c), ooff);
         const auto obuf = delta_buf((T*)a.o + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          buf_store(obuf, ooff[r], a.scale * fmaf(gam[r], qs[r], pu[r]), T());
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            buf_store(obuf, ooff[r] + 16 * n * sizeof(T), a.scale * fmaf(gam[r], qs[n][r], pu[n][r]), T());
         load_p(next);
       }
       __syncthreads();
     }
     if (OUT && in)
       for (int t = sq.n + (id >> 4); t < a.L; t += 16)
-        put1((T*)a.o + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          put1((T*)a.o + (((size_t)b * a.L + t) * a.H + h) * a.dv + col + 16 * n, 0.f);
   }
 }
 // ---------------------------------------------------------------------------- single steps
@@ -614,25 +661,32 @@ void prep_mode(const DeltaArgs& a, bool vec, DeltaPrep mode, hipStream_t st) {
   else if (mode == kPrepStates) prep_t<T, kPrepStates>(a, vec, st);
   else prep_t<T, kPrepBackward>(a, vec, st);
 }
-template <typename T, int DK, bool VEC, bool OUT>
-hipError_t walk_one(const DeltaArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int bytes = WalkLds<T, DK>::bytes;
+template <typename T, int DK, bool VEC, bool OUT, int NC>
+hipError_t walk_one(const DeltaArgs& a, hipStream_t st) {
+  constexpr int bytes = WalkLds<T, DK, NC>::bytes;
   static_assert(bytes <= 160 * 1024, "LDS of a CU");
-  const hipError_t e = hipFuncSetAttribute((const void*)k_delta_walk<T, DK, VEC, OUT>,
+  // heads side by side in steps of 8: a head's columns then lie on one XCD and share its L2
+  const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 16 * NC - 1) / (16 * NC));
+  const hipError_t e = hipFuncSetAttribute((const void*)k_delta_walk<T, DK, VEC, OUT, NC>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  k_delta_walk<T, DK, VEC, OUT><<<grid, 512, bytes, st>>>(a);
+  k_delta_walk<T, DK, VEC, OUT, NC><<<grid, 512, bytes, st>>>(a);
   return hipGetLastError();
 }
 template <typename T>
 hipError_t walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
-  // heads side by side in steps of 8: a head's columns then lie on one XCD and share its L2
-  const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 15) / 16);
+  const bool two = walk_two_tiles(a);
   hipError_t e = hipSuccess;
   with_dk<T>(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;
     constexpr bool VEC = decltype(v)::value;
-    e = a.o ? walk_one<T, DK, VEC, true>(a, grid, st) : walk_one<T, DK, VEC, false>(a, grid, st);
+    if constexpr (VEC) {
+      if (two) {
+        e = a.o ? walk_one<T, DK, VEC, true, 2>(a, st) : walk_one<T, DK, VEC, false, 2>(a, st);
+        return;
+      }
+    }
+    e = a.o ? walk_one<T, DK, VEC, true, 1>(a, st) : walk_one<T, DK, VEC, false, 1>(a, st);
   });
   return e;
 }

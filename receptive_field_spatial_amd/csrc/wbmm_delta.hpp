@@ -102,6 +102,15 @@ constexpr size_t delta_p_bytes(bool bf16) { return (size_t)kDeltaFrags * 1024 * 
 constexpr size_t kDeltaTtBytes = (size_t)kDeltaFrags * 1024 * 3;
 
 DeltaArgs delta_args(const DeltaRequest& r);
+// Whether a workgroup of the walks takes two column tiles, which share its operands (K, T and P in registers
+// and LDS) and fill each other's waits: where tiles outnumber the CUs. Then (512 steps, dk = dv = 64, 16-column tiles;
+// us forward and backward of one against two): bf16 288 tiles 20.6, 32.7 against 19.8, 25.2, 768 48.5, 68.0
+// against 33.6, 50.5, 2048 155, 261 against 97, 161; up to 256 a tile each is the shorter walk: 14.6, 19.0
+// against 19.2, 24.6. fp32 288: 41.8, 59.3 against 27.3, 40.3. Of the measured ones only bf16 with dk = 128 and 640 tiles
+// loses (forward 44.0 against 51.2).
+inline bool walk_two_tiles(const DeltaArgs& a) {
+  return a.dv % 32 == 0 && (int64_t)a.B * a.H * (a.dv / 16) > 256;
+}
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
 // 16 bytes at a time of everything that lies in rows of dk or dv.

@@ -14,17 +14,17 @@ namespace {
 //   B    R = T^T dU (= dv)                               P^T G, K, K^T, Q^T and diag(y) G of the next chunk
 //   C    D = y_C D + M - K^T diag(y) R                   do of the one after
 // D after each chunk and R stay in the workspace for k_delta_grads.
-template <typename T, int DK>
+template <typename T, int DK, int NC>
 struct BackLds {
   static constexpr int PI = DeltaType<T, true>::PI, KS = DK / 32, NT = DK / 16;
   static constexpr int d = 0;                              // D
-  static constexpr int x = d + KS * 3 * 1024;              // dU
-  static constexpr int r = x + 2 * 3 * 1024;               // -diag(y) R
-  static constexpr int g = r + 2 * 3 * 1024;               // diag(y) G
-  static constexpr int o = g + 2 * 3 * 1024;               // do
-  static constexpr int m = o + 2 * PI * 1024;              // M, as results lie
-  static constexpr int pg = m + NT * 1024;                 // P^T G, as results lie
-  static constexpr int qt = pg + 4 * 1024;                 // Q^T
+  static constexpr int x = d + NC * KS * 3 * 1024;              // dU
+  static constexpr int r = x + NC * 2 * 3 * 1024;               // -diag(y) R
+  static constexpr int g = r + NC * 2 * 3 * 1024;               // diag(y) G
+  static constexpr int o = g + NC * 2 * 3 * 1024;               // do
+  static constexpr int m = o + NC * 2 * PI * 1024;              // M, as results lie
+  static constexpr int pg = m + NC * NT * 1024;                 // P^T G, as results lie
+  static constexpr int qt = pg + NC * 4 * 1024;                 // Q^T
   static constexpr int cols = NT * kTileBytes<PI>;
   static constexpr int kt = qt + cols;                     // K^T, of two chunks where they fit
   static constexpr int rows = 4 * KS * PI * 1024;
@@ -35,12 +35,13 @@ struct BackLds {
   static constexpr int bytes = k + (direct ? 0 : rows);
 };
 
-template <typename T, int DK, bool VEC>
+template <typename T, int DK, bool VEC, int NC>
 __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
-  using Lds = BackLds<T, DK>;
+  using Lds = BackLds<T, DK, NC>;
   constexpr int PI = Ty::PI, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
   constexpr bool TWO = Lds::two, DIRECT = Lds::direct;
+  constexpr int kD = KS * 3 * 1024, kX = 2 * 3 * 1024, kO = 2 * PI * 1024, kM = NT * 1024;   // of a column tile
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   const int bh = blockIdx.x;
   if (bh >= a.B * a.H) return;
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
   const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
-  const int col = blockIdx.y * 16 + row;
+  const int col = blockIdx.y * (16 * NC) + row;
   const bool in = col < a.dv;
   const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
   };
 
   if (walker) {
-    v4f D[OWN];
+    v4f D[NC][OWN];
     uint32_t soff[OWN][4], roff[4], voff[4], koff = 0;
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
@@ -73,7 +74,9 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
         const int k = walk_entry(w * OWN + i, 4 * gq + r);
         const bool own = w * OWN + i < NT && k < a.dk && in;
         soff[i][r] = own ? (uint32_t)(k * a.dv + col) * 4 : kNowhere;
-        D[i][r] = a.ds_last ? buf_load<float>(delta_buf(a.ds_last + bh * sdim), soff[i][r]) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          D[n][i][r] = a.ds_last ? buf_load<float>(delta_buf(a.ds_last + bh * sdim), soff[i][r] + 64 * n) : 0.f;
       }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -83,15 +86,19 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) buf_store(buf, soff[i][r], D[i][r], 0.f);
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) buf_store(buf, soff[i][r] + 64 * n, D[n][i][r], 0.f);
     };
     auto share_state = [&] {
 #pragma unroll
       for (int i = 0; i < OWN; ++i) {
         const int tile = w * OWN + i;
         if (tile < NT)
-          lds_half<3>(sm + Lds::d, tile >> 1, lane, tile & 1,
-                      split4<3>(D[i][0], D[i][1], D[i][2], D[i][3]));
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            lds_half<3>(sm + Lds::d + n * kD, tile >> 1, lane, tile & 1,
+                        split4<3>(D[n][i][0], D[n][i][1], D[n][i][2], D[n][i][3]));
       }
     };
     Frag<3> t[2];
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       const size_t ch = (size_t)bh * a.chunks + c;
       const int next = c > 0 ? c - 1 : 0;
       put_state(a.D + ch * sdim);
-      v4f kd = zero, kp[KS];
+      v4f kp[NC][KS];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         Frag<PI> f;
@@ -142,50 +149,74 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
         } else {
           f = lds_frag<PI>(sm + Lds::k, w * KS + s, lane);
         }
-        kp[s] = mma<PI, 3>(f, lds_frag<3>(sm + Lds::d, s, lane), zero);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) kp[n][s] = mma<PI, 3>(f, lds_frag<3>(sm + Lds::d + n * kD, s, lane), zero);
       }
 #pragma unroll
-      for (int s = 0; s < KS; ++s) kd += kp[s];
-      const v4f pg = *(const v4f*)(sm + Lds::pg + w * 1024 + lane * 16);
-      lds_half<3>(sm + Lds::x, w >> 1, lane, w & 1,
-                  split4<3>(fmaf(end[0], kd[0], pg[0]), fmaf(end[1], kd[1], pg[1]),
-                            fmaf(end[2], kd[2], pg[2]), fmaf(end[3], kd[3], pg[3])));
+      for (int n = 0; n < NC; ++n) {
+        v4f kd = zero;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kd += kp[n][s];
+        const v4f pg = *(const v4f*)(sm + Lds::pg + (4 * n + w) * 1024 + lane * 16);
+        lds_half<3>(sm + Lds::x + n * kX, w >> 1, lane, w & 1,
+                    split4<3>(fmaf(end[0], kd[0], pg[0]), fmaf(end[1], kd[1], pg[1]),
+                              fmaf(end[2], kd[2], pg[2]), fmaf(end[3], kd[3], pg[3])));
+      }
       load_k(next);
       __syncthreads();
-      v4f rr = mma_short(t[1], lds_frag<3>(sm + Lds::x, 1, lane));
-      if (w < 2) rr += mma_short(t[0], lds_frag<3>(sm + Lds::x, 0, lane));
-      lds_half<3>(sm + Lds::r, w >> 1, lane, w & 1,
-                  split4<3>(-gam[0] * rr[0], -gam[1] * rr[1], -gam[2] * rr[2], -gam[3] * rr[3]));
+      v4f rr[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) rr[n] = mma_short(t[1], lds_frag<3>(sm + Lds::x + n * kX, 1, lane));
+      if (w < 2)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) rr[n] += mma_short(t[0], lds_frag<3>(sm + Lds::x + n * kX, 0, lane));
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        lds_half<3>(sm + Lds::r + n * kX, w >> 1, lane, w & 1,
+                    split4<3>(-gam[0] * rr[n][0], -gam[1] * rr[n][1], -gam[2] * rr[n][2], -gam[3] * rr[n][3]));
       load_t(next);
       const auto rbuf = delta_buf(a.R + ch * kDeltaChunk * a.dv);
       const auto vbuf = delta_buf((T*)a.dval + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        buf_store(rbuf, roff[r], rr[r], 0.f);
-        buf_store(vbuf, voff[r], rr[r], T());
-      }
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          buf_store(rbuf, roff[r] + 64 * n, rr[n][r], 0.f);
+          buf_store(vbuf, voff[r] + 16 * n * sizeof(T), rr[n][r], T());
+        }
       if (c == endc) value_offsets(delta_rows(sq, next), voff);
       __syncthreads();
       const unsigned char* kt = sm + Lds::kt + (TWO ? c & 1 : 0) * Lds::cols;
-      v4f more[OWN];
+      v4f more[NC][OWN];
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) {
-        D[i] *= last;
-        more[i] = w * OWN + i < NT ? *(const v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16) : zero;
-      }
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+          D[n][i] *= last;
+          more[n][i] = w * OWN + i < NT
+                           ? *(const v4f*)(sm + Lds::m + n * kM + (w * OWN + i) * 1024 + lane * 16) : zero;
+        }
       load_last(next);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const Frag<3> f = lds_frag<3>(sm + Lds::r, s, lane);
+        Frag<3> f[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) f[n] = lds_frag<3>(sm + Lds::r + n * kX, s, lane);
 #pragma unroll
         for (int i = 0; i < OWN; ++i)
           if (w * OWN + i < NT) {
-            v4f& to = s ? more[i] : D[i];
-            to = mma<PI, 3>(lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane), f, to);
+            const Frag<PI> kf = lds_frag<PI>(kt + (w * OWN + i) * kTileBytes<PI>, s, lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              v4f& to = s ? more[n][i] : D[n][i];
+              to = mma<PI, 3>(kf, f[n], to);
+            }
           }
       }
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) D[i] += more[i];
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) D[n][i] += more[n][i];
       share_state();
       __syncthreads();
     }
@@ -195,7 +226,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
     const bool block = tg < 16;      // a 4 x 8 block of K and of Q
     Raw8<T, VEC> kb[4], qb[4];
     Frag<3> p[2];
-    uint32_t g[4], g2[4];            // do of the next chunk and of the one after
+    uint32_t g[NC][4], g2[NC][4];    // do of the next chunk and of the one after
     v4f gam = zero;
     uint32_t boff[4], goff[4];
     auto load_kq = [&](int c) {
@@ -212,11 +243,13 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       for (int j = 0; j < 4; ++j) qb[j] = raw8<T, VEC>(qbuf, boff[j], 8 * dg, a.dk);
       gam = *(const v4f*)&a.gates[(size_t)bh * a.chunks + c].gam[16 * w + 4 * gq];
     };
-    auto load_g = [&](int c, uint32_t (&to)[4]) {
+    auto load_g = [&](int c, uint32_t (&to)[NC][4]) {
       if (c == endc || c == endc - 1) value_offsets(delta_rows(sq, c), goff);
       const auto obuf = delta_buf((const T*)a.dout + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) to[r] = raw1<T>(obuf, goff[r]);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) to[n][r] = raw1<T>(obuf, goff[r] + 16 * n * sizeof(T));
     };
     auto load_p = [&](int c) {
       const unsigned char* Pm = a.Pt + ((size_t)bh * a.chunks + c) * kDeltaTtBytes;
@@ -237,19 +270,32 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       if (block) lds_cols<PI>(sm + Lds::qt, tg, dg, lo, hi);
     };
     auto share_g = [&] {             // diag(y) G
-      lds_half<3>(sm + Lds::g, w >> 1, lane, w & 1,
-                  split4<3>(a.scale * gam[0] * wide1<T>(g[0]), a.scale * gam[1] * wide1<T>(g[1]),
-                            a.scale * gam[2] * wide1<T>(g[2]), a.scale * gam[3] * wide1<T>(g[3])));
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        lds_half<3>(sm + Lds::g + n * kX, w >> 1, lane, w & 1,
+                    split4<3>(a.scale * gam[0] * wide1<T>(g[n][0]), a.scale * gam[1] * wide1<T>(g[n][1]),
+                              a.scale * gam[2] * wide1<T>(g[n][2]), a.scale * gam[3] * wide1<T>(g[n][3])));
     };
-    auto share_o = [&](const uint32_t (&o)[4]) {
-      lds_half<PI>(sm + Lds::o, w >> 1, lane, w & 1,
-                   split4<PI>(wide1<T>(o[0]), wide1<T>(o[1]), wide1<T>(o[2]), wide1<T>(o[3])));
+    auto share_o = [&](const uint32_t (&o)[NC][4]) {
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        lds_half<PI>(sm + Lds::o + n * kO, w >> 1, lane, w & 1,
+                     split4<PI>(wide1<T>(o[n][0]), wide1<T>(o[n][1]), wide1<T>(o[n][2]), wide1<T>(o[n][3])));
     };
     auto form_pg = [&] {
-      v4f pg = zero;
-      if (w < 2) pg = mma<3, PI>(p[0], lds_frag<PI>(sm + Lds::o, 0, lane), pg);
-      pg = mma<3, PI>(p[1], lds_frag<PI>(sm + Lds::o, 1, lane), pg);
-      *(v4f*)(sm + Lds::pg + w * 1024 + lane * 16) = pg * a.scale;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        v4f pg = zero;
+        if (w < 2) pg = mma<3, PI>(p[0], lds_frag<PI>(sm + Lds::o + n * kO, 0, lane), pg);
+        pg = mma<3, PI>(p[1], lds_frag<PI>(sm + Lds::o + n * kO, 1, lane), pg);
+        *(v4f*)(sm + Lds::pg + (4 * n + w) * 1024 + lane * 16) = pg * a.scale;
+      }
+    };
+    auto next_g = [&] {
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) g[n][r] = g2[n][r];
     };
     auto back = [&](int c, int by) { return c >= by ? c - by : 0; };
     if (nch > 0) {
@@ -267,8 +313,7 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
     __syncthreads();
     if (nch > 0) {
       share_o(g2);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) g[r] = g2[r];
+      next_g();
       load_p(back(endc, 1));
       load_g(back(endc, 2), g2);
       if (TWO) load_kq(back(endc, 1));
@@ -279,12 +324,18 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
         if (w * OWN + i < NT) {
-          v4f m = zero;
+          v4f m[NC];
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
-            m = mma<PI, 3>(lds_frag<PI>(sm + Lds::qt + (w * OWN + i) * kTileBytes<PI>, s, lane),
-                           lds_frag<3>(sm + Lds::g, s, lane), m);
-          *(v4f*)(sm + Lds::m + (w * OWN + i) * 1024 + lane * 16) = m;
+          for (int n = 0; n < NC; ++n) m[n] = zero;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const Frag<PI> f = lds_frag<PI>(sm + Lds::qt + (w * OWN + i) * kTileBytes<PI>, s, lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) m[n] = mma<PI, 3>(f, lds_frag<3>(sm + Lds::g + n * kX, s, lane), m[n]);
+          }
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            *(v4f*)(sm + Lds::m + n * kM + (w * OWN + i) * 1024 + lane * 16) = m[n];
         }
       if (!TWO) {
         share_k(c, false, true);
@@ -299,14 +350,15 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
       if (TWO) load_kq(back(c, 2));
       __syncthreads();
       share_o(g2);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) g[r] = g2[r];
+      next_g();
       load_g(back(c, 3), g2);
       __syncthreads();
     }
     if (in)
       for (int t = sq.n + (id >> 4); t < a.L; t += 16)
-        put1((T*)a.dval + (((size_t)b * a.L + t) * a.H + h) * a.dv + col, 0.f);
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          put1((T*)a.dval + (((size_t)b * a.L + t) * a.H + h) * a.dv + col + 16 * n, 0.f);
   }
 }
 
@@ -750,18 +802,29 @@ void with_dk(int dk, bool vec, F f) {
 
 template <typename T>
 hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
-  const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 15) / 16);
   hipError_t e = hipSuccess;
   with_dk(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;
     constexpr bool VEC = decltype(v)::value;
-    constexpr int back = BackLds<T, DK>::bytes;
-    static_assert(back <= 160 * 1024, "LDS of a CU");
-    e = hipFuncSetAttribute((const void*)k_delta_walk_bwd<T, DK, VEC>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, back);
-    if (e != hipSuccess) return;
-    k_delta_walk_bwd<T, DK, VEC><<<grid, 512, back, st>>>(a);
-    e = hipGetLastError();
+    auto walk = [&](auto n) {
+      constexpr int NC = decltype(n)::value;
+      constexpr int back = BackLds<T, DK, NC>::bytes;
+      static_assert(back <= 160 * 1024, "LDS of a CU");
+      const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 16 * NC - 1) / (16 * NC));
+      e = hipFuncSetAttribute((const void*)k_delta_walk_bwd<T, DK, VEC, NC>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, back);
+      if (e != hipSuccess) return;
+      k_delta_walk_bwd<T, DK, VEC, NC><<<grid, 512, back, st>>>(a);
+      e = hipGetLastError();
+    };
+    bool done = false;
+    if constexpr (VEC && BackLds<T, DK, 2>::bytes <= 160 * 1024) {
+      if (walk_two_tiles(a)) {
+        walk(std::integral_constant<int, 2>());
+        done = true;
+      }
+    }
+    if (!done) walk(std::integral_constant<int, 1>());
     if (e != hipSuccess) return;
     constexpr int bytes = GradLds<T, DK, VEC>::bytes;
     static_assert(bytes <= 160 * 1024, "LDS of a CU");

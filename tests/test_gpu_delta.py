@@ -335,6 +335,31 @@ def test_many_heads_and_batches_are_each_their_own():
             assert all(torch.equal(a[b:b + 1], x) for a, x in zip(gr, one.backward(o1[2])))
 
 
+@pytest.mark.parametrize("dt,B,Hk,H,dk,dv,reverse,s0", [
+    (F32, 40, 2, 4, 24, 32, False, True), (BF16, 40, 1, 1, 128, 128, True, True), (F32, 140, 1, 1, 128, 32, False, False),
+    (BF16, 70, 1, 2, 40, 64, True, False), (F32, 44, 1, 2, 64, 64, True, True), (BF16, 130, 1, 3, 32, 32, False, True),
+    (BF16, 70, 1, 2, 33, 64, False, True)])
+def test_sequences_of_a_large_padded_batch(dt, B, Hk, H, dk, dv, reverse, s0):
+    """Batches that are walked two tiles of columns at a time: each sequence as in a batch of its own."""
+    print(f"\n[case] delta large {B} heads {Hk}/{H} {dk}x{dv} {dt}", flush=True)
+    L = 130
+    lens = [L - (37 * b) % (L + 9) for b in range(B)]
+    c = Case(B, L, Hk, H, dk, dv, dt, reverse, lens, s0, seed=137)
+    out = c.forward()
+    gr = c.backward(out[2])
+    for b in (0, 1, 3, B - 1):
+        one = Case(1, L, Hk, H, dk, dv, dt, reverse, [lens[b]], s0)
+        for n in ("q", "k", "v", "g", "beta", "do", "dl") + (("s0",) if s0 else ()):
+            setattr(one, n, getattr(c, n)[b:b + 1].contiguous())
+        o1 = one.forward()
+        g1 = one.backward(o1[2])
+        assert all(torch.equal(a[b:b + 1], x) for a, x in zip(out, o1))
+        assert all(torch.equal(a[b:b + 1], x) for a, x in zip(gr, g1))
+        if b == 1:
+            one.check_forward(*o1)
+            one.check_backward(g1)
+
+
 def test_offsets_past_32_bits():
     """Tensors of 4.3e9 bytes, and one sequence that is: its end equals a run from the states kept there."""
     for B, L in ((1030, 512), (1, 1030 * 512)):
