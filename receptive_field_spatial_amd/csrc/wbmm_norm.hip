@@ -43,6 +43,7 @@ struct NormArgs {
   uint8_t* scales;
   double* part;                    // [workgroups][len]
   float eps, inv;                  // inv = 1 / len
+  double inv64;
   int fmt;
   uint32_t len, rows;              // rows = outer * inner
   uint32_t tiles;
@@ -93,8 +94,8 @@ __device__ __forceinline__ void carry_add(float& acc, float& c, float x) {
 
 // Sum over the LPR lanes of a row, in every one of them. LPR = 256: the workgroup's, through sm
 // (4 floats, another set for each call between two barriers).
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v, float* sm) {
+template <int LPR, typename S>
+__device__ __forceinline__ S row_sum(S v, S* sm) {
 #pragma unroll
   for (int d = 1; d < (LPR < 64 ? LPR : 64); d *= 2) v += __shfl_xor(v, d);
   if (LPR == 256) {
@@ -111,6 +112,25 @@ __device__ __forceinline__ float rstd_of(float sum, float inv, float eps) {
   // one Newton step for the last bit; infinities, zeros and NaN are left as they are
   const float f = fmaf(r * 0.5f, fmaf(-m * r, r, 1.f), r);
   return __builtin_isfinite(f) && r > 0.f ? f : r;
+}
+
+// The forward's rstd, in two floats. A code of 8 bits, and a bf16 y, hang on y's last bit where y lies between
+// two of them, so y is formed to that bit: the sum in fp64, y = t (rstd w) with one rounding. Of 12.4 M fp32 y 10 to
+// 30 codes differed from those of the exact y before, 1 to 9 now (t's own rounding); of bf16 y none. 128 x
+// 96 x 3136 fp32 takes 90 us with either, 50176 rows of 192 bf16 from the last-level cache 12.8 for 11.5.
+struct Rstd {
+  float hi, lo;
+  __device__ __forceinline__ float y(float t, float w) const {
+    const float f = hi * w;
+    return fmaf(t, f, t * fmaf(lo, w, fmaf(hi, w, -f)));
+  }
+};
+__device__ __forceinline__ Rstd rstd_of(double sum, const NormArgs& a) {
+  const double m = fma(sum, a.inv64, (double)a.eps), r = __builtin_amdgcn_rsq(m);
+  // a Newton step; infinities, zeros and NaN are left as they are
+  const double f = fma(r * 0.5, fma(-m * r, r, 1.0), r);
+  const float hi = (float)(__builtin_isfinite(f) && r > 0.0 ? f : r);
+  return {hi, __builtin_isfinite(hi) && hi > 0.f ? (float)(f - (double)hi) : 0.f};
 }
 
 // ---------------------------------------------------------------------------- rows
@@ -165,7 +185,7 @@ struct RowPieces {
 template <typename T, int LPR, int K, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_norm_rows(NormArgs a) {
   constexpr int RPW = kThreads / LPR;   // rows of a workgroup
-  __shared__ float sm[4];
+  __shared__ double sm[4];
   const RowPieces<T, LPR, K, VEC> pc{(int)(threadIdx.x % LPR), a.len};
   const uint32_t row = blockIdx.x * RPW + threadIdx.x / LPR;
   const bool live = row < a.rows;
@@ -183,19 +203,19 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows(NormArgs a) {
   }
   float w[K][kP];
   pc.weights(a.w, w);
-  float sum = 0.f;
+  double sum = 0.0;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < kP; ++j) sum = fmaf(t[k][j], t[k][j], sum);
-  const float rstd = rstd_of(row_sum<LPR>(sum, sm), a.inv, a.eps);
+    for (int j = 0; j < kP; ++j) sum = fma((double)t[k][j], (double)t[k][j], sum);
+  const Rstd rstd = rstd_of(row_sum<LPR>(sum, sm), a);
   if (!live) return;   // no barrier and no exchange across rows from here on
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (a.s) pc.store((T*)a.s + base, k, t[k]);
     float y[kP];
 #pragma unroll
-    for (int j = 0; j < kP; ++j) y[j] = t[k][j] * rstd * w[k][j];
+    for (int j = 0; j < kP; ++j) y[j] = rstd.y(t[k][j], w[k][j]);
     pc.store((T*)a.y + base, k, y);
     if (VEC && a.codes) {   // len a multiple of 32: a group is a quad's, in or out together
       uint32_t m = 0;
@@ -227,19 +247,19 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows(NormArgs a) {
 // Rows longer than the registers: the workgroup reads a row twice.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_rows_long(NormArgs a) {
-  __shared__ float sm[4];
+  __shared__ double sm[4];
   const size_t base = (size_t)blockIdx.x * a.len;
   const T *x = (const T*)a.x + base, *res = a.res ? (const T*)a.res + base : nullptr;
-  float sum = 0.f, c = 0.f;
+  double sum = 0.0;
   for (uint32_t e = threadIdx.x; e < a.len; e += kThreads) {
     const float t = load_f32<T>(x, e) + (res ? load_f32<T>(res, e) : 0.f);
-    carry_add(sum, c, t * t);
+    sum = fma((double)t, (double)t, sum);
   }
-  const float rstd = rstd_of(row_sum<256>(sum, sm), a.inv, a.eps);
+  const Rstd rstd = rstd_of(row_sum<256>(sum, sm), a);
   for (uint32_t e = threadIdx.x; e < a.len; e += kThreads) {
     const float t = load_f32<T>(x, e) + (res ? load_f32<T>(res, e) : 0.f);
     if (a.s) put((T*)a.s + base + e, t);
-    put((T*)a.y + base + e, t * rstd * (a.w ? a.w[e] : 1.f));
+    put((T*)a.y + base + e, rstd.y(t, a.w ? a.w[e] : 1.f));
   }
 }
 
@@ -375,15 +395,15 @@ __device__ __forceinline__ void store_n(T* p, const float (&v)[VW]) {
   else *(uint32_t*)p = bf_bits(v[0]) | (bf_bits(v[1]) << 16);
 }
 
-// Sum over the workgroup's waves of each lane's VW values, in every wave; sm: NW * 64 * VW floats.
-template <int VW>
-__device__ __forceinline__ void wave_join(float (&v)[VW], float* sm, int NW) {
+// Sum over the workgroup's waves of each lane's VW values, in every wave; sm: NW * 64 * VW of them.
+template <int VW, typename S>
+__device__ __forceinline__ void wave_join(S (&v)[VW], S* sm, int NW) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
 #pragma unroll
   for (int j = 0; j < VW; ++j) sm[(wv * VW + j) * 64 + lane] = v[j];
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < VW; ++j) v[j] = 0.f;
+  for (int j = 0; j < VW; ++j) v[j] = 0;
   for (int q = 0; q < NW; ++q)
 #pragma unroll
     for (int j = 0; j < VW; ++j) v[j] += sm[(q * VW + j) * 64 + lane];
@@ -470,14 +490,15 @@ __device__ __forceinline__ void col_codes(const NormArgs& a, size_t at, float (&
 // N: entries of the axis per wave that are kept in registers; 0: any number, read twice.
 template <typename T, int VW, int N>
 __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float sm[];
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  double* const sm = (double*)lds;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   const ColAt c = col_at<VW>(a, blockIdx.x);
   const T* x = (const T*)a.x + c.base;
   const T* res = a.res ? (const T*)a.res + c.base : nullptr;
-  float sq[VW];
+  double sq[VW];
 #pragma unroll
-  for (int j = 0; j < VW; ++j) sq[j] = 0.f;
+  for (int j = 0; j < VW; ++j) sq[j] = 0.0;
   auto sum_at = [&](uint32_t e, float (&t)[VW]) {
     load_n<T, VW>(x + (size_t)e * c.stride, t);
     if (res) {
@@ -487,11 +508,11 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
       for (int j = 0; j < VW; ++j) t[j] += r[j];
     }
   };
-  auto finish = [&](uint32_t e, const float (&t)[VW], const float (&rstd)[VW], float w) {
+  auto finish = [&](uint32_t e, const float (&t)[VW], const Rstd (&rstd)[VW], float w) {
     const size_t at = c.base + (size_t)e * c.stride;
     float y[VW];
 #pragma unroll
-    for (int j = 0; j < VW; ++j) y[j] = t[j] * rstd[j] * w;
+    for (int j = 0; j < VW; ++j) y[j] = rstd[j].y(t[j], w);
     if (c.live) {
       if (a.s) store_n<T, VW>((T*)a.s + at, t);
       store_n<T, VW>((T*)a.y + at, y);
@@ -518,30 +539,27 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
     for (int k = 0; k < N; ++k)
       if (wv + NW * k < (int)a.len)
 #pragma unroll
-        for (int j = 0; j < VW; ++j) sq[j] = fmaf(t[k][j], t[k][j], sq[j]);
+        for (int j = 0; j < VW; ++j) sq[j] = fma((double)t[k][j], (double)t[k][j], sq[j]);
     wave_join<VW>(sq, sm, NW);
-    float rstd[VW];
+    Rstd rstd[VW];
 #pragma unroll
-    for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a.inv, a.eps);
+    for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const uint32_t e = wv + NW * k;
       if (e < a.len) finish(e, t[k], rstd, w[k]);
     }
   } else {
-    float cc[VW];
-#pragma unroll
-    for (int j = 0; j < VW; ++j) cc[j] = 0.f;
     for (uint32_t e = wv; e < a.len; e += NW) {
       float t[VW];
       sum_at(e, t);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) carry_add(sq[j], cc[j], t[j] * t[j]);
+      for (int j = 0; j < VW; ++j) sq[j] = fma((double)t[j], (double)t[j], sq[j]);
     }
     wave_join<VW>(sq, sm, NW);
-    float rstd[VW];
+    Rstd rstd[VW];
 #pragma unroll
-    for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a.inv, a.eps);
+    for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a);
     for (uint32_t e = wv; e < a.len; e += NW) {
       float t[VW];
       sum_at(e, t);
@@ -556,7 +574,8 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
 template <typename T, int N, bool DW>
 __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
   constexpr int VW = 1;
-  extern __shared__ __attribute__((aligned(16))) float sm[];
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  float* const sm = (float*)lds;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   const int lane = threadIdx.x & 63;
   constexpr int M = N > 0 ? N : 1;
@@ -751,7 +770,7 @@ NormArgs args_of(const NormRequest& r) {
   NormArgs a{};
   a.x = r.x; a.res = r.res; a.w = r.w; a.dy = r.dy; a.s = r.s; a.y = r.y;
   a.codes = r.codes; a.scales = r.scales; a.part = (double*)r.ws;
-  a.eps = r.eps; a.inv = (float)(1.0 / (double)r.len); a.fmt = r.fmt;
+  a.eps = r.eps; a.inv64 = 1.0 / (double)r.len; a.inv = (float)a.inv64; a.fmt = r.fmt;
   a.len = (uint32_t)r.len; a.rows = (uint32_t)(r.outer * r.inner);
   a.inner = fast_div((uint32_t)r.inner);
   return a;
@@ -834,7 +853,7 @@ bool forward_t(const NormRequest& r, hipStream_t st) {   // whether the codes we
   with_cols(s, [&](auto vw, auto n) {
     constexpr int VW = decltype(vw)::value, N = decltype(n)::value;
     if constexpr (N * VW <= kColFwd && (VW == 1 || (sizeof(T) == 2 && N > 0)))
-      k_norm_cols<T, VW, N><<<dim3(a.tiles), 64 * s.nw, s.nw * 64 * VW * 4, st>>>(a);
+      k_norm_cols<T, VW, N><<<dim3(a.tiles), 64 * s.nw, s.nw * 64 * VW * 8, st>>>(a);
   });
   return a.codes != nullptr;
 }
