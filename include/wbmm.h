@@ -453,9 +453,8 @@ wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inner, int dt
  * what stands before a mixer. Tensors are dense (outer, len, inner) and normed over len, for every
  * (outer, inner): the channels of a map are (B, C, H W) in NCHW, (B H W, C, 1) in NHWC.
  *   t = x + residual,   y = t weight / sqrt(mean_len(t^2) + eps).
- * Computed in fp32 from the sum as it is; s and y are rounded once (RNE). Squares are fp32: |t| beyond
- * about 1.8e19 makes their mean infinite and y zero there. An infinity or NaN in t reaches its own
- * (outer, inner) only.
+ * t is formed in fp32 and normed as it is, its squares summed in fp64; s and y are rounded once (RNE). An
+ * infinity or NaN in t reaches its own (outer, inner) only.
  * dtype:    of x, residual, s and y: WBMM_F32 or WBMM_BF16.
  * residual: device tensor, or NULL. weight: device fp32 [len], or NULL for ones.
  * s:        device tensor, t in dtype (what the backward takes), or NULL. May be x or residual itself.
@@ -478,6 +477,7 @@ wbmm_status wbmm_rmsnorm_forward(int64_t outer, int64_t len, int64_t inner, int 
  * the sum that it stored:
  *   r = 1 / sqrt(mean(s^2) + eps),   h = s r,
  *   dx = ds + r (weight dy - h mean(weight dy h)),   dweight = sum over (outer, inner) of dy h.
+ * Computed in fp32: |s| beyond about 1.8e19 makes the mean of its squares infinite and r zero there.
  * s:       the forward's s (its x where there was no residual). dy: gradient of y.
  * ds:      gradient of s from elsewhere (the residual's further way), or NULL for zeros.
  * dx:      device tensor in dtype, the gradient of x and of residual alike, or NULL to skip.
@@ -506,7 +506,8 @@ wbmm_status wbmm_rmsnorm_backward(int64_t outer, int64_t len, int64_t inner, int
  *             checkpoints in WBMM_CKPT_E4M3 (n code bytes and ceil(n / WBMM_CKPT_GROUP) scale bytes each;
  *             all zero bytes are zero states). They are read as wbmm_ckpt_unpack gives them. What is
  *             stored is rounded to one of the two neighbouring code values at random, to the value
- *             itself on average, a root above zero never to 0; random words are Philox 4x32 with 7
+ *             itself on average, a root above zero never to 0 (v, the root's square, moves up to 1/16 further
+ *             than unrounded, on average, as the root's variance joins it); random words are Philox 4x32 with 7
  *             rounds, counter (index / 4 as 64 bits, tensor, t), key `seed`, word index % 4, its low
  *             16 bits for m and its high ones for the root. A group that holds an infinity or a NaN
  *             becomes NaN, as in wbmm_ckpt_pack.

@@ -17,7 +17,9 @@
 //
 // Bound by memory: 28 bytes an element with fp32 states and gradients, 16.1 with 8-bit ones. A
 // workgroup takes 4096 elements of one tensor, a thread twice 8 neighbouring ones; four lanes hold a
-// group of 32. Sums, products and quotients are rounded one by one (no fused multiply-add), so that
+// group of 32. Measured: 52.5 M parameters with fp32 states 262 us (5.6 TB/s, part of it from the
+// last-level cache), with 8-bit ones, bf16 gradients and a bf16 copy 172 (4.9 TB/s); 0.44 M 6.2 us.
+// Sums, products and quotients are rounded one by one (no fused multiply-add), so that
 // a result does not depend on how the compiler pairs them: a code may hang on a last bit.
 #pragma clang fp contract(off)
 #include "wbmm_adamw.hpp"
