@@ -799,7 +799,8 @@ def wbmm_rmsnorm_backward(s, dy, dim: int, *, weight=None, ds=None, eps: float =
                           dweight=True, workspace=None, stream=None):
     """Gradients of wbmm_rmsnorm_forward at the sum s that it returned. ds: gradient of s from
     elsewhere, or None. Returns (dx, dweight): dx in s's dtype is the gradient of x and of the
-    residual, dweight fp32 (None without a weight); an output passed as False is skipped."""
+    residual, dweight fp32 (None without a weight, unless a tensor is given); an output passed as False
+    is skipped."""
     if stream is not None:
         with _on_stream(stream, "s", s):
             return wbmm_rmsnorm_backward(s, dy, dim, weight=weight, ds=ds, eps=eps, dx=dx,
@@ -810,8 +811,9 @@ def wbmm_rmsnorm_backward(s, dy, dim: int, *, weight=None, ds=None, eps: float =
     sp, dyp = _need("s", s, shape, dtype, idx), _need("dy", dy, shape, dtype, idx)
     wp, dsp = _opt("weight", weight, (length,), f32, idx), _opt("ds", ds, shape, dtype, idx)
     dx, dxp = _out("dx", dx, shape, dtype, idx, s)
-    dweight, dwp = _out("dweight", dweight if weight is not None else None, (length,), f32, idx,
-                        weight)
+    if dweight is True and weight is None:
+        dweight = None
+    dweight, dwp = _out("dweight", dweight, (length,), f32, idx, weight)
     need = 0 if dwp is None else wbmm_rmsnorm_backward_workspace_bytes(outer, length, inner)
     ws, wsp, wsb = _workspace(need, workspace, idx)
     _check(_lib().wbmm_rmsnorm_backward(outer, length, inner, dt, eps, sp, wp, dyp, dsp, dxp, dwp,

@@ -360,6 +360,30 @@ def test_sequences_of_a_large_padded_batch(dt, B, Hk, H, dk, dv, reverse, s0):
             one.check_backward(g1)
 
 
+def test_refused_tensors():
+    M = R()
+    c = Case(2, 70, 1, 2, 16, 20, F32, seed=1)
+    q, k, v, g, b = c.inputs()
+    bad = [(q[:1], k, v, g, b), (q, k[..., :8], v, g, b), (q, k, v.bfloat16(), g, b), (q, k, v, g[:, :5], b),
+           (q, k, v, g, b.cpu()), (q.half(), k, v, g, b), (q, k.transpose(0, 1).contiguous().transpose(0, 1), v, g, b),
+           (q.repeat(1, 1, 3, 1), k.repeat(1, 1, 3, 1), v, g, b)]
+    for args in bad:
+        with pytest.raises(M.WbmmError):
+            M.wbmm_delta_forward(*args)
+        with pytest.raises(M.WbmmError):
+            M.wbmm_delta_backward(*args, c.do)
+    lens = torch.tensor([70, 3], dtype=torch.int32, device="cuda")
+    states = c.forward()[2]
+    for kw in (dict(s0=c.s0[:1]), dict(s0=c.s0.bfloat16()), dict(lens=lens.long()), dict(lens=lens[:1]), dict(o=v),
+               dict(scale=float("inf")), dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(M.WbmmError):
+            M.wbmm_delta_forward(q, k, v, g, b, **kw)
+    for kw in (dict(states=states[:, :, :1]), dict(states=states, s0=c.s0), dict(dv=c.do), dict(ds_last=c.dl[0]),
+               dict(states=states, ds0=states[:, :, 0]), dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(M.WbmmError):
+            M.wbmm_delta_backward(q, k, v, g, b, c.do, **kw)
+
+
 def test_offsets_past_32_bits():
     """Tensors of 4.3e9 bytes, and one sequence that is: its end equals a run from the states kept there."""
     for B, L in ((1030, 512), (1, 1030 * 512)):

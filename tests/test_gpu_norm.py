@@ -203,6 +203,34 @@ def test_infinities_and_nan_stay_in_their_row(o, c, i):
     assert y[0, :, 0].isnan().all() and y[o - 1, 5, i - 1].isnan()
 
 
+def test_weight_gradient_without_a_weight():
+    """A tensor given is written: the gradient of a weight of ones."""
+    s, dy = mk((50, 64, 1), 2.0, 1), mk((50, 64, 1), 1.0, 2)
+    dw = torch.zeros(64, device="cuda")
+    dx, got = R().wbmm_rmsnorm_backward(s, dy, 1, dweight=dw)
+    want = R().wbmm_rmsnorm_backward(s, dy, 1, weight=torch.ones(64, device="cuda"))
+    assert got is dw and torch.equal(dw, want[1]) and torch.equal(dx, want[0])
+    assert R().wbmm_rmsnorm_backward(s, dy, 1)[1] is None
+
+
+def test_refused_tensors():
+    M = R()
+    x, w = mk((4, 6, 8), 1.0, 1), torch.ones(6, device="cuda")
+    for kw in (dict(residual=x.bfloat16()), dict(residual=x[:2]), dict(weight=w[:5]), dict(weight=w.double()),
+               dict(y=x), dict(residual=x.cpu()), dict(codes=x), dict(fmt="int4"), dict(s=x.transpose(0, 1))):
+        with pytest.raises(M.WbmmError):
+            M.wbmm_rmsnorm_forward(x, 1, **{"weight": w, **kw})
+    for bad in (x.half(), x.cpu(), x.transpose(0, 2)):
+        with pytest.raises(M.WbmmError):
+            M.wbmm_rmsnorm_forward(bad, 1)
+    with pytest.raises(M.WbmmError):
+        M.wbmm_rmsnorm_forward(x, 3)
+    for kw in (dict(dx=x), dict(ds=x[0]), dict(weight=torch.ones(7, device="cuda")),
+               dict(weight=w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(M.WbmmError):
+            M.wbmm_rmsnorm_backward(x, x.clone(), 1, **kw)
+
+
 def test_zero_rows():
     x = torch.zeros(4, 64, 1, device="cuda")
     y, _, _ = R().wbmm_rmsnorm_forward(x, 1, eps=1e-6)
