@@ -281,14 +281,15 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
   unsigned char* const s_u = s_e + NC * kX;               // U
   unsigned char* const s_k = s_u + NC * kU;               // K, and K^T
   unsigned char* const s_kt = s_k + kRows;
-  const int bh = blockIdx.x;
+  const DeltaWalkAt at = delta_walk_at((a.dv + 16 * NC - 1) / (16 * NC));
+  const int bh = at.bh;
   if (bh >= a.B * a.H) return;
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = wid & 3, row = lane & 15, gq = lane >> 4;
   const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
-  const int col = blockIdx.y * (16 * NC) + row;     // NC = 2: and the 16th after it
+  const int col = at.tile * (16 * NC) + row;     // NC = 2: and the 16th after it
   const bool in = col < a.dv;
   const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
@@ -674,8 +675,7 @@ template <typename T, int DK, bool VEC, bool OUT, int NC>
 hipError_t walk_one(const DeltaArgs& a, hipStream_t st) {
   constexpr int bytes = WalkLds<T, DK, NC>::bytes;
   static_assert(bytes <= 160 * 1024, "LDS of a CU");
-  // heads side by side in steps of 8: a head's columns then lie on one XCD and share its L2
-  const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 16 * NC - 1) / (16 * NC));
+  const dim3 grid = delta_walk_grid(a, (a.dv + 16 * NC - 1) / (16 * NC));
   const hipError_t e = hipFuncSetAttribute((const void*)k_delta_walk<T, DK, VEC, OUT, NC>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;

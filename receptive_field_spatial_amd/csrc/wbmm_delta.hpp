@@ -102,15 +102,16 @@ constexpr size_t delta_p_bytes(bool bf16) { return (size_t)kDeltaFrags * 1024 * 
 constexpr size_t kDeltaTtBytes = (size_t)kDeltaFrags * 1024 * 3;
 
 DeltaArgs delta_args(const DeltaRequest& r);
-// Whether a workgroup of the walks takes two column tiles, which share its operands (K, T and P in registers
-// and LDS) and fill each other's waits: where tiles outnumber the CUs. Then (512 steps, dk = dv = 64, 16-column tiles;
-// us forward and backward of one against two): bf16 288 tiles 20.6, 32.7 against 19.8, 25.2, 768 48.5, 68.0
-// against 33.6, 50.5, 2048 155, 261 against 97, 161; up to 256 a tile each is the shorter walk: 14.6, 19.0
-// against 19.2, 24.6. fp32 288: 41.8, 59.3 against 27.3, 40.3. Of the measured ones only bf16 with dk = 128 and 640 tiles
-// loses (forward 44.0 against 51.2).
-inline bool walk_two_tiles(const DeltaArgs& a) {
-  return a.dv % 32 == 0 && (int64_t)a.B * a.H * (a.dv / 16) > 256;
-}
+// Tiles of 16 columns that a workgroup of the walks takes. More than one share its operands (K, T and P in registers
+// and LDS) and fill each other's waits; they pay where tiles outnumber the CUs: 512 steps, dk = dv = 64,
+// bf16, us forward and backward of one against two: 288 tiles 20.6, 32.7 against 19.8, 25.2, 768 48.5, 68.0 against
+// 33.6, 50.5; up to 256 a tile each is the shorter walk: 14.6, 19.0 against 19.2, 24.6. fp32 288: 41.8, 59.3 against
+// 27.3, 40.3. Of the measured ones only bf16 with dk = 128 and 640 tiles loses (forward 44.0 against 51.2). The
+// backward, of which a CU holds one workgroup, takes four from 513 tiles on where LDS has room (bf16 with dk <= 64,
+// fp32 with dk <= 32; bf16, 784 steps): 768 tiles 80 against 88, 1024 85 against 112, 512 57 against 45.
+inline int64_t walk_tiles(const DeltaArgs& a) { return (int64_t)a.B * a.H * (a.dv / 16); }
+inline bool walk_two_tiles(const DeltaArgs& a) { return a.dv % 32 == 0 && walk_tiles(a) > 256; }
+inline bool walk_four_tiles(const DeltaArgs& a) { return a.dv % 64 == 0 && walk_tiles(a) > 512; }
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
 // 16 bytes at a time of everything that lies in rows of dk or dv.

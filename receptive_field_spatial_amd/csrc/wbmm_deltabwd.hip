@@ -45,14 +45,15 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
   constexpr bool TWO = Lds::two, DIRECT = Lds::direct;
   constexpr int kD = KS * 3 * 1024, kX = 2 * 3 * 1024, kO = 2 * PI * 1024, kM = NT * 1024;   // of a column tile
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
-  const int bh = blockIdx.x;
+  const DeltaWalkAt at = delta_walk_at((a.dv + 16 * NC - 1) / (16 * NC));
+  const int bh = at.bh;
   if (bh >= a.B * a.H) return;
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = wid & 3, row = lane & 15, gq = lane >> 4;
   const bool walker = wid < 4;
   const int b = bh / a.H, h = bh - b * a.H, hk = h / a.rep;
   const DeltaSeq sq = delta_seq(a, b);
-  const int col = blockIdx.y * (16 * NC) + row;
+  const int col = at.tile * (16 * NC) + row;
   const bool in = col < a.dv;
   const int nch = (sq.n + kDeltaChunk - 1) / kDeltaChunk, endc = nch - 1;
   const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
@@ -814,7 +815,7 @@ hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
       constexpr int NC = decltype(n)::value;
       constexpr int back = BackLds<T, DK, NC>::bytes;
       static_assert(back <= 160 * 1024, "LDS of a CU");
-      const dim3 grid((a.B * a.H + 7) / 8 * 8, (a.dv + 16 * NC - 1) / (16 * NC));
+      const dim3 grid = delta_walk_grid(a, (a.dv + 16 * NC - 1) / (16 * NC));
       e = hipFuncSetAttribute((const void*)k_delta_walk_bwd<T, DK, VEC, NC>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, back);
       if (e != hipSuccess) return;
@@ -822,8 +823,14 @@ hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
       e = hipGetLastError();
     };
     bool done = false;
+    if constexpr (VEC && BackLds<T, DK, 4>::bytes <= 160 * 1024) {
+      if (walk_four_tiles(a)) {
+        walk(std::integral_constant<int, 4>());
+        done = true;
+      }
+    }
     if constexpr (VEC && BackLds<T, DK, 2>::bytes <= 160 * 1024) {
-      if (walk_two_tiles(a)) {
+      if (!done && walk_two_tiles(a)) {
         walk(std::integral_constant<int, 2>());
         done = true;
       }

@@ -338,7 +338,9 @@ def test_many_heads_and_batches_are_each_their_own():
 @pytest.mark.parametrize("dt,B,Hk,H,dk,dv,reverse,s0", [
     (F32, 40, 2, 4, 24, 32, False, True), (BF16, 40, 1, 1, 128, 128, True, True), (F32, 140, 1, 1, 128, 32, False, False),
     (BF16, 70, 1, 2, 40, 64, True, False), (F32, 44, 1, 2, 64, 64, True, True), (BF16, 130, 1, 3, 32, 32, False, True),
-    (BF16, 70, 1, 2, 33, 64, False, True)])
+    (BF16, 70, 1, 2, 33, 64, False, True), (BF16, 70, 1, 2, 64, 64, True, True), (BF16, 150, 1, 1, 24, 64, False, True),
+    (BF16, 70, 1, 1, 64, 128, False, False), (F32, 150, 1, 1, 64, 64, False, True),
+    (F32, 150, 1, 1, 24, 64, True, True)])
 def test_sequences_of_a_large_padded_batch(dt, B, Hk, H, dk, dv, reverse, s0):
     """Batches that are walked two tiles of columns at a time: each sequence as in a batch of its own."""
     print(f"\n[case] delta large {B} heads {Hk}/{H} {dk}x{dv} {dt}", flush=True)
@@ -358,6 +360,23 @@ def test_sequences_of_a_large_padded_batch(dt, B, Hk, H, dk, dv, reverse, s0):
         if b == 1:
             one.check_forward(*o1)
             one.check_backward(g1)
+
+
+def test_more_heads_than_a_row_of_the_grid():
+    """2^18 and a few sequences: the last ones as in a batch of their own."""
+    B, L, d = (1 << 18) + 21, 9, 8
+    c = Case(64, L, 1, 1, d, d, BF16, seed=190)
+    big = Case(1, 1, 1, 1, 1, 1, BF16)
+    for n in ("q", "k", "v", "g", "beta", "s0", "do", "dl"):
+        t = getattr(c, n)
+        x = t[:1].expand(B, *t.shape[1:]).contiguous()
+        x[-64:] = t
+        setattr(big, n, x)
+    out, want = big.forward(), c.forward()
+    gr, wg = big.backward(out[2]), c.backward(want[2])
+    for a, b in zip((*out, *gr), (*want, *wg)):
+        assert torch.equal(a[-64:], b) and torch.equal(a[:5], b[:1].expand(5, *b.shape[1:]))
+        assert torch.equal(a[1 << 17], b[0])
 
 
 def test_refused_tensors():
