@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 // Bound by the length of a chunk's chain: three LDS round trips, four products one after the other and three
 // splittings into bf16 parts, 1.5 to 2 us a chunk of which loads that always hit would save 0.1. So 4 x 8 heads of
 // 128 over 8192 steps (128 chunks, one workgroup a CU) take 245 us, a single head 207; 192 heads of 64 over
-// 784 steps 49.5, with one tile a workgroup 66. K S formed from a walker's own rows of S and K from registers, the
+// 784 steps 43.5, with one tile a workgroup 66. K S formed from a walker's own rows of S and K from registers, the
 // parts joined in LDS, measured 183 for the single head, but 250 to 260 for 4 x 8.
 // LDS of a workgroup. Two chunks' K^T, where they fit (all but fp32 with 96 < dk): the next one is then
 // written while this one is read, and K is loaded a whole chunk ahead.

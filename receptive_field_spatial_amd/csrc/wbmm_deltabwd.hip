@@ -8,13 +8,13 @@ namespace wbmm {
 namespace {
 
 // ---------------------------------------------------------------------------- the walk back
-// As the forward's walk: one workgroup per head and 16 columns of dv, four walkers and four helpers.
+// As the forward's walk: one workgroup per head and NC tiles of 16 columns of dv, four walkers and four helpers.
 //        walkers                                         helpers
 //   A    dU = P^T G + diag(y_C / y) K D                  M = Q^T diag(y) G
 //   B    R = T^T dU (= dv)                               P^T G, K, K^T, Q^T and diag(y) G of the next chunk
 //   C    D = y_C D + M - K^T diag(y) R                   do of the one after
 // D after each chunk and R stay in the workspace for k_delta_grads. Bound as the forward's, with D and R to store:
-// 192 heads of 64, 784 steps, bf16: 80 us with two tiles a workgroup, 104 with one; 30 heads of 48 x 40
+// 192 heads of 64, 784 steps, bf16: 70 to 79 us with four tiles a workgroup, 88 with two, 104 with one; 30 heads of 48 x 40
 // over 1531 steps, fp32: 75 us, 3.1 a chunk.
 template <typename T, int DK, int NC>
 struct BackLds {
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
     float rv[4] = {0.f, 0.f, 0.f, 0.f}, sd = 0.f;     // v.R of this lane's rows; <S0, D>
 
     // Of a piece: 4 x 4 blocks of S0 (threads below 256) or of D (the others), rows of do and R as
-    // operands, v and R as results lie. The next piece's loads are issued once this one's are in LDS.
+    // operands, v and R as results lie. (The next piece's in flight meanwhile would take 36 more registers, and
+    // with them one of the two workgroups of a CU.)
     constexpr int kBlk = (DK * 2 + 255) / 256;
     const bool second = hf == 1;     // the same for a whole wave, and known to be
     const auto mbuf = second ? dbuf : sbuf;

@@ -15,7 +15,7 @@
 //           there; the waves' sums meet in LDS.
 // Longer axes than the registers hold are read twice, the second time from a cache.
 //
-// Measured: forward bf16 with codes, 50176 rows of 192, 16.2 us (87 MB, 5.4 TB/s); backward fp32, 128 x 96 x
+// Measured: forward bf16 with codes, 50176 rows of 192, 17.0 us (87 MB, 5.1 TB/s); backward fp32, 128 x 96 x
 // 3136, 115 us (617 MB, 5.4 TB/s) and 4.4 for dw's partials; single rows 2 us, a launch's own time.
 //
 // dw: fp32 sums with their rounding errors carried along (the sum of any number of terms is good to
