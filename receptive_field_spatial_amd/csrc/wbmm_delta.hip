@@ -29,7 +29,7 @@ __device__ __forceinline__ constexpr int lds_tile(int i, int j) { return (i * (i
 // A wave's share of a chunk: column tile W, all of whose loops are then of known length.
 template <typename T, DeltaPrep MODE>
 struct DeltaOwn {
-  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO;   // parts
+  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO, PM = DeltaType<T, true>::PM;
   static constexpr bool WANTP = MODE != kPrepStates;
   unsigned char* s_all;
   const double* s_cum;
@@ -152,7 +152,7 @@ struct DeltaOwn {
       put<PT>(T_, tri_frag(W, s), split8<PT>(v));
       if (MODE == kPrepForward) {
         rows_of(s_n, s, v);
-        put<PO>(P_, tri_frag(W, s), split8<PO>(v));
+        put<PM>(P_, tri_frag(W, s), packed<PM>(v));
       }
     }
   }
@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 // written while this one is read, and K is loaded a whole chunk ahead.
 template <typename T, int DK, int NC>
 struct WalkLds {
-  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO, KS = DK / 32;
+  static constexpr int PI = DeltaType<T, true>::PI, KS = DK / 32;
   static constexpr int rows = 4 * KS * PI * 1024, cols = (DK / 16) * kTileBytes<PI>;
-  static constexpr int rest = NC * (KS * 3 + 12 + 2 * PO) * 1024 + rows;
+  static constexpr int rest = NC * (KS * 3 + 18) * 1024 + rows;
   static constexpr bool two = rest + 2 * cols <= 160 * 1024;
   static constexpr int bytes = rest + (two ? 2 : 1) * cols;
 };
@@ -270,16 +270,16 @@ struct WalkLds {
 template <typename T, int DK, bool VEC, bool OUT, int NC>
 __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>::PI == 1 ? 4 : 2)) k_delta_walk(DeltaArgs a) {
   using Ty = DeltaType<T, VEC>;
-  constexpr int PI = Ty::PI, PO = Ty::PO, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
+  constexpr int PI = Ty::PI, PM = Ty::PM, KS = DK / 32, NT = DK / 16, OWN = (NT + 3) / 4;
   constexpr bool TWO = WalkLds<T, DK, NC>::two;
   constexpr int kRows = WalkLds<T, DK, NC>::rows, kCols = TWO ? WalkLds<T, DK, NC>::cols : 0;
-  constexpr int kS = KS * 3 * 1024, kX = 2 * 3 * 1024, kU = 2 * PO * 1024;   // of a column tile
+  constexpr int kS = KS * 3 * 1024, kX = 2 * 3 * 1024;   // of a column tile
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   unsigned char* const s_s = sm;                          // the state
   unsigned char* const s_x = s_s + NC * kS;               // X
   unsigned char* const s_e = s_x + NC * kX;               // diag(y_C / y) U
   unsigned char* const s_u = s_e + NC * kX;               // U
-  unsigned char* const s_k = s_u + NC * kU;               // K, and K^T
+  unsigned char* const s_k = s_u + NC * kX;               // K, and K^T
   unsigned char* const s_kt = s_k + kRows;
   const DeltaWalkAt at = delta_walk_at((a.dv + 16 * NC - 1) / (16 * NC));
   const int bh = at.bh;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
         lds_half<3>(s_e + n * kX, w >> 1, lane, w & 1,
                     split4<3>(end[0] * u[n][0], end[1] * u[n][1], end[2] * u[n][2], end[3] * u[n][3]));
         if constexpr (OUT)
-          lds_half<PO>(s_u + n * kU, w >> 1, lane, w & 1, split4<PO>(u[n][0], u[n][1], u[n][2], u[n][3]));
+          lds_half<3>(s_u + n * kX, w >> 1, lane, w & 1, split4<3>(u[n][0], u[n][1], u[n][2], u[n][3]));
       }
       load_t(next);
       __syncthreads();
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
     const int id = threadIdx.x - 256, dg = id % (DK / 8), tg = id / (DK / 8);
     const bool block = tg < 16;      // a 4 x 8 block of K
     Raw8<T, VEC> kb[4], q[OUT ? KS : 1];
-    Frag<PO> p[2];
+    Frag<PM> p[2];
     v4f gam = zero;
     uint32_t boff[4], qoff = 0, ooff[4];
     auto block_offsets = [&](const DeltaRows& rows) {
@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
       if constexpr (OUT) {
         const size_t ch = (size_t)bh * a.chunks + c;
         const unsigned char* Pm = a.P + ch * delta_p_bytes(PI == 1);
-        p[0] = mem_frag<PO>(Pm, tri_frag(w, 0), lane);
-        p[1] = mem_frag<PO>(Pm, tri_frag(w, second), lane);
+        p[0] = mem_frag<PM>(Pm, tri_frag(w, 0), lane);
+        p[1] = mem_frag<PM>(Pm, tri_frag(w, second), lane);
         gam = *(const v4f*)&a.gates[ch].gam[16 * w + 4 * gq];
       }
     };
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
           halves<PI>(q[s], lo, hi);
 #pragma unroll
           for (int n = 0; n < NC; ++n)
-            qs[n] = mma<PI, PO>(join<PI>(lo, hi), lead<PO>(lds_frag<3>(s_s + n * kS, s, lane)), qs[n]);
+            qs[n] = mma<PI, 3>(join<PI>(lo, hi), lds_frag<3>(s_s + n * kS, s, lane), qs[n]);
         }
       }
       load_q(next);
@@ -518,10 +518,10 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
       if constexpr (OUT) {
         v4f pu[NC];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) pu[n] = mma<PO, PO>(p[0], lds_frag<PO>(s_u + n * kU, 0, lane), zero);
+        for (int n = 0; n < NC; ++n) pu[n] = mma<3, 3>(parts(p[0]), lds_frag<3>(s_u + n * kX, 0, lane), zero);
         if (w >= 2)
 #pragma unroll
-          for (int n = 0; n < NC; ++n) pu[n] = mma<PO, PO>(p[1], lds_frag<PO>(s_u + n * kU, 1, lane), pu[n]);
+          for (int n = 0; n < NC; ++n) pu[n] = mma<3, 3>(parts(p[1]), lds_frag<3>(s_u + n * kX, 1, lane), pu[n]);
         if (c == endc) value_offsets(delta_rows(sq, c), ooff);
         const auto obuf = delta_buf((T*)a.o + (delta_low(a, sq, b, c) * a.H + h) * a.dv);
 #pragma unroll

@@ -47,6 +47,23 @@ __device__ __forceinline__ Frag<P> split8(const float (&v)[8]) {
   return join<P>(split4<P>(v[0], v[1], v[2], v[3]), split4<P>(v[4], v[5], v[6], v[7]));
 }
 
+// A matrix of the first launch as an operand in memory: in its three parts, or (M = 2, bf16 tensors) as its 8 fp32
+// entries, whose size is two parts' and whose three parts are the reader's to form.
+template <int M>
+__device__ __forceinline__ Frag<M> packed(const float (&v)[8]) {
+  if constexpr (M == 3) return split8<3>(v);
+  Frag<M> f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    f.p[i] = __builtin_bit_cast(u32x4, v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]});
+  return f;
+}
+__device__ __forceinline__ Frag<3> parts(const Frag<3>& f) { return f; }
+__device__ __forceinline__ Frag<3> parts(const Frag<2>& f) {
+  const v4f a = __builtin_bit_cast(v4f, f.p[0]), b = __builtin_bit_cast(v4f, f.p[1]);
+  return join<3>(split4<3>(a[0], a[1], a[2], a[3]), split4<3>(b[0], b[1], b[2], b[3]));
+}
+
 // acc + A B over 32 terms: the products of parts i, j with i + j below the larger number of parts.
 template <int PA, int PB>
 __device__ __forceinline__ v4f mma(const Frag<PA>& a, const Frag<PB>& b, v4f acc) {
@@ -68,13 +85,6 @@ __device__ __forceinline__ v4f mma_short(const Frag<3>& a, const Frag<3>& b) {
   lo = mfma_bf16(a.p[2], b.p[0], lo);
   hi = mfma_bf16(a.p[0], b.p[0], hi);
   return hi + lo;
-}
-template <int P, int N>
-__device__ __forceinline__ Frag<P> lead(const Frag<N>& f) {   // the P leading parts
-  Frag<P> r;
-#pragma unroll
-  for (int i = 0; i < P; ++i) r.p[i] = f.p[i];
-  return r;
 }
 
 // Frags in LDS: part p of frag f at base + (f * P + p) * 1024, a lane's 16 bytes in slot(lane), half h 8 of
@@ -132,8 +142,8 @@ inline dim3 delta_walk_grid(const DeltaArgs& a, int tiles) {
   return dim3((uint32_t)row * 8 * tiles, (octets + row - 1) / row);
 }
 
-// Types of a tensor's elements: parts of an input, parts of what only reaches an output, a quad of
-// entries, and a quad as it is loaded (nothing is done to it before it is used: the loads of a chunk are
+// Types of a tensor's elements: parts of an input, parts of what only reaches a gradient, how P is kept (see
+// packed), a quad of entries, and a quad as it is loaded (nothing is done to it before it is used: the loads of a chunk are
 // in flight while the chunk before it is computed).
 struct Raw16 {
   uint32_t e[4];
@@ -142,13 +152,13 @@ template <typename T, bool VEC>
 struct DeltaType;
 template <bool VEC>
 struct DeltaType<uint16_t, VEC> {
-  static constexpr int PI = 1, PO = 2;
+  static constexpr int PI = 1, PO = 2, PM = 2;
   using Quad = Half<1>;
   using Raw = typename std::conditional<VEC, u32x2, Raw16>::type;
 };
 template <bool VEC>
 struct DeltaType<float, VEC> {
-  static constexpr int PI = 3, PO = 3;
+  static constexpr int PI = 3, PO = 3, PM = 3;
   using Quad = v4f;
   using Raw = v4f;
 };

@@ -481,3 +481,57 @@ def test_gradients_by_differences():
         want = float((gr.double() * d.double()).sum())
         scale = float(gr.double().norm())
         assert abs((up - down) / (2 * h) - want) <= 1e-3 * scale + 1e-3, name
+
+
+def wide(c):
+    """The same case in fp32: bf16 values as they are."""
+    w = Case(1, 1, 1, 1, 1, 1, F32)
+    for n in ("q", "k", "v", "g", "beta", "do"):
+        setattr(w, n, getattr(c, n).float())
+    w.s0, w.dl, w.lens, w.hl, w.reverse, w.dk = c.s0, c.dl, c.lens, c.hl, c.reverse, c.dk
+    return w
+
+
+def overwritten(dk, dv, keys, times, old, beta):
+    """`keys` keys written `times` times each over a state `old` times larger than what is written: what a
+    query with the same key reads is a small difference of large products."""
+    L = keys * times
+    c = Case(1, L, 1, 1, dk, dv, BF16, gate=20.0, seed=201)
+    c.k[:] = c.k[:, :keys].repeat(1, times, 1, 1)
+    c.q, c.beta[:] = c.k.clone(), beta
+    c.s0 *= old
+    return c
+
+
+BITS = SIZES + [(70, 130, 1, 1, 64, 128), (40, 130, 2, 4, 24, 32), (44, 70, 1, 2, 64, 64), (44, 70, 1, 1, 128, 128)]
+
+
+def same_as_wide(name, c, states):
+    w = wide(c)
+    a, b = c.forward(states=states), w.forward(states=states)
+    pairs = [("o", a[0], b[0]), ("s_last", a[1], b[1])]
+    if states:
+        pairs += [("states", a[2], b[2])]
+        pairs += zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), c.backward(a[2]), w.backward(b[2]))
+        pairs += zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), c.backward(None), w.backward(None))
+    for n, x, y in pairs:
+        y = y.to(x.dtype)
+        assert torch.equal(x, y), (name, n, int((x != y).sum()), x.numel())
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("B,L,Hk,H,dk,dv", BITS)
+def test_bf16_forward_is_the_fp32_one_rounded_once(B, L, Hk, H, dk, dv, reverse):
+    """bf16 inputs are exact in fp32, and what is formed of them is held as in an fp32 call: its products and sums
+    are the same ones, in the same order, so the results are the fp32 call's, rounded, bit for bit."""
+    print(f"\n[case] delta bits {B}x{L} heads {Hk}/{H} {dk}x{dv} rev={reverse}", flush=True)
+    same_as_wide("forward", Case(B, L, Hk, H, dk, dv, BF16, reverse, seed=211), False)
+
+
+@pytest.mark.parametrize("dk,dv,keys,times,old,beta", [(64, 64, 8, 8, 1000.0, 6.0), (128, 48, 16, 4, 1.0, 8.0),
+                                                       (33, 17, 5, 30, 1000.0, 6.0)])
+def test_bf16_reads_of_overwritten_keys(dk, dv, keys, times, old, beta):
+    c = overwritten(dk, dv, keys, times, old, beta)
+    if old == 1.0:
+        c.v.zero_()
+    same_as_wide("overwritten", c, False)
