@@ -558,7 +558,7 @@ wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, do
  * Sizes:    B, L, Hk, H >= 1, Hk dividing H; 1 <= dk, dv <= 128.
  * dtype:    of q, k, v, g, beta and o: WBMM_F32 or WBMM_BF16. Sums and the state are fp32, products good
  *           to 2^-24 of their factors. A bf16 call gives what the fp32 call of the same values gives,
- *           rounded (RNE); bf16 gradients are formed to 2^-17 of their factors before that.
+ *           rounded (RNE).
  * reverse:  nonzero: sequences run from their last position to their first.
  * q, k:     device [B][L][Hk][dk]; head h uses key head h / (H / Hk). v: device [B][L][H][dv].
  * g, beta:  device [B][L][H]. g is held to [-87, 87].

@@ -29,7 +29,7 @@ __device__ __forceinline__ constexpr int lds_tile(int i, int j) { return (i * (i
 // A wave's share of a chunk: column tile W, all of whose loops are then of known length.
 template <typename T, DeltaPrep MODE>
 struct DeltaOwn {
-  static constexpr int PI = DeltaType<T, true>::PI, PO = DeltaType<T, true>::PO, PM = DeltaType<T, true>::PM;
+  static constexpr int PI = DeltaType<T, true>::PI, PM = DeltaType<T, true>::PM;
   static constexpr bool WANTP = MODE != kPrepStates;
   unsigned char* s_all;
   const double* s_cum;
@@ -137,7 +137,7 @@ struct DeltaOwn {
         if (MODE == kPrepForward) s_n[lds_tile(W + i, W) + (4 * gq + r) * 20 + row] = qk[i][r];
       }
     __syncthreads();
-    constexpr int PT = MODE == kPrepBackward ? PO : 3;
+    constexpr int PT = MODE == kPrepBackward ? PM : 3;
     auto rows_of = [&](const float* m, int s, float (&v)[8]) {   // row tile W, terms 32 s ..
       const v4f x = *(const v4f*)&m[lds_tile(W, 2 * s) + row * 20 + 4 * gq];
       v4f y = zero;
@@ -149,7 +149,7 @@ struct DeltaOwn {
     for (int s = 0; 2 * s <= W; ++s) {
       float v[8];
       rows_of(s_t, s, v);
-      put<PT>(T_, tri_frag(W, s), split8<PT>(v));
+      put<PT>(T_, tri_frag(W, s), packed<PT>(v));
       if (MODE == kPrepForward) {
         rows_of(s_n, s, v);
         put<PM>(P_, tri_frag(W, s), packed<PM>(v));

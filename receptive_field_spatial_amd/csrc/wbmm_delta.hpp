@@ -24,7 +24,7 @@
 // Products run on the bf16 matrix cores at fp32 accuracy. An fp32 number is the sum of three bf16
 // numbers to 2^-25, so the states, T, X, U and D are taken in three parts and the products that matter
 // (up to 2^-24) are formed; bf16 tensors are one part as they are, so that a bf16 call gives what the fp32 call of the
-// same values gives, rounded. (What only reaches a bf16 gradient, dq, dk, dg and dbeta, takes two parts, 2^-17.) Sums are fp32, running sums of
+// same values gives, rounded. Sums are fp32, running sums of
 // log a and of d log y fp64.
 //
 // Layouts. v_mfma_f32_16x16x32_bf16: with l the lane, an A operand is row l % 16 and 8 terms of the sum, a
@@ -93,8 +93,8 @@ struct DeltaArgs {
 
 // What of a chunk's own matrices a launch of launch_delta_prep forms.
 enum DeltaPrep { kPrepForward, kPrepStates, kPrepBackward };
-// Bytes per chunk of a head: T in three parts (backward: as many as the outputs need), P in three or, for bf16
-// tensors, in fp32 (12 KB for 18; the walk's helpers have the time to part it), the transposes in three.
+// Bytes per chunk of a head: the walk's T and the transposes in three parts; P, which the walk's helpers have the time
+// to part, and the gradients' T in three or, for bf16 tensors, in fp32 (12 KB for 18).
 constexpr size_t delta_t_bytes(bool bf16, bool backward) {
   return (size_t)kDeltaFrags * 1024 * (bf16 && backward ? 2 : 3);
 }

@@ -373,19 +373,20 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
 // transposes, decays, row sums. 2496 chunks of one head of 64, bf16: 110 us; 240 of three heads, fp32: 49.
 template <typename T, int DK, bool VEC>
 struct GradLds {
-  static constexpr int PI = DeltaType<T, VEC>::PI, PO = DeltaType<T, VEC>::PO, NT = DK / 16, KS = DK / 32;
+  static constexpr int PI = DeltaType<T, VEC>::PI, NT = DK / 16, KS = DK / 32;
   static constexpr int sn = 0;                            // S0, terms along dv: NT frags
-  static constexpr int sk = sn + NT * PO * 1024;          // S0, terms along dk: KS x 2
-  static constexpr int dn = sk + KS * 2 * PO * 1024;      // D, terms along dv: NT
-  static constexpr int xf = dn + NT * PO * 1024;          // X: 2 x 2
-  static constexpr int uf = xf + 4 * PO * 1024;           // U as rows: 4
-  static constexpr int walk = uf + 4 * PO * 1024;
+  static constexpr int sk = sn + NT * 3 * 1024;          // S0, terms along dk: KS x 2
+  static constexpr int dn = sk + KS * 2 * 3 * 1024;      // D, terms along dv: NT
+  static constexpr int xf = dn + NT * 3 * 1024;          // X: 2 x 2
+  static constexpr int uf = xf + 4 * 3 * 1024;           // U as rows: 4
+  static constexpr int walk = uf + 4 * 3 * 1024;
   static constexpr int kt = 0;                            // afterwards: K^T and Q^T, NT x 2 each
   static constexpr int kTileB = 2 * PI * 1024;
   static constexpr int qt = kt + NT * kTileB;
   static constexpr int after = qt + NT * kTileB;
-  static constexpr int mat = walk > after ? walk : after; // dP and N: 64 rows of 68 floats each
-  static constexpr int red = mat + 2 * 64 * 68 * 4;       // row sums
+  static constexpr int mat = after;                       // and dP and N: 64 rows of 68 floats each
+  static constexpr int end = mat + 2 * 64 * 68 * 4;
+  static constexpr int red = walk > end ? walk : end;     // row sums
   static constexpr int bytes = red + 7 * 64 * 4;
 };
 
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
   using Lds = GradLds<T, DK, VEC>;
   using Ty = DeltaType<T, VEC>;
   using Fy = DeltaType<float, VEC>;
-  constexpr int PI = Lds::PI, PO = Lds::PO, KS = Lds::KS, NT = Lds::NT, NTH = NT / 2;
+  constexpr int PI = Lds::PI, PM = Ty::PM, KS = Lds::KS, NT = Lds::NT, NTH = NT / 2;
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   float* mat = (float*)(sm + Lds::mat);
   float* red = (float*)(sm + Lds::red);
@@ -492,8 +493,6 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
     const auto vbuf = delta_buf((const T*)a.v + (low * a.H + h) * a.dv);
     const auto gbuf = delta_buf((const T*)a.dout + (low * a.H + h) * a.dv);
     const unsigned char* Tm = a.T + ch * delta_t_bytes(PI == 1, true);
-    const Frag<PO> tf0 = mem_frag<PO>(Tm, tri_frag(w, 0), lane);
-    const Frag<PO> tf1 = mem_frag<PO>(Tm, tri_frag(w, w >> 1), lane);
     float gam[4], end[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -555,42 +554,45 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
           unsigned char* to = sm + (second ? Lds::dn : Lds::sn);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            lds_half<PO>(to, k4 >> 2, (n4 & 3) * 16 + 4 * (k4 & 3) + r, n4 >> 2,
-                         split4<PO>(ms[m][r][0], ms[m][r][1], ms[m][r][2], ms[m][r][3]));
+            lds_half<3>(to, k4 >> 2, (n4 & 3) * 16 + 4 * (k4 & 3) + r, n4 >> 2,
+                         split4<3>(ms[m][r][0], ms[m][r][1], ms[m][r][2], ms[m][r][3]));
           if (!second)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              lds_half<PO>(sm + Lds::sk, (k4 >> 3) * 2 + (n4 >> 2), (k4 & 3) * 16 + 4 * (n4 & 3) + r,
+              lds_half<3>(sm + Lds::sk, (k4 >> 3) * 2 + (n4 >> 2), (k4 & 3) * 16 + 4 * (n4 & 3) + r,
                            (k4 >> 2) & 1,
-                           split4<PO>(ms[m][0][r], ms[m][1][r], ms[m][2][r], ms[m][3][r]));
+                           split4<3>(ms[m][0][r], ms[m][1][r], ms[m][2][r], ms[m][3][r]));
         }
       }
       const Frag<PI> gf = operand<PI>(g0, g1);
-      const Frag<PO> rf = join<PO>(split4<PO>(r0[0], r0[1], r0[2], r0[3]),
-                                   split4<PO>(r1[0], r1[1], r1[2], r1[3]));
+      const Frag<3> rf = join<3>(split4<3>(r0[0], r0[1], r0[2], r0[3]),
+                                   split4<3>(r1[0], r1[1], r1[2], r1[3]));
       float x[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         x[r] = wide1<T>(v[r]);
         rv[r] = fmaf(rd[r], x[r], rv[r]);
       }
+      // for every piece again: kept over them, with the three parts, they would not fit the registers (276 us for 234)
+      const Frag<PM> tf0 = mem_frag<PM>(Tm, tri_frag(w, 0), lane);
+      const Frag<PM> tf1 = mem_frag<PM>(Tm, tri_frag(w, w >> 1), lane);
       __syncthreads();
       // X = V - diag(y) K S0, this wave's 16 rows and 16 columns
       v4f ks = zero;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        ks = mma<PI, PO>(kf[s], lds_frag<PO>(sm + Lds::sk, 2 * s + hf, lane), ks);
+        ks = mma<PI, 3>(kf[s], lds_frag<3>(sm + Lds::sk, 2 * s + hf, lane), ks);
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] -= gam[r] * ks[r];
-      lds_half<PO>(sm + Lds::xf, (w >> 1) * 2 + hf, lane, w & 1, split4<PO>(x[0], x[1], x[2], x[3]));
+      lds_half<3>(sm + Lds::xf, (w >> 1) * 2 + hf, lane, w & 1, split4<3>(x[0], x[1], x[2], x[3]));
       __syncthreads();
-      v4f u = mma<PO, PO>(tf0, lds_frag<PO>(sm + Lds::xf, hf, lane), zero);
-      if (w >= 2) u = mma<PO, PO>(tf1, lds_frag<PO>(sm + Lds::xf, 2 + hf, lane), u);
+      v4f u = mma<3, 3>(parts(tf0), lds_frag<3>(sm + Lds::xf, hf, lane), zero);
+      if (w >= 2) u = mma<3, 3>(parts(tf1), lds_frag<3>(sm + Lds::xf, 2 + hf, lane), u);
       {   // U as rows: entry (16 w + 4 gq + r, 16 hf + row) of the piece
-        const Half<PO> uh = split4<PO>(u[0], u[1], u[2], u[3]);
+        const Half<3> uh = split4<3>(u[0], u[1], u[2], u[3]);
 #pragma unroll
-        for (int p = 0; p < PO; ++p) {
-          unsigned char* to = sm + Lds::uf + (w * PO + p) * 1024 + hf * 8 + (row & 3) * 2;
+        for (int p = 0; p < 3; ++p) {
+          unsigned char* to = sm + Lds::uf + (w * 3 + p) * 1024 + hf * 8 + (row & 3) * 2;
           const int l = (row >> 2) * 16 + 4 * gq;
           *(uint16_t*)(to + slot(l) * 16) = (uint16_t)uh.p[p].x;
           *(uint16_t*)(to + slot(l + 1) * 16) = (uint16_t)(uh.p[p].x >> 16);
@@ -599,21 +601,21 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
         }
       }
       __syncthreads();
-      const Frag<PO> uw = lds_frag<PO>(sm + Lds::uf, w, lane);
+      const Frag<3> uw = lds_frag<3>(sm + Lds::uf, w, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i <= w) {
-          const Frag<PO> ui = lds_frag<PO>(sm + Lds::uf, i, lane);
-          if (hf == 0) pn[i] = mma<PI, PO>(gf, ui, pn[i]);
-          else pn[i] = mma<PO, PO>(rf, ui, pn[i]);
+          const Frag<3> ui = lds_frag<3>(sm + Lds::uf, i, lane);
+          if (hf == 0) pn[i] = mma<PI, 3>(gf, ui, pn[i]);
+          else pn[i] = mma<3, 3>(rf, ui, pn[i]);
         }
 #pragma unroll
       for (int i = 0; i < NTH; ++i) {
-        const Frag<PO> sf = lds_frag<PO>(sm + Lds::sn, hf * NTH + i, lane);
-        const Frag<PO> df = lds_frag<PO>(sm + Lds::dn, hf * NTH + i, lane);
-        dq[i] = mma<PI, PO>(gf, sf, dq[i]);
-        rowg[i] = mma<PO, PO>(rf, sf, rowg[i]);
-        colg[i] = mma<PO, PO>(uw, df, colg[i]);
+        const Frag<3> sf = lds_frag<3>(sm + Lds::sn, hf * NTH + i, lane);
+        const Frag<3> df = lds_frag<3>(sm + Lds::dn, hf * NTH + i, lane);
+        dq[i] = mma<PI, 3>(gf, sf, dq[i]);
+        rowg[i] = mma<3, 3>(rf, sf, rowg[i]);
+        colg[i] = mma<3, 3>(uw, df, colg[i]);
         if (w == (i & 3)) sd += dot(sf, df);      // <S0, D>, each tile by one wave
       }
     }
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
         qr[i][r] = buf_load<T>(qbuf, off);
       }
     }
+    __syncthreads();              // the pieces' operands have been read
     // dP and N to LDS, with their decays
     {
       const float one = hf == 0 ? a.scale : -1.f;
@@ -661,7 +664,6 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
           }
         }
     }
-    __syncthreads();              // the pieces' operands have been read
 #pragma unroll
     for (int m = 0; m < kRowBlk; ++m) {
       const int id = (tid & 255) + 256 * m, dg = id % (DK / 4), tg = id / (DK / 4);
@@ -699,12 +701,12 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
         if (2 * s + 1 <= w) a1 = *(const v4f*)(m + 16), b1 = *(const v4f*)(m + 64 * 68 + 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[e] = a0[e], p[4 + e] = a1[e], q[e] = b0[e], q[4 + e] = b1[e];
-        const Frag<PO> pf = split8<PO>(p), nf = split8<PO>(q);
+        const Frag<3> pf = split8<3>(p), nf = split8<3>(q);
 #pragma unroll
         for (int i = 0; i < NTH; ++i) {
           const Frag<PI> kt = lds_frag<PI>(sm + Lds::kt + (hf * NTH + i) * Lds::kTileB, s, lane);
-          dq[i] = mma<PO, PI>(pf, kt, dq[i]);
-          rowg[i] = mma<PO, PI>(nf, kt, rowg[i]);
+          dq[i] = mma<3, PI>(pf, kt, dq[i]);
+          rowg[i] = mma<3, PI>(nf, kt, rowg[i]);
         }
       }
       if (2 * s + 1 >= w) {
@@ -717,12 +719,12 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
           p[4 + e] = m[(16 + e) * 68];
           q[4 + e] = m[(80 + e) * 68];
         }
-        const Frag<PO> pf = split8<PO>(p), nf = split8<PO>(q);
+        const Frag<3> pf = split8<3>(p), nf = split8<3>(q);
 #pragma unroll
         for (int i = 0; i < NTH; ++i) {
           const int at = (hf * NTH + i) * Lds::kTileB;
-          colg[i] = mma<PO, PI>(pf, lds_frag<PI>(sm + Lds::qt + at, s, lane), colg[i]);
-          colg[i] = mma<PO, PI>(nf, lds_frag<PI>(sm + Lds::kt + at, s, lane), colg[i]);
+          colg[i] = mma<3, PI>(pf, lds_frag<PI>(sm + Lds::qt + at, s, lane), colg[i]);
+          colg[i] = mma<3, PI>(nf, lds_frag<PI>(sm + Lds::kt + at, s, lane), colg[i]);
         }
       }
     }

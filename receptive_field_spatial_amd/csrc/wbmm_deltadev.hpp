@@ -142,8 +142,8 @@ inline dim3 delta_walk_grid(const DeltaArgs& a, int tiles) {
   return dim3((uint32_t)row * 8 * tiles, (octets + row - 1) / row);
 }
 
-// Types of a tensor's elements: parts of an input, parts of what only reaches a gradient, how P is kept (see
-// packed), a quad of entries, and a quad as it is loaded (nothing is done to it before it is used: the loads of a chunk are
+// Types of a tensor's elements: parts of an input, how P and the gradients' T are kept (see packed), a quad of
+// entries, and a quad as it is loaded (nothing is done to it before it is used: the loads of a chunk are
 // in flight while the chunk before it is computed).
 struct Raw16 {
   uint32_t e[4];
@@ -152,13 +152,13 @@ template <typename T, bool VEC>
 struct DeltaType;
 template <bool VEC>
 struct DeltaType<uint16_t, VEC> {
-  static constexpr int PI = 1, PO = 2, PM = 2;
+  static constexpr int PI = 1, PM = 2;
   using Quad = Half<1>;
   using Raw = typename std::conditional<VEC, u32x2, Raw16>::type;
 };
 template <bool VEC>
 struct DeltaType<float, VEC> {
-  static constexpr int PI = 3, PO = 3, PM = 3;
+  static constexpr int PI = 3, PM = 3;
   using Quad = v4f;
   using Raw = v4f;
 };

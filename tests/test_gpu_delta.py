@@ -535,3 +535,16 @@ def test_bf16_reads_of_overwritten_keys(dk, dv, keys, times, old, beta):
     if old == 1.0:
         c.v.zero_()
     same_as_wide("overwritten", c, False)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("B,L,Hk,H,dk,dv", BITS)
+def test_bf16_gradients_are_the_fp32_ones_rounded_once(B, L, Hk, H, dk, dv, reverse):
+    print(f"\n[case] delta gradient bits {B}x{L} heads {Hk}/{H} {dk}x{dv} rev={reverse}", flush=True)
+    same_as_wide("backward", Case(B, L, Hk, H, dk, dv, BF16, reverse, seed=221), True)
+
+
+@pytest.mark.parametrize("dk,dv,keys,times,old,beta", [(64, 64, 8, 8, 1000.0, 6.0), (128, 48, 16, 4, 1.0, 8.0),
+                                                       (33, 17, 5, 30, 1000.0, 6.0)])
+def test_bf16_gradients_at_overwritten_keys(dk, dv, keys, times, old, beta):
+    same_as_wide("overwritten", overwritten(dk, dv, keys, times, old, beta), True)
