@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
       gt.cum[lane] = cum;
       gt.gam[lane] = __builtin_amdgcn_exp2f((float)cum);
       gt.end[lane] = __builtin_amdgcn_exp2f((float)(__shfl(cum, 63) - cum));
-      gt.b[lane] = be;
+      const float f = expf(-fabsf(x));
+      gt.nb[lane] = live ? (x > 0.f ? f : 1.f) / (1.f + f) : 0.f;
       gt.na[lane] = live ? (g > 0.f ? e : 1.f) / (1.f + e) : 0.f;
     }
     share(kr, s_all);

@@ -65,10 +65,11 @@ size_t delta_backward_workspace(int64_t B, int64_t L, int H, int dk, int dv, boo
 hipError_t launch_delta_forward(const DeltaRequest& r, hipStream_t st);
 hipError_t launch_delta_backward(const DeltaRequest& r, hipStream_t st);
 
-// The gates of a chunk: log2 y (fp64), y, y_C / y, b and 1 - a.
+// The gates of a chunk: log2 y (fp64), y, y_C / y, 1 - b and 1 - a (each from its own exponential: b and a are 1 to
+// all their bits long before these are 0).
 struct DeltaGates {
   double cum[kDeltaChunk];
-  float gam[kDeltaChunk], end[kDeltaChunk], b[kDeltaChunk], na[kDeltaChunk];
+  float gam[kDeltaChunk], end[kDeltaChunk], nb[kDeltaChunk], na[kDeltaChunk];
 };
 
 struct DeltaArgs {

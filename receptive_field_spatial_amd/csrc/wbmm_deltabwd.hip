@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
       const uint32_t off = rows.off(lane, (uint32_t)a.H * sizeof(T));
       buf_store(delta_buf((T*)a.dg + low * a.H + h), off, (float)d * gt.na[lane], T());
       buf_store(delta_buf((T*)a.dbeta + low * a.H + h), off,
-                (red[4 * 64 + lane] + red[5 * 64 + lane] + rowk) * (1.f - gt.b[lane]), T());
+                (red[4 * 64 + lane] + red[5 * 64 + lane] + rowk) * gt.nb[lane], T());
     }
   }
   const int tidl = here(threadIdx.x), gql = (tidl & 63) >> 4, rowl = tidl & 15;

@@ -548,3 +548,22 @@ def test_bf16_gradients_are_the_fp32_ones_rounded_once(B, L, Hk, H, dk, dv, reve
                                                        (33, 17, 5, 30, 1000.0, 6.0)])
 def test_bf16_gradients_at_overwritten_keys(dk, dv, keys, times, old, beta):
     same_as_wide("overwritten", overwritten(dk, dv, keys, times, old, beta), True)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("L,dk,dv", [(70, 16, 20), (130, 64, 48), (64, 128, 32)])
+def test_gradient_of_a_saturated_write_gate(L, dk, dv, dt):
+    """beta of 10 to 20 and of -10 to -20: dbeta is (1 - b) times a dot product that errs by 256 half steps of its
+    bound, dv M M_D, and 1 - b comes from an exponential, a sum and a quotient, 8 half steps of itself; so the
+    smallest of them are as good as the largest."""
+    c = Case(2, L, 1, 2, dk, dv, dt, seed=231)
+    c.beta = (torch.from_numpy(synth.normal_f32((2, L, 2), 2.0, 232)).cuda().clamp(-5, 5) + 15).to(dt)
+    c.beta[1] *= -1
+    got = f64(c.backward(c.forward()[2])[4])
+    x = [f64(t) for t in c.inputs()]
+    M = K.delta_forward(*x, f64(c.s0), None, False, dk ** -0.5)[3]
+    *w, MD, _ = K.delta_backward(*x, f64(c.s0), f64(c.do), f64(c.dl), None, False, dk ** -0.5)
+    nb = 1 / (1 + np.exp(x[4]))
+    want, h = w[4], half(dt)
+    near("dbeta", got, want, 256 * U * dv * nb * (M * MD)[:, None] * (1 + h) + (8 * U + h) * np.abs(want))
+    assert np.all(got[0] != 0) and np.abs(want[0]).max() > 100 * np.abs(want[0]).min() > 0
