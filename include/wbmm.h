@@ -453,8 +453,9 @@ wbmm_status wbmm_scan_backward(int64_t outer, int64_t len, int64_t inner, int dt
  * what stands before a mixer. Tensors are dense (outer, len, inner) and normed over len, for every
  * (outer, inner): the channels of a map are (B, C, H W) in NCHW, (B H W, C, 1) in NHWC.
  *   t = x + residual,   y = t weight / sqrt(mean_len(t^2) + eps).
- * t is formed in fp32 and normed as it is, its squares summed in fp64; s and y are rounded once (RNE). An
- * infinity or NaN in t reaches its own (outer, inner) only.
+ * t is formed in fp32 and normed as it is, its squares summed and y's products formed in fp64; s and y are
+ * rounded once (RNE; a bf16 y by way of fp32). An infinity or NaN in t reaches its own (outer, inner) only,
+ * one in a weight its own entries only.
  * dtype:    of x, residual, s and y: WBMM_F32 or WBMM_BF16.
  * residual: device tensor, or NULL. weight: device fp32 [len], or NULL for ones.
  * s:        device tensor, t in dtype (what the backward takes), or NULL. May be x or residual itself.

@@ -117,23 +117,17 @@ __device__ __forceinline__ float rstd_of(float sum, float inv, float eps) {
   return __builtin_isfinite(f) && r > 0.f ? f : r;
 }
 
-// The forward's rstd, in two floats. A code of 8 bits, and a bf16 y, hang on y's last bit where y lies between
-// two of them, so y is formed to that bit: the sum in fp64, y = t (rstd w) with one rounding. Of 12.4 M fp32 y 10 to
-// 30 codes differed from those of the exact y before, 1 to 9 now (t's own rounding); of bf16 y none. 128 x
-// 96 x 3136 fp32 takes 90 us with either, 50176 rows of 192 bf16 from the last-level cache 12.8 for 11.5.
-struct Rstd {
-  float hi, lo;
-  __device__ __forceinline__ float y(float t, float w) const {
-    const float f = hi * w;
-    return fmaf(t, f, t * fmaf(lo, w, fmaf(hi, w, -f)));
-  }
-};
-__device__ __forceinline__ Rstd rstd_of(double sum, const NormArgs& a) {
+// The forward's rstd, and y from it. A code of 8 bits, and a bf16 y, hang on y's last bit where y lies between two of
+// them, so y is formed to that bit: sum and products in fp64, y = t (rstd w) with one rounding, right also where rstd or
+// rstd w is past fp32's range or w is infinite.
+__device__ __forceinline__ double rstd_of(double sum, const NormArgs& a) {
   const double m = fma(sum, a.inv64, (double)a.eps), r = __builtin_amdgcn_rsq(m);
   // a Newton step; infinities, zeros and NaN are left as they are
   const double f = fma(r * 0.5, fma(-m * r, r, 1.0), r);
-  const float hi = (float)(__builtin_isfinite(f) && r > 0.0 ? f : r);
-  return {hi, __builtin_isfinite(hi) && hi > 0.f ? (float)(f - (double)hi) : 0.f};
+  return __builtin_isfinite(f) && r > 0.0 ? f : r;
+}
+__device__ __forceinline__ float y_of(float t, double rstd, float w) {
+  return (float)((double)t * (rstd * (double)w));
 }
 
 // ---------------------------------------------------------------------------- rows
@@ -211,14 +205,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows(NormArgs a) {
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int j = 0; j < kP; ++j) sum = fma((double)t[k][j], (double)t[k][j], sum);
-  const Rstd rstd = rstd_of(row_sum<LPR>(sum, sm), a);
+  const double rstd = rstd_of(row_sum<LPR>(sum, sm), a);
   if (!live) return;   // no barrier and no exchange across rows from here on
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (a.s) pc.store((T*)a.s + base, k, t[k]);
     float y[kP];
 #pragma unroll
-    for (int j = 0; j < kP; ++j) y[j] = rstd.y(t[k][j], w[k][j]);
+    for (int j = 0; j < kP; ++j) y[j] = y_of(t[k][j], rstd, w[k][j]);
     pc.store((T*)a.y + base, k, y);
     if (VEC && a.codes) {   // len a multiple of 32: a group is a quad's, in or out together
       uint32_t m = 0;
@@ -258,11 +252,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_long(NormArgs a) {
     const float t = load_f32<T>(x, e) + (res ? load_f32<T>(res, e) : 0.f);
     sum = fma((double)t, (double)t, sum);
   }
-  const Rstd rstd = rstd_of(row_sum<256>(sum, sm), a);
+  const double rstd = rstd_of(row_sum<256>(sum, sm), a);
   for (uint32_t e = threadIdx.x; e < a.len; e += kThreads) {
     const float t = load_f32<T>(x, e) + (res ? load_f32<T>(res, e) : 0.f);
     if (a.s) put((T*)a.s + base + e, t);
-    put((T*)a.y + base + e, rstd.y(t, a.w ? a.w[e] : 1.f));
+    put((T*)a.y + base + e, y_of(t, rstd, a.w ? a.w[e] : 1.f));
   }
 }
 
@@ -511,11 +505,11 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
       for (int j = 0; j < VW; ++j) t[j] += r[j];
     }
   };
-  auto finish = [&](uint32_t e, const float (&t)[VW], const Rstd (&rstd)[VW], float w) {
+  auto finish = [&](uint32_t e, const float (&t)[VW], const double (&rstd)[VW], float w) {
     const size_t at = c.base + (size_t)e * c.stride;
     float y[VW];
 #pragma unroll
-    for (int j = 0; j < VW; ++j) y[j] = rstd[j].y(t[j], w);
+    for (int j = 0; j < VW; ++j) y[j] = y_of(t[j], rstd[j], w);
     if (c.live) {
       if (a.s) store_n<T, VW>((T*)a.s + at, t);
       store_n<T, VW>((T*)a.y + at, y);
@@ -544,7 +538,7 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
 #pragma unroll
         for (int j = 0; j < VW; ++j) sq[j] = fma((double)t[k][j], (double)t[k][j], sq[j]);
     wave_join<VW>(sq, sm, NW);
-    Rstd rstd[VW];
+    double rstd[VW];
 #pragma unroll
     for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a);
 #pragma unroll
@@ -560,7 +554,7 @@ __global__ void __launch_bounds__(1024) k_norm_cols(NormArgs a) {
       for (int j = 0; j < VW; ++j) sq[j] = fma((double)t[j], (double)t[j], sq[j]);
     }
     wave_join<VW>(sq, sm, NW);
-    Rstd rstd[VW];
+    double rstd[VW];
 #pragma unroll
     for (int j = 0; j < VW; ++j) rstd[j] = rstd_of(sq[j], a);
     for (uint32_t e = wv; e < a.len; e += NW) {

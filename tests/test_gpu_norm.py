@@ -309,3 +309,55 @@ def test_replayed_and_on_another_stream():
     y = M.wbmm_rmsnorm_forward(x, 1, residual=r, weight=w, stream=side)[0]
     side.synchronize()
     assert torch.equal(y, want[0])
+
+
+EXACT = [(50, 192, 1), (9, 32, 1), (77, 97, 1), (3, 1544, 1), (2, 6152, 1), (4, 192, 66), (2, 8, 33), (2, 100, 49),
+         (1, 600, 66), (2, 257, 96)]
+
+
+def to_the_last_bit(got, want, dt):
+    """y is formed in fp64 and rounded to fp32, and from there to bf16: off by half a step of its own type, and in
+    bf16 by as much more as a value next to a tie moves in fp32, 2^-17 of the half step; twice the fp64 part
+    (34 roundings of 2^-53) on top. NaN where the oracle has it, infinite past the type's range."""
+    bits = 24 if dt == F32 else 8
+    with np.errstate(all="ignore"):
+        e = np.maximum(np.floor(np.log2(np.abs(want))), -126)
+        e[want == 0] = -126
+    half_step = 2.0 ** (e - bits)
+    past = np.abs(want) >= (2 - 2.0 ** -bits) * 2.0 ** 127
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[past], np.copysign(np.inf, want[past]))
+    rest = ~past & ~nan
+    more = 2.0 ** -20 if dt == F32 else 2.0 ** -15
+    bad = np.abs(got[rest] - want[rest]) > half_step[rest] * (1 + more)
+    assert not bad.any(), (got[rest][bad][:5], want[rest][bad][:5])
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("o,c,i", EXACT)
+def test_forward_to_the_last_bit(o, c, i, dt):
+    x, wt = mk((o, c, i), 1.0, 31, dt), 1 + mk((c,), 0.2, 32)
+    y = R().wbmm_rmsnorm_forward(x, 1, weight=wt)[0]
+    to_the_last_bit(f64(y), K.norm_forward(f64(x), None, f64(wt), float(np.float32(1e-6)))[1], dt)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("o,c,i", EXACT)
+def test_forward_with_extreme_weights_and_rows(o, c, i, dt):
+    """Infinite and NaN weights, products of rstd and weight beyond fp32 in either direction, rows whose rstd is, rows of
+    zeros: what the formula gives, in its own element."""
+    print(f"\n[case] norm extremes {o}x{c}x{i} {dt}", flush=True)
+    x, wt = mk((o, c, i), 1.0, 33, dt), 1 + mk((c,), 0.2, 34)
+    few = [float("inf"), 3e38, -float("inf"), 1e-30, 0.0, float("nan"), -3e38, 2e-38]
+    wt[:8] = torch.tensor(few)
+    rows = x.permute(0, 2, 1).reshape(-1, c)
+    n = rows.shape[0]
+    for k, f in enumerate((1e-20, 1e20, 3e-39, 0.0, 1e30)):
+        rows[k * n // 7 + n // 9] *= f
+    x = rows.view(o, i, c).permute(0, 2, 1).contiguous()
+    for eps in (0.0, 1e-6):
+        y = R().wbmm_rmsnorm_forward(x, 1, weight=wt, eps=eps)[0]
+        with np.errstate(all="ignore"):
+            want = K.norm_forward(f64(x), None, f64(wt), float(np.float32(eps)))[1]     # the call takes a float
+        to_the_last_bit(f64(y), want, dt)
