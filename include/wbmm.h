@@ -478,7 +478,8 @@ wbmm_status wbmm_rmsnorm_forward(int64_t outer, int64_t len, int64_t inner, int 
  * the sum that it stored:
  *   r = 1 / sqrt(mean(s^2) + eps),   h = s r,
  *   dx = ds + r (weight dy - h mean(weight dy h)),   dweight = sum over (outer, inner) of dy h.
- * Computed in fp32: |s| beyond about 1.8e19 makes the mean of its squares infinite and r zero there.
+ * The two sums over len and r are fp64, so that s may be as large or as small as fp32 goes, as in the
+ * forward; weight dy, h and the mean are fp32.
  * s:       the forward's s (its x where there was no residual). dy: gradient of y.
  * ds:      gradient of s from elsewhere (the residual's further way), or NULL for zeros.
  * dx:      device tensor in dtype, the gradient of x and of residual alike, or NULL to skip.

@@ -45,8 +45,8 @@ struct NormArgs {
   uint8_t* codes;
   uint8_t* scales;
   double* part;                    // [workgroups][len]
-  float eps, inv;                  // inv = 1 / len
-  double inv64;
+  float eps;
+  double inv64;                    // 1 / len
   int fmt;
   uint32_t len, rows;              // rows = outer * inner
   uint32_t tiles;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void carry_add(float& acc, float& c, float x) {
 }
 
 // Sum over the LPR lanes of a row, in every one of them. LPR = 256: the workgroup's, through sm
-// (4 floats, another set for each call between two barriers).
+// (4 of them, another set for each call between two barriers).
 template <int LPR, typename S>
 __device__ __forceinline__ S row_sum(S v, S* sm) {
 #pragma unroll
@@ -109,15 +109,7 @@ __device__ __forceinline__ S row_sum(S v, S* sm) {
   return v;
 }
 
-__device__ __forceinline__ float rstd_of(float sum, float inv, float eps) {
-  const float m = fmaf(sum, inv, eps);
-  float r = __builtin_amdgcn_rsqf(m);
-  // one Newton step for the last bit; infinities, zeros and NaN are left as they are
-  const float f = fmaf(r * 0.5f, fmaf(-m * r, r, 1.f), r);
-  return __builtin_isfinite(f) && r > 0.f ? f : r;
-}
-
-// The forward's rstd, and y from it. A code of 8 bits, and a bf16 y, hang on y's last bit where y lies between two of
+// rstd, and y from it. Sums are fp64 (squares of fp32 numbers can neither overflow nor vanish there). A code of 8 bits, and a bf16 y, hang on y's last bit where y lies between two of
 // them, so y is formed to that bit: sum and products in fp64, y = t (rstd w) with one rounding, right also where rstd or
 // rstd w is past fp32's range or w is infinite.
 __device__ __forceinline__ double rstd_of(double sum, const NormArgs& a) {
@@ -128,6 +120,11 @@ __device__ __forceinline__ double rstd_of(double sum, const NormArgs& a) {
 }
 __device__ __forceinline__ float y_of(float t, double rstd, float w) {
   return (float)((double)t * (rstd * (double)w));
+}
+// Backward: h, and dx without ds from g = w dy, h and m = mean(w dy h).
+__device__ __forceinline__ float h_of(float t, double rstd) { return (float)((double)t * rstd); }
+__device__ __forceinline__ float dx_of(float g, float h, float m, double rstd) {
+  return (float)(rstd * (double)fmaf(-m, h, g));
 }
 
 // ---------------------------------------------------------------------------- rows
@@ -265,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_long(NormArgs a) {
 template <typename T, int LPR, int K, bool VEC, bool DW>
 __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
   constexpr int RPW = kThreads / LPR;
-  __shared__ float sm[2][2][4];
+  __shared__ double sm[2][2][4];
   __shared__ float red[DW && LPR < 256 ? kThreads * kP : 1];
   const RowPieces<T, LPR, K, VEC> pc{(int)(threadIdx.x % LPR), a.len};
   float w[K][kP], dw[K][kP], dc[K][kP];
@@ -287,29 +284,31 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
     if (a.res && a.y)
 #pragma unroll
       for (int k = 0; k < K; ++k) pc.load((const T*)a.res + base, k, r[k]);
-    float sq = 0.f, dot = 0.f;
+    double sq = 0.0, dot = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
-        sq = fmaf(t[k][j], t[k][j], sq);
-        dot = fmaf(t[k][j], g[k][j] * w[k][j], dot);
+        sq = fma((double)t[k][j], (double)t[k][j], sq);
+        dot = fma((double)t[k][j], (double)(g[k][j] * w[k][j]), dot);
       }
     // two turns use different words: a wave still reads the last turn's while another writes
     sq = row_sum<LPR>(sq, sm[turn][0]);
     dot = row_sum<LPR>(dot, sm[turn][1]);
-    const float rstd = rstd_of(sq, a.inv, a.eps);
-    const float f = dot * rstd * rstd * a.inv;      // mean(w dy h) rstd
+    const double rstd = rstd_of(sq, a);
+    const float mean = (float)(dot * rstd * a.inv64);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) t[k][j] = h_of(t[k][j], rstd);
       if (DW && live)
 #pragma unroll
-        for (int j = 0; j < kP; ++j) carry_add(dw[k][j], dc[k][j], g[k][j] * (t[k][j] * rstd));
+        for (int j = 0; j < kP; ++j) carry_add(dw[k][j], dc[k][j], g[k][j] * t[k][j]);
       if (a.y && live) {
         float d[kP];
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
-          d[j] = rstd * fmaf(-f, t[k][j], g[k][j] * w[k][j]);
+          d[j] = dx_of(g[k][j] * w[k][j], t[k][j], mean, rstd);
           if (a.res) d[j] += r[k][j];
         }
         pc.store((T*)a.y + base, k, d);
@@ -344,30 +343,31 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
 // Rows longer than the registers; dw's sums are kept in fp64 in the workgroup's partial.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_rows_long_bwd(NormArgs a) {
-  __shared__ float sm[2][2][4];
+  __shared__ double sm[2][2][4];
   double* part = a.part ? a.part + (size_t)blockIdx.x * a.len : nullptr;
   int turn = 0;
   for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const size_t base = (size_t)row * a.len;
     const T *x = (const T*)a.x + base, *dy = (const T*)a.dy + base;
     const T* res = a.res ? (const T*)a.res + base : nullptr;
-    float sq = 0.f, sc = 0.f, dot = 0.f, dc = 0.f;
+    double sq = 0.0, dot = 0.0;
     for (uint32_t e = threadIdx.x; e < a.len; e += kThreads) {
       const float t = load_f32<T>(x, e), g = load_f32<T>(dy, e) * (a.w ? a.w[e] : 1.f);
-      carry_add(sq, sc, t * t);
-      carry_add(dot, dc, t * g);
+      sq = fma((double)t, (double)t, sq);
+      dot = fma((double)t, (double)g, dot);
     }
     sq = row_sum<256>(sq, sm[turn][0]);
     dot = row_sum<256>(dot, sm[turn][1]);
-    const float rstd = rstd_of(sq, a.inv, a.eps), f = dot * rstd * rstd * a.inv;
+    const double rstd = rstd_of(sq, a);
+    const float mean = (float)(dot * rstd * a.inv64);
     for (uint32_t e = threadIdx.x; e < a.len; e += kThreads) {
-      const float t = load_f32<T>(x, e), g = load_f32<T>(dy, e);
+      const float h = h_of(load_f32<T>(x, e), rstd), g = load_f32<T>(dy, e);
       if (part) {   // this thread's own elements in every row
-        const double add = (double)(g * (t * rstd));
+        const double add = (double)(g * h);
         part[e] = row == blockIdx.x ? add : part[e] + add;
       }
       if (a.y) {
-        const float d = rstd * fmaf(-f, t, g * (a.w ? a.w[e] : 1.f));
+        const float d = dx_of(g * (a.w ? a.w[e] : 1.f), h, mean, rstd);
         put((T*)a.y + base + e, res ? d + load_f32<T>(res, e) : d);
       }
     }
@@ -572,7 +572,7 @@ template <typename T, int N, bool DW>
 __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
   constexpr int VW = 1;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  float* const sm = (float*)lds;
+  double* const sm = (double*)lds;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   const int lane = threadIdx.x & 63;
   constexpr int M = N > 0 ? N : 1;
@@ -585,36 +585,41 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
     const ColAt c = col_at<VW>(a, tile);
     const T *x = (const T*)a.x + c.base, *dy = (const T*)a.dy + c.base;
     const T* res = a.res ? (const T*)a.res + c.base : nullptr;
-    float sq[VW], dot[VW], rstd[VW], f[VW];
+    double sq[VW], dot[VW], rstd[VW];
+    float mean[VW];
 #pragma unroll
-    for (int j = 0; j < VW; ++j) sq[j] = dot[j] = 0.f;
+    for (int j = 0; j < VW; ++j) sq[j] = dot[j] = 0.0;
     auto join = [&] {
-      float* at = sm + turn * NW * 2 * VW * 64;
-      float both[2 * VW];
+      double* at = sm + turn * NW * 2 * VW * 64;
+      double both[2 * VW];
 #pragma unroll
       for (int j = 0; j < VW; ++j) both[j] = sq[j], both[VW + j] = dot[j];
       wave_join<2 * VW>(both, at, NW);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
-        rstd[j] = rstd_of(both[j], a.inv, a.eps);
-        f[j] = both[VW + j] * rstd[j] * rstd[j] * a.inv;
+        rstd[j] = rstd_of(both[j], a);
+        mean[j] = (float)(both[VW + j] * rstd[j] * a.inv64);
       }
     };
-    auto finish = [&](uint32_t e, const float (&t)[VW], const float (&g)[VW],
+    auto finish = [&](uint32_t e, const float (&h)[VW], const float (&g)[VW],
                       const float (&r)[VW], float w) {
       if (!a.y || !c.live) return;
       float d[VW];
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
-        d[j] = rstd[j] * fmaf(-f[j], t[j], g[j] * w);
+        d[j] = dx_of(g[j] * w, h[j], mean[j], rstd[j]);
         if (res) d[j] += r[j];
       }
       store_n<T, VW>((T*)a.y + c.base + (size_t)e * c.stride, d);
     };
-    auto dw_of = [&](const float (&t)[VW], const float (&g)[VW]) {
+    auto to_h = [&](float (&t)[VW]) {
+#pragma unroll
+      for (int j = 0; j < VW; ++j) t[j] = h_of(t[j], rstd[j]);
+    };
+    auto dw_of = [&](const float (&h)[VW], const float (&g)[VW]) {
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < VW; ++j) s = fmaf(g[j], t[j] * rstd[j], s);
+      for (int j = 0; j < VW; ++j) s = fmaf(g[j], h[j], s);
       return c.live ? s : 0.f;
     };
     if constexpr (N > 0) {
@@ -637,22 +642,20 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
         if (wv + NW * k < (int)a.len)
 #pragma unroll
           for (int j = 0; j < VW; ++j) {
-            sq[j] = fmaf(t[k][j], t[k][j], sq[j]);
-            dot[j] = fmaf(t[k][j], g[k][j] * w[k], dot[j]);
+            sq[j] = fma((double)t[k][j], (double)t[k][j], sq[j]);
+            dot[j] = fma((double)t[k][j], (double)(g[k][j] * w[k]), dot[j]);
           }
       join();
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const uint32_t e = wv + NW * k;
         if (e < a.len) {
+          to_h(t[k]);
           if (DW) carry_add(dw[k], dc[k], dw_of(t[k], g[k]));
           finish(e, t[k], g[k], r[k], w[k]);
         }
       }
     } else {
-      float sc[VW], gc[VW];
-#pragma unroll
-      for (int j = 0; j < VW; ++j) sc[j] = gc[j] = 0.f;
       for (uint32_t e = wv; e < a.len; e += NW) {
         float t[VW], g[VW];
         load_n<T, VW>(x + (size_t)e * c.stride, t);
@@ -660,8 +663,8 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
         const float w = a.w ? a.w[e] : 1.f;
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-          carry_add(sq[j], sc[j], t[j] * t[j]);
-          carry_add(dot[j], gc[j], t[j] * (g[j] * w));
+          sq[j] = fma((double)t[j], (double)t[j], sq[j]);
+          dot[j] = fma((double)t[j], (double)(g[j] * w), dot[j]);
         }
       }
       join();
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
         float t[VW], g[VW];
         load_n<T, VW>(x + (size_t)e * c.stride, t);
         load_n<T, VW>(dy + (size_t)e * c.stride, g);
+        to_h(t);
         if (DW) {
           const double s = wave_sum_f64_last((double)dw_of(t, g));
           if (lane == 63) part[e] = tile == blockIdx.x ? s : part[e] + s;
@@ -767,7 +771,7 @@ NormArgs args_of(const NormRequest& r) {
   NormArgs a{};
   a.x = r.x; a.res = r.res; a.w = r.w; a.dy = r.dy; a.s = r.s; a.y = r.y;
   a.codes = r.codes; a.scales = r.scales; a.part = (double*)r.ws;
-  a.eps = r.eps; a.inv64 = 1.0 / (double)r.len; a.inv = (float)a.inv64; a.fmt = r.fmt;
+  a.eps = r.eps; a.inv64 = 1.0 / (double)r.len; a.fmt = r.fmt;
   a.len = (uint32_t)r.len; a.rows = (uint32_t)(r.outer * r.inner);
   a.inner = fast_div((uint32_t)r.inner);
   return a;
@@ -878,7 +882,7 @@ void backward_t(const NormRequest& r, hipStream_t st) {
     groups = dw && a.tiles > (uint32_t)kDwGroups ? kDwGroups : (int)a.tiles;
     with_cols(s, [&](auto vw, auto n) {
       constexpr int VW = decltype(vw)::value, N = decltype(n)::value;
-      const size_t lds = (size_t)2 * s.nw * 2 * VW * 64 * 4;
+      const size_t lds = (size_t)2 * s.nw * 2 * VW * 64 * 8;
       if constexpr (N <= kColBwd && VW == 1) {
         if (dw)
           k_norm_cols_bwd<T, N, true><<<dim3(groups), 64 * s.nw, lds, st>>>(a);

@@ -361,3 +361,25 @@ def test_forward_with_extreme_weights_and_rows(o, c, i, dt):
         with np.errstate(all="ignore"):
             want = K.norm_forward(f64(x), None, f64(wt), float(np.float32(eps)))[1]     # the call takes a float
         to_the_last_bit(f64(y), want, dt)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("o,c,i", EXACT + [(2, 20001, 1), (3, 17, 100), (1, 2048, 64)])
+def test_backward_of_extreme_rows(o, c, i, dt):
+    """Rows of 1e18 to 1e38 and of 1e-20 to the subnormal numbers, whose squares are past fp32's range: as good as any
+    other row (their sums are fp64). The bounds are those of the other rows; what is subnormal in the result
+    may be off by one of its steps."""
+    print(f"\n[case] norm bwd extremes {o}x{c}x{i} {dt}", flush=True)
+    s, dy = mk((o, c, i), 1.0, 35, dt), mk((o, c, i), 1.0, 36, dt)
+    wt = 1 + mk((c,), 0.2, 37)
+    rows, g = (t.permute(0, 2, 1).reshape(-1, c) for t in (s, dy))
+    n = rows.shape[0]
+    for r, f in {k * n // 7 + n // 9: f for k, f in enumerate((1e18, 2e19, 1e38 / 6, 1e-20, 1e-30, 3e-39))}.items():
+        rows[r] *= f
+        g[r] *= 1e-6 if f < 1 else 1.0
+    s, dy = (t.view(o, i, c).permute(0, 2, 1).contiguous() for t in (rows, g))
+    for eps in (0.0, 1e-6):
+        dx, dw = R().wbmm_rmsnorm_backward(s, dy, 1, weight=wt, eps=eps)
+        wdx, wdw, mag, wmag = K.norm_backward(f64(s), f64(dy), None, f64(wt), float(np.float32(eps)))
+        near(f64(dx), wdx, 48 * U * mag * (1 + half(dt)) + half(dt) * np.abs(wdx) + 2.0 ** (-149 if dt == F32 else -133))
+        near(f64(dw), wdw, 32 * U * wmag + U * np.abs(wdw))
