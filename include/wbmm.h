@@ -483,8 +483,7 @@ wbmm_status wbmm_rmsnorm_forward(int64_t outer, int64_t len, int64_t inner, int 
  * s:       the forward's s (its x where there was no residual). dy: gradient of y.
  * ds:      gradient of s from elsewhere (the residual's further way), or NULL for zeros.
  * dx:      device tensor in dtype, the gradient of x and of residual alike, or NULL to skip.
- * dweight: device fp32 [len], or NULL to skip. Summed in a fixed order, in fp32 with the roundings
- *          carried along, then in fp64.
+ * dweight: device fp32 [len], or NULL to skip. Summed in fp64 in a fixed order.
  * workspace: wbmm_rmsnorm_backward_workspace_bytes(...) bytes, 16-byte aligned; not needed without
  *          dweight. Calls that share one must be ordered on one stream.
  * Errors as in the forward, and WBMM_E_WORKSPACE.

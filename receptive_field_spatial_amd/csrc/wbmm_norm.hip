@@ -18,8 +18,7 @@
 // Measured: forward bf16 with codes, 50176 rows of 192, 17.0 us (87 MB, 5.1 TB/s); backward fp32, 128 x 96 x
 // 3136, 115 us (617 MB, 5.4 TB/s) and 4.4 for dw's partials; single rows 2 us, a launch's own time.
 //
-// dw: fp32 sums with their rounding errors carried along (the sum of any number of terms is good to
-// two half steps), then fp64 partials of a workgroup, added in a fixed order by a second launch.
+// dw: fp64 sums of fp32 products, then partials of a workgroup, added in a fixed order by a second launch.
 #include "wbmm_ckpt.hpp"
 #include "wbmm_launch.hpp"
 #include "wbmm_norm.hpp"
@@ -87,13 +86,6 @@ __device__ __forceinline__ void narrow8(uint16_t* p, const float (&v)[kP]) {
 }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)bf_bits(v); }
-
-// acc + x with what the sum rounds away kept in c.
-__device__ __forceinline__ void carry_add(float& acc, float& c, float x) {
-  const float y = x - c, t = acc + y;
-  c = (t - acc) - y;
-  acc = t;
-}
 
 // Sum over the LPR lanes of a row, in every one of them. LPR = 256: the workgroup's, through sm
 // (4 of them, another set for each call between two barriers).
@@ -263,14 +255,15 @@ template <typename T, int LPR, int K, bool VEC, bool DW>
 __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
   constexpr int RPW = kThreads / LPR;
   __shared__ double sm[2][2][4];
-  __shared__ float red[DW && LPR < 256 ? kThreads * kP : 1];
+  __shared__ double red[DW && LPR < 256 ? kThreads * kP : 1];
   const RowPieces<T, LPR, K, VEC> pc{(int)(threadIdx.x % LPR), a.len};
-  float w[K][kP], dw[K][kP], dc[K][kP];
+  float w[K][kP];
+  double dw[K][kP];
   pc.weights(a.w, w);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < kP; ++j) dw[k][j] = dc[k][j] = 0.f;
+    for (int j = 0; j < kP; ++j) dw[k][j] = 0.0;
   int turn = 0;
   for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, turn ^= 1) {
     const uint32_t row = tile * RPW + threadIdx.x / LPR;
@@ -303,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
       for (int j = 0; j < kP; ++j) t[k][j] = h_of(t[k][j], rstd);
       if (DW && live)
 #pragma unroll
-        for (int j = 0; j < kP; ++j) carry_add(dw[k][j], dc[k][j], g[k][j] * t[k][j]);
+        for (int j = 0; j < kP; ++j) dw[k][j] += (double)(g[k][j] * t[k][j]);
       if (a.y && live) {
         float d[kP];
 #pragma unroll
@@ -322,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
     if (LPR == 256) {
 #pragma unroll
       for (int j = 0; j < kP; ++j)
-        if (pc.el(k, j) < a.len) part[pc.el(k, j)] = (double)dw[k][j];
+        if (pc.el(k, j) < a.len) part[pc.el(k, j)] = dw[k][j];
     } else {
       __syncthreads();
 #pragma unroll
@@ -333,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(NormArgs a) {
         const int l = i % LPR, j = i / LPR;
         const uint32_t e = VEC ? (uint32_t)(l + LPR * k) * kP + j : l + LPR * (uint32_t)(kP * k + j);
         double s = 0;
-        for (int q = 0; q < RPW; ++q) s += (double)red[j * kThreads + q * LPR + l];
+        for (int q = 0; q < RPW; ++q) s += red[j * kThreads + q * LPR + l];
         if (e < a.len) part[e] = s;
       }
     }
@@ -576,9 +569,9 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   const int lane = threadIdx.x & 63;
   constexpr int M = N > 0 ? N : 1;
-  float dw[M], dc[M];
+  double dw[M];
 #pragma unroll
-  for (int k = 0; k < M; ++k) dw[k] = dc[k] = 0.f;
+  for (int k = 0; k < M; ++k) dw[k] = 0.0;
   double* part = DW ? a.part + (size_t)blockIdx.x * a.len : nullptr;
   int turn = 0;
   for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, turn ^= 1) {
@@ -651,7 +644,7 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
         const uint32_t e = wv + NW * k;
         if (e < a.len) {
           to_h(t[k]);
-          if (DW) carry_add(dw[k], dc[k], dw_of(t[k], g[k]));
+          if (DW) dw[k] += (double)dw_of(t[k], g[k]);
           finish(e, t[k], g[k], r[k], w[k]);
         }
       }
@@ -687,7 +680,7 @@ __global__ void __launch_bounds__(1024) k_norm_cols_bwd(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const uint32_t e = wv + NW * k;
-      const double s = wave_sum_f64_last((double)dw[k]);
+      const double s = wave_sum_f64_last(dw[k]);
       if (lane == 63 && e < a.len) part[e] = s;
     }
   }
@@ -738,7 +731,7 @@ bool rows_vec(const NormRequest& r) {
 // the fewest idle lanes (50176 rows of bf16, 192 entries: 8 lanes x 3 pieces): 19.1 us for 20.9 backward, 8 rows
 // 4.7 for 6.6; 264 entries, half of whose lanes idle: 8.5 for 7.5 forward. A workgroup's 256 lanes only
 // where a wave's 3 pieces end: 20000 rows of 768 in 16.4 us with 64 x 2, 22.4 with 256 x 1. More than 3 pieces
-// would not leave a backward (three tensors and dw with its carry, 40 registers a piece) two
+// would not leave a backward (three tensors and dw in fp64, 40 registers a piece) two
 // workgroups per SIMD.
 struct RowShape { int lpr, k; };
 RowShape row_shape(int64_t len) {

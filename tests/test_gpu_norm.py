@@ -383,3 +383,20 @@ def test_backward_of_extreme_rows(o, c, i, dt):
         wdx, wdw, mag, wmag = K.norm_backward(f64(s), f64(dy), None, f64(wt), float(np.float32(eps)))
         near(f64(dx), wdx, 48 * U * mag * (1 + half(dt)) + half(dt) * np.abs(wdx) + 2.0 ** (-149 if dt == F32 else -133))
         near(f64(dw), wdw, 32 * U * wmag + U * np.abs(wdw))
+
+
+@pytest.mark.parametrize("o,c,i", [(20000, 96, 1), (20000, 33, 1), (700, 6152, 1), (70, 12, 650), (3, 40, 40000), (40, 600, 66)])
+def test_infinite_gradients_in_the_weights_sums(o, c, i):
+    """dweight of an entry is the sum of its terms: infinite where one is, NaN where two cancel, the same as before
+    everywhere else."""
+    s, dy, w = mk((o, c, i), 1.0, 41), mk((o, c, i), 1.0, 42), torch.ones(c, device="cuda")
+    inf = float("inf")
+    for e, at in ((3, (0, 0)), (5, (o - 1, i - 1)), (7, (1, 0)), (7, (o - 2, i - 1))):
+        s[at[0], e, at[1]] = 1.0
+    clean = R().wbmm_rmsnorm_backward(s, dy, 1, weight=w, dx=False)[1]
+    dy[0, 3, 0], dy[o - 1, 5, i - 1] = inf, -inf
+    dy[1, 7, 0], dy[o - 2, 7, i - 1] = inf, -inf
+    got = R().wbmm_rmsnorm_backward(s, dy, 1, weight=w, dx=False)[1]
+    assert got[3] == inf and got[5] == -inf and got[7].isnan()
+    rest = [e for e in range(c) if e not in (3, 5, 7)]
+    assert torch.equal(got[rest], clean[rest])
