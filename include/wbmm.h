@@ -507,11 +507,13 @@ wbmm_status wbmm_rmsnorm_backward(int64_t outer, int64_t len, int64_t inner, int
  *             checkpoints in WBMM_CKPT_E4M3 (n code bytes and ceil(n / WBMM_CKPT_GROUP) scale bytes each;
  *             all zero bytes are zero states). They are read as wbmm_ckpt_unpack gives them. What is
  *             stored is rounded to one of the two neighbouring code values at random, to the value
- *             itself on average, a root above zero never to 0 (v, the root's square, moves up to 1/16 further
- *             than unrounded, on average, as the root's variance joins it); random words are Philox 4x32 with 7
- *             rounds, counter (index / 4 as 64 bits, tensor, t), key `seed`, word index % 4, its low
- *             16 bits for m and its high ones for the root. A group that holds an infinity or a NaN
- *             becomes NaN, as in wbmm_ckpt_pack.
+ *             itself on average; but a root above zero never to 0: one below the least code, 2^-17 of its
+ *             group's largest, is held at that code until the group's scale falls. v, the root's square, moves
+ *             further than unrounded, on average, as the root's variance joins it: by up to 1/16 where the
+ *             codes are normal (roots from 2^-13 of their group's largest on, at least), by 1 / (2 n) at the
+ *             n-th of the 8 least. Random words are Philox 4x32 with 7 rounds, counter (index / 4 as 64
+ *             bits, tensor, t), key `seed`, word index % 4, its low 16 bits for m and its high ones for the
+ *             root. A group that holds an infinity or a NaN becomes NaN, as in wbmm_ckpt_pack.
  *   p_bf16:   a copy of p in bf16 (RNE), written, or NULL: what a bf16 forward reads.
  * wbmm_adamw_plan checks `count` such tensors and lays out a table for them in HOST memory (table_bytes
  *   at least wbmm_adamw_plan_bytes(...), 8-byte aligned); the caller copies it to the device and keeps

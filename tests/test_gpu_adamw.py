@@ -256,3 +256,29 @@ def test_refused_plans():
                dict(step=torch.ones(2, dtype=torch.int32, device="cuda")), dict(lr_factor=torch.ones(1))):
         with pytest.raises(M.WbmmError):
             M.wbmm_adamw_step(plan, **{"lr": 0.1, **kw})
+
+
+def test_eight_bit_states_past_32_bits():
+    """2^32 + 5000 parameters with bf16 gradients and 8-bit states: the first 4000 and the last 5000, which lie from
+    element 2^32 on, equal the oracle after two steps, codes, scales and the counters of the random words."""
+    n, k = (1 << 32) + 5000, 5000
+    p, g = torch.ones(n, device="cuda"), torch.ones(n, dtype=BF16, device="cuda")
+    m, v = zeros8(n), zeros8(n)
+    for part in (slice(0, 4000), slice(n - k, n)):
+        g[part] = dev(synth.normal_f32((part.stop - part.start,), 1.0, 2)).to(BF16)
+    plan = R().wbmm_adamw_plan([p], [g], [m], [v], weight_decay=0.1)
+
+    def host(part):
+        groups = slice(part.start // 32, -(-part.stop // 32))
+        get = lambda t: t.cpu().numpy()  # noqa: E731
+        return (get(p[part]), g[part].float().cpu().numpy(), *((get(c[part]), get(s[groups])) for c, s in (m, v)))
+
+    for step in (1, 2):
+        before = [host(part) for part in (slice(0, 4000), slice(n - k, n))]
+        R().wbmm_adamw_step(plan, lr=KW["lr"], betas=(KW["b1"], KW["b2"]), eps=KW["eps"], step=step, seed=77)
+        for part, (p0, g0, m0, v0) in zip((slice(0, 4000), slice(n - k, n)), before):
+            wp, wm, wv = K.adamw(p0, g0, m0, v0, wd=0.1, step=step, seed=77, first=part.start, **KW)
+            p1, _, m1, v1 = host(part)
+            assert same(p1, wp) and same(m1, wm) and same(v1, wv), (part, step)
+        if step == 1:      # equal parameters, gradients and states; from then on the states' roundings differ
+            assert torch.all(p[1 << 20::1 << 20] == p[1 << 20])
