@@ -79,9 +79,10 @@ def _dither(x, u, keep):
 
 
 def adamw(p, g, m, v, *, lr, b1, b2, eps, wd, step, tensor=0, seed=0, lr_factor=None,
-          grad_factor=None):
+          grad_factor=None, first=0):
     """One tensor's step in fp32, operation by operation. m, v: fp32 arrays, or (codes, scales) of m
-    and of v's root. Returns p, m, v in the same forms."""
+    and of v's root. first: the index of the arrays' first element in its tensor (a multiple of 32). Returns p, m, v
+    in the same forms."""
     f = np.float32
     lr = lr * float(lr_factor) if lr_factor is not None else lr
     k1, k2 = f(lr / (1 - b1 ** step)), f(1 / np.sqrt(1 - b2 ** step))
@@ -103,7 +104,7 @@ def adamw(p, g, m, v, *, lr, b1, b2, eps, wd, step, tensor=0, seed=0, lr_factor=
     if not small:
         return p, mm, vv
     n = p.size
-    words = philox(np.arange(-(-n // 4)), tensor, step, seed).reshape(-1)[:n]
+    words = philox(first // 4 + np.arange(-(-n // 4)), tensor, step, seed).reshape(-1)[:n]
     um = (words & np.uint64(0xffff)).astype(f) * f(2.0 ** -16)
     ur = (words >> np.uint64(16)).astype(f) * f(2.0 ** -16)
     return p, _dither(mm, um, False), _dither(root, ur, True)
@@ -163,6 +164,7 @@ def delta_backward(q, k, v, g, beta, s0, do, ds_last, lens, reverse, scale):
     B, L, H, dv_ = v.shape
     Hk, dk_ = q.shape[2:]
     a, b = _sig(np.clip(g, -87, 87)), _sig(beta)
+    na, nb = _sig(-np.clip(g, -87, 87)), _sig(-beta)       # 1 - a and 1 - b, where a and b are 1 in fp64 too
     dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
     dg, dbe, ds0 = np.zeros_like(g), np.zeros_like(beta), np.zeros((B, H, dk_, dv_))
     MD, dots = np.zeros((B, H)), np.zeros_like(g)
@@ -191,9 +193,9 @@ def delta_backward(q, k, v, g, beta, s0, do, ds_last, lens, reverse, scale):
                 dq[i, p, hk] += tq
                 dk[i, p, hk] += row + col
                 dv[i, p, h] = bb * Dk
-                dbe[i, p, h] = bb * (1 - bb) * (Dk @ err)
+                dbe[i, p, h] = bb * nb[i, p, h] * (Dk @ err)
                 dA = D - bb * np.outer(kk, Dk)
-                dg[i, p, h] = (1 - aa) * (dA * A).sum()
+                dg[i, p, h] = na[i, p, h] * (dA * A).sum()
                 mags[t] = (np.linalg.norm(qq) * np.linalg.norm(tq) + np.linalg.norm(kk) *
                            (np.linalg.norm(row) + np.linalg.norm(col)))
                 D = aa * dA
@@ -204,3 +206,40 @@ def delta_backward(q, k, v, g, beta, s0, do, ds_last, lens, reverse, scale):
                 dots[i, p, h] = mags[t // CHUNK * CHUNK: e].sum()
             ds0[i, h], MD[i, h] = D, top
     return dq, dk, dv, dg, dbe, ds0, MD, dots
+
+
+def delta_gate_bounds(q, k, v, g, beta, s0, do, ds_last, lens, reverse, scale):
+    """What dg and dbeta are sums of, in the order that a chunked computation forms them, fp64, (B, L, H) each:
+    the size of dg's terms (the dot products of the steps from t to its chunk's end, and of the state after the chunk
+    with its gradient, taken as independent), of dbeta's, and that last product's own share of dg."""
+    B, L, H, dv = v.shape
+    Hk, dk = q.shape[2:]
+    a, b = _sig(np.clip(g, -87, 87)), _sig(beta)
+    na, nb = _sig(-np.clip(g, -87, 87)), _sig(-beta)
+    tg, tb, last = (np.zeros((B, L, H)) for _ in range(3))
+    for i in range(B):
+        order = _seq(L, L if lens is None else lens[i], reverse)
+        for h in range(H):
+            hk = h // (H // Hk)
+            run = [np.zeros((dk, dv)) if s0 is None else s0[i, h]]
+            for p in order:
+                kk, A = k[i, p, hk], a[i, p, h] * run[-1]
+                run.append(A + b[i, p, h] * np.outer(kk, v[i, p, h] - kk @ A))
+            D = np.zeros((dk, dv)) if ds_last is None else ds_last[i, h]
+            sq, whole, size = 0.0, 0.0, 0.0
+            for t in range(len(order) - 1, -1, -1):
+                p, norm = order[t], np.linalg.norm
+                if t == len(order) - 1 or (t + 1) % CHUNK == 0:
+                    S = run[t + 1]
+                    whole, size = (S * D).sum(), 2 * norm(S) * norm(D) / np.sqrt(dk * dv)
+                    sq = size ** 2
+                qq, kk, bb, A = q[i, p, hk], k[i, p, hk], b[i, p, h], a[i, p, h] * run[t]
+                G = scale * do[i, p, h]
+                D = D + np.outer(qq, G)
+                Dk = kk @ D
+                row, col = bb * norm(A @ Dk), bb * norm(D @ (v[i, p, h] - kk @ A))
+                sq += (norm(qq) * norm(run[t + 1] @ G) + norm(kk) * (row + col)) ** 2
+                tg[i, p, h], last[i, p, h] = na[i, p, h] * np.sqrt(sq), na[i, p, h] * whole
+                tb[i, p, h] = nb[i, p, h] * (norm(v[i, p, h]) * bb * norm(Dk) + norm(kk) * row)
+                D = a[i, p, h] * (D - bb * np.outer(kk, Dk))
+    return tg, tb, last

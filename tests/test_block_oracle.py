@@ -121,3 +121,62 @@ def test_delta_overwrites_a_key():
     big = np.full((1, 2, 1), 40.0)
     o, last, _, _ = K.delta_forward(one, one, v, big, big, None, None, False, 1.0)
     assert np.allclose(o[0, :, 0, 0], [3, 5]) and np.allclose(last[0, 0, :, 0], [5, 0])
+
+
+def _delta_case(B, L, Hk, H, dk, dv, gate):
+    mk = lambda *s: rng.standard_normal(s)  # noqa: E731
+    unit = lambda t: t / np.linalg.norm(t, axis=-1, keepdims=True)  # noqa: E731
+    return ([unit(mk(B, L, Hk, dk)), unit(mk(B, L, Hk, dk)), mk(B, L, H, dv), 1.5 * mk(B, L, H) + gate, mk(B, L, H)],
+            0.3 * mk(B, H, dk, dv), mk(B, L, H, dv), mk(B, H, dk, dv), None, False, dk ** -0.5)
+
+
+def test_the_bounds_of_the_gates_gradients_see_mistakes():
+    """The bounds that the GPU tests hold dg and dbeta to: zeros, a wrong sign, 2 % too little and a missing <S_C, D>
+    are outside of them in some head at every size and gate. dg itself is below fp32's roundings of what it is
+    summed from where a gate lets nothing pass (-100); there only what is missing shows."""
+    pytest.importorskip("torch")
+    from tests.test_gpu_delta import GATES, gate_bounds
+    n = lambda t: np.sqrt((t * t).sum(1))  # noqa: E731
+    for size, gate in GATES:
+        args = _delta_case(*size, gate)
+        want = K.delta_backward(*args[0], *args[1:])[3:5]
+        _, _, last = K.delta_gate_bounds(*args[0], *args[1:])
+        for h in (2.0 ** -24, 2.0 ** -8):
+            tol = gate_bounds(*args, want, h)
+            for w, t in zip(want, tol):
+                if gate > -100 or w is want[1]:
+                    for wrong in (0 * w, -w, w * 0.98):
+                        assert (n(wrong - w) > t).any(), (size, gate, h)
+            assert (n(last) > tol[0]).any(), (size, gate, h)
+
+
+@pytest.mark.parametrize("lens,reverse", [(None, False), ([70, 3], True)])
+def test_the_gates_gradients_from_their_terms(lens, reverse):
+    """d log y_i = q.dq + k.row - k.col, summed from t to the chunk's end, and <S_C, D>: the identity that the bounds
+    (and the kernels) rest on, against the step-by-step gradient."""
+    args = list(_delta_case(2, 70, 1, 2, 8, 5, 1.0))
+    args[4], args[5] = lens, reverse
+    (q, k, v, g, be), s0, do, dl, _, _, scale = args
+    w = K.delta_backward(*args[0], *args[1:])
+    _, _, last = K.delta_gate_bounds(*args[0], *args[1:])
+    for i in range(2):
+        order = K._seq(70, 70 if lens is None else lens[i], reverse)
+        for h in range(2):
+            a, b = 1 / (1 + np.exp(-g[i, :, h])), 1 / (1 + np.exp(-be[i, :, h]))
+            run, D = [s0[i, h]], dl[i, h]
+            for p in order:
+                A = a[p] * run[-1]
+                run.append(A + b[p] * np.outer(k[i, p, 0], v[i, p, h] - k[i, p, 0] @ A))
+            tail = 0.0
+            for t in range(len(order) - 1, -1, -1):
+                p, kk, qq = order[t], k[i, order[t], 0], q[i, order[t], 0]
+                if t == len(order) - 1 or (t + 1) % K.CHUNK == 0:
+                    tail = (run[t + 1] * D).sum()
+                    assert np.isclose((1 - a[p]) * tail, last[i, p, h])
+                G = scale * do[i, p, h]
+                D = D + np.outer(qq, G)
+                A, Dk = a[p] * run[t], kk @ D
+                row, col = -b[p] * (A @ Dk), b[p] * (D @ (v[i, p, h] - kk @ A))
+                tail += qq @ (run[t + 1] @ G) + kk @ row - kk @ col
+                assert np.isclose((1 - a[p]) * tail, w[3][i, p, h], atol=1e-12)
+                D = a[p] * (D - b[p] * np.outer(kk, Dk))

@@ -567,3 +567,32 @@ def test_gradient_of_a_saturated_write_gate(L, dk, dv, dt):
     want, h = w[4], half(dt)
     near("dbeta", got, want, 256 * U * dv * nb * (M * MD)[:, None] * (1 + h) + (8 * U + h) * np.abs(want))
     assert np.all(got[0] != 0) and np.abs(want[0]).max() > 100 * np.abs(want[0]).min() > 0
+
+
+# With 3 as the gate at every size, and from nothing to everything at one.
+GATES = [(s, 3.0) for s in SIZES] + [((2, 150, 1, 2, 32, 24), g) for g in (-100.0, -6.0, 0.0, 12.0, 100.0)]
+
+
+def gate_bounds(x, s0, do, dl, lens, reverse, scale, want, h):
+    """How far dg and dbeta of a head may be off in norm: the terms of their sums are dot products that err by 256 half
+    steps of their factors' norms; the rest is a sum over 64 steps, the factors 1 - a and 1 - b (8 half
+    steps) and a rounding to fp32, 16 half steps of the result in all, before its own rounding."""
+    tg, tb, _ = K.delta_gate_bounds(*x, s0, do, dl, lens, reverse, scale)
+    n = lambda t: np.sqrt((t * t).sum(1))  # noqa: E731
+    return [256 * U * n(t) + (16 * U + h) * n(w) + 2.0 ** -126 * w.shape[1] ** 0.5 for t, w in zip((tg, tb), want)]
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("size,gate", GATES)
+def test_gate_gradients_of_each_head(size, gate, dt, reverse):
+    B, L, Hk, H, dk, dv = size
+    print(f"\n[case] delta gates {size} {gate} {dt} rev={reverse}", flush=True)
+    lens = [max(L - 7, 1)] * B if reverse else None
+    c = Case(*size, dt, reverse, lens, gate=gate, seed=241)
+    got = [f64(t) for t in c.backward(c.forward()[2])[3:5]]
+    args = [f64(t) for t in c.inputs()], f64(c.s0), f64(c.do), f64(c.dl), lens, reverse, dk ** -0.5
+    want = K.delta_backward(*args[0], *args[1:])[3:5]
+    for name, x, w, tol in zip(("dg", "dbeta"), got, want, gate_bounds(*args, want, half(dt))):
+        off = np.sqrt(((x - w) ** 2).sum(1))
+        assert np.all(off <= tol), (name, off / tol)
