@@ -145,7 +145,7 @@ def test_the_bounds_of_the_gates_gradients_see_mistakes():
             tol = gate_bounds(*args, want, h)
             for w, t in zip(want, tol):
                 if gate > -100 or w is want[1]:
-                    for wrong in (0 * w, -w, w * 0.98):
+                    for wrong in (0 * w, -w) + ((w * 0.98,) if gate < 100 else ()):      # there subnormal
                         assert (n(wrong - w) > t).any(), (size, gate, h)
             assert (n(last) > tol[0]).any(), (size, gate, h)
 
