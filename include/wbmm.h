@@ -576,9 +576,10 @@ wbmm_status wbmm_adamw_step(const void* table, int64_t count, int64_t chunks, do
  *           WBMM_DELTA_CHUNK, ... in the order the sequence runs (its last state past its end).
  * workspace: wbmm_delta_forward_workspace_bytes(...) bytes, 16-byte aligned (NULL when 0: up to 8
  *           steps). Calls that share one must be ordered on one stream.
- * An infinity or NaN in q reaches its own o; in k, v, g, beta or the state it makes o of the head NaN from
- * the chunk of WBMM_DELTA_CHUNK steps on that it lies in (in v and in a column of the state: in its own
- * column). No atomics: bitwise reproducible.
+ * An infinity or NaN in q reaches its own o; one in k, v or the state, and a NaN in g or beta (infinite ones are
+ * gates as any other), makes o of the head NaN from the chunk of WBMM_DELTA_CHUNK steps on that it lies in
+ * (in v and in a column of the state: in its own column). fp32 numbers that bf16 has no finite value for
+ * (3.39e38 and more) may count as infinite. No atomics: bitwise reproducible.
  * Errors: WBMM_E_INVALID (sizes, dtype, scale, NULL or overlapping buffers), WBMM_E_UNSUPPORTED (dk or dv >
  * 128, Hk dk or H dv > 2^22, more than 2^22 chunks over all heads, L > 2^28, misaligned pointer),
  * WBMM_E_WORKSPACE, WBMM_E_HIP.
@@ -607,7 +608,9 @@ wbmm_status wbmm_delta_forward(int64_t B, int64_t L, int Hk, int H, int dk, int 
  * dq, dk, dv, dg, dbeta: device tensors in dtype, written; 0 past the end of a sequence. ds0: device fp32
  *           [B][H][dk][dv], written, or NULL; may be ds_last itself.
  * workspace: wbmm_delta_backward_workspace_bytes(...) bytes, 16-byte aligned.
- * An infinity or NaN makes the gradients of its head NaN where they depend on it, in whole chunks.
+ * An infinity or NaN makes the gradients of its head NaN where they depend on it, in whole chunks (g and
+ * beta: a NaN). dg is (1 - a) times a sum over a chunk's steps, good to the last bits of its largest terms:
+ * where a gate forgets nearly everything (g below -10) the sum itself may be smaller than those.
  * Errors as in the forward; also WBMM_E_INVALID for s0 beside states.
  */
 size_t wbmm_delta_backward_workspace_bytes(int64_t B, int64_t L, int Hk, int H, int dk, int dv,
