@@ -685,7 +685,7 @@ hipError_t walk_one(const DeltaArgs& a, hipStream_t st) {
 }
 template <typename T>
 hipError_t walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
-  const bool two = walk_two_tiles(a);
+  const bool two = walk_two_tiles_forward(a, sizeof(T) == 2);
   hipError_t e = hipSuccess;
   with_dk<T>(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;

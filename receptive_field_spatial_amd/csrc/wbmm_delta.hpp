@@ -104,15 +104,26 @@ constexpr size_t kDeltaTtBytes = (size_t)kDeltaFrags * 1024 * 3;
 
 DeltaArgs delta_args(const DeltaRequest& r);
 // Tiles of 16 columns that a workgroup of the walks takes. More than one share its operands (K, T and P in registers
-// and LDS) and fill each other's waits; they pay where tiles outnumber the CUs: 512 steps, dk = dv = 64,
-// bf16, us forward and backward of one against two: 288 tiles 20.6, 32.7 against 19.8, 25.2, 768 48.5, 68.0 against
-// 33.6, 50.5; up to 256 a tile each is the shorter walk: 14.6, 19.0 against 19.2, 24.6. fp32 288: 41.8, 59.3 against
-// 27.3, 40.3. Of the measured ones only bf16 with dk = 128 and 640 tiles loses (forward 44.0 against 51.2). The
-// backward, of which a CU holds one workgroup, takes four from 513 tiles on where LDS has room (bf16 with dk <= 64,
-// fp32 with dk <= 32; bf16, 784 steps): 768 tiles 80 against 88, 1024 85 against 112, 512 57 against 45.
+// and LDS) and fill each other's waits; they pay where tiles outnumber the CUs. us of whole calls over 512 steps, dv = 64,
+// one against two tiles, forward and backward: bf16, dk = 64, 640 tiles 50.1, 122.9 against 46.9, 122.7, 1024 62.3,
+// 188.7 against 54.0, 175.5; 288 34.6, 80.0 against 34.9, 73.5; fp32 288 56.1, 122.8 against 42.4, 104.9, 1024
+// 117.1, 309.9 against 90.4, 276.1. Up to 256 tiles one each is the shorter walk: bf16, dk = 64, 256 tiles 28.5, 54.9
+// against 34.0, 62.0.
+// The forward of bf16 with dk > 64 has two workgroups of one tile on a CU, or one of two: there two tiles pay where each
+// has a CU of its own (512 tiles of dv = 128: 43.2 for 44.8) and, with the rounds' ends, from 2.75 rounds of them on (1408
+// tiles of 64 127.0 for 136.4, of 128 107.4 for 106.4; 2048 180.8 for 210.3, 145.8 for 154.8), not in between (640 77.8 for
+// 67.0, 69.7 for 58.8; 1280 122.7 for 120.2, 105.7 for 94.7).
+// The backward, of which a CU holds one workgroup, takes four where two do not fit a round and LDS has room (bf16
+// with dk <= 64, fp32 with dk <= 32): bf16, dk = 64, four against two: 512 tiles 98.1 against 87.4, 640 114.4 against 122.7,
+// 2048 345 against 374; fp32, dk = 32, 512 117.2 against 106.8, 640 136.4 against 157.6.
+constexpr int64_t kDeltaCus = 256;         // of the chip
 inline int64_t walk_tiles(const DeltaArgs& a) { return (int64_t)a.B * a.H * (a.dv / 16); }
-inline bool walk_two_tiles(const DeltaArgs& a) { return a.dv % 32 == 0 && walk_tiles(a) > 256; }
-inline bool walk_four_tiles(const DeltaArgs& a) { return a.dv % 64 == 0 && walk_tiles(a) > 512; }
+inline bool walk_two_tiles(const DeltaArgs& a) { return a.dv % 32 == 0 && walk_tiles(a) > kDeltaCus; }
+inline bool walk_four_tiles(const DeltaArgs& a) { return a.dv % 64 == 0 && walk_tiles(a) > 2 * kDeltaCus; }
+inline bool walk_two_tiles_forward(const DeltaArgs& a, bool bf16) {
+  const int64_t groups = ((int64_t)a.B * a.H + 7) / 8 * 8 * (a.dv / 32);   // as launched, whole octets of heads
+  return walk_two_tiles(a) && (!bf16 || a.dk <= 64 || groups <= kDeltaCus || 4 * groups >= 11 * kDeltaCus);
+}
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool vec, DeltaPrep mode, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, bool vec, hipStream_t st);
 // 16 bytes at a time of everything that lies in rows of dk or dv.

@@ -596,3 +596,17 @@ def test_gate_gradients_of_each_head(size, gate, dt, reverse):
     for name, x, w, tol in zip(("dg", "dbeta"), got, want, gate_bounds(*args, want, half(dt))):
         off = np.sqrt(((x - w) ** 2).sum(1))
         assert np.all(off <= tol), (name, off / tol)
+
+
+@pytest.mark.parametrize("B,dv", [(64, 128), (70, 128), (90, 96), (180, 128)])
+def test_large_batches_of_wide_keys(B, dv):
+    """bf16 with 128 key entries, on either side of where a workgroup takes two tiles: each sequence as in a batch of its
+    own, of which a tile is a workgroup's."""
+    c = Case(B, 130, 1, 1, 128, dv, BF16, seed=251)
+    out = c.forward()
+    gr = c.backward(None)
+    for b in (0, B // 2, B - 1):
+        one = Case(1, 130, 1, 1, 128, dv, BF16)
+        for n in ("q", "k", "v", "g", "beta", "s0", "do", "dl"):
+            setattr(one, n, getattr(c, n)[b:b + 1].contiguous())
+        assert all(torch.equal(a[b:b + 1], x) for a, x in zip((*out, *gr), (*one.forward(), *one.backward(None))))
