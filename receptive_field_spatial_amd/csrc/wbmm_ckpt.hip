@@ -48,13 +48,6 @@ __device__ __forceinline__ void load8(const T* __restrict__ p, size_t e, size_t 
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f2bf(v); }
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {  // over the lane's group of four lanes
-  const uint32_t a = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xf, 0xf, true);
-  x = x > a ? x : a;
-  const uint32_t b = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xf, 0xf, true);
-  return x > b ? x : b;
-}
-
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_ckpt_pack(const T* __restrict__ x, size_t n,
                                                         uint8_t* __restrict__ codes,
@@ -72,26 +65,17 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(const T* __restrict__ x,
       const uint32_t b = __float_as_uint(v[q][j]) & 0x7fffffffu;
       m = b > m ? b : m;
     }
-    m = quad_max(m);
+    m = ckpt_quad_max(m);
     const bool bad = m >= 0x7f800000u;
-    const uint32_t over = FMT == kFmtInt8 ? 0x7e0000u : 0x600000u;
-    int byte = (int)(m >> 23) - (FMT == kFmtInt8 ? 6 : 8) + ((m & 0x7fffffu) > over ? 1 : 0);
-    byte = byte < 1 ? 1 : byte;
-    const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
+    const int byte = ckpt_scale_byte(bad ? 0 : m, FMT);
+    const float inv = ckpt_inverse(byte);
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] = bad ? 0.f : v[q][4 * h + j] * inv;
-      if constexpr (FMT == kFmtInt8) {
-        w[h] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[h] |= ((uint32_t)(int)rintf(s[j]) & 0xffu) << (8 * j);
-      } else {
-        int p = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
-        w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], p, true);
-      }
+      w[h] = ckpt_encode4(s, FMT);
     }
     if (VEC && e + kE <= n) {
       *(uint2*)(codes + e) = make_uint2(w[0], w[1]);

@@ -648,20 +648,9 @@ constexpr int kDeltaSteps = 8;
 
 int64_t chunks_of(int64_t L) { return (L + kDeltaChunk - 1) / kDeltaChunk; }
 
-template <typename T, typename F>
-void with_dk(int dk, bool vec, F f) {
-  auto go = [&](auto d) {
-    if (vec) f(d, std::true_type());
-    else f(d, std::false_type());
-  };
-  if (dk <= 32) go(std::integral_constant<int, 32>());
-  else if (dk <= 64) go(std::integral_constant<int, 64>());
-  else go(std::integral_constant<int, 128>());
-}
-
 template <typename T, DeltaPrep MODE>
 void prep_t(const DeltaArgs& a, bool vec, hipStream_t st) {
-  with_dk<T>(a.dk, vec, [&](auto d, auto v) {
+  with_dk(a.dk, vec, [&](auto d, auto v) {
     k_delta_prep<T, decltype(d)::value, decltype(v)::value, MODE>
         <<<dim3(a.B * a.H * a.chunks), 256, 0, st>>>(a);
   });
@@ -687,7 +676,7 @@ template <typename T>
 hipError_t walk_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   const bool two = walk_two_tiles_forward(a, sizeof(T) == 2);
   hipError_t e = hipSuccess;
-  with_dk<T>(a.dk, vec, [&](auto d, auto v) {
+  with_dk(a.dk, vec, [&](auto d, auto v) {
     constexpr int DK = decltype(d)::value;
     constexpr bool VEC = decltype(v)::value;
     if constexpr (VEC) {

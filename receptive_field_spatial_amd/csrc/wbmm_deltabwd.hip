@@ -797,17 +797,6 @@ __global__ void __launch_bounds__(512, (DK < 128 && DeltaType<T, VEC>::PI == 1 ?
   }
 }
 
-template <typename F>
-void with_dk(int dk, bool vec, F f) {
-  auto go = [&](auto d) {
-    if (vec) f(d, std::true_type());
-    else f(d, std::false_type());
-  };
-  if (dk <= 32) go(std::integral_constant<int, 32>());
-  else if (dk <= 64) go(std::integral_constant<int, 64>());
-  else go(std::integral_constant<int, 128>());
-}
-
 template <typename T>
 hipError_t backward_t(const DeltaArgs& a, bool vec, hipStream_t st) {
   hipError_t e = hipSuccess;

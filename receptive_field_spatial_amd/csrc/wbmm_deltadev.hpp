@@ -360,4 +360,16 @@ __device__ __forceinline__ Frag<P> mem_frag(const unsigned char* base, int f, in
   return r;
 }
 
+// Calls f with the next of the three widths of a key that kernels are made for, and with VEC.
+template <typename F>
+inline void with_dk(int dk, bool vec, F f) {
+  auto go = [&](auto d) {
+    if (vec) f(d, std::true_type());
+    else f(d, std::false_type());
+  };
+  if (dk <= 32) go(std::integral_constant<int, 32>());
+  else if (dk <= 64) go(std::integral_constant<int, 64>());
+  else go(std::integral_constant<int, 128>());
+}
+
 }  // namespace wbmm
