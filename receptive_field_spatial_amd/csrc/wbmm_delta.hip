@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(256, (DeltaType<T, VEC>::PI == 1 ? 4 : DK < 12
 //   C    S = y_C S + K^T diag(y_C / y) U            o = scale (diag(y) Q S + P U)
 // Loads are issued a chunk before their use, right after the last use of their registers.
 // Bound by the length of a chunk's chain: three LDS round trips, four products one after the other and three
-// splittings into bf16 parts, 1.5 to 2 us a chunk of which loads that always hit would save 0.1. So 4 x 8 heads of
-// 128 over 8192 steps (128 chunks, one workgroup a CU) take 245 us, a single head 207; 192 heads of 64 over
-// 784 steps 43.5, with one tile a workgroup 66. K S formed from a walker's own rows of S and K from registers, the
-// parts joined in LDS, measured 183 for the single head, but 250 to 260 for 4 x 8.
+// splittings into bf16 parts, 1.9 to 2.2 us a chunk of which loads that always hit would save 0.1. So 4 x 8 heads of
+// 128 over 8192 steps (128 chunks, one workgroup a CU) take 284 us, a single head 238; 192 heads of 64 over
+// 784 steps 50, with one tile a workgroup 55 to 60. With o from two parts of S, U and P, which lose what a bf16 o shows
+// where a key is overwritten, these were 245, 207 and 43.5 (the helpers' products and LDS reads); Q S over two phases,
+// U shared in fp32 and parted by the helpers, or P parted a phase earlier gain nothing. K S formed from a walker's own rows
+// of S and K from registers, the parts joined in LDS, measured 183 for 207, but 250 to 260 for the 4 x 8's 245.
 // LDS of a workgroup. Two chunks' K^T, where they fit (all but fp32 with 96 < dk): the next one is then
 // written while this one is read, and K is loaded a whole chunk ahead.
 template <typename T, int DK, int NC>
@@ -543,7 +545,8 @@ __global__ void __launch_bounds__(512, (NC == 2 && DK <= 64 && DeltaType<T, VEC>
 }
 // ---------------------------------------------------------------------------- single steps
 // One launch, S in registers; a step is two sums across the wave one after the other, 0.9 us (1.1 with dk = 128).
-// 48 heads of 64 x 64, one step: 5.2 us; 2048 heads of 128 x 128 are bound by S in and out: 117 us, 2.3 TB/s.
+// 48 heads of 64 x 64, one step: 5.1 us; 2048 heads of 128 x 128 118 us, 2.3 TB/s, 44 % of what a copy reaches: S comes
+// and goes in 64-byte pieces of its rows by accesses of 4 bytes.
 // A wave per head and 16 columns: lane 4 i + c has rows i, i + 16, ... of four of them in registers.
 template <typename T, int RW>
 __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
@@ -642,8 +645,8 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
 }
 
 // Longest sequences that go step by step. A step adds 0.9 to 1.1 us to one launch, a chunk costs two launches
-// whatever its length: 8 steps of 64 sequences, 3 heads of 64, 12.8 us for 14.9 (12: 16.5 for 14.9); 8 x 6 heads
-// of 64 11.1 for 10.3, 8 heads of 128 14.1 for 11.6, 256 x 8 of them 153 for 206.
+// whatever its length. us for 4, 8 and 12 steps, chunks: 64 x 3 heads of 64 8.9, 12.3, 16.0, 14.0; 8 x 6 of them
+// 7.3, 10.7, 14.4, 10.5; 8 x 8 heads of 128 11.3, 16.1, 20.7, 14.0, 256 x 8 of them 130, 154, 182, 214.
 constexpr int kDeltaSteps = 8;
 
 int64_t chunks_of(int64_t L) { return (L + kDeltaChunk - 1) / kDeltaChunk; }

@@ -14,8 +14,8 @@ namespace {
 //   B    R = T^T dU (= dv)                               P^T G, K, K^T, Q^T and diag(y) G of the next chunk
 //   C    D = y_C D + M - K^T diag(y) R                   do of the one after
 // D after each chunk and R stay in the workspace for k_delta_grads. Bound as the forward's, with D and R to store:
-// 192 heads of 64, 784 steps, bf16: 70 to 79 us with four tiles a workgroup, 88 with two, 104 with one; 30 heads of 48 x 40
-// over 1531 steps, fp32: 75 us, 3.1 a chunk.
+// 192 heads of 64, 784 steps, bf16: 70 to 75 us with four tiles a workgroup, 85 to 88 with two, 98 to 102 with one; 30 heads
+// of 48 x 40 over 1531 steps, fp32: 75 us, 3.1 a chunk.
 template <typename T, int DK, int NC>
 struct BackLds {
   static constexpr int PI = DeltaType<T, true>::PI, KS = DK / 32, NT = DK / 16;
@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(512) k_delta_walk_bwd(DeltaArgs a) {
 // One workgroup of 8 waves per chunk of a key head, its heads one after the other. Wave (w, hf) has row
 // tile w of the 64 steps, and of everything along dk the half hf; the (64 x 64) dP is hf = 0's and N hf =
 // 1's. dv is walked in pieces of 32 columns, whose S0 and D are staged in LDS as operands. Bound by vector
-// issue (1500 instructions a wave and chunk, 53 % of the cycles; the matrix cores 12 %): splitting S0, D, dP and N,
-// transposes, decays, row sums. 2496 chunks of one head of 64, bf16: 110 us; 240 of three heads, fp32: 49.
+// issue (2000 instructions a wave and chunk, 59 % of the cycles; the matrix cores 17 %): splitting S0, D, dP and N,
+// transposes, decays, row sums. 2496 chunks of one head of 64, bf16: 132 us (110 with two parts of what now has three);
+// 240 of three heads, fp32: 47.
 template <typename T, int DK, bool VEC>
 struct GradLds {
   static constexpr int PI = DeltaType<T, VEC>::PI, NT = DK / 16, KS = DK / 32;

@@ -15,8 +15,11 @@
 //           there; the waves' sums meet in LDS.
 // Longer axes than the registers hold are read twice, the second time from a cache.
 //
-// Measured: forward bf16 with codes, 50176 rows of 192, 17.0 us (87 MB, 5.1 TB/s); backward fp32, 128 x 96 x
-// 3136, 115 us (617 MB, 5.4 TB/s) and 4.4 for dw's partials; single rows 2 us, a launch's own time.
+// Measured: forward bf16 with codes, 50176 rows of 192, 17.5 us (87 MB, 5.0 TB/s); backward fp32, 128 x 96 x
+// 3136, 110 to 113 us (617 MB, 5.5 TB/s, part of it from the last-level cache) and 4.4 for dw's partials; single rows 2 us, a
+// launch's own time. Far from that: columns of more than 256 entries (forward 512), read twice, 128 x 384 x 196 bf16
+// forward 27 us, backward 54 (77 MB each); few columns, 8 x 768 x 49 bf16 35 and 44 us on 7 workgroups; rows of more than
+// 6144, 2000 of 8192 bf16 42 and 194 us (131 MB each).
 //
 // dw: fp64 sums of fp32 products, then partials of a workgroup, added in a fixed order by a second launch.
 #include "wbmm_ckpt.hpp"
